@@ -16,6 +16,12 @@ Use (torch tensors on the current device, the current stream)::
     binding.compress_norm_rope_store_ex(cfg, token_to_req_indices, positions, slot_mapping, block_table,
                                         state_cache, rms_w, eps, cos_sin_cache, k_cache,
                                         kv_slot_mapping, kv_block_size)
+    # around it: block tables and per-token arrays on the GPU, attention over the cache it writes
+    binding.extend_block_tables(seq_lens, held, block_table, free_blocks, taken, compress_ratio, block_size)
+    binding.build_slot_maps(seq_lens, query_lens, state_table, 8, kv_table, kv_block_size, 128, query_start,
+                            token_to_req_indices, positions, slot_mapping, kv_slot_mapping, kv_lens)
+    binding.decode_attention(q, k_cache, kv_block_size, kv_table, kv_lens, scale, out, lse=lse, sink=sink)
+    binding.merge_attention(part_out, part_lse, out, lse=lse)
     bits = binding.device_errors()      # out-of-range indices (tokens skipped), wait time-outs
 
 Calls are asynchronous and CUDA-graph capturable after ``binding.reserve_workspace(max_tokens)``;
@@ -23,7 +29,8 @@ Calls are asynchronous and CUDA-graph capturable after ``binding.reserve_workspa
 """
 import importlib
 
-__all__ = ["compress_norm_rope_store", "compress_norm_rope_store_ex"]
+__all__ = ["compress_norm_rope_store", "compress_norm_rope_store_ex", "extend_block_tables", "build_slot_maps",
+           "decode_attention", "merge_attention"]
 
 
 def __getattr__(name):

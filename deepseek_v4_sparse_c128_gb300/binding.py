@@ -13,14 +13,15 @@ from typing import Optional
 
 from . import build as _build
 
-C128_I32, C128_I64, C128_F32, C128_U8 = 1, 2, 3, 4
+C128_I32, C128_I64, C128_F32, C128_U8, C128_BF16 = 1, 2, 3, 4, 5
 STATUS = {
     0: "C128_OK", 1: "C128_ERR_NULL_PTR", 2: "C128_ERR_DTYPE", 3: "C128_ERR_SHAPE", 4: "C128_ERR_STRIDE",
     5: "C128_ERR_ALIGN", 6: "C128_ERR_UNSUPPORTED", 7: "C128_ERR_ARG", 8: "C128_ERR_CUDA", 9: "C128_ERR_NOMEM",
     10: "C128_ERR_TOO_MANY_TOKENS", 11: "C128_ERR_CAPTURE",
 }
 NOALLOC_MAX_TOKENS = 65536  # C128_NOALLOC_MAX_TOKENS
-DEV_BITS = {1: "BAD_REQ", 2: "BAD_BT_COL", 4: "BAD_BLOCK", 8: "BAD_COS_ROW", 16: "BAD_KV_SLOT", 32: "TIMEOUT"}
+DEV_BITS = {1: "BAD_REQ", 2: "BAD_BT_COL", 4: "BAD_BLOCK", 8: "BAD_COS_ROW", 16: "BAD_KV_SLOT", 32: "TIMEOUT",
+            64: "NO_FREE_BLOCK", 128: "BAD_LENGTH"}
 
 # Every entry point the header declares, with its ctypes signature.
 EXPORTS = (
@@ -39,6 +40,11 @@ EXPORTS = (
     "c128_get_info",
     "c128_read_probe",
     "c128_release_all",
+    "c128_extend_block_tables",
+    "c128_build_slot_maps",
+    "c128_decode_attention",
+    "c128_decode_attention_workspace",
+    "c128_merge_attention",
 )
 
 
@@ -111,6 +117,11 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     i32 = ctypes.c_int32
     L.c128_read_probe.argtypes = [vp, i64, i32, i32, i32, vp, vp]
     L.c128_release_all.argtypes = []
+    L.c128_extend_block_tables.argtypes = [T, T, T, T, T, i32, i64, T, T, vp]
+    L.c128_build_slot_maps.argtypes = [T, T, T, i64, T, i64, i32, T, T, T, T, T, T, vp]
+    L.c128_decode_attention.argtypes = [T, T, i64, T, T, ctypes.c_float, T, T, T, T, vp]
+    L.c128_decode_attention_workspace.argtypes = [i64, ctypes.POINTER(i64)]
+    L.c128_merge_attention.argtypes = [T, T, T, T, vp]
     for name in EXPORTS:
         if name != "c128_status_string":
             getattr(L, name).restype = ctypes.c_int
@@ -131,7 +142,7 @@ def _dtype_code(t) -> int:
     import torch
     if _TORCH_DTYPES is None:
         _TORCH_DTYPES = {torch.int32: C128_I32, torch.int64: C128_I64, torch.float32: C128_F32,
-                         torch.uint8: C128_U8}
+                         torch.uint8: C128_U8, torch.bfloat16: C128_BF16}
     if t.dtype not in _TORCH_DTYPES:
         raise TypeError(f"unsupported dtype {t.dtype}")
     return _TORCH_DTYPES[t.dtype]
@@ -282,6 +293,122 @@ class PreparedCall:
         rc = self._fn(*self._args)
         if rc != 0:
             raise C128Error(rc, self._name)
+
+
+# ------------------------------------------------------------- the operators around the compressor
+def _refs(*tensors):
+    """Descriptors of the tensors (None stays None), which all have to be on the current CUDA device."""
+    import torch
+    current = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got one on {t.device}")
+        current = torch.cuda.current_device() if current is None else current
+        if t.device.index != current:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{current}")
+    return [None if t is None else ctypes.byref(describe(t)) for t in tensors]
+
+
+def _extend_block_tables(seq_lens, held, block_table, free_blocks, taken, compress_ratio: int, block_size: int,
+                         held_out=None, taken_out=None):
+    held_out = held if held_out is None else held_out
+    taken_out = taken if taken_out is None else taken_out
+    a = _refs(seq_lens, held, block_table, free_blocks, taken, held_out, taken_out)
+    return "c128_extend_block_tables", (*a[:5], int(compress_ratio), int(block_size), *a[5:]), ()
+
+
+def _build_slot_maps(seq_lens, query_lens, state_table, state_block: int, kv_table, kv_block_size: int,
+                     compress_ratio: int, query_start, token_to_req_indices, positions, slot_mapping, kv_slot_mapping,
+                     kv_lens):
+    a = _refs(seq_lens, query_lens, state_table, kv_table, query_start, token_to_req_indices, positions, slot_mapping,
+              kv_slot_mapping, kv_lens)
+    return "c128_build_slot_maps", (*a[:3], int(state_block), a[3], int(kv_block_size), int(compress_ratio), *a[4:]), ()
+
+
+def _decode_attention(q, k_cache, kv_block_size: int, block_table, kv_lens, scale: float, out, lse=None, sink=None,
+                      workspace=None):
+    import torch
+    if workspace is None:
+        workspace = torch.empty(decode_attention_workspace(q.shape[1]), dtype=torch.uint8, device=q.device)
+    a = _refs(q, k_cache, block_table, kv_lens, sink, out, lse, workspace)
+    return "c128_decode_attention", (*a[:2], int(kv_block_size), *a[2:4], float(scale), *a[4:]), (workspace,)
+
+
+def _merge_attention(part_out, part_lse, out, lse=None):
+    return "c128_merge_attention", (*_refs(part_out, part_lse, out, lse),), ()
+
+
+_OPS = {"extend_block_tables": _extend_block_tables, "build_slot_maps": _build_slot_maps,
+        "decode_attention": _decode_attention, "merge_attention": _merge_attention}
+
+
+class PreparedOp:
+    """One of the operators below with its descriptors built once, for repeated calls on the same
+    tensors: ``PreparedOp("decode_attention", q, k_cache, ...)`` takes the arguments of the function
+    of that name, and calling the object is a single C-ABI call. The tensors must stay alive and keep
+    their storage; the stream is fixed when the object is built (default: the current torch stream).
+    A ``decode_attention`` without a ``workspace`` gets one of its own, kept with the object."""
+
+    def __init__(self, op: str, *args, stream=None, **kw):
+        self._name, c_args, owned = _OPS[op](*args, **kw)
+        self._keep = (args, kw, owned)
+        self._fn = getattr(lib(), self._name)
+        self._args = (*c_args, _stream_handle(stream))
+
+    def __call__(self) -> None:
+        rc = self._fn(*self._args)
+        if rc != 0:
+            raise C128Error(rc, self._name)
+
+
+def extend_block_tables(seq_lens, held, block_table, free_blocks, taken, compress_ratio: int, block_size: int,
+                        held_out=None, taken_out=None, stream=None) -> None:
+    """Give every request the blocks its length now needs, out of ``free_blocks[taken:]``, in place in
+    ``block_table`` (c128_extend_block_tables in include/c128compress.h). ``held`` and ``taken`` are
+    updated in place unless ``held_out`` / ``taken_out`` are given."""
+    PreparedOp("extend_block_tables", seq_lens, held, block_table, free_blocks, taken, compress_ratio, block_size,
+               held_out=held_out, taken_out=taken_out, stream=stream)()
+
+
+def build_slot_maps(seq_lens, query_lens, state_table, state_block: int, kv_table, kv_block_size: int,
+                    compress_ratio: int, query_start, token_to_req_indices, positions, slot_mapping, kv_slot_mapping,
+                    kv_lens, stream=None) -> None:
+    """The per-token arrays that compress_norm_rope_store takes for one step, from the requests'
+    lengths and block tables (c128_build_slot_maps in include/c128compress.h). The last six tensors
+    are written."""
+    PreparedOp("build_slot_maps", seq_lens, query_lens, state_table, state_block, kv_table, kv_block_size,
+               compress_ratio, query_start, token_to_req_indices, positions, slot_mapping, kv_slot_mapping, kv_lens,
+               stream=stream)()
+
+
+def decode_attention_workspace(num_heads: int) -> int:
+    """Bytes of workspace a decode_attention call with ``num_heads`` heads needs."""
+    n = ctypes.c_int64(0)
+    _check(lib().c128_decode_attention_workspace(int(num_heads), ctypes.byref(n)), "c128_decode_attention_workspace")
+    return n.value
+
+
+def decode_attention(q, k_cache, kv_block_size: int, block_table, kv_lens, scale: float, out, lse=None, sink=None,
+                     workspace=None, stream=None) -> None:
+    """Attention of one new token per request over its entries of the paged FP8 ``k_cache``
+    (c128_decode_attention in include/c128compress.h); ``out`` and ``lse`` are written. ``workspace``
+    (uint8, decode_attention_workspace bytes) is scratch; without one the call takes one from torch's
+    allocator."""
+    if workspace is None:
+        import torch
+        workspace = torch.empty(decode_attention_workspace(q.shape[1]), dtype=torch.uint8, device=q.device)
+        if stream is not None:  # the allocator must not hand it out again before that stream is done with it
+            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    PreparedOp("decode_attention", q, k_cache, kv_block_size, block_table, kv_lens, scale, out, lse=lse, sink=sink,
+               workspace=workspace, stream=stream)()
+
+
+def merge_attention(part_out, part_lse, out, lse=None, stream=None) -> None:
+    """Join attentions over different sets of entries by their log-sum-exp (c128_merge_attention in
+    include/c128compress.h); ``out`` and ``lse`` are written."""
+    PreparedOp("merge_attention", part_out, part_lse, out, lse=lse, stream=stream)()
 
 
 def call_status(*args, **kw) -> int:

@@ -8,11 +8,13 @@
 #include <utility>
 #include <vector>
 
+#include "c128_check.h"
 #include "c128_internal.h"
 #include "c128compress.h"
 
 namespace {
 
+using namespace c128::check;
 using c128::WsHeader;
 
 constexpr int kVersion = 1;
@@ -95,39 +97,6 @@ int workspace_for(int dev, cudaStream_t stream, int64_t tokens, WsHeader** out) 
   *out = w.ptr;
   return C128_OK;
 }
-
-// ----------------------------------------------------------------------- descriptor checks
-int check_desc(const c128_tensor_t* t, int dtype, int ndim) {
-  if (t == nullptr) return C128_ERR_NULL_PTR;
-  if (t->dtype != dtype) return C128_ERR_DTYPE;
-  if (t->ndim != ndim) return C128_ERR_SHAPE;
-  for (int i = 0; i < ndim; ++i)
-    if (t->shape[i] < 0) return C128_ERR_SHAPE;
-  return C128_OK;
-}
-int64_t numel(const c128_tensor_t* t) {
-  int64_t n = 1;
-  for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
-  return n;
-}
-int check_data(const c128_tensor_t* t) {
-  if (numel(t) > 0 && t->data == nullptr) return C128_ERR_NULL_PTR;
-  return C128_OK;
-}
-int check_vector(const c128_tensor_t* t, int dtype, int64_t n) {
-  int rc = check_desc(t, dtype, 1);
-  if (rc) return rc;
-  if (t->shape[0] != n) return C128_ERR_SHAPE;
-  if (n > 1 && t->stride[0] != 1) return C128_ERR_STRIDE;
-  return check_data(t);
-}
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-#define C128_TRY(expr)         \
-  do {                         \
-    const int rc_ = (expr);    \
-    if (rc_ != C128_OK) return rc_; \
-  } while (0)
 
 // Bytes of token data and of scales per k_cache slot, per cache format.
 int64_t token_bytes(int fmt) { return fmt == C128_FORMAT_SPARSE_FP8 ? c128::kTokenStride : fmt == C128_FORMAT_INDEXER_FP8 ? 128 : 64; }
@@ -300,6 +269,23 @@ int validate_args(const c128_tensor_t* ttr, const c128_tensor_t* pos, const c128
                   const c128_tensor_t* cs, const c128_tensor_t* kc, const c128_tensor_t* kvslot,
                   int64_t kv_block_size, const c128_tensor_t* comp_out, Params* out, const c128_config_t* cfg) {
   return validate_call(ttr, pos, slot, bt, state, rms_w, eps, cs, kc, kvslot, kv_block_size, comp_out, out, cfg);
+}
+
+int stream_errors(cudaStream_t stream, unsigned int** err, int* sm_count) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return C128_ERR_CUDA;
+  try {
+    std::lock_guard<std::mutex> lk(g_mu);
+    DeviceInfo* di = nullptr;
+    C128_TRY(device_info(dev, &di));
+    WsHeader* ws = nullptr;
+    C128_TRY(workspace_for(dev, stream, 1, &ws));
+    *err = &ws->err;
+    *sm_count = di->sm_count;
+  } catch (...) {  // the maps' node allocations
+    return C128_ERR_NOMEM;
+  }
+  return C128_OK;
 }
 }  // namespace c128
 

@@ -114,6 +114,10 @@ int validate_args(const c128_tensor_t* ttr, const c128_tensor_t* pos, const c128
                   int64_t kv_block_size, const c128_tensor_t* comp_out, Params* out,
                   const c128_config_t* cfg = nullptr);
 
+// The sticky error word of the (current device, stream) workspace, which is made if the stream has
+// none (C128_ERR_CAPTURE while it is being captured), and the device's number of SMs.
+int stream_errors(cudaStream_t stream, unsigned int** err, int* sm_count);
+
 // Enqueue zeroing of the per-call counters, the planning kernel and the compress kernel.
 cudaError_t launch(const Params& p, const LaunchCfg& cfg, cudaStream_t stream);
 // The kernels for configurations other than C128 (after plan_kernel): windows of at most 8 rows

@@ -1,0 +1,131 @@
+// c128_merge_attention: partial attentions joined by their log-sum-exp. With top = max_p lse_p and
+// w_p = exp(lse_p - top): out = sum_p w_p o_p / sum_p w_p, lse = top + log(sum_p w_p).
+//
+// A pass over memory and nothing else: 1 KB per part and row read, 1 KB written. One warp per row of
+// 512 values, 16 per lane in two 16-byte pieces (bf16), so that each load of a warp covers 512
+// consecutive bytes and the loads of four parts are in flight before the first is used.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "c128_serving.h"
+
+namespace c128 {
+namespace {
+
+constexpr int kMergeThreads = 256;
+
+// Values [c, c + 8) of a row.
+template <bool F32>
+struct Piece;
+template <>
+struct Piece<true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* row, int c) {
+    a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(row) + c));
+    b = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(row) + c) + 1);
+  }
+  __device__ __forceinline__ void add(float w, float (&acc)[8]) const {
+    acc[0] = fmaf(w, a.x, acc[0]), acc[1] = fmaf(w, a.y, acc[1]), acc[2] = fmaf(w, a.z, acc[2]), acc[3] = fmaf(w, a.w, acc[3]);
+    acc[4] = fmaf(w, b.x, acc[4]), acc[5] = fmaf(w, b.y, acc[5]), acc[6] = fmaf(w, b.z, acc[6]), acc[7] = fmaf(w, b.w, acc[7]);
+  }
+};
+template <>
+struct Piece<false> {
+  uint4 a;
+  __device__ __forceinline__ void load(const void* row, int c) {
+    a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c));
+  }
+  __device__ __forceinline__ void add(float w, float (&acc)[8]) const {
+    const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[2 * i] = fmaf(w, __uint_as_float(v[i] << 16), acc[2 * i]);
+      acc[2 * i + 1] = fmaf(w, __uint_as_float(v[i] & 0xffff0000u), acc[2 * i + 1]);
+    }
+  }
+};
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+template <bool PART_F32, bool OUT_F32>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
+  if (row >= p.requests * p.heads) return;
+  const int64_t r = row / p.heads, h = row % p.heads;
+  constexpr int kPartBytes = PART_F32 ? 4 : 2;
+  const float* lse_in = p.part_lse + r * p.lse_in_r + h * p.lse_in_h;
+  const char* part = static_cast<const char*>(p.part) + (r * p.part_stride_r + h * p.part_stride_h) * kPartBytes;
+
+  float top = -INFINITY;
+  for (int64_t i = 0; i < p.parts; ++i) {
+    const float l = lse_in[i * p.lse_in_p];
+    top = l > top || l != l ? l : top;  // a NaN stays
+  }
+  const float shift = top == -INFINITY ? 0.f : top;
+  float acc[2][8] = {};
+  float sum = 0.f;
+  constexpr int kFlight = 4;
+  for (int64_t i0 = 0; i0 < p.parts; i0 += kFlight) {
+    Piece<PART_F32> v[kFlight][2];
+    float w[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      w[k] = 0.f;
+      if (i0 + k < p.parts) {
+        w[k] = expf(lse_in[(i0 + k) * p.lse_in_p] - shift);
+        const char* src = part + (i0 + k) * p.part_stride_p * kPartBytes;
+        v[k][0].load(src, 8 * lane);
+        v[k][1].load(src, 256 + 8 * lane);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      if (i0 + k < p.parts && w[k] != 0.f) {  // a part without weight may hold anything
+        sum += w[k];
+        v[k][0].add(w[k], acc[0]);
+        v[k][1].add(w[k], acc[1]);
+      }
+    }
+  }
+  __syncwarp();  // out and lse may be one of the parts: every lane has read them by here
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    float* a = acc[g];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] *= inv;
+    const int64_t at = r * p.out_stride_r + h * p.out_stride_h + 256 * g + 8 * lane;
+    if (OUT_F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+      o[0] = make_float4(a[0], a[1], a[2], a[3]);
+      o[1] = make_float4(a[4], a[5], a[6], a[7]);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
+          make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7]));
+    }
+  }
+  if (p.lse != nullptr && lane == 0) p.lse[r * p.lse_stride_r + h * p.lse_stride_h] = sum == 0.f ? -INFINITY : top + logf(sum);
+}
+
+}  // namespace
+
+cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
+  constexpr int kRows = kMergeThreads / 32;
+  const unsigned grid = static_cast<unsigned>((p.requests * p.heads + kRows - 1) / kRows);
+  if (p.part_f32) {
+    if (p.out_f32) merge_kernel<true, true><<<grid, kMergeThreads, 0, stream>>>(p);
+    else merge_kernel<true, false><<<grid, kMergeThreads, 0, stream>>>(p);
+  } else {
+    if (p.out_f32) merge_kernel<false, true><<<grid, kMergeThreads, 0, stream>>>(p);
+    else merge_kernel<false, false><<<grid, kMergeThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace c128

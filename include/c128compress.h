@@ -66,12 +66,13 @@ enum {
     C128_I64 = 2,
     C128_F32 = 3,
     C128_U8 = 4,
+    C128_BF16 = 5,
 };
 
 /* A strided view of caller-owned device memory. shape/stride beyond ndim are ignored. */
 typedef struct c128_tensor {
     void* data;          /* device pointer (may be NULL only when the tensor is empty) */
-    int32_t dtype;       /* one of C128_I32, C128_I64, C128_F32, C128_U8 */
+    int32_t dtype;       /* one of C128_I32, C128_I64, C128_F32, C128_U8, C128_BF16 */
     int32_t ndim;        /* 1 .. 4 */
     int64_t shape[4];
     int64_t stride[4];   /* in elements */
@@ -105,6 +106,8 @@ enum {
     C128_DEV_BAD_COS_ROW = 8,    /* window start (p/128)*128 >= cos_sin_cache.shape[0] */
     C128_DEV_BAD_KV_SLOT = 16,   /* kv_slot_mapping[t] >= k_cache.shape[0] * kv_block_size */
     C128_DEV_TIMEOUT = 32,       /* a pipeline wait exceeded its time limit; the kernel gave up */
+    C128_DEV_NO_FREE_BLOCK = 64, /* c128_extend_block_tables: the list of free blocks ran out */
+    C128_DEV_BAD_LENGTH = 128,   /* a length, count or block total that cannot be (see each call) */
 };
 
 /*
@@ -320,6 +323,132 @@ int c128_debug_stall_first_window_ex(const c128_config_t* config,
                                      const c128_tensor_t* kv_slot_mapping,
                                      int64_t kv_block_size,
                                      c128_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Around the compressor: the block tables and per-token arrays its call takes, made on the GPU from
+ * the requests' lengths, and the attention of a decode step over the cache it writes. The calls
+ * follow the rules above: caller-owned tensors, host checks that return C128_ERR_* before anything
+ * is launched, asynchronous on `stream` and capturable, device error bits in the stream's workspace
+ * (read with c128_device_errors; a stream without a workspace gets one, so the first call on a
+ * stream that is being captured returns C128_ERR_CAPTURE unless c128_reserve_workspace came before).
+ * All tensors live on the current device. Unless a call says otherwise, an output overlaps no input
+ * and no other output.
+ */
+
+/*
+ * c128_extend_block_tables — give every request the blocks that its length now needs, from a list
+ * of free blocks. With entries(n) = floor(n / compress_ratio) and needed = ceil(entries(seq_lens[r])
+ * / block_size), request r gets max(0, needed - held[r]) blocks; the requests are served in order:
+ *   block_table[r, held[r] + j] = free_blocks[taken + (blocks given to requests before r) + j]
+ * and held_out[r] = max(held[r], needed), taken_out = taken + (all blocks given). compress_ratio is
+ * 1 for the state cache and the compressor's ratio for the k_cache.
+ *
+ *   seq_lens    [R]      int32   length of each request
+ *   held        [R]      int32   blocks it holds already
+ *   block_table [R, MB]  int32   in place; stride[1] == 1, stride[0] >= MB. Entries other than the
+ *                                ones given are left as they were
+ *   free_blocks [F]      int32   block ids, F < 2^31
+ *   taken       [1]      int64   ids of free_blocks given away already
+ *   held_out    [R]      int32   may be `held` itself (else: no overlap)
+ *   taken_out   [1]      int64   may be `taken` itself
+ *
+ * Device error bits: C128_DEV_NO_FREE_BLOCK - the list ran out: the first request that it cannot
+ * serve in full and every later one that needs blocks get none and keep their count;
+ * C128_DEV_BAD_BT_COL - a request needs more than MB blocks (it gets none, the others are served);
+ * C128_DEV_BAD_LENGTH - a negative length (counts as 0) or held count (the request gets none), or
+ * taken outside [0, F] (nobody gets any).
+ * Results do not depend on scheduling: no atomics, the same inputs give the same tables.
+ */
+int c128_extend_block_tables(const c128_tensor_t* seq_lens, const c128_tensor_t* held,
+                             const c128_tensor_t* block_table, const c128_tensor_t* free_blocks,
+                             const c128_tensor_t* taken, int32_t compress_ratio, int64_t block_size,
+                             const c128_tensor_t* held_out, const c128_tensor_t* taken_out,
+                             c128_stream_t stream);
+
+/*
+ * c128_build_slot_maps — the per-token arrays of one step. Request r has seq_lens[r] tokens, the
+ * last query_lens[r] of them new; the step's tokens are those of request 0, then of request 1, ...
+ * Token i of request r sits at position p = seq_lens[r] - query_lens[r] + i and gets
+ *   token_to_req_indices = r, positions = p,
+ *   slot_mapping = state_table[r, p / state_block] * state_block + p % state_block,
+ *   kv_slot_mapping = the same of entry p / compress_ratio in kv_table with kv_block_size where p
+ *                     ends a window ((p + 1) % compress_ratio == 0), -1 elsewhere.
+ * Rows of the per-token arrays behind the last token (a batch padded to a captured size) get request
+ * 0, position 0 and slots -1, which compress_norm_rope_store skips.
+ *
+ *   seq_lens, query_lens [R] int32; state_table [R, MBs], kv_table [R, MBk] int32 (rows may be
+ *   padded); query_start [R + 1] int32: the index of each request's first token, and their number;
+ *   token_to_req_indices [T] int32; positions, slot_mapping, kv_slot_mapping [T] int64; kv_lens [R]
+ *   int32: floor(seq_lens[r] / compress_ratio), the entries of the request's cache once the step's
+ *   windows are stored. T < 2^31.
+ *
+ * Device error bits: C128_DEV_BAD_LENGTH - a negative length (counts as 0), query_lens[r] >
+ * seq_lens[r] (tokens at negative positions get slots -1), or more tokens than T (those behind are
+ * dropped); C128_DEV_BAD_BT_COL - a position behind the end of its table (slot -1);
+ * C128_DEV_BAD_BLOCK - a negative block id where one is needed (slot -1).
+ */
+int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* query_lens,
+                         const c128_tensor_t* state_table, int64_t state_block,
+                         const c128_tensor_t* kv_table, int64_t kv_block_size, int32_t compress_ratio,
+                         const c128_tensor_t* query_start, const c128_tensor_t* token_to_req_indices,
+                         const c128_tensor_t* positions, const c128_tensor_t* slot_mapping,
+                         const c128_tensor_t* kv_slot_mapping, const c128_tensor_t* kv_lens,
+                         c128_stream_t stream);
+
+/*
+ * c128_decode_attention — attention of one new token per request over its entries of the paged
+ * k_cache, in the layout that the C128_FORMAT_SPARSE_FP8 compressor stores. Entry j is the vector
+ * k_j of 512 values that its record stands for: e4m3 code x 2^(scale byte - 127) for the 448 "nope"
+ * columns, the bf16 values for the 64 rope columns. It is key and value at once, for all heads:
+ *   s_hj = scale * <q[r,h], k_j>,  j = 0 .. kv_lens[r] - 1
+ *   lse[r,h] = log(sum_j exp(s_hj) + exp(sink[h]))       (the sink term only if `sink` is given)
+ *   out[r,h] = sum_j exp(s_hj - lse[r,h]) k_j
+ * A request without entries gets zeros and an lse of sink[h], or -inf without a sink.
+ *
+ *   q           [R, H, 512]   bf16   stride[2] == 1, other strides >= 512 and multiples of 8, data
+ *                                    16-byte aligned; 1 <= H <= 1024
+ *   k_cache     [NKB, bs, W]  uint8  as for compress_norm_rope_store; kv_block_size == bs
+ *   block_table [R, MB]       int32  k_cache block of entries b*bs .. b*bs + bs - 1 of request r
+ *   kv_lens     [R]           int32  entries of each request; bytes behind them are never used
+ *   scale                     fp32   finite
+ *   sink        [H]           fp32   may be NULL
+ *   out         [R, H, 512]   bf16 or fp32, strides as for q (fp32: multiples of 4)
+ *   lse         [R, H]        fp32   positive strides; may be NULL
+ *   workspace   [n]           uint8  at least c128_decode_attention_workspace bytes, 256-byte
+ *                                    aligned; scratch of this call: calls that can overlap on the
+ *                                    GPU need one each (so do graphs that are replayed at once)
+ *
+ * Products take bf16 operands (the entries are exact in bf16 for scale bytes 8 .. 246; the softmax
+ * weights are rounded to bf16) and add up in fp32; the softmax statistics are fp32.
+ * Device error bits: C128_DEV_BAD_BT_COL - kv_lens[r] > MB*bs (the entries behind are left out);
+ * C128_DEV_BAD_BLOCK - a block id outside [0, NKB) (its entries are left out); C128_DEV_BAD_LENGTH
+ * - a negative kv_lens[r] (counts as 0); C128_DEV_TIMEOUT.
+ */
+int c128_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
+                          const c128_tensor_t* block_table, const c128_tensor_t* kv_lens, float scale,
+                          const c128_tensor_t* sink, const c128_tensor_t* out, const c128_tensor_t* lse,
+                          const c128_tensor_t* workspace, c128_stream_t stream);
+
+/* Bytes of workspace that c128_decode_attention needs on the current device for `num_heads` heads,
+ * whatever the requests and their lengths. */
+int c128_decode_attention_workspace(int64_t num_heads, int64_t* bytes);
+
+/*
+ * c128_merge_attention — join attentions of the same queries over different sets of entries (the
+ * parts of a cache, or the compressed cache and the window of recent tokens) by their log-sum-exp:
+ *   lse[r,h] = log(sum_p exp(part_lse[p,r,h])),
+ *   out[r,h] = sum_p exp(part_lse[p,r,h] - lse[r,h]) part_out[p,r,h].
+ * A part whose lse is -inf saw nothing and its part_out is not used, whatever it holds; where every
+ * part is so, out is 0 and lse -inf. At most one part may have had a sink.
+ *
+ *   part_out [P, R, H, 512] bf16 or fp32, stride[3] == 1, rows 16-byte aligned, P >= 1
+ *   part_lse [P, R, H]      fp32, any positive strides
+ *   out      [R, H, 512]    bf16 or fp32 (fp32 sums, rounded once), stride[2] == 1, rows 16-byte
+ *                           aligned. May be one of the parts (part_out[p], same type and strides)
+ *   lse      [R, H]         fp32, positive strides; may be NULL, or the part_lse[p] of that part
+ */
+int c128_merge_attention(const c128_tensor_t* part_out, const c128_tensor_t* part_lse,
+                         const c128_tensor_t* out, const c128_tensor_t* lse, c128_stream_t stream);
 
 /* Human-readable name of a return code (static string, never NULL). */
 const char* c128_status_string(int status);
