@@ -783,7 +783,6 @@ cudaError_t launch_small_kernel(const Params& p, const LaunchCfg& cfg, cudaStrea
 // (or score) part of a row, kv / score part, row within a state block, state block. The box takes
 // head columns of kv and of score for each of its rows. False when the layout does not fit such a
 // map (the caller then uses per-row bulk copies or another kernel).
-namespace {
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -797,7 +796,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
-}  // namespace
 
 bool encode_state_map(const Params& p, int head, int box_rows, CUtensorMap* map) {
   const int cw = head < 256 ? head : 256;

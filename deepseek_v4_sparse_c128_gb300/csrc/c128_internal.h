@@ -1,6 +1,7 @@
 // Internal declarations shared by the kernel translation unit and the C-ABI layer.
 #pragma once
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -132,6 +133,7 @@ cudaError_t launch_indexer_windows(const Params& p, const LaunchCfg& cfg, cudaSt
 cudaError_t prepare_indexer_windows();
 // Tensor map of the state cache for tiled loads of `box_rows` rows x (head kv + head score
 // columns); false when the layout does not allow one (c128_c4.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // NULL if the driver has none
 bool encode_state_map(const Params& p, int head, int box_rows, CUtensorMap* map);
 int compress_smem_bytes();
 cudaError_t prepare_device(int device);  // one-time function attributes

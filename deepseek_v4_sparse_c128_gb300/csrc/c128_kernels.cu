@@ -25,6 +25,7 @@
 // Every wait is bounded (kWaitTimeoutNs); on expiry the kernel records C128_DEV_TIMEOUT, drains
 // its own copies in flight and returns.
 #include "c128_device.cuh"
+#include "c128_serving.h"
 
 namespace c128 {
 namespace {
@@ -692,6 +693,7 @@ cudaError_t prepare_device(int /*device*/) {
   if (e == cudaSuccess) e = set_direct_smem<true>(a);
   if (e == cudaSuccess) e = prepare_small();
   if (e == cudaSuccess) e = prepare_indexer_windows();
+  if (e == cudaSuccess) e = prepare_decode();
   return e;
 }
 

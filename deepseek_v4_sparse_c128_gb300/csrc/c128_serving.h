@@ -65,6 +65,7 @@ struct DecodeParams {
   unsigned int* err;
 };
 cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stream);
+cudaError_t prepare_decode();  // function attributes, once per device
 int64_t decode_workspace_bytes(int heads, int sm_count);
 
 struct MergeParams {
