@@ -105,20 +105,50 @@ struct Scratch {
   }
 };
 
+// A bounded wait that looks at the clock and the abort flag only now and then: reading the global
+// timer takes longer than most of these waits (a try alone lets the hardware suspend the thread).
+__device__ __noinline__ bool decode_wait_slow(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (abort_flag != nullptr && *abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitTimeoutNs) return false;
+  }
+}
+__device__ __forceinline__ bool decode_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
+  for (int i = 0; i < 4; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return decode_wait_slow(bar, parity, abort_flag);
+}
+
 // ------------------------------------------------------------------------------------ tcgen05
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
-  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | static_cast<uint64_t>(leading >> 4) << 16 |
-         static_cast<uint64_t>(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;  // 128-byte swizzle
+// Shared-memory operand with the 128-byte swizzle: the low half holds the address and the leading
+// byte offset (of the next 64 rows of an M-major operand, unused for K-major), the high half the
+// offset of the next 8 rows. Steps along an operand are added to the low half, in 16-byte units.
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t leading) {
+  return (addr & 0x3ffff) >> 4 | leading >> 4 << 16;
+}
+constexpr uint32_t kDescHigh = 1024u >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint64_t desc64(uint32_t low) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(kDescHigh));
+  return d;
 }
 __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_mn_major) {  // bf16 x bf16 -> fp32
   return 1u << 4 | 1u << 7 | 1u << 10 | (a_mn_major ? 1u << 15 : 0u) | static_cast<uint32_t>(n >> 3) << 17 |
          static_cast<uint32_t>(m >> 4) << 24;
 }
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
+}
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t desc, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(desc),
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(desc64(a_low)), "l"(desc64(b_low)), "r"(desc),
       "r"(static_cast<uint32_t>(add))
       : "memory");
 }
@@ -314,7 +344,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   volatile int* const abort_flag = &sm.abort;
   // A wait of a whole warp, with one answer for all its lanes; false: give up (the CTA ends).
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_suspend(bar, parity, abort_flag));
+    const bool ok = __all_sync(0xffffffffu, decode_wait(bar, parity, abort_flag));
     if (!ok && lane == 0) {
       *abort_flag = 1;
       atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
@@ -492,15 +522,19 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------------ issue the products
-    if (lane == 0) {
-      const uint32_t q_at = smem_addr(sm.q), k_at = smem_addr(sm.k[0]), p_at = smem_addr(sm.p[0]);
+    // One elected thread in one branch: the compiler then keeps descriptors in uniform registers, and
+    // a product issues faster than it runs (32 cycles for S, 39 to 48 for O, bound by the reads of the
+    // operands from shared memory). Behind a test of the lane each took 66 to 75 cycles to issue.
+    if (elect_one()) {
+      const uint32_t q_at = desc_low(smem_addr(sm.q), 16), ks_at = desc_low(smem_addr(sm.k[0]), 16);
+      const uint32_t kv_at = desc_low(smem_addr(sm.k[0]), kChunkBytes), p_at = desc_low(smem_addr(sm.p[0]), 16);
       constexpr uint32_t s_desc = mma_desc(kGroup, kTile, false);
       const uint32_t o_desc = mma_desc(128, heads16, true);
       int seg = -1, prev_flags = 0, prev_seg = 0;
       bool failed = false, loading = false;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (failed) return false;
-        if (mbar_wait_suspend(bar, parity, abort_flag)) return true;
+        if (decode_wait(bar, parity, abort_flag)) return true;
         *abort_flag = 1;
         atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
         failed = true;
@@ -515,8 +549,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks) {
-            const uint64_t a = smem_desc(k_at + buf * kTileBytes + 2 * mt * kChunkBytes + ks * 2048, kChunkBytes, 1024);
-            const uint64_t b = smem_desc(p_at + buf * (kGroup * kTile * 2) + ks * 32, 16, 1024);
+            const uint32_t a = kv_at + ((buf * kTileBytes + 2 * mt * kChunkBytes + ks * 2048) >> 4);
+            const uint32_t b = p_at + ((buf * (kGroup * kTile * 2) + ks * 32) >> 4);
             mma(tmem + mt * kGroup, a, b, o_desc, !(flags & kFirst) || ks > 0);
           }
         }
@@ -548,8 +582,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t a = smem_desc(q_at + c * (kGroup * 128) + ks * 32, 16, 1024);
-            const uint64_t b = smem_desc(k_at + buf * kTileBytes + c * kChunkBytes + ks * 32, 16, 1024);
+            const uint32_t a = q_at + ((c * (kGroup * 128) + ks * 32) >> 4);
+            const uint32_t b = ks_at + ((buf * kTileBytes + c * kChunkBytes + ks * 32) >> 4);
             mma(tmem + kTmemS + buf * kTile, a, b, s_desc, c + ks > 0);
           }
         }
@@ -562,8 +596,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (!failed && i > 0) product_pv(i - 1, prev_flags, prev_seg);
       // nothing may be in flight when the CTA ends
       mma_commit(&sm.drained);
-      mbar_wait_suspend(&sm.drained, 0, nullptr);
-      if (loading) mbar_wait_suspend(&sm.q_full, seg & 1, nullptr);
+      decode_wait(&sm.drained, 0, nullptr);
+      if (loading) decode_wait(&sm.q_full, seg & 1, nullptr);
     }
     __syncwarp();
   } else {
