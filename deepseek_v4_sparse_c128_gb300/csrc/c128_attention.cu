@@ -1,31 +1,36 @@
 // c128_decode_attention: attention of one new token per request over its entries of the paged FP8
 // cache, on the tcgen05 tensor cores.
 //
-//   S = Q K^T            per tile of 64 entries: M = 64 heads, N = 64 entries, K = 512
-//   P = exp2(c S - m)    c = scale * log2(e), m a running reference per head, in registers
-//   O^T += K^T P^T       M = 128 columns (4 times), N = heads, K = 64 entries
+//   S^T = K Q^T            per tile of 64 entries: M = 64 entries, N = heads, K = 512
+//   P^T = exp2(c S^T - m)  c = scale * log2(e), m a running reference per head
+//   O^T += K^T P^T         M = 128 columns (4 times), N = heads, K = 64 entries
 //   out = O / sum P
 //
 // An entry is key and value, so a tile is decoded once, to bf16 in shared memory (exact: an e4m3 code
-// has 4 significant bits and its scale is a power of two), and both products read it from there: as
-// B with the 512 columns along K, and as A with them along M. Taking O transposed makes the heads the
-// N of the second product, so its work and its TMEM columns go with the heads there are, and leaves
-// 128 of the 512 columns for two S tiles. Heads are dealt out in groups of 64; a group decodes the
-// cache for itself (the second group's reads hit L2).
+// has 4 significant bits and its scale is a power of two), and both products read it from there as
+// their A: with the 512 columns along K, and with them along M. Taking both products transposed makes
+// the heads their N, so their work, their reads of shared memory (which bound them) and their TMEM
+// columns go with the heads there are, and leaves room for two S tiles beside O. It also leaves the
+// softmax next to nothing to exchange: a thread holds two entries and some heads, and keeps its own
+// sums to the end. Heads are dealt out in groups of 64; a group decodes the cache for itself (the
+// second group's reads hit L2).
 //
-// The running reference m is not the maximum itself: it is raised only when a score passes it by more
-// than 2^8, because raising it means rescaling O in TMEM. P then stays below 2^8 and its sum exact
-// enough in fp32, whatever the scores do.
+// The running reference m is not the maximum: it is the score of the run's first entry, and is raised
+// (to the maximum so far, rescaling O in TMEM) only when a score passes it by a factor of 2^32. P, its
+// sums and O are floating point, so a common factor costs no precision, and 2^32 times 2^25 entries of
+// 2^70 is still inside the range.
 //
 // Work is dealt out in tiles: the requests' tiles, one after the other, are cut into as many equal
 // runs as there are CTAs, so a long request is shared by many CTAs and a CTA takes many short ones. A
 // request that is cut leaves fp32 partial results in the workspace, joined by a second kernel.
 //
-// Roles of the 14 warps (each wait is bounded, see c128_device.cuh):
-//   0..7   decode the entries of a tile into shared memory, the next tile's bytes already in registers
-//   8..11  softmax of S, rescaling of O, results
-//   12     one thread issues the products and the queries' TMA loads
-//   13     walks the runs: per tile the address of each entry (through the block table), prefetched
+// Roles of the 22 warps (each wait is bounded, see c128_device.cuh):
+//   0..15  decode: eight warps the even tiles, eight the odd ones, the next tile's bytes already in
+//          registers. Tiles pass to the products and back in quarters (128 columns), so that S starts
+//          behind the first quarter and a quarter that O has taken is decoded into again at once
+//   16..19 softmax of S, rescaling of O, results
+//   20     one thread issues the products and the queries' TMA loads
+//   21     walks the runs: per tile the address of each entry (through the block table), prefetched
 //          to L2 a few tiles ahead
 #include <cuda_runtime.h>
 
@@ -44,14 +49,47 @@ constexpr int kGroup = 64;          // heads per CTA
 constexpr int kChunks = kHead / 64; // 64-column chunks of 128 bytes (bf16): one swizzle atom wide
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kTileBytes = kChunks * kChunkBytes;  // a decoded tile: 64 KiB
-constexpr int kFillWarps = 8, kSoftWarps = 4;
-constexpr int kMmaWarp = kFillWarps + kSoftWarps, kIndexWarp = kMmaWarp + 1;
+constexpr int kQuarters = 4;        // of a tile's columns: 128 each, an M of the second product
+constexpr int kFillWarps = 8, kSoftWarps = 4;  // fill warps per tile buffer
+constexpr int kSoftWarp = 2 * kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 1;
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
 constexpr int kRing = 4;            // tiles the index warp may be ahead
-constexpr float kSlack = 8.f;       // log2 units a score may pass the reference by
+constexpr float kSlack = 32.f;      // log2 units a score may pass the reference by
 constexpr int kTmemCols = 512, kTmemS = 256;  // O in columns 0..255, two S tiles behind it
 
-enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kOdd = 8 };  // of its run of one request's tiles; kOdd: an odd run
+
+struct Task {  // a request that a CTA starts and leaves to the columns behind it, if parts > 0
+  int32_t request, parts, column, group_heads;
+};
+
+// How a call's heads and scratch are laid out for head groups of `group` heads (16, 32 or 64). CTA
+// column c of every group has two slots for partial results: 2c for the request it continues, 2c + 1
+// for the one it starts and does not finish.
+struct Layout {
+  int groups, columns, heads, ctas;  // head groups, CTA columns, heads held per slot and group
+  Layout() = default;
+  __host__ __device__ Layout(int all_heads, int sms, int group) {
+    groups = (all_heads + group - 1) / group;
+    columns = sms / groups > 0 ? sms / groups : 1;
+    heads = groups > 1 ? group : (all_heads + 15) / 16 * 16;
+    ctas = sms > columns * groups ? sms : columns * groups;
+  }
+  __host__ __device__ int64_t rows() const { return 2ll * columns * groups * heads; }
+  __host__ __device__ int64_t lse_at() const { return (ctas * static_cast<int64_t>(sizeof(Task)) + 255) / 256 * 256; }
+  __host__ __device__ int64_t out_at() const { return lse_at() + (rows() * 4 + 255) / 256 * 256; }
+  // smaller groups need no more than the largest
+  __host__ __device__ int64_t bytes() const { return out_at() + rows() * kHead * 4; }
+  __device__ int64_t row(int slot, int group, int head) const {
+    return (static_cast<int64_t>(slot) * groups + group) * heads + head;
+  }
+  // A partial result is kept as the threads that make and join it hold it: per 32 columns and 4 heads
+  // 32 x 4 floats, column by column. Where `row` starts its 512 x heads floats, the block of `cols32`
+  // and `head4`:
+  __device__ int64_t block(int slot, int group, int cols32, int head4) const {
+    return row(slot, group, 0) * kHead + (static_cast<int64_t>(cols32) * (heads / 4) + head4) * 128;
+  }
+};
 
 struct TileDesc {
   const uint8_t* data[kTile];    // record of each entry, NULL where there is none
@@ -67,59 +105,50 @@ struct DecodeSmem {
   alignas(1024) uint8_t k[2][kTileBytes];
   alignas(1024) uint8_t p[2][kGroup * kTile * 2];
   TileDesc ring[kRing];
-  alignas(16) float factor[kGroup];
-  alignas(16) float inv[kGroup];
+  alignas(16) float ref[kGroup];      // the running references m
+  alignas(16) float factor[kGroup];   // what O is rescaled by
+  alignas(16) float inv[kGroup];      // 1 / sum
+  float by_warp[kSoftWarps][kGroup];  // maxima or sums of the softmax warps' entries
   uint64_t ring_full[kRing], ring_free[kRing];
-  uint64_t k_full[2], s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t k_full[2][2];              // half of a tile's columns decoded
+  uint64_t k_free[2][kQuarters];      // O has taken the quarter (the last: O is done)
+  uint64_t s_full[2], s_free[2], p_full[2];
   uint64_t q_full, q_free, o_free, drained;
-  uint64_t soft;                 // barrier of the softmax warps
-  int32_t vote[2][kSoftWarps];
+  uint64_t inv_full;             // `inv` and `done` of a finished run are there
+  int32_t done_request, done_part;
   int64_t warp_sums[kDecodeThreads / 32];
-  int64_t total;                 // tiles of all requests
-  int64_t first_tile;            // of the run's first request: its tiles before the run
+  int64_t begin, end;            // the column's tiles
+  int64_t first_tile;            // of the first request: its tiles before the column's
   int32_t first_request;
+  Layout lay;                    // read back where results are written, to keep registers free
+  int32_t group, group_heads;
   uint32_t tmem;
   volatile int abort;
 };
 static_assert(sizeof(DecodeSmem) <= 232448, "shared memory of one SM");
 
-struct Task {  // a request that CTA column c shares with the ones behind it
-  int32_t request, parts;
-};
-
-// Scratch of a call: tasks, log2-sum-exps and fp32 results of partial requests. Column c of CTAs has
-// two slots: 2c for the request it continues, 2c + 1 for the one it starts and does not finish.
-struct Scratch {
-  int columns, groups, heads;  // CTA columns, head groups, heads held per slot and group
-  __host__ __device__ Scratch(int all_heads, int sms) {
-    groups = (all_heads + kGroup - 1) / kGroup;
-    columns = sms / groups > 0 ? sms / groups : 1;
-    heads = groups > 1 ? kGroup : (all_heads + 15) / 16 * 16;
-  }
-  __host__ __device__ int64_t rows() const { return 2ll * columns * groups * heads; }
-  __host__ __device__ int64_t lse_at() const { return (columns * static_cast<int64_t>(sizeof(Task)) + 255) / 256 * 256; }
-  __host__ __device__ int64_t out_at() const { return lse_at() + (rows() * 4 + 255) / 256 * 256; }
-  __host__ __device__ int64_t bytes() const { return out_at() + rows() * kHead * 4; }
-  __device__ int64_t row(int slot, int group, int head) const {
-    return (static_cast<int64_t>(slot) * groups + group) * heads + head;
-  }
-};
-
-// A bounded wait that looks at the clock and the abort flag only now and then: reading the global
-// timer takes longer than most of these waits (a try alone lets the hardware suspend the thread).
-__device__ __noinline__ bool decode_wait_slow(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
-  const uint64_t t0 = global_timer_ns();
+// The bounded wait of this kernel, inline and on the SM's clock: a call would have to keep the many
+// values that live across it out of registers, and the global timer takes longer than most waits.
+constexpr uint32_t kWaitCycles = 2000000000u;  // about a second; the 32-bit clock wraps after two
+__device__ __forceinline__ bool decode_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
+  if (mbar_try_wait_suspend(bar, parity)) return true;
+  const uint32_t t0 = clock();
   for (;;) {
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_suspend(bar, parity)) return true;
     if (abort_flag != nullptr && *abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) return false;
+    if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) return false;
   }
 }
-__device__ __forceinline__ bool decode_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
-  for (int i = 0; i < 4; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return decode_wait_slow(bar, parity, abort_flag);
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, P;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // ------------------------------------------------------------------------------------ tcgen05
@@ -135,8 +164,8 @@ __device__ __forceinline__ uint64_t desc64(uint32_t low) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(kDescHigh));
   return d;
 }
-__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_mn_major) {  // bf16 x bf16 -> fp32
-  return 1u << 4 | 1u << 7 | 1u << 10 | (a_mn_major ? 1u << 15 : 0u) | static_cast<uint32_t>(n >> 3) << 17 |
+__host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool mn_major) {  // bf16 x bf16 -> fp32
+  return 1u << 4 | 1u << 7 | 1u << 10 | (mn_major ? 3u << 15 : 0u) | static_cast<uint32_t>(n >> 3) << 17 |
          static_cast<uint32_t>(m >> 4) << 24;
 }
 __device__ __forceinline__ bool elect_one() {
@@ -161,16 +190,11 @@ __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// 16 lanes x 64 columns: thread t gets rows t/4 and t/4 + 8, columns 8g + 2(t%4) and + 1 in x[4g ..]
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t addr, uint32_t (&x)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]),
-        "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]),
-        "=r"(x[17]), "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]), "=r"(x[24]),
-        "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
-      : "r"(addr));
+// 16 lanes x 16 columns: thread t gets rows t/4 and t/4 + 8, columns 8g + 2(t%4) and + 1 in x[4g ..]
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t addr, uint32_t (&x)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+               : "r"(addr));
 }
 // 32 lanes x 16 columns, a lane's columns in one thread
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t addr, uint32_t (&x)[16]) {
@@ -197,31 +221,52 @@ __device__ __forceinline__ void load_query_box(void* dst, const CUtensorMap* map
       : "memory");
 }
 
-// ------------------------------------------------------------------------------------- decoding
-// Two e4m3 codes (bytes lo, lo + 1 of w) to bf16: the code's exponent and mantissa moved to the bf16
-// fields give the value times 2^-120 (subnormals included, bf16 keeps them), `mul` puts 2^120 and the
-// scale back.
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t spread, uint32_t mul) {
-  uint32_t x = (spread & 0x80008000u) | ((spread >> 4) & 0x07f007f0u), y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(mul));
-  return y;
+// Barrier of the softmax warps with the OR of `pred` over them.
+__device__ __forceinline__ bool soft_vote(bool pred) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(out)
+      : "r"(static_cast<uint32_t>(pred)), "n"(32 * kSoftWarps)
+      : "memory");
+  return out != 0;
 }
-// The same by way of fp32, for NaN codes and scales whose 2^(120 + e) has no bf16.
-__device__ __noinline__ uint32_t codes_to_bf16_any(uint32_t two, int scale_byte) {
-  float v[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t b = (two >> (8 * i)) & 0xffu, mag = b & 0x7fu;
-    const float a = mag == 0x7fu ? NAN : __uint_as_float(mag << 20) * 0x1p120f;
-    v[i] = ldexpf(b & 0x80u ? -a : a, scale_byte - 127);
-  }
-  return pack_bf16x2(v[0], v[1]);
-}
-constexpr int kMaxFastScale = 134;  // 2^(134 - 127 + 120) = 2^127
 
-__device__ __forceinline__ uint4 ld16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+// ------------------------------------------------------------------------------------- decoding
+// Two e4m3 codes times a power of two to bf16x2, by way of fp16 (exact, NaN stays NaN) and fp32. 53
+// cycles of a scheduler per 16 codes and warp; moving the bits into bf16 fields and multiplying there
+// took 85, most of it half-rate integer operations, NaN codes aside.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint16_t two, float scale) {
+  uint32_t h;
+  float x, y;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.f32.f16 %0, lo;\n\t"
+      "cvt.f32.f16 %1, hi;\n}"
+      : "=f"(x), "=f"(y)
+      : "r"(h));
+  return pack_bf16x2(x * scale, y * scale);
+}
+// 2^(byte - 127): the byte is the float's exponent field (0: the subnormal 2^-127).
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
+
+// Read once and past L1, whose memory the tiles and the products use.
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld8(const uint8_t* p) {
+  uint2 v;
+  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ uint4 ld8x2(const uint8_t* p) {
-  const uint2 a = __ldg(reinterpret_cast<const uint2*>(p)), b = __ldg(reinterpret_cast<const uint2*>(p) + 1);
+  const uint2 a = ld8(p), b = ld8(p + 8);
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -243,43 +288,60 @@ __device__ __forceinline__ int64_t entries_of(const DecodeParams& p, int64_t r, 
 // A request without entries still takes a (masked) tile: its results are written like any other's.
 __device__ __forceinline__ int64_t tiles_of(int64_t entries) { return entries > 0 ? (entries + kTile - 1) / kTile : 1; }
 
-// First tile of CTA column c when `total` tiles are dealt to `columns` columns, and the column of a tile.
-__device__ __forceinline__ int64_t run_begin(int64_t c, int64_t total, int64_t columns) { return c * total / columns; }
-__device__ __forceinline__ int64_t column_of(int64_t tile, int64_t total, int64_t columns) {
-  return ((tile + 1) * columns - 1) / total;
-}
+// `total` tiles dealt to `columns` CTA columns, the first `extra` of them one tile more than the rest.
+// A cut that would fall within `snap` tiles of a request's begin or end is moved there: a cut request
+// costs its partial results (2 KB per head and part, written and read again), about what a tile or
+// two take.
+constexpr int kSnap = 1, kSnapShare = 2;
+struct Deal {
+  int64_t share, extra;
+  int snap;
+  __device__ Deal(int64_t total, int columns) {
+    if (total < (1ll << 32)) {  // a 64-bit division is a hundred instructions
+      share = static_cast<uint32_t>(total) / static_cast<uint32_t>(columns);
+    } else {
+      share = total / columns;
+    }
+    extra = total - share * columns;
+    snap = share >= kSnapShare ? kSnap : 0;
+  }
+  __device__ int64_t begin(int column) const { return share * column + min(static_cast<int64_t>(column), extra); }
+  __device__ int column_of(int64_t tile) const {
+    const int64_t longer = extra * (share + 1);
+    const int64_t t = tile < longer ? tile : tile - longer, d = tile < longer ? share + 1 : share;
+    const int64_t q = t < (1ll << 32) ? static_cast<uint32_t>(t) / static_cast<uint32_t>(d) : t / d;
+    return static_cast<int>(tile < longer ? q : extra + q);
+  }
+};
+
+constexpr int kBoxHeads = 16;  // heads of a TMA load of queries
 
 template <bool ALIGN16>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
-    decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap q_map, const Scratch scratch, int box_heads) {
+    decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap q_map, const int sms) {
   extern __shared__ uint8_t smem_raw[];
   DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = blockIdx.x % scratch.groups, column = blockIdx.x / scratch.groups;
-  const int heads = min(kGroup, p.heads - group * kGroup);
-  const int heads16 = (heads + 15) & ~15;
   unsigned int err = 0;
 
-  launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.ring_full[i], 1);
       mbar_init(&sm.ring_free[i], kFillWarps + kSoftWarps + 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.k_full[i], kFillWarps);
+      for (int k = 0; k < 2; ++k) mbar_init(&sm.k_full[i][k], kFillWarps);
+      for (int k = 0; k < kQuarters; ++k) mbar_init(&sm.k_free[i][k], 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.s_free[i], kSoftWarps);
       mbar_init(&sm.p_full[i], kSoftWarps);
-      mbar_init(&sm.pv_done[i], 1);
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_free, 1);
-    mbar_init(&sm.o_free, kSoftWarps);
+    mbar_init(&sm.o_free, kSoftWarps + kFillWarps);
+    mbar_init(&sm.inv_full, kSoftWarps);
     mbar_init(&sm.drained, 1);
-    mbar_init(&sm.soft, kSoftWarps);
     sm.abort = 0;
-    sm.first_request = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -288,12 +350,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (box_heads < kGroup)  // rows of absent heads, which the loads never write
-    for (int i = threadIdx.x; i < kGroup * kHead * 2 / 16; i += kDecodeThreads)
-      reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
-  async_proxy_fence();
-
-  // The run of this column: sum the requests' tiles, then find the first and the last request.
+  launch_dependents();
+  grid_dependency_wait();  // what the kernels before this one wrote is read from here on
+  // Sum the requests' tiles (each thread a stretch of requests)...
   const int64_t per = (p.requests + kDecodeThreads - 1) / kDecodeThreads;
   const int64_t r_begin = min(threadIdx.x * per, p.requests), r_end = min(r_begin + per, p.requests);
   int64_t mine = 0;
@@ -315,26 +374,49 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (w < warp) base += s;
     total += s;
   }
-  const int64_t columns = min(static_cast<int64_t>(scratch.columns), total);
-  const int64_t begin = column < columns ? run_begin(column, total, columns) : 0;
-  const int64_t end = column < columns ? run_begin(column + 1, total, columns) : 0;
-  Task* const tasks = reinterpret_cast<Task*>(p.workspace);
-  if (column >= columns) {
-    if (group == 0 && threadIdx.x == 0) tasks[column] = Task{0, 0};
-  } else if (mine > 0 && base < end && base + mine > begin) {
-    for (int64_t r = r_begin, at = base; r < r_end && at < end; ++r) {
+  // ...choose the head groups: smaller ones while there are CTAs for a tile each, since the fewer
+  // heads a CTA has, the sooner it has loaded their queries and stored their results...
+  int group_heads = kGroup;
+  if (total * ((p.heads + 31) / 32) <= sms) group_heads = 32;
+  if (total * ((p.heads + 15) / 16) <= sms) group_heads = 16;
+  const Layout lay(p.heads, sms, group_heads);
+  const int group = blockIdx.x % lay.groups, column = blockIdx.x / lay.groups;
+  const int heads = min(group_heads, p.heads - group * group_heads);
+  const int heads16 = (heads + 15) & ~15;
+  // ...and find this column's run: its first request, and whether its last one goes on behind it.
+  const int columns = static_cast<int>(min(static_cast<int64_t>(lay.columns), total));
+  const bool idle = column >= columns;
+  const Deal deal(total, columns);
+  const int64_t cut0 = idle ? 0 : deal.begin(column), cut1 = idle ? 0 : deal.begin(column + 1);
+  Task* const task = reinterpret_cast<Task*>(p.workspace) + blockIdx.x;
+  if (threadIdx.x == 0) {
+    sm.lay = lay;
+    sm.group = group;
+    sm.group_heads = group_heads;
+    if (idle) *task = Task{0, 0, 0, 0};
+  }
+  if (!idle && mine > 0 && base < cut1 && base + mine > cut0) {
+    for (int64_t r = r_begin, at = base; r < r_end && at < cut1; ++r) {
       unsigned int ignore = 0;
-      const int64_t n = tiles_of(entries_of(p, r, &ignore));
-      if (begin >= at && begin < at + n) {
-        sm.first_request = static_cast<int32_t>(r);
-        sm.first_tile = begin - at;
+      const int64_t n = tiles_of(entries_of(p, r, &ignore)), next = at + n;
+      const bool holds0 = cut0 >= at && cut0 < next, holds1 = cut1 > at && cut1 <= next;
+      if (holds0) {  // cut0 is this request's begin, or inside it, where it may move
+        const bool back = cut0 - at <= deal.snap, on = !back && next - cut0 <= deal.snap;
+        sm.first_request = static_cast<int32_t>(on ? r + 1 : r);
+        sm.first_tile = back || on ? 0 : cut0 - at;
+        sm.begin = back ? at : on ? next : cut0;
       }
-      if (group == 0 && end - 1 >= at && end - 1 < at + n) {
-        const bool shared = at >= begin && at + n > end;
-        tasks[column] = Task{static_cast<int32_t>(r),
-                             shared ? static_cast<int32_t>(column_of(at + n - 1, total, columns)) - column + 1 : 0};
+      if (holds1) {
+        const bool on = next - cut1 <= deal.snap && cut1 - at > deal.snap || cut1 == next, back = !on && cut1 - at <= deal.snap;
+        sm.end = on ? next : back ? at : cut1;
+        // cut inside: does the request begin in this column? Then this column's task is to join it,
+        // with every column that has a cut of it as its begin
+        const bool inside = !on && !back;
+        const bool begins_here = at > cut0 || cut0 - at <= deal.snap;
+        *task = Task{static_cast<int32_t>(r),
+                     inside && begins_here && group == 0 ? deal.column_of(next - deal.snap - 1) - column + 1 : 0, column, group_heads};
       }
-      at += n;
+      at = next;
     }
   }
   if (blockIdx.x == 0 && err) atomicOr(p.err, err);
@@ -352,11 +434,62 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     return ok;
   };
 
-  if (column >= columns) {
+  // A run's results: O of all heads times 1 / sum, to the output or the workspace. The softmax warps
+  // and the eight warps that decoded the run's last tile share the work, three warps (`rank`) to each
+  // quarter of the TMEM lanes.
+  auto store_results = [&](int rank, int64_t request, int part) {
+    tmem_fence_after();
+    const int quarter = warp & 3, group0 = sm.group * sm.group_heads;
+    const uint32_t o_at = sm.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+#pragma unroll 1
+    for (int item = rank; item < heads16 / 4; item += 3) {  // 16 heads of 128 columns each
+      const int mt = item & 3, h = (item >> 2) * 16;
+      const int col = mt * 128 + 32 * quarter + lane;
+      uint32_t o[16];
+      tmem_ld_32x16(o_at + mt * kGroup + h, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&sm.inv[h + k]);
+        o[k] = __float_as_uint(__uint_as_float(o[k]) * f.x), o[k + 1] = __float_as_uint(__uint_as_float(o[k + 1]) * f.y);
+        o[k + 2] = __float_as_uint(__uint_as_float(o[k + 2]) * f.z), o[k + 3] = __float_as_uint(__uint_as_float(o[k + 3]) * f.w);
+      }
+      if (part >= 0) {
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.workspace + sm.lay.out_at()) +
+                                              sm.lay.block(part, sm.group, 4 * mt + quarter, h / 4)) + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dst[32 * k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        continue;
+      }
+      const int64_t row = request * p.out_stride_r + (group0 + h) * p.out_stride_h;
+      if (p.out_f32) {
+        float* dst = static_cast<float*>(p.out) + row + col;
+#pragma unroll
+        for (int k = 0; k < 16; ++k, dst += p.out_stride_h)
+          if (h + k < heads) *dst = __uint_as_float(o[k]);
+      } else {
+        // neighbouring lanes swap halves of a pair of heads, so that each stores two columns of one
+        uint16_t* dst = static_cast<uint16_t*>(p.out) + row + (lane & 1) * p.out_stride_h + (col & ~1);
+#pragma unroll
+        for (int k = 0; k < 16; k += 2, dst += 2 * p.out_stride_h) {
+          const float mine_ = __uint_as_float(lane & 1 ? o[k + 1] : o[k]);
+          const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(lane & 1 ? o[k] : o[k + 1]), 1);
+          if (h + k + (lane & 1) < heads)
+            *reinterpret_cast<uint32_t*>(dst) = lane & 1 ? pack_bf16x2(other, mine_) : pack_bf16x2(mine_, other);
+        }
+      }
+    }
+    tmem_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.o_free);
+  };
+
+  if (idle) {
     // no tiles
   } else if (warp == kIndexWarp) {
     // -------------------------------------------------------------------------- walk the run
     int64_t r = sm.first_request, tile = sm.first_tile;
+    int64_t left = sm.end - sm.begin;
     int64_t started = tile;  // the request's tile at which this run takes it up
     const uint32_t bs = static_cast<uint32_t>(p.kv_bs);
     int64_t window = r;      // lanes hold the lengths of requests window .. window + 31
@@ -371,17 +504,18 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         id[h] = key < nn ? __ldg(p.table + rr * p.table_stride + static_cast<uint32_t>(key) / bs) : -1;
       }
     };
-    load_ids(r, tile, n);
-    int64_t left = end - begin;
-    for (int i = 0; left >= 0; ++i, --left) {
+    int odd = 0;
+    if (left > 0) load_ids(r, tile, n);
+    for (int i = 0; left > -2; ++i, --left) {
       const int slot = i % kRing;
       if (i >= kRing && !warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1)) break;
       TileDesc& d = sm.ring[slot];
-      if (left == 0) {
-        if (lane == 0) d.flags = kEnd;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring_full[slot]);
-        break;
+      if (left <= 0) {  // the end, once for each half of the decoding warps
+        if (lane == 0) {
+          d.flags = kEnd;
+          mbar_arrive(&sm.ring_full[slot]);
+        }
+        continue;
       }
       const int64_t tiles = tiles_of(n);
       uint64_t mask = 0;
@@ -397,14 +531,30 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const uint8_t* blk = p.kc + static_cast<int64_t>(ok ? id[h] : 0) * p.kc_stride0;
         from[h] = ok ? blk + static_cast<int64_t>(off) * kTokenStride : nullptr;
         sc[h] = blk + p.kv_bs * kTokenStride + static_cast<int64_t>(off) * kScaleDim;
+        d.data[32 * h + lane] = from[h];
+        d.scales[32 * h + lane] = sc[h];
         mask |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * h);
       }
-      const bool last_of_request = tile + 1 == tiles, last = last_of_request || left == 1;
-      const int64_t here = r;
-      const int flags = (tile == started ? kFirst : 0) | (last ? kLast : 0);
-      const int part = started == 0 && last_of_request ? -1 : 2 * column + (started == 0 ? 1 : 0);
-      // the next tile's block ids are on their way while this tile is written
+      const bool last_of_request = tile + 1 == tiles;
+      if (lane == 0) {
+        d.mask = mask;
+        d.flags = (tile == started ? kFirst : 0) | (last_of_request || left == 1 ? kLast : 0) | odd;
+        d.request = static_cast<int32_t>(r);
+        d.part = started == 0 && last_of_request ? -1 : 2 * column + (started == 0 ? 1 : 0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ring_full[slot]);
+      // Into L2, line by line (a bulk prefetch is one operation per lane, some 40 cycles each).
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (from[h] != nullptr) {
+#pragma unroll
+          for (int b = 0; b < kTokenStride; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from[h] + b));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(sc[h]));
+        }
+      }
       if (last_of_request) {
+        odd ^= kOdd;
         ++r;
         tile = started = 0;
         if (r - window >= 32) {
@@ -416,51 +566,31 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         ++tile;
       }
       if (left > 1) load_ids(r, tile, n);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        d.data[32 * h + lane] = from[h];
-        d.scales[32 * h + lane] = sc[h];
-        if (from[h] != nullptr) {
-          if (ALIGN16) {
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from[h]), "n"(kTokenStride) : "memory");
-          } else {
-#pragma unroll
-            for (int b = 0; b < kTokenStride; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from[h] + b));
-          }
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(sc[h]));
-        }
-      }
-      if (lane == 0) {
-        d.mask = mask;
-        d.flags = flags;
-        d.request = static_cast<int32_t>(here);
-        d.part = part;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.ring_full[slot]);
     }
     if (err) atomicOr(p.err, err);
-  } else if (warp < kFillWarps) {
+  } else if (warp < 2 * kFillWarps) {
     // ------------------------------------------------------------------------ decode the entries
     // Four threads per entry; thread `sub` of an entry takes the 16 bytes sub, sub + 4, ...: of the
     // codes a quarter of each 64-column chunk, so load j belongs to scale j.
-    const int key = 8 * warp + (lane >> 2), sub = lane & 3;
+    const int buf = warp / kFillWarps;  // and the parity of this warp's tiles
+    const int key = 8 * (warp % kFillWarps) + (lane >> 2), sub = lane & 3;
+    const uint32_t dst = smem_addr(sm.k[buf]) + key * 128;
+    const uint32_t swz = static_cast<uint32_t>(key & 7) << 4;
     uint4 raw[9];
     uint2 sc;
-    const uint32_t row = smem_addr(sm.k[0]) + key * 128;
-    const uint32_t swz = static_cast<uint32_t>(key & 7) << 4;
     const uint8_t* src = nullptr;
     const uint8_t* ssrc = nullptr;
     auto load = [&](int j) { return src == nullptr ? make_uint4(0, 0, 0, 0) : ALIGN16 ? ld16(src + 64 * j + 16 * sub) : ld8x2(src + 64 * j + 16 * sub); };
+    auto load_scales = [&] { return src == nullptr ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : ld8(ssrc); };
     bool more = false;
+    int flags = 0;
     // take tile i's addresses out of the ring
     auto fetch = [&](int i) -> bool {
       const int slot = i % kRing;
-      if (!warp_wait(&sm.ring_full[slot], (i / kRing) & 1)) {
-        more = false;
-        return false;
-      }
-      more = (sm.ring[slot].flags & kEnd) == 0;
+      more = false;
+      if (!warp_wait(&sm.ring_full[slot], (i / kRing) & 1)) return false;
+      flags = sm.ring[slot].flags;
+      more = (flags & kEnd) == 0;
       if (more) {
         src = sm.ring[slot].data[key];
         ssrc = sm.ring[slot].scales[key];
@@ -469,56 +599,70 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       return true;
     };
-    fetch(0);
+    fetch(buf);
     if (more) {
+      sc = load_scales();
 #pragma unroll
       for (int j = 0; j < 9; ++j) raw[j] = load(j);
-      sc = src == nullptr ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(ssrc));
     }
-    for (int i = 0; more; ++i) {
-      const int buf = i & 1;
-      if (!fetch(i + 1)) break;
-      const uint2 sc_now = sc;
-      if (more) sc = src == nullptr ? make_uint2(0, 0) : __ldg(reinterpret_cast<const uint2*>(ssrc));
-      if (i >= 2 && !warp_wait(&sm.pv_done[buf], (i / 2 - 1) & 1)) break;
-      const uint32_t dst = row + buf * kTileBytes;
-      const uint32_t hi = sc_now.y & 0x00ffffffu;
-      const bool big = __vcmpgtu4(sc_now.x, 0x01010101u * kMaxFastScale) != 0 || __vcmpgtu4(hi, 0x01010101u * kMaxFastScale) != 0;
-#pragma unroll
-      for (int j = 0; j < 7; ++j) {
-        const uint32_t sb = ((j < 4 ? sc_now.x : hi) >> (8 * (j & 3))) & 0xffu;
+    for (int i = buf; more; i += 2) {
+      const uint2 now = sc;
+      auto decode = [&](int j, uint32_t (&o)[8]) {
+        const float scale = scale_of(((j < 4 ? now.x : now.y) >> (8 * (j & 3))) & 0xffu);
         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-        uint32_t nan = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) nan |= ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-        uint32_t o[8];
-        if (!big && nan == 0) {
-          const uint32_t mul = (sb + 120u) * 0x00800080u;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[2 * k] = codes_to_bf16(__byte_perm(w[k], 0, 0x1404), mul);
-            o[2 * k + 1] = codes_to_bf16(__byte_perm(w[k], 0, 0x3424), mul);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[2 * k] = codes_to_bf16_any(w[k], static_cast<int>(sb));
-            o[2 * k + 1] = codes_to_bf16_any(w[k] >> 16, static_cast<int>(sb));
-          }
+        for (int k = 0; k < 4; ++k) {
+          o[2 * k] = codes_to_bf16(static_cast<uint16_t>(w[k]), scale);
+          o[2 * k + 1] = codes_to_bf16(static_cast<uint16_t>(w[k] >> 16), scale);
         }
+      };
+      auto store = [&](int j, const uint32_t (&o)[8]) {
         const uint32_t at = dst + j * kChunkBytes;
         sts16(at + ((32u * sub) ^ swz), o[0], o[1], o[2], o[3]);
         sts16(at + ((32u * sub + 16u) ^ swz), o[4], o[5], o[6], o[7]);
-        if (more) raw[j] = load(j);
-      }
+      };
+      auto taken = [&](int quarter) { return i < 2 || warp_wait(&sm.k_free[buf][quarter], (i / 2 - 1) & 1); };
+      auto publish = [&](int half) {
+        async_proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.k_full[buf][half]);
+      };
+      // The first half is decoded into registers before its room in the buffer is free.
+      uint32_t o[3][8];
 #pragma unroll
-      for (int j = 7; j < 9; ++j) {  // the rope columns are bf16 already
+      for (int j = 0; j < 3; ++j) decode(j, o[j]);
+      if (!taken(0)) break;
+      store(0, o[0]);
+      store(1, o[1]);
+      decode(3, o[0]);
+      if (!taken(1)) break;
+      store(2, o[2]);
+      store(3, o[0]);
+      publish(0);
+#pragma unroll
+      for (int j = 4; j < 7; ++j) decode(j, o[j - 4]);
+      if (!taken(2)) break;
+      store(4, o[0]);
+      store(5, o[1]);
+      if (!taken(3)) break;
+      store(6, o[2]);
+#pragma unroll
+      for (int j = 7; j < 9; ++j)  // the rope columns are bf16 already
         sts16(dst + 7 * kChunkBytes + ((64u * (j - 7) + 16u * sub) ^ swz), raw[j].x, raw[j].y, raw[j].z, raw[j].w);
-        if (more) raw[j] = load(j);
+      publish(1);
+      const int done = flags;
+      if (!fetch(i + 2)) break;
+      if (more) {
+        sc = load_scales();
+#pragma unroll
+        for (int j = 0; j < 9; ++j) raw[j] = load(j);
       }
-      async_proxy_fence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[buf]);
+      if (done & kLast) {
+        // O being done, the runs before this one are finished with, and the parity means this run
+        if (!warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1)) break;
+        if (!warp_wait(&sm.inv_full, done & kOdd ? 1 : 0)) break;
+        store_results(1 + (warp % kFillWarps) / 4, sm.done_request, sm.done_part);
+      }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------------ issue the products
@@ -528,257 +672,340 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (elect_one()) {
       const uint32_t q_at = desc_low(smem_addr(sm.q), 16), ks_at = desc_low(smem_addr(sm.k[0]), 16);
       const uint32_t kv_at = desc_low(smem_addr(sm.k[0]), kChunkBytes), p_at = desc_low(smem_addr(sm.p[0]), 16);
-      constexpr uint32_t s_desc = mma_desc(kGroup, kTile, false);
+      const uint32_t s_desc = mma_desc(kTile, heads16, false);
       const uint32_t o_desc = mma_desc(128, heads16, true);
-      int seg = -1, prev_flags = 0, prev_seg = 0;
-      bool failed = false, loading = false;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (failed) return false;
-        if (decode_wait(bar, parity, abort_flag)) return true;
+      const int boxes = heads16 / kBoxHeads;
+      const uint32_t box_bytes = static_cast<uint32_t>(min(p.heads, kBoxHeads)) * 128;
+      int s_next = 0, o_next = 0;      // tiles whose S and whose O come next; S is at most one tile ahead
+      int s_seg = -1, o_seg = -1;      // requests begun
+      int flags = 0, o_flags = 0, s_flags = 0;  // of the tile next for S, for O, and of the one between
+      enum { kAwaitTile, kAwaitQueryRoom, kAwaitQueries, kAwaitHalf, kAwaitRest } stage = kAwaitTile;
+      bool ended = false, failed = false, loading = false;
+      int idle_turns = 0;
+      uint32_t t0 = 0;
+      for (;;) {
+        bool progress = false;
+        // S of the next tile, as far as it can go without waiting
+        if (!ended && s_next <= o_next + 1) {
+          const int slot = s_next % kRing, buf = s_next & 1;
+          if (stage == kAwaitTile && mbar_test(&sm.ring_full[slot], (s_next / kRing) & 1)) {
+            flags = sm.ring[slot].flags;
+            progress = true;
+            if (flags & kEnd) {
+              ended = true;
+            } else {
+              stage = flags & kFirst ? kAwaitQueryRoom : kAwaitHalf;
+              if (flags & kFirst) ++s_seg;
+            }
+          }
+          if (stage == kAwaitQueryRoom && (s_seg == 0 || mbar_test(&sm.q_free, (s_seg - 1) & 1))) {
+            const int request = sm.ring[slot].request;
+            mbar_arrive_expect_tx(&sm.q_full, static_cast<uint32_t>(boxes * kChunks) * box_bytes);
+            for (int b = 0; b < boxes; ++b)
+              for (int c = 0; c < kChunks; ++c)
+                load_query_box(sm.q + c * (kGroup * 128) + b * (kBoxHeads * 128), &q_map, 64 * c,
+                               group * group_heads + b * kBoxHeads, request, &sm.q_full);
+            loading = true;
+            stage = kAwaitQueries;
+            progress = true;
+          }
+          if (stage == kAwaitQueries && mbar_test(&sm.q_full, s_seg & 1)) {
+            loading = false;
+            stage = kAwaitHalf;
+            progress = true;
+          }
+          auto half_of_s = [&](int half) {
+            tmem_fence_after();
+#pragma unroll
+            for (int k = 0; k < kChunks / 2; ++k) {
+              const int c = half * (kChunks / 2) + k;
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) {
+                const uint32_t a = q_at + ((c * (kGroup * 128) + ks * 32) >> 4);
+                const uint32_t b = ks_at + ((buf * kTileBytes + c * kChunkBytes + ks * 32) >> 4);
+                mma(tmem + kTmemS + buf * kGroup, b, a, s_desc, half + k + ks > 0);
+              }
+            }
+          };
+          if (!ended && stage == kAwaitHalf && (s_next < 2 || mbar_test(&sm.s_free[buf], (s_next / 2 - 1) & 1)) &&
+              mbar_test(&sm.k_full[buf][0], (s_next / 2) & 1)) {
+            mbar_arrive(&sm.ring_free[slot]);
+            half_of_s(0);
+            stage = kAwaitRest;
+            progress = true;
+          }
+          if (stage == kAwaitRest && mbar_test(&sm.k_full[buf][1], (s_next / 2) & 1)) {
+            half_of_s(1);
+            mma_commit(&sm.s_full[buf]);
+            if (flags & kLast) mma_commit(&sm.q_free);
+            if (s_next == o_next) o_flags = flags; else s_flags = flags;
+            ++s_next;
+            stage = kAwaitTile;
+            progress = true;
+          }
+        }
+        // O^T += K^T P^T of the oldest tile whose P is there
+        if (!failed && o_next < s_next && mbar_test(&sm.p_full[o_next & 1], (o_next / 2) & 1)) {
+          const bool first = o_flags & kFirst;
+          if (!first || o_seg < 0 || mbar_test(&sm.o_free, o_seg & 1)) {
+            const int buf = o_next & 1;
+            if (first) ++o_seg;
+            tmem_fence_after();
+#pragma unroll
+            for (int mt = 0; mt < kQuarters; ++mt) {
+#pragma unroll
+              for (int ks = 0; ks < kTile / 16; ++ks) {
+                const uint32_t a = kv_at + ((buf * kTileBytes + 2 * mt * kChunkBytes + ks * 2048) >> 4);
+                const uint32_t b = p_at + ((buf * (kGroup * kTile * 2) + ks * 2048) >> 4);
+                mma(tmem + mt * kGroup, a, b, o_desc, !first || ks > 0);
+              }
+              mma_commit(&sm.k_free[buf][mt]);
+            }
+            o_flags = s_flags;
+            ++o_next;
+            progress = true;
+          }
+        }
+        if (failed || (ended && o_next == s_next)) break;
+        if (progress) {
+          idle_turns = 0;
+        } else {
+          if (idle_turns++ == 0) t0 = clock();
+          __nanosleep(20);  // tests in a tight loop take shared-memory cycles from the products
+          if ((idle_turns & 63) == 0 && (*abort_flag || static_cast<uint32_t>(clock()) - t0 > kWaitCycles)) failed = true;
+        }
+      }
+      if (failed) {
         *abort_flag = 1;
         atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
-        failed = true;
-        return false;
-      };
-      auto product_pv = [&](int i, int flags, int s) {  // O^T += K^T P^T of tile i
-        const int buf = i & 1;
-        if (!wait(&sm.p_full[buf], (i / 2) & 1)) return;
-        if ((flags & kFirst) && s > 0 && !wait(&sm.o_free, (s - 1) & 1)) return;
-        tmem_fence_after();
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks) {
-            const uint32_t a = kv_at + ((buf * kTileBytes + 2 * mt * kChunkBytes + ks * 2048) >> 4);
-            const uint32_t b = p_at + ((buf * (kGroup * kTile * 2) + ks * 32) >> 4);
-            mma(tmem + mt * kGroup, a, b, o_desc, !(flags & kFirst) || ks > 0);
-          }
-        }
-        mma_commit(&sm.pv_done[buf]);
-      };
-      int i = 0;
-      for (; !failed; ++i) {
-        const int slot = i % kRing, buf = i & 1;
-        if (!wait(&sm.ring_full[slot], (i / kRing) & 1)) break;
-        const int flags = sm.ring[slot].flags;
-        if (flags & kEnd) break;
-        const int request = sm.ring[slot].request;
-        mbar_arrive(&sm.ring_free[slot]);
-        if (flags & kFirst) {
-          ++seg;
-          if (seg > 0 && !wait(&sm.q_free, (seg - 1) & 1)) break;
-          mbar_arrive_expect_tx(&sm.q_full, static_cast<uint32_t>(box_heads) * kHead * 2);
-          for (int c = 0; c < kChunks; ++c)
-            load_query_box(sm.q + c * (kGroup * 128), &q_map, 64 * c, group * kGroup, request, &sm.q_full);
-          loading = true;
-          if (i > 0) product_pv(i - 1, prev_flags, prev_seg);
-          if (!wait(&sm.q_full, seg & 1)) break;
-          loading = false;
-        }
-        if (!wait(&sm.k_full[buf], (i / 2) & 1)) break;
-        if (i >= 2 && !wait(&sm.s_free[buf], (i / 2 - 1) & 1)) break;
-        tmem_fence_after();
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t a = q_at + ((c * (kGroup * 128) + ks * 32) >> 4);
-            const uint32_t b = ks_at + ((buf * kTileBytes + c * kChunkBytes + ks * 32) >> 4);
-            mma(tmem + kTmemS + buf * kTile, a, b, s_desc, c + ks > 0);
-          }
-        }
-        mma_commit(&sm.s_full[buf]);
-        if (flags & kLast) mma_commit(&sm.q_free);
-        if (!(flags & kFirst) && i > 0) product_pv(i - 1, prev_flags, prev_seg);
-        prev_flags = flags;
-        prev_seg = seg;
       }
-      if (!failed && i > 0) product_pv(i - 1, prev_flags, prev_seg);
       // nothing may be in flight when the CTA ends
       mma_commit(&sm.drained);
       decode_wait(&sm.drained, 0, nullptr);
-      if (loading) decode_wait(&sm.q_full, seg & 1, nullptr);
+      if (loading) decode_wait(&sm.q_full, s_seg & 1, nullptr);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------------------------ softmax
-    const int w = warp - kFillWarps;                 // TMEM lanes 32w .. 32w + 31
+    const int w = warp - kSoftWarp;                  // TMEM lanes 32w .. 32w + 31
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
-    const int h0 = 16 * w + (lane >> 2), h1 = h0 + 8;  // this thread's two heads of S
-    const bool active = 16 * w < heads16;
+    const int key0 = 16 * w + (lane >> 2), key1 = key0 + 8;  // this thread's two entries of a tile
+    const int h0 = 2 * (lane & 3);  // and its heads: h0 and h0 + 1 of every 8
     const float c2 = p.scale * kLog2e;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    // Barrier of the four warps (a bounded one, so that a warp that gave up holds up no other) with
-    // the OR of `pred` over them. A warp is at most one barrier ahead, hence two sets of votes.
-    uint32_t soft_phase = 0;
-    bool any = false;
-    auto soft_sync = [&](bool pred) {
-      const bool mine_ = __any_sync(0xffffffffu, pred);
-      __syncwarp();
-      if (lane == 0) {
-        sm.vote[soft_phase][w] = mine_;
-        mbar_arrive(&sm.soft);
-      }
-      const bool ok = warp_wait(&sm.soft, soft_phase);
-      const int* v = sm.vote[soft_phase];
-      any = (v[0] | v[1] | v[2] | v[3]) != 0;
-      soft_phase ^= 1;
-      return ok;
+    float l[kGroup / 4];            // its sums: of heads 8g + h0 and + 1 in l[2g], l[2g + 1]
+    // Barriers of the four warps, on a hardware barrier, which has no time limit. So a warp whose wait
+    // ran out does not leave: it says so at the next barrier, which it reaches as the others do, and
+    // all four leave there.
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead) dead = !warp_wait(bar, parity);
     };
     for (int i = 0;; ++i) {
       const int slot = i % kRing, buf = i & 1;
-      if (!warp_wait(&sm.ring_full[slot], (i / kRing) & 1)) break;
-      const int flags = sm.ring[slot].flags;
-      if (flags & kEnd) break;
+      wait(&sm.ring_full[slot], (i / kRing) & 1);
+      const int flags = dead ? 0 : sm.ring[slot].flags;
+      if (flags & kEnd) {  // the two votes that a warp whose wait ran out here takes part in
+        soft_vote(true);
+        soft_vote(true);
+        break;
+      }
+      wait(&sm.s_full[buf], (i / 2) & 1);
+      tmem_fence_after();
+      // The scores are read from TMEM twice, 16 heads at a time, once to look for one that passes its
+      // head's reference: kept in registers between, they would spill, and a spill here is a trip to
+      // L2, beside the little L1 that the tiles leave.
       const uint64_t mask = sm.ring[slot].mask;
+      const bool in0 = mask >> key0 & 1, in1 = mask >> key1 & 1;
+      const bool first = flags & kFirst;
+      const uint32_t s_at = tmem + lanes + kTmemS + buf * kGroup;
+      auto scores = [&](int h, uint32_t (&x)[8]) {  // log2-scaled, -inf where there is no entry
+        tmem_ld_16x16(s_at + h, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          x[k] = (k & 2 ? in1 : in0) ? __float_as_uint(__uint_as_float(x[k]) * c2) : 0xff800000u;
+      };
+      bool raise = dead;
+      if (first) {
+        // the entry's holders write its scores down; without one the references are -inf
+        const int entry = mask != 0 ? __ffsll(static_cast<long long>(mask)) - 1 : 0;
+        if (entry / 16 == w) {
+#pragma unroll 1
+          for (int h = 0; h < heads16; h += 16) {
+            uint32_t x[8];
+            scores(h, x);
+            if ((lane >> 2) == (entry & 7)) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+                *reinterpret_cast<uint2*>(&sm.ref[h + 8 * g + h0]) =
+                    entry & 8 ? make_uint2(x[4 * g + 2], x[4 * g + 3]) : make_uint2(x[4 * g], x[4 * g + 1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < kGroup / 4; ++g) l[g] = 0.f;
+        if (soft_vote(dead)) {
+          soft_vote(true);
+          break;
+        }
+      }
+      {
+#pragma unroll 1
+        for (int h = 0; h < heads16; h += 16) {
+          uint32_t x[8];
+          scores(h, x);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float2 m = *reinterpret_cast<const float2*>(&sm.ref[h + 8 * g + h0]);
+            const bool real0 = h + 8 * g + h0 < heads, real1 = h + 8 * g + h0 + 1 < heads;
+            raise |= real0 && fmaxf(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 2])) > m.x + kSlack;
+            raise |= real1 && fmaxf(__uint_as_float(x[4 * g + 1]), __uint_as_float(x[4 * g + 3])) > m.y + kSlack;
+          }
+        }
+      }
+      if (soft_vote(raise)) {
+        // New references: the maxima so far of all heads. O and the sums are rescaled to them.
+        if (soft_vote(dead)) break;
+#pragma unroll 1
+        for (int h = 0; h < heads16; h += 16) {
+          uint32_t x[8];
+          scores(h, x);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(__uint_as_float(x[4 * g + e]), __uint_as_float(x[4 * g + 2 + e]));
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              if (lane < 4) sm.by_warp[w][h + 8 * g + h0 + e] = top;
+            }
+          }
+        }
+        soft_vote(false);
+        float to[kGroup / 32];  // two heads per lane of every warp
+        float f[kGroup / 32];
+#pragma unroll
+        for (int a = 0; a < kGroup / 32; ++a) {
+          const int h = 32 * a + lane;
+          const float was = sm.ref[h];
+          to[a] = fmaxf(fmaxf(fmaxf(sm.by_warp[0][h], sm.by_warp[1][h]), fmaxf(sm.by_warp[2][h], sm.by_warp[3][h])), was);
+          f[a] = to[a] == -INFINITY ? 1.f : ex2_approx(was - to[a]);
+        }
+        soft_vote(false);  // all have read the old ones
+        if (w == 0) {
+#pragma unroll
+          for (int a = 0; a < kGroup / 32; ++a) sm.ref[32 * a + lane] = to[a], sm.factor[32 * a + lane] = f[a];
+        }
+        if (!first) wait(&sm.k_free[(i - 1) & 1][kQuarters - 1], ((i - 1) / 2) & 1);
+        if (soft_vote(dead)) break;
+#pragma unroll
+        for (int g = 0; g < kGroup / 8; ++g) {
+          if (8 * g < heads16) {
+            l[2 * g] *= sm.factor[8 * g + h0];
+            l[2 * g + 1] *= sm.factor[8 * g + h0 + 1];
+          }
+        }
+        if (!first) {
+          tmem_fence_after();
+#pragma unroll 1
+          for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll 1
+            for (int h = 0; h < heads16; h += 16) {
+              uint32_t o[16];
+              const uint32_t at = tmem + lanes + mt * kGroup + h;
+              tmem_ld_32x16(at, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.factor[h + k]);
+              tmem_st_32x16(at, o);
+            }
+          }
+          tmem_wait_st();
+          tmem_fence_before();
+        }
+      }
+      // the P of two tiles ago has been used
+      if (i >= 2) wait(&sm.k_free[buf][kQuarters - 1], (i / 2 - 1) & 1);
+      {
+        const uint32_t p_at = smem_addr(sm.p[buf]) + key0 * 128 + 2 * h0;
+        const uint32_t swz = static_cast<uint32_t>(key0 & 7) << 4;  // key1 & 7 is the same
+#pragma unroll
+        for (int b = 0; b < kGroup / 16; ++b) {
+          if (16 * b < heads16) {
+            uint32_t x[8];
+            scores(16 * b, x);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float2 m = *reinterpret_cast<const float2*>(&sm.ref[16 * b + 8 * g + h0]);
+              m.x = m.x == -INFINITY ? 0.f : m.x;
+              m.y = m.y == -INFINITY ? 0.f : m.y;
+              float e[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                e[k] = ex2_approx(__uint_as_float(x[4 * g + k]) - (k & 1 ? m.y : m.x));
+                l[4 * b + 2 * g + (k & 1)] += e[k];
+              }
+              const uint32_t at = p_at + ((16u * (2 * b + g)) ^ swz);
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack_bf16x2(e[0], e[1])) : "memory");
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(pack_bf16x2(e[2], e[3])) : "memory");
+            }
+          }
+        }
+        tmem_fence_before();
+        async_proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+      }
       const int request = sm.ring[slot].request, part = sm.ring[slot].part;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
-      if (!warp_wait(&sm.s_full[buf], (i / 2) & 1)) break;
-      tmem_fence_after();
-      uint32_t x[32];
-      tmem_ld_16x64(tmem + lanes + kTmemS + buf * kTile, x);
-      tmem_wait_ld();
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.s_free[buf]);
-      // log2-scaled scores, -inf where there is no entry
-      float top[2] = {-INFINITY, -INFINITY};
-      const uint64_t bits = mask >> (2 * (lane & 3));
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool in = (bits >> (8 * g + (k & 1))) & 1;
-          const float t = in ? __uint_as_float(x[4 * g + k]) * c2 : -INFINITY;
-          x[4 * g + k] = __float_as_uint(t);
-          top[k >> 1] = fmaxf(top[k >> 1], t);
-        }
+      if (lane == 0) {
+        mbar_arrive(&sm.p_full[buf]);
+        mbar_arrive(&sm.ring_free[slot]);
       }
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], 1));
-        top[a] = fmaxf(top[a], __shfl_xor_sync(0xffffffffu, top[a], 2));
-      }
-      if (flags & kFirst) {
-        m[0] = top[0], m[1] = top[1];
-        l[0] = l[1] = 0.f;
-      } else if (!soft_sync(active && (top[0] > m[0] + kSlack || top[1] > m[1] + kSlack))) {
-        break;
-      } else if (any) {
-        // raise the references of all heads, and O and the sums with them
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const float to = fmaxf(m[a], top[a]);
-          const float f = to == -INFINITY ? 1.f : ex2_approx(m[a] - to);
-          m[a] = to;
-          l[a] *= f;
-          if ((lane & 3) == 0) sm.factor[a == 0 ? h0 : h1] = f;
-        }
-        if (!soft_sync(false)) break;
-        if (!warp_wait(&sm.pv_done[(i - 1) & 1], ((i - 1) / 2) & 1)) break;
-        tmem_fence_after();
-        for (int mt = 0; mt < 4; ++mt) {
-          for (int h = 0; h < heads16; h += 16) {
-            uint32_t o[16];
-            const uint32_t at = tmem + lanes + mt * kGroup + h;
-            tmem_ld_32x16(at, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.factor[h + k]);
-            tmem_st_32x16(at, o);
-          }
-        }
-        tmem_wait_st();
-        tmem_fence_before();
-      }
-      const float shift[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-      if (i >= 2 && !warp_wait(&sm.pv_done[buf], (i / 2 - 1) & 1)) break;  // the P of two tiles ago has been used
-      if (active) {
-        const uint32_t p_at = smem_addr(sm.p[buf]) + 4 * (lane & 3);
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float e[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            e[k] = ex2_approx(__uint_as_float(x[4 * g + k]) - shift[k >> 1]);
-            l[k >> 1] += e[k];
-          }
-          const uint32_t at = static_cast<uint32_t>((g ^ (h0 & 7)) << 4);  // h1 & 7 == h0 & 7
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_at + h0 * 128 + at), "r"(pack_bf16x2(e[0], e[1])) : "memory");
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_at + h1 * 128 + at), "r"(pack_bf16x2(e[2], e[3])) : "memory");
-        }
-        async_proxy_fence();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[buf]);
       if (!(flags & kLast)) continue;
 
       // ---------------------------------------------------------------------- the run's result
       const bool whole = part < 0;
+      const int group0 = sm.group * sm.group_heads;  // the first head of this CTA
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        l[a] += __shfl_xor_sync(0xffffffffu, l[a], 1);
-        l[a] += __shfl_xor_sync(0xffffffffu, l[a], 2);
-        const int h = a == 0 ? h0 : h1;
-        const int64_t head = group * kGroup + h;
-        if ((lane & 3) == 0) {
-          float sum = l[a], to = shift[a], f = 1.f;
-          if (whole && p.sink != nullptr && h < heads) {  // one more score, with a value of zero
-            const float s = __ldg(p.sink + head) * kLog2e;
-            to = fmaxf(m[a], s);
-            to = to == -INFINITY ? 0.f : to;
-            f = ex2_approx(shift[a] - to);
-            sum = sum == 0.f ? ex2_approx(s - to) : sum * f + ex2_approx(s - to);
-          }
-          sm.inv[h] = l[a] == 0.f ? 0.f : f / sum;
-          if (h < heads) {
-            const float lse2 = sum == 0.f ? -INFINITY : to + log2f(sum);
-            if (!whole)
-              reinterpret_cast<float*>(p.workspace + scratch.lse_at())[scratch.row(part, group, h)] = lse2;
-            else if (p.lse != nullptr)
-              p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
+      for (int g = 0; g < kGroup / 8; ++g) {
+        if (8 * g < heads16) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float sum = l[2 * g + e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane < 4) sm.by_warp[w][8 * g + h0 + e] = sum;
           }
         }
       }
-      if (!soft_sync(false)) break;
-      if (!warp_wait(&sm.pv_done[buf], (i / 2) & 1)) break;
-      tmem_fence_after();
-      for (int mt = 0; mt < 4; ++mt) {
-        const int col = mt * 128 + 32 * w + lane;
-        for (int h = 0; h < heads; h += 16) {
-          uint32_t o[16];
-          tmem_ld_32x16(tmem + lanes + mt * kGroup + h, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sm.inv[h + k]);
-          if (!whole) {
-            float* dst = reinterpret_cast<float*>(p.workspace + scratch.out_at()) + scratch.row(part, group, h) * kHead + col;
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (h + k < heads) dst[k * kHead] = __uint_as_float(o[k]);
-          } else if (p.out_f32) {
-            float* dst = static_cast<float*>(p.out) + request * p.out_stride_r + (group * kGroup + h) * p.out_stride_h + col;
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (h + k < heads) dst[k * p.out_stride_h] = __uint_as_float(o[k]);
-          } else {
-            // neighbouring lanes swap halves of a pair of heads, so that each stores two columns of one
-            uint16_t* dst = static_cast<uint16_t*>(p.out) + request * p.out_stride_r +
-                            (group * kGroup + h + (lane & 1)) * p.out_stride_h + (col & ~1);
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float mine_ = __uint_as_float(lane & 1 ? o[k + 1] : o[k]);
-              const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(lane & 1 ? o[k] : o[k + 1]), 1);
-              if (h + k + (lane & 1) < heads)
-                *reinterpret_cast<uint32_t*>(dst + k * p.out_stride_h) = lane & 1 ? pack_bf16x2(other, mine_) : pack_bf16x2(mine_, other);
-            }
-          }
+      // O is done; with it the last run's results have been stored, and `inv` is free
+      wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
+      if (soft_vote(dead)) break;
+      if (w < 2 && 32 * w + lane < heads) {
+        const int h = 32 * w + lane;
+        const int64_t head = group0 + h;
+        const float own = (sm.by_warp[0][h] + sm.by_warp[1][h]) + (sm.by_warp[2][h] + sm.by_warp[3][h]), ref = sm.ref[h];
+        float sum = own, to = ref == -INFINITY ? 0.f : ref, f = 1.f;
+        if (whole && p.sink != nullptr) {  // one more score, with a value of zero
+          const float s = __ldg(p.sink + head) * kLog2e;
+          const float top = fmaxf(ref, s), shift = top == -INFINITY ? 0.f : top;
+          f = ex2_approx(to - shift);
+          sum = own == 0.f ? ex2_approx(s - shift) : own * f + ex2_approx(s - shift);
+          to = shift;
         }
+        sm.inv[h] = own == 0.f ? 0.f : f / sum;
+        const float lse2 = sum == 0.f ? -INFINITY : to + log2f(sum);
+        if (!whole)
+          reinterpret_cast<float*>(p.workspace + sm.lay.lse_at())[sm.lay.row(part, sm.group, h)] = lse2;
+        else if (p.lse != nullptr)
+          p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
       }
-      tmem_fence_before();
-      if (!soft_sync(false)) break;  // sm.inv is free again
-      if (lane == 0) mbar_arrive(&sm.o_free);
+      if (w == 0 && lane == 0) sm.done_request = request, sm.done_part = part;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.inv_full);
+      soft_vote(false);
+      store_results(0, request, part);
     }
   }
   tmem_fence_before();
@@ -790,84 +1017,94 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 }
 
 // ------------------------------------------------------------------- join the partial results
-// One warp per (cut request, head, quarter of the columns): out = sum_k 2^(lse_k - L) part_k.
+// out = sum_k 2^(lse_k - L) part_k. One warp per cut request, 4 heads and 32 columns: 16 bytes per lane
+// and part, as the parts are laid out.
 constexpr int kJoinThreads = 256;
-constexpr int kMaxColumns = 1024;
+constexpr int kMaxCtas = 1024;
 
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p, const Scratch scratch) {
-  __shared__ int s_owner[kMaxColumns];
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p, const int sms, const int ctas) {
+  __shared__ int16_t s_owner[kMaxCtas];
   __shared__ int s_count;
+  launch_dependents();
   grid_dependency_wait();
   const Task* tasks = reinterpret_cast<const Task*>(p.workspace);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {  // the columns that start a cut request, in order
+  if (warp == 0) {  // the CTAs that start a cut request, in order
     int count = 0;
-    for (int c0 = 0; c0 < scratch.columns; c0 += 32) {
-      const bool has = c0 + lane < scratch.columns && tasks[c0 + lane].parts > 0;
+    for (int c0 = 0; c0 < ctas; c0 += 32) {
+      const bool has = c0 + lane < ctas && tasks[c0 + lane].parts > 0;
       const unsigned vote = __ballot_sync(0xffffffffu, has);
-      if (has) s_owner[count + __popc(vote & ((1u << lane) - 1))] = c0 + lane;
+      if (has) s_owner[count + __popc(vote & ((1u << lane) - 1))] = static_cast<int16_t>(c0 + lane);
       count += __popc(vote);
     }
     if (lane == 0) s_count = count;
   }
   __syncthreads();
-  const int64_t items = static_cast<int64_t>(s_count) * p.heads * 4;
+  const int heads4 = (p.heads + 3) / 4;
+  const int64_t items = static_cast<int64_t>(s_count) * heads4 * 16;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + warp; item < items;
        item += static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32)) {
-    const int quarter = static_cast<int>(item & 3);
-    const int64_t head = (item >> 2) % p.heads;
-    const int column = s_owner[(item >> 2) / p.heads];
-    const Task t = tasks[column];
-    const int group = static_cast<int>(head / kGroup), h = static_cast<int>(head % kGroup);
-    const float* lse = reinterpret_cast<const float*>(p.workspace + scratch.lse_at());
-    const float* part = reinterpret_cast<const float*>(p.workspace + scratch.out_at());
-    auto row = [&](int k) { return scratch.row(k == 0 ? 2 * column + 1 : 2 * (column + k), group, h); };
+    const int cols32 = static_cast<int>(item & 15);
+    const int head = static_cast<int>((item >> 4) % heads4) * 4;
+    const Task t = tasks[s_owner[(item >> 4) / heads4]];
+    const Layout lay(p.heads, sms, t.group_heads);
+    const int group = head / t.group_heads, h = head % t.group_heads;
+    const float* lse = reinterpret_cast<const float*>(p.workspace + lay.lse_at());
+    const float* part = reinterpret_cast<const float*>(p.workspace + lay.out_at());
+    auto slot = [&](int k) { return k == 0 ? 2 * t.column + 1 : 2 * (t.column + k); };
+    // the parts' statistics: lane = 4 * part + head within eight parts, reduced over the parts
+    const int hh = lane & 3;
+    const bool real = head + hh < p.heads;
     float top = -INFINITY;
     bool nan = false;
-    for (int k = lane; k < t.parts; k += 32) {
-      const float v = lse[row(k)];
+    for (int k = lane >> 2; k < t.parts; k += 8) {
+      const float v = real ? lse[lay.row(slot(k), group, h + hh)] : -INFINITY;
       nan |= v != v;
       top = fmaxf(top, v);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    nan = __any_sync(0xffffffffu, nan);
-    const float sink = p.sink != nullptr ? __ldg(p.sink + head) * kLog2e : -INFINITY;
+    for (int o = 4; o < 32; o <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), o) != 0;
+    }
+    const float sink = p.sink != nullptr && real ? __ldg(p.sink + head + hh) * kLog2e : -INFINITY;
     top = fmaxf(top, sink);
-    const float shift = top == -INFINITY ? 0.f : top;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = p.sink != nullptr ? ex2_approx(sink - shift) : 0.f;
-    constexpr int kFlight = 8;
-    for (int k0 = 0; k0 < t.parts; k0 += kFlight) {
-      float4 v[kFlight];
-      float w[kFlight];
+    const float shift = nan ? NAN : top == -INFINITY ? 0.f : top;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum = lane < 4 ? ex2_approx(sink - shift) : 0.f;  // lane 4k + hh: of head hh, parts k, k + 8, ...
+    for (int k0 = 0; k0 < t.parts; k0 += 8) {
+      const int k = k0 + (lane >> 2);
+      const float w = k < t.parts && real ? ex2_approx(lse[lay.row(slot(k), group, h + hh)] - shift) : 0.f;
+      sum += w;
+      float4 v[8];
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        w[k] = 0.f;
-        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + k < t.parts) {
-          const int64_t at = row(k0 + k);
-          w[k] = ex2_approx(lse[at] - shift);
-          v[k] = *reinterpret_cast<const float4*>(part + at * kHead + 128 * quarter + 4 * lane);
+      for (int u = 0; u < 8; ++u)
+        if (k0 + u < t.parts)
+          v[u] = *(reinterpret_cast<const float4*>(part + lay.block(slot(k0 + u), group, cols32, h / 4)) + lane);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w0 = __shfl_sync(0xffffffffu, w, 4 * u), w1 = __shfl_sync(0xffffffffu, w, 4 * u + 1);
+        const float w2 = __shfl_sync(0xffffffffu, w, 4 * u + 2), w3 = __shfl_sync(0xffffffffu, w, 4 * u + 3);
+        if (k0 + u < t.parts) {
+          acc[0] = fmaf(w0, v[u].x, acc[0]), acc[1] = fmaf(w1, v[u].y, acc[1]);
+          acc[2] = fmaf(w2, v[u].z, acc[2]), acc[3] = fmaf(w3, v[u].w, acc[3]);
         }
       }
+    }
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k) {
-        sum += w[k];
-        acc.x = fmaf(w[k], v[k].x, acc.x), acc.y = fmaf(w[k], v[k].y, acc.y);
-        acc.z = fmaf(w[k], v[k].z, acc.z), acc.w = fmaf(w[k], v[k].w, acc.w);
+    for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float v = acc[k] * __shfl_sync(0xffffffffu, inv, k);
+      const int64_t at = t.request * p.out_stride_r + (head + k) * p.out_stride_h + 32 * cols32 + lane;
+      if (head + k < p.heads) {
+        if (p.out_f32) static_cast<float*>(p.out)[at] = v;
+        else static_cast<uint16_t*>(p.out)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
       }
     }
-    if (nan) sum = NAN;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t at = t.request * p.out_stride_r + head * p.out_stride_h + 128 * quarter + 4 * lane;
-    if (p.out_f32)
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (p.lse != nullptr && quarter == 0 && lane == 0)
-      p.lse[t.request * p.lse_stride_r + head * p.lse_stride_h] =
+    if (p.lse != nullptr && cols32 == 0 && lane < 4 && real)
+      p.lse[t.request * p.lse_stride_r + (head + lane) * p.lse_stride_h] =
           sum == 0.f ? -INFINITY : (shift + log2f(sum)) * 0.69314718055994531f;
   }
 }
@@ -875,13 +1112,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
 constexpr int kDecodeSmemBytes = sizeof(DecodeSmem) + 1024;
 static_assert(kDecodeSmemBytes <= 232448, "shared memory of one SM, with its alignment");
 
-// The queries as [512, heads, requests]; a box is 64 columns of `box` heads of one request.
-bool encode_query_map(const DecodeParams& p, int box, CUtensorMap* map) {
+// The queries as [512, heads, requests]; a box is 64 columns of 16 heads of one request.
+bool encode_query_map(const DecodeParams& p, CUtensorMap* map) {
   const cuuint64_t dims[3] = {kHead, static_cast<cuuint64_t>(p.heads), static_cast<cuuint64_t>(p.requests)};
   // the stride of a dimension with one index does not matter but has to be valid
   const cuuint64_t strides[2] = {p.heads > 1 ? static_cast<cuuint64_t>(p.q_stride_h) * 2 : kHead * 2,
                                  p.requests > 1 ? static_cast<cuuint64_t>(p.q_stride_r) * 2 : kHead * 2};
-  const cuuint32_t size[3] = {64, static_cast<cuuint32_t>(box), 1};
+  const cuuint32_t size[3] = {64, static_cast<cuuint32_t>(p.heads < kBoxHeads ? p.heads : kBoxHeads), 1};
   const cuuint32_t step[3] = {1, 1, 1};
   auto enc = tensor_map_encoder();
   return enc != nullptr &&
@@ -898,31 +1135,33 @@ cudaError_t prepare_decode() {
   return e != cudaSuccess ? e : cudaFuncSetAttribute(decode_kernel<false>, a, kDecodeSmemBytes);
 }
 
-int64_t decode_workspace_bytes(int heads, int sm_count) { return Scratch(heads, sm_count).bytes(); }
+int64_t decode_workspace_bytes(int heads, int sm_count) { return Layout(heads, sm_count, kGroup).bytes(); }
 
 cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stream) {
-  const Scratch scratch(p.heads, sm_count);
-  const int box = p.heads < kGroup ? p.heads : kGroup;
   CUtensorMap map;
-  if (!encode_query_map(p, box, &map)) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(scratch.columns * scratch.groups);
+  if (!encode_query_map(p, &map)) return cudaErrorInvalidValue;
+  const int ctas = Layout(p.heads, sm_count, kGroup).ctas;
+  if (ctas > kMaxCtas) return cudaErrorInvalidValue;
   const bool align16 = p.kc_stride0 % 16 == 0;  // records then start on 16 bytes, else on 8
-  if (align16) decode_kernel<true><<<grid, kDecodeThreads, kDecodeSmemBytes, stream>>>(p, map, scratch, box);
-  else decode_kernel<false><<<grid, kDecodeThreads, kDecodeSmemBytes, stream>>>(p, map, scratch, box);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int64_t cut = p.requests < scratch.columns ? p.requests : scratch.columns;  // requests that can be cut
-  const int64_t ctas = (cut * p.heads * 4 + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(static_cast<unsigned>(ctas < 8 * sm_count ? ctas : 8 * sm_count));
-  lc.blockDim = dim3(kJoinThreads);
+  lc.gridDim = dim3(static_cast<unsigned>(ctas));
+  lc.blockDim = dim3(kDecodeThreads);
+  lc.dynamicSmemBytes = kDecodeSmemBytes;
   lc.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, join_kernel, p, scratch);
+  const cudaError_t e = align16 ? cudaLaunchKernelEx(&lc, decode_kernel<true>, p, map, sm_count)
+                                : cudaLaunchKernelEx(&lc, decode_kernel<false>, p, map, sm_count);
+  if (e != cudaSuccess) return e;
+  const int64_t cut = p.requests < ctas ? p.requests : ctas;  // requests that can be cut
+  const int64_t join_ctas = (cut * ((p.heads + 3) / 4) * 16 + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  lc.gridDim = dim3(static_cast<unsigned>(join_ctas < 8 * sm_count ? join_ctas : 8 * sm_count));
+  lc.blockDim = dim3(kJoinThreads);
+  lc.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&lc, join_kernel, p, sm_count, ctas);
 }
 
 }  // namespace c128
