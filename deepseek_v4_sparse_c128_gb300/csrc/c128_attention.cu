@@ -15,22 +15,25 @@
 // sums to the end. Heads are dealt out in groups of 64; a group decodes the cache for itself (the
 // second group's reads hit L2).
 //
-// The running reference m is not the maximum: it is the score of the run's first entry, and is raised
-// (to the maximum so far, rescaling O in TMEM) only when a score passes it by a factor of 2^32. P, its
-// sums and O are floating point, so a common factor costs no precision, and 2^32 times 2^25 entries of
-// 2^70 is still inside the range.
+// The running reference m need not be the maximum: P, its sums and O are floating point, so a common
+// factor costs no precision. So m is 0 where that does, that is where every head has a score within
+// 2^+-32 of 1 in the first tile, and none above it (2^32 times 2^25 entries of 2^70 is still inside
+// the range). Else it is raised or lowered to the maximum so far, O in TMEM rescaled with it.
 //
 // Work is dealt out in tiles: the requests' tiles, one after the other, are cut into as many equal
 // runs as there are CTAs, so a long request is shared by many CTAs and a CTA takes many short ones. A
 // request that is cut leaves fp32 partial results in the workspace, joined by a second kernel.
 //
-// Roles of the 22 warps (each wait is bounded, see c128_device.cuh):
-//   0..15  decode: eight warps the even tiles, eight the odd ones, the next tile's bytes already in
-//          registers. Tiles pass to the products and back in quarters (128 columns), so that S starts
-//          behind the first quarter and a quarter that O has taken is decoded into again at once
-//   16..19 softmax of S, rescaling of O, results
-//   20     one thread issues the products and the queries' TMA loads
-//   21     walks the runs: per tile the address of each entry (through the block table), prefetched
+// Roles of the 19 warps (each wait is bounded; five warps to a scheduler leave them 96 registers, and a
+// spill would be a trip to L2, beside the little L1 that the tiles leave):
+//   0..7   decode the entries of a tile, in registers until the buffer has room, the next tile's bytes
+//          on their way meanwhile. Tiles pass to S in halves of the columns and come back from O in
+//          quarters
+//   8..15  softmax, four warps for either half of the heads; rescaling of O; results
+//   16, 17 one thread each issues the first product (and the queries' TMA loads) and the second. Two,
+//          so that either waits for its own operands: one thread that looks for whichever is ready
+//          first takes a third of all issued instructions, and holds up the warps beside it
+//   18     walks the runs: per tile the address of each entry (through the block table), prefetched
 //          to L2 a few tiles ahead
 #include <cuda_runtime.h>
 
@@ -50,14 +53,14 @@ constexpr int kChunks = kHead / 64; // 64-column chunks of 128 bytes (bf16): one
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kTileBytes = kChunks * kChunkBytes;  // a decoded tile: 64 KiB
 constexpr int kQuarters = 4;        // of a tile's columns: 128 each, an M of the second product
-constexpr int kFillWarps = 8, kSoftWarps = 4;  // fill warps per tile buffer
-constexpr int kSoftWarp = 2 * kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 1;
+constexpr int kFillWarps = 8, kSoftWarps = 8;
+constexpr int kSoftWarp = kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
 constexpr int kRing = 4;            // tiles the index warp may be ahead
-constexpr float kSlack = 32.f;      // log2 units a score may pass the reference by
+constexpr float kSlack = 32.f;      // log2 units a score may be from the reference
 constexpr int kTmemCols = 512, kTmemS = 256;  // O in columns 0..255, two S tiles behind it
 
-enum : int { kFirst = 1, kLast = 2, kEnd = 4, kOdd = 8 };  // of its run of one request's tiles; kOdd: an odd run
+enum : int { kFirst = 1, kLast = 2, kEnd = 4 };  // first or last of its run of one request's tiles
 
 struct Task {  // a request that a CTA starts and leaves to the columns behind it, if parts > 0
   int32_t request, parts, column, group_heads;
@@ -69,7 +72,7 @@ struct Task {  // a request that a CTA starts and leaves to the columns behind i
 struct Layout {
   int groups, columns, heads, ctas;  // head groups, CTA columns, heads held per slot and group
   Layout() = default;
-  __host__ __device__ Layout(int all_heads, int sms, int group) {
+  Layout(int all_heads, int sms, int group) {
     groups = (all_heads + group - 1) / group;
     columns = sms / groups > 0 ? sms / groups : 1;
     heads = groups > 1 ? group : (all_heads + 15) / 16 * 16;
@@ -91,6 +94,11 @@ struct Layout {
   }
 };
 
+struct Layouts {  // made on the host: their divisions would stand in front of the kernel's work
+  Layout of[3];   // for groups of 16, 32 and 64 heads
+  int sms;
+};
+
 struct TileDesc {
   const uint8_t* data[kTile];    // record of each entry, NULL where there is none
   const uint8_t* scales[kTile];
@@ -108,7 +116,7 @@ struct DecodeSmem {
   alignas(16) float ref[kGroup];      // the running references m
   alignas(16) float factor[kGroup];   // what O is rescaled by
   alignas(16) float inv[kGroup];      // 1 / sum
-  float by_warp[kSoftWarps][kGroup];  // maxima or sums of the softmax warps' entries
+  float by_warp[4][kGroup];           // maxima or sums of 16 entries each
   uint64_t ring_full[kRing], ring_free[kRing];
   uint64_t k_full[2][2];              // half of a tile's columns decoded
   uint64_t k_free[2][kQuarters];      // O has taken the quarter (the last: O is done)
@@ -168,6 +176,10 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool mn_major) {  
   return 1u << 4 | 1u << 7 | 1u << 10 | (mn_major ? 3u << 15 : 0u) | static_cast<uint32_t>(n >> 3) << 17 |
          static_cast<uint32_t>(m >> 4) << 24;
 }
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
@@ -190,11 +202,25 @@ __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// 16 lanes x 16 columns: thread t gets rows t/4 and t/4 + 8, columns 8g + 2(t%4) and + 1 in x[4g ..]
-__device__ __forceinline__ void tmem_ld_16x16(uint32_t addr, uint32_t (&x)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
-               : "r"(addr));
+// 16 lanes x N columns: thread t gets rows t/4 and t/4 + 8, columns 8g + 2(t%4) and + 1 in x[4g ..]
+template <int N>
+__device__ __forceinline__ void tmem_ld_scores(uint32_t addr, uint32_t (&x)[N / 2]) {
+  if constexpr (N == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]),
+          "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+        : "r"(addr));
+  } else if constexpr (N == 16) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                 : "r"(addr));
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(addr));
+  }
 }
 // 32 lanes x 16 columns, a lane's columns in one thread
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t addr, uint32_t (&x)[16]) {
@@ -236,23 +262,31 @@ __device__ __forceinline__ bool soft_vote(bool pred) {
 }
 
 // ------------------------------------------------------------------------------------- decoding
-// Two e4m3 codes times a power of two to bf16x2, by way of fp16 (exact, NaN stays NaN) and fp32. 53
-// cycles of a scheduler per 16 codes and warp; moving the bits into bf16 fields and multiplying there
-// took 85, most of it half-rate integer operations, NaN codes aside.
-__device__ __forceinline__ uint32_t codes_to_bf16(uint16_t two, float scale) {
-  uint32_t h;
-  float x, y;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "mov.b32 {lo, hi}, %2;\n\t"
-      "cvt.f32.f16 %0, lo;\n\t"
-      "cvt.f32.f16 %1, hi;\n}"
-      : "=f"(x), "=f"(y)
-      : "r"(h));
-  return pack_bf16x2(x * scale, y * scale);
+// Two e4m3 codes to fp32, times an fp16 scale: to fp16 (exact, NaN stays NaN), then a product of fp16
+// operands in fp32. With the packing to bf16 50 cycles of a scheduler per 16 codes and warp; moving the
+// bits into bf16 fields and multiplying there took 85, most of it half-rate integer operations.
+__device__ __forceinline__ float2 codes_to_f32(uint16_t two, uint16_t scale) {
+  float2 v;
+  asm("{\n\t.reg .b32 h;\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %2;\n\t"
+      "mov.b32 {lo, hi}, h;\n\t"
+      "fma.rn.f32.f16 %0, lo, %3, 0f00000000;\n\t"
+      "fma.rn.f32.f16 %1, hi, %3, 0f00000000;\n}"
+      : "=f"(v.x), "=f"(v.y)
+      : "h"(two), "h"(scale));
+  return v;
 }
-// 2^(byte - 127): the byte is the float's exponent field (0: the subnormal 2^-127).
+// 2^(byte - 127): the byte is the float's exponent field (0: the subnormal 2^-127). Between 2^-24 and
+// 2^15 it is an fp16 too.
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
+__device__ __forceinline__ bool scales_fit_f16(uint32_t w) {
+  return (__vcmpltu4(w, 0x01010101u * 103) | __vcmpgtu4(w, 0x01010101u * 142)) == 0;
+}
+__device__ __forceinline__ uint16_t to_f16(float x) {
+  uint16_t h;
+  asm("cvt.rn.f16.f32 %0, %1;" : "=h"(h) : "f"(x));
+  return h;
+}
 
 // Read once and past L1, whose memory the tiles and the products use.
 __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
@@ -292,7 +326,10 @@ __device__ __forceinline__ int64_t tiles_of(int64_t entries) { return entries > 
 // A cut that would fall within `snap` tiles of a request's begin or end is moved there: a cut request
 // costs its partial results (2 KB per head and part, written and read again), about what a tile or
 // two take.
-constexpr int kSnap = 1, kSnapShare = 2;
+#ifndef C128_SNAP
+#define C128_SNAP 2
+#endif
+constexpr int kSnap = C128_SNAP;
 struct Deal {
   int64_t share, extra;
   int snap;
@@ -303,7 +340,7 @@ struct Deal {
       share = total / columns;
     }
     extra = total - share * columns;
-    snap = share >= kSnapShare ? kSnap : 0;
+    snap = static_cast<int>(min(share / 2, static_cast<int64_t>(kSnap)));
   }
   __device__ int64_t begin(int column) const { return share * column + min(static_cast<int64_t>(column), extra); }
   __device__ int column_of(int64_t tile) const {
@@ -314,11 +351,65 @@ struct Deal {
   }
 };
 
+// A run's results: O of all heads times 1 / sum, to the output or the workspace. The softmax and the
+// decoding warps share the work, four warps (`rank`) to each quarter of the TMEM lanes.
+__device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams& p, int heads, int rank) {
+  int tid = threadIdx.x;
+  asm volatile("" : "+r"(tid));  // keeps what follows from being computed ahead, and in registers, in the callers' loops
+  const int warp = tid >> 5, lane = tid & 31, heads16 = (heads + 15) & ~15;
+  const int64_t request = sm.done_request;
+  const int part = sm.done_part;
+  tmem_fence_after();
+  const int quarter = warp & 3, group0 = sm.group * sm.group_heads;
+  const uint32_t o_at = sm.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+#pragma unroll 1
+  for (int item = rank; item < heads16 / 4; item += (kFillWarps + kSoftWarps) / 4) {  // 16 heads of 128 columns each
+    const int mt = item & 3, h = (item >> 2) * 16;
+    const int col = mt * 128 + 32 * quarter + lane;
+    uint32_t o[16];
+    tmem_ld_32x16(o_at + mt * kGroup + h, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; k += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&sm.inv[h + k]);
+      o[k] = __float_as_uint(__uint_as_float(o[k]) * f.x), o[k + 1] = __float_as_uint(__uint_as_float(o[k + 1]) * f.y);
+      o[k + 2] = __float_as_uint(__uint_as_float(o[k + 2]) * f.z), o[k + 3] = __float_as_uint(__uint_as_float(o[k + 3]) * f.w);
+    }
+    if (part >= 0) {
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.workspace + sm.lay.out_at()) +
+                                            sm.lay.block(part, sm.group, 4 * mt + quarter, h / 4)) + lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dst[32 * k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      continue;
+    }
+    const int64_t row = request * p.out_stride_r + (group0 + h) * p.out_stride_h;
+    if (p.out_f32) {
+      float* dst = static_cast<float*>(p.out) + row + col;
+#pragma unroll
+      for (int k = 0; k < 16; ++k, dst += p.out_stride_h)
+        if (h + k < heads) *dst = __uint_as_float(o[k]);
+    } else {
+      // neighbouring lanes swap halves of a pair of heads, so that each stores two columns of one
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + row + (lane & 1) * p.out_stride_h + (col & ~1);
+#pragma unroll
+      for (int k = 0; k < 16; k += 2, dst += 2 * p.out_stride_h) {
+        const float mine_ = __uint_as_float(lane & 1 ? o[k + 1] : o[k]);
+        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(lane & 1 ? o[k] : o[k + 1]), 1);
+        if (h + k + (lane & 1) < heads)
+          *reinterpret_cast<uint32_t*>(dst) = lane & 1 ? pack_bf16x2(other, mine_) : pack_bf16x2(mine_, other);
+      }
+    }
+  }
+  tmem_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm.o_free);
+}
+
 constexpr int kBoxHeads = 16;  // heads of a TMA load of queries
 
-template <bool ALIGN16>
+template <bool ALIGN16, int HEADS>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
-    decode_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap q_map, const int sms) {
+    decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ Layouts layouts) {
   extern __shared__ uint8_t smem_raw[];
   DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -327,7 +418,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.ring_full[i], 1);
-      mbar_init(&sm.ring_free[i], kFillWarps + kSoftWarps + 1);
+      mbar_init(&sm.ring_free[i], kFillWarps + kSoftWarps + 2);
     }
     for (int i = 0; i < 2; ++i) {
       for (int k = 0; k < 2; ++k) mbar_init(&sm.k_full[i][k], kFillWarps);
@@ -340,7 +431,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     mbar_init(&sm.q_free, 1);
     mbar_init(&sm.o_free, kSoftWarps + kFillWarps);
     mbar_init(&sm.inv_full, kSoftWarps);
-    mbar_init(&sm.drained, 1);
+    mbar_init(&sm.drained, 2);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -367,20 +458,20 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  int64_t base = incl - mine, total = 0;
+  int64_t warps = lane < kDecodeThreads / 32 ? sm.warp_sums[lane] : 0;
 #pragma unroll
-  for (int w = 0; w < kDecodeThreads / 32; ++w) {
-    const int64_t s = sm.warp_sums[w];
-    if (w < warp) base += s;
-    total += s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, warps, o);
+    if (lane >= o) warps += u;
   }
+  const int64_t total = __shfl_sync(0xffffffffu, warps, 31);
+  const int64_t base = __shfl_sync(0xffffffffu, warps, warp) - __shfl_sync(0xffffffffu, incl, 31) + incl - mine;
   // ...choose the head groups: smaller ones while there are CTAs for a tile each, since the fewer
   // heads a CTA has, the sooner it has loaded their queries and stored their results...
-  int group_heads = kGroup;
-  if (total * ((p.heads + 31) / 32) <= sms) group_heads = 32;
-  if (total * ((p.heads + 15) / 16) <= sms) group_heads = 16;
-  const Layout lay(p.heads, sms, group_heads);
-  const int group = blockIdx.x % lay.groups, column = blockIdx.x / lay.groups;
+  const int size = HEADS == 16 || total * layouts.of[0].groups <= layouts.sms ? 0 : HEADS == 32 || total * layouts.of[1].groups <= layouts.sms ? 1 : 2;
+  const Layout& lay = layouts.of[size];
+  const int group_heads = 16 << size;
+  const int column = static_cast<int>(blockIdx.x / static_cast<unsigned>(lay.groups)), group = blockIdx.x - column * lay.groups;
   const int heads = min(group_heads, p.heads - group * group_heads);
   const int heads16 = (heads + 15) & ~15;
   // ...and find this column's run: its first request, and whether its last one goes on behind it.
@@ -422,7 +513,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   if (blockIdx.x == 0 && err) atomicOr(p.err, err);
   err = 0;
   __syncthreads();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);  // known to be the same in the whole warp
   volatile int* const abort_flag = &sm.abort;
   // A wait of a whole warp, with one answer for all its lanes; false: give up (the CTA ends).
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
@@ -432,56 +523,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
     }
     return ok;
-  };
-
-  // A run's results: O of all heads times 1 / sum, to the output or the workspace. The softmax warps
-  // and the eight warps that decoded the run's last tile share the work, three warps (`rank`) to each
-  // quarter of the TMEM lanes.
-  auto store_results = [&](int rank, int64_t request, int part) {
-    tmem_fence_after();
-    const int quarter = warp & 3, group0 = sm.group * sm.group_heads;
-    const uint32_t o_at = sm.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-#pragma unroll 1
-    for (int item = rank; item < heads16 / 4; item += 3) {  // 16 heads of 128 columns each
-      const int mt = item & 3, h = (item >> 2) * 16;
-      const int col = mt * 128 + 32 * quarter + lane;
-      uint32_t o[16];
-      tmem_ld_32x16(o_at + mt * kGroup + h, o);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 16; k += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&sm.inv[h + k]);
-        o[k] = __float_as_uint(__uint_as_float(o[k]) * f.x), o[k + 1] = __float_as_uint(__uint_as_float(o[k + 1]) * f.y);
-        o[k + 2] = __float_as_uint(__uint_as_float(o[k + 2]) * f.z), o[k + 3] = __float_as_uint(__uint_as_float(o[k + 3]) * f.w);
-      }
-      if (part >= 0) {
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.workspace + sm.lay.out_at()) +
-                                              sm.lay.block(part, sm.group, 4 * mt + quarter, h / 4)) + lane;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) dst[32 * k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        continue;
-      }
-      const int64_t row = request * p.out_stride_r + (group0 + h) * p.out_stride_h;
-      if (p.out_f32) {
-        float* dst = static_cast<float*>(p.out) + row + col;
-#pragma unroll
-        for (int k = 0; k < 16; ++k, dst += p.out_stride_h)
-          if (h + k < heads) *dst = __uint_as_float(o[k]);
-      } else {
-        // neighbouring lanes swap halves of a pair of heads, so that each stores two columns of one
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + row + (lane & 1) * p.out_stride_h + (col & ~1);
-#pragma unroll
-        for (int k = 0; k < 16; k += 2, dst += 2 * p.out_stride_h) {
-          const float mine_ = __uint_as_float(lane & 1 ? o[k + 1] : o[k]);
-          const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(lane & 1 ? o[k] : o[k + 1]), 1);
-          if (h + k + (lane & 1) < heads)
-            *reinterpret_cast<uint32_t*>(dst) = lane & 1 ? pack_bf16x2(other, mine_) : pack_bf16x2(mine_, other);
-        }
-      }
-    }
-    tmem_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.o_free);
   };
 
   if (idle) {
@@ -504,18 +545,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         id[h] = key < nn ? __ldg(p.table + rr * p.table_stride + static_cast<uint32_t>(key) / bs) : -1;
       }
     };
-    int odd = 0;
     if (left > 0) load_ids(r, tile, n);
-    for (int i = 0; left > -2; ++i, --left) {
+    for (int i = 0; left >= 0; ++i, --left) {
       const int slot = i % kRing;
       if (i >= kRing && !warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1)) break;
       TileDesc& d = sm.ring[slot];
-      if (left <= 0) {  // the end, once for each half of the decoding warps
+      if (left == 0) {
         if (lane == 0) {
           d.flags = kEnd;
           mbar_arrive(&sm.ring_full[slot]);
         }
-        continue;
+        break;
       }
       const int64_t tiles = tiles_of(n);
       uint64_t mask = 0;
@@ -538,7 +578,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const bool last_of_request = tile + 1 == tiles;
       if (lane == 0) {
         d.mask = mask;
-        d.flags = (tile == started ? kFirst : 0) | (last_of_request || left == 1 ? kLast : 0) | odd;
+        d.flags = (tile == started ? kFirst : 0) | (last_of_request || left == 1 ? kLast : 0);
         d.request = static_cast<int32_t>(r);
         d.part = started == 0 && last_of_request ? -1 : 2 * column + (started == 0 ? 1 : 0);
       }
@@ -554,7 +594,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
       }
       if (last_of_request) {
-        odd ^= kOdd;
         ++r;
         tile = started = 0;
         if (r - window >= 32) {
@@ -568,22 +607,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (left > 1) load_ids(r, tile, n);
     }
     if (err) atomicOr(p.err, err);
-  } else if (warp < 2 * kFillWarps) {
+  } else if (warp < kFillWarps) {
     // ------------------------------------------------------------------------ decode the entries
     // Four threads per entry; thread `sub` of an entry takes the 16 bytes sub, sub + 4, ...: of the
     // codes a quarter of each 64-column chunk, so load j belongs to scale j.
-    const int buf = warp / kFillWarps;  // and the parity of this warp's tiles
-    const int key = 8 * (warp % kFillWarps) + (lane >> 2), sub = lane & 3;
-    const uint32_t dst = smem_addr(sm.k[buf]) + key * 128;
-    const uint32_t swz = static_cast<uint32_t>(key & 7) << 4;
+    const int key = 8 * warp + (lane >> 2), sub = lane & 3;
+    // where its first 16 bytes go: decoded codes to two places of a chunk, rope values to one
+    const uint32_t row = smem_addr(sm.k[0]) + key * 128, swz = static_cast<uint32_t>(key & 7) << 4;
+    const uint32_t dst0 = row + ((32u * sub) ^ swz), dst1 = row + ((32u * sub + 16u) ^ swz);
+    const uint32_t dst_rope = row + 7 * kChunkBytes + ((16u * sub) ^ swz);
     uint4 raw[9];
     uint2 sc;
     const uint8_t* src = nullptr;
     const uint8_t* ssrc = nullptr;
-    auto load = [&](int j) { return src == nullptr ? make_uint4(0, 0, 0, 0) : ALIGN16 ? ld16(src + 64 * j + 16 * sub) : ld8x2(src + 64 * j + 16 * sub); };
-    auto load_scales = [&] { return src == nullptr ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : ld8(ssrc); };
     bool more = false;
     int flags = 0;
+    auto load = [&](int j) {
+      if (src == nullptr) raw[j] = make_uint4(0, 0, 0, 0);
+      else raw[j] = ALIGN16 ? ld16(src + 64 * j) : ld8x2(src + 64 * j);
+    };
+    auto load_scales = [&] { sc = src == nullptr ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : ld8(ssrc); };
     // take tile i's addresses out of the ring
     auto fetch = [&](int i) -> bool {
       const int slot = i % kRing;
@@ -593,33 +636,58 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       more = (flags & kEnd) == 0;
       if (more) {
         src = sm.ring[slot].data[key];
+        if (src != nullptr) src += 16 * sub;
         ssrc = sm.ring[slot].scales[key];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
       }
       return true;
     };
-    fetch(buf);
+    // the results of the run that tile i ended
+    int runs = 0;
+    auto results = [&](int i) {
+      // O being done, the runs before this one are finished with, and the parity means this run
+      const bool ok = warp_wait(&sm.k_free[i & 1][kQuarters - 1], (i / 2) & 1) && warp_wait(&sm.inv_full, runs & 1);
+      ++runs;
+      if (ok) store_results(sm, p, heads, 2 + warp / 4);
+      return ok;
+    };
+    bool ok = fetch(0);
     if (more) {
-      sc = load_scales();
+      load_scales();
 #pragma unroll
-      for (int j = 0; j < 9; ++j) raw[j] = load(j);
+      for (int j = 0; j < 9; ++j) load(j);
     }
-    for (int i = buf; more; i += 2) {
+    bool last1 = false, last2 = false;  // the tile before and the one before it ended a run
+    int i = 0;
+    for (; ok && more; ++i) {
+      if (last2 && !(ok = results(i - 2))) break;
+      const int buf = i & 1;
+      const bool last = flags & kLast;
       const uint2 now = sc;
+      const bool fits = scales_fit_f16(now.x) && scales_fit_f16(now.y | 127u << 24);  // the eighth is padding
       auto decode = [&](int j, uint32_t (&o)[8]) {
         const float scale = scale_of(((j < 4 ? now.x : now.y) >> (8 * (j & 3))) & 0xffu);
+        const uint16_t half = fits ? to_f16(scale) : 0x3c00;  // one
         const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+        float2 v[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          o[2 * k] = codes_to_bf16(static_cast<uint16_t>(w[k]), scale);
-          o[2 * k + 1] = codes_to_bf16(static_cast<uint16_t>(w[k] >> 16), scale);
+          v[2 * k] = codes_to_f32(static_cast<uint16_t>(w[k]), half);
+          v[2 * k + 1] = codes_to_f32(static_cast<uint16_t>(w[k] >> 16), half);
         }
+        if (!fits) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k].x *= scale, v[k].y *= scale;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(v[k].x, v[k].y);
+        if (more) load(j);  // of the next tile
       };
       auto store = [&](int j, const uint32_t (&o)[8]) {
-        const uint32_t at = dst + j * kChunkBytes;
-        sts16(at + ((32u * sub) ^ swz), o[0], o[1], o[2], o[3]);
-        sts16(at + ((32u * sub + 16u) ^ swz), o[4], o[5], o[6], o[7]);
+        const uint32_t at = buf * kTileBytes + j * kChunkBytes;
+        sts16(dst0 + at, o[0], o[1], o[2], o[3]);
+        sts16(dst1 + at, o[4], o[5], o[6], o[7]);
       };
       auto taken = [&](int quarter) { return i < 2 || warp_wait(&sm.k_free[buf][quarter], (i / 2 - 1) & 1); };
       auto publish = [&](int half) {
@@ -627,176 +695,150 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.k_full[buf][half]);
       };
-      // The first half is decoded into registers before its room in the buffer is free.
-      uint32_t o[3][8];
+      if (!(ok = fetch(i + 1))) break;
+      if (more) load_scales();
+      // As much as there are registers for is decoded before its room in the buffer is free.
+      uint32_t o[4][8];
 #pragma unroll
-      for (int j = 0; j < 3; ++j) decode(j, o[j]);
-      if (!taken(0)) break;
+      for (int j = 0; j < 4; ++j) decode(j, o[j]);
+      if (!(ok = taken(0))) break;
       store(0, o[0]);
       store(1, o[1]);
-      decode(3, o[0]);
-      if (!taken(1)) break;
+      if (!(ok = taken(1))) break;
       store(2, o[2]);
-      store(3, o[0]);
+      store(3, o[3]);
       publish(0);
 #pragma unroll
       for (int j = 4; j < 7; ++j) decode(j, o[j - 4]);
-      if (!taken(2)) break;
+      if (!(ok = taken(2))) break;
       store(4, o[0]);
       store(5, o[1]);
-      if (!taken(3)) break;
+      if (!(ok = taken(3))) break;
       store(6, o[2]);
 #pragma unroll
-      for (int j = 7; j < 9; ++j)  // the rope columns are bf16 already
-        sts16(dst + 7 * kChunkBytes + ((64u * (j - 7) + 16u * sub) ^ swz), raw[j].x, raw[j].y, raw[j].z, raw[j].w);
+      for (int j = 7; j < 9; ++j) {  // the rope columns are bf16 already
+        sts16((dst_rope + buf * kTileBytes) ^ (64u * (j - 7)), raw[j].x, raw[j].y, raw[j].z, raw[j].w);
+        if (more) load(j);
+      }
       publish(1);
-      const int done = flags;
-      if (!fetch(i + 2)) break;
-      if (more) {
-        sc = load_scales();
-#pragma unroll
-        for (int j = 0; j < 9; ++j) raw[j] = load(j);
-      }
-      if (done & kLast) {
-        // O being done, the runs before this one are finished with, and the parity means this run
-        if (!warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1)) break;
-        if (!warp_wait(&sm.inv_full, done & kOdd ? 1 : 0)) break;
-        store_results(1 + (warp % kFillWarps) / 4, sm.done_request, sm.done_part);
-      }
+      last2 = last1;
+      last1 = last;
     }
-  } else if (warp == kMmaWarp) {
+    if (ok && last2) ok = results(i - 2);
+    if (ok && last1) results(i - 1);
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ------------------------------------------------------------------------ issue the products
     // One elected thread in one branch: the compiler then keeps descriptors in uniform registers, and
-    // a product issues faster than it runs (32 cycles for S, 39 to 48 for O, bound by the reads of the
-    // operands from shared memory). Behind a test of the lane each took 66 to 75 cycles to issue.
+    // a product issues faster than it runs (23 to 32 cycles for S, 39 to 48 for O, bound by the reads of
+    // the operands from shared memory). Behind a test of the lane each took 66 to 75 cycles to issue.
+    // The buffer is a constant of the lambdas for the same reason.
     if (elect_one()) {
-      const uint32_t q_at = desc_low(smem_addr(sm.q), 16), ks_at = desc_low(smem_addr(sm.k[0]), 16);
-      const uint32_t kv_at = desc_low(smem_addr(sm.k[0]), kChunkBytes), p_at = desc_low(smem_addr(sm.p[0]), 16);
-      const uint32_t s_desc = mma_desc(kTile, heads16, false);
-      const uint32_t o_desc = mma_desc(128, heads16, true);
-      const int boxes = heads16 / kBoxHeads;
-      const uint32_t box_bytes = static_cast<uint32_t>(min(p.heads, kBoxHeads)) * 128;
-      int s_next = 0, o_next = 0;      // tiles whose S and whose O come next; S is at most one tile ahead
-      int s_seg = -1, o_seg = -1;      // requests begun
-      int flags = 0, o_flags = 0, s_flags = 0;  // of the tile next for S, for O, and of the one between
-      enum { kAwaitTile, kAwaitQueryRoom, kAwaitQueries, kAwaitHalf, kAwaitRest } stage = kAwaitTile;
-      bool ended = false, failed = false, loading = false;
-      int idle_turns = 0;
-      uint32_t t0 = 0;
-      for (;;) {
-        bool progress = false;
-        // S of the next tile, as far as it can go without waiting
-        if (!ended && s_next <= o_next + 1) {
-          const int slot = s_next % kRing, buf = s_next & 1;
-          if (stage == kAwaitTile && mbar_test(&sm.ring_full[slot], (s_next / kRing) & 1)) {
-            flags = sm.ring[slot].flags;
-            progress = true;
-            if (flags & kEnd) {
-              ended = true;
-            } else {
-              stage = flags & kFirst ? kAwaitQueryRoom : kAwaitHalf;
-              if (flags & kFirst) ++s_seg;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (decode_wait(bar, parity, abort_flag)) return true;
+        *abort_flag = 1;
+        atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
+        return false;
+      };
+      const uint32_t k_at = smem_addr(sm.k[0]);
+      if (warp == kMmaWarp) {
+        const uint32_t q_at = desc_low(smem_addr(sm.q), 16), ks_at = desc_low(k_at, 16);
+        const uint32_t desc = mma_desc(kTile, heads16, false);
+        const int boxes = heads16 / kBoxHeads;
+        const uint32_t box_bytes = static_cast<uint32_t>(min(p.heads, kBoxHeads)) * 128;
+        auto half_of_s = [&](auto buffer, auto which) {
+          constexpr int buf = decltype(buffer)::value, half = decltype(which)::value;
+          tmem_fence_after();
+#pragma unroll
+          for (int k = 0; k < kChunks / 2; ++k) {
+            constexpr int c0 = half * (kChunks / 2);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint32_t a = ks_at + ((buf * kTileBytes + (c0 + k) * kChunkBytes + ks * 32) >> 4);
+              const uint32_t b = q_at + (((c0 + k) * (kGroup * 128) + ks * 32) >> 4);
+              mma(tmem + kTmemS + buf * kGroup, a, b, desc, half + k + ks > 0);
             }
           }
-          if (stage == kAwaitQueryRoom && (s_seg == 0 || mbar_test(&sm.q_free, (s_seg - 1) & 1))) {
-            const int request = sm.ring[slot].request;
+        };
+        int seg = -1;  // requests begun
+        bool loading = false;
+        for (int i = 0;; ++i) {
+          const int slot = i % kRing, buf = i & 1;
+          if (!wait(&sm.ring_full[slot], (i / kRing) & 1)) break;
+          const int flags = sm.ring[slot].flags, request = sm.ring[slot].request;
+          if (flags & kEnd) break;
+          mbar_arrive(&sm.ring_free[slot]);
+          if (flags & kFirst) {
+            if (++seg > 0 && !wait(&sm.q_free, (seg - 1) & 1)) break;
             mbar_arrive_expect_tx(&sm.q_full, static_cast<uint32_t>(boxes * kChunks) * box_bytes);
             for (int b = 0; b < boxes; ++b)
               for (int c = 0; c < kChunks; ++c)
                 load_query_box(sm.q + c * (kGroup * 128) + b * (kBoxHeads * 128), &q_map, 64 * c,
                                group * group_heads + b * kBoxHeads, request, &sm.q_full);
             loading = true;
-            stage = kAwaitQueries;
-            progress = true;
           }
-          if (stage == kAwaitQueries && mbar_test(&sm.q_full, s_seg & 1)) {
+          if (i >= 2 && !wait(&sm.s_free[buf], (i / 2 - 1) & 1)) break;
+          if (loading) {
+            if (!wait(&sm.q_full, seg & 1)) break;
             loading = false;
-            stage = kAwaitHalf;
-            progress = true;
           }
-          auto half_of_s = [&](int half) {
-            tmem_fence_after();
-#pragma unroll
-            for (int k = 0; k < kChunks / 2; ++k) {
-              const int c = half * (kChunks / 2) + k;
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks) {
-                const uint32_t a = q_at + ((c * (kGroup * 128) + ks * 32) >> 4);
-                const uint32_t b = ks_at + ((buf * kTileBytes + c * kChunkBytes + ks * 32) >> 4);
-                mma(tmem + kTmemS + buf * kGroup, b, a, s_desc, half + k + ks > 0);
-              }
-            }
-          };
-          if (!ended && stage == kAwaitHalf && (s_next < 2 || mbar_test(&sm.s_free[buf], (s_next / 2 - 1) & 1)) &&
-              mbar_test(&sm.k_full[buf][0], (s_next / 2) & 1)) {
-            mbar_arrive(&sm.ring_free[slot]);
-            half_of_s(0);
-            stage = kAwaitRest;
-            progress = true;
-          }
-          if (stage == kAwaitRest && mbar_test(&sm.k_full[buf][1], (s_next / 2) & 1)) {
-            half_of_s(1);
-            mma_commit(&sm.s_full[buf]);
-            if (flags & kLast) mma_commit(&sm.q_free);
-            if (s_next == o_next) o_flags = flags; else s_flags = flags;
-            ++s_next;
-            stage = kAwaitTile;
-            progress = true;
-          }
+          if (!wait(&sm.k_full[buf][0], (i / 2) & 1)) break;
+          if (buf) half_of_s(Const<1>(), Const<0>()); else half_of_s(Const<0>(), Const<0>());
+          if (!wait(&sm.k_full[buf][1], (i / 2) & 1)) break;
+          if (buf) half_of_s(Const<1>(), Const<1>()); else half_of_s(Const<0>(), Const<1>());
+          mma_commit(&sm.s_full[buf]);
+          if (flags & kLast) mma_commit(&sm.q_free);
         }
-        // O^T += K^T P^T of the oldest tile whose P is there
-        if (!failed && o_next < s_next && mbar_test(&sm.p_full[o_next & 1], (o_next / 2) & 1)) {
-          const bool first = o_flags & kFirst;
-          if (!first || o_seg < 0 || mbar_test(&sm.o_free, o_seg & 1)) {
-            const int buf = o_next & 1;
-            if (first) ++o_seg;
-            tmem_fence_after();
+        if (loading) decode_wait(&sm.q_full, seg & 1, nullptr);  // nothing may be in flight when the CTA ends
+      } else {
+        const uint32_t kv_at = desc_low(k_at, kChunkBytes), p_at = desc_low(smem_addr(sm.p[0]), 16);
+        const uint32_t desc = mma_desc(128, heads16, true);
+        auto product_o = [&](auto buffer, bool first) {
+          constexpr int buf = decltype(buffer)::value;
+          tmem_fence_after();
 #pragma unroll
-            for (int mt = 0; mt < kQuarters; ++mt) {
+          for (int mt = 0; mt < kQuarters; ++mt) {
 #pragma unroll
-              for (int ks = 0; ks < kTile / 16; ++ks) {
-                const uint32_t a = kv_at + ((buf * kTileBytes + 2 * mt * kChunkBytes + ks * 2048) >> 4);
-                const uint32_t b = p_at + ((buf * (kGroup * kTile * 2) + ks * 2048) >> 4);
-                mma(tmem + mt * kGroup, a, b, o_desc, !first || ks > 0);
-              }
-              mma_commit(&sm.k_free[buf][mt]);
+            for (int ks = 0; ks < kTile / 16; ++ks) {
+              const uint32_t a = kv_at + ((buf * kTileBytes + 2 * mt * kChunkBytes + ks * 2048) >> 4);
+              const uint32_t b = p_at + ((buf * (kGroup * kTile * 2) + ks * 2048) >> 4);
+              mma(tmem + mt * kGroup, a, b, desc, !first || ks > 0);
             }
-            o_flags = s_flags;
-            ++o_next;
-            progress = true;
+            mma_commit(&sm.k_free[buf][mt]);
           }
-        }
-        if (failed || (ended && o_next == s_next)) break;
-        if (progress) {
-          idle_turns = 0;
-        } else {
-          if (idle_turns++ == 0) t0 = clock();
-          __nanosleep(20);  // tests in a tight loop take shared-memory cycles from the products
-          if ((idle_turns & 63) == 0 && (*abort_flag || static_cast<uint32_t>(clock()) - t0 > kWaitCycles)) failed = true;
+        };
+        int seg = -1;
+        for (int i = 0;; ++i) {
+          const int slot = i % kRing, buf = i & 1;
+          if (!wait(&sm.ring_full[slot], (i / kRing) & 1)) break;
+          const int flags = sm.ring[slot].flags;
+          if (flags & kEnd) break;
+          mbar_arrive(&sm.ring_free[slot]);
+          if (!wait(&sm.p_full[buf], (i / 2) & 1)) break;
+          // the results of the run before are out of O
+          if ((flags & kFirst) && ++seg > 0 && !wait(&sm.o_free, (seg - 1) & 1)) break;
+          if (buf) product_o(Const<1>(), flags & kFirst); else product_o(Const<0>(), flags & kFirst);
         }
       }
-      if (failed) {
-        *abort_flag = 1;
-        atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
-      }
-      // nothing may be in flight when the CTA ends
       mma_commit(&sm.drained);
       decode_wait(&sm.drained, 0, nullptr);
-      if (loading) decode_wait(&sm.q_full, s_seg & 1, nullptr);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------------------------ softmax
-    const int w = warp - kSoftWarp;                  // TMEM lanes 32w .. 32w + 31
+    constexpr int kOwn = HEADS / 2;                  // heads of four warps
+    const int w = warp & 3;                          // TMEM lanes 32w .. 32w + 31
+    const int own = (warp - kSoftWarp) / 4 * kOwn;   // this warp's first head
+    const bool lead = own == 0;
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     const int key0 = 16 * w + (lane >> 2), key1 = key0 + 8;  // this thread's two entries of a tile
-    const int h0 = 2 * (lane & 3);  // and its heads: h0 and h0 + 1 of every 8
+    const int h0 = own + 2 * (lane & 3);  // and its heads: h0 and h0 + 1, and on in steps of 8
     const float c2 = p.scale * kLog2e;
-    float l[kGroup / 4];            // its sums: of heads 8g + h0 and + 1 in l[2g], l[2g + 1]
-    // Barriers of the four warps, on a hardware barrier, which has no time limit. So a warp whose wait
+    float l[kOwn / 4];             // its sums: of heads h0 + 8g and + 1 in l[2g], l[2g + 1]
+    // Barriers of the eight warps, on a hardware barrier, which has no time limit. So a warp whose wait
     // ran out does not leave: it says so at the next barrier, which it reaches as the others do, and
-    // all four leave there.
+    // all of them leave there.
     bool dead = false;
+    bool zero = true, fresh = true;  // the references are 0; the run has had no entry yet
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!dead) dead = !warp_wait(bar, parity);
     };
@@ -811,73 +853,79 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       wait(&sm.s_full[buf], (i / 2) & 1);
       tmem_fence_after();
-      // The scores are read from TMEM twice, 16 heads at a time, once to look for one that passes its
-      // head's reference: kept in registers between, they would spill, and a spill here is a trip to
-      // L2, beside the little L1 that the tiles leave.
       const uint64_t mask = sm.ring[slot].mask;
       const bool in0 = mask >> key0 & 1, in1 = mask >> key1 & 1;
       const bool first = flags & kFirst;
       const uint32_t s_at = tmem + lanes + kTmemS + buf * kGroup;
-      auto scores = [&](int h, uint32_t (&x)[8]) {  // log2-scaled, -inf where there is no entry
-        tmem_ld_16x16(s_at + h, x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          x[k] = (k & 2 ? in1 : in0) ? __float_as_uint(__uint_as_float(x[k]) * c2) : 0xff800000u;
-      };
-      bool raise = dead;
       if (first) {
-        // the entry's holders write its scores down; without one the references are -inf
-        const int entry = mask != 0 ? __ffsll(static_cast<long long>(mask)) - 1 : 0;
-        if (entry / 16 == w) {
-#pragma unroll 1
-          for (int h = 0; h < heads16; h += 16) {
-            uint32_t x[8];
-            scores(h, x);
-            if ((lane >> 2) == (entry & 7)) {
+        fresh = zero = true;
 #pragma unroll
-              for (int g = 0; g < 2; ++g)
-                *reinterpret_cast<uint2*>(&sm.ref[h + 8 * g + h0]) =
-                    entry & 8 ? make_uint2(x[4 * g + 2], x[4 * g + 3]) : make_uint2(x[4 * g], x[4 * g + 1]);
+        for (int g = 0; g < kOwn / 4; ++g) l[g] = 0.f;
+      }
+      // the P of two tiles ago has been used
+      if (i >= 2) wait(&sm.k_free[buf][kQuarters - 1], (i / 2 - 1) & 1);
+      // P with the references as they are, and whether any is off; if so once more with new ones.
+      float sums[kOwn / 4];
+      bool off = dead, left = false;
+      for (;;) {
+        const bool any = fresh && __any_sync(0xffffffffu, in0 || in1);  // else no entry here speaks for a head
+        const uint32_t p_at = smem_addr(sm.p[buf]) + key0 * 128 + 4 * (lane & 3);
+        const uint32_t swz = static_cast<uint32_t>(key0 & 7) << 4;  // key1 & 7 is the same
+        float top = -INFINITY;  // the highest score over its reference
+        if (own < heads16) {
+          uint32_t x[kOwn / 2];
+          tmem_ld_scores<kOwn>(s_at + own, x);  // scores of absent heads are there, and not used
+          tmem_wait_ld();
+          uint32_t packed[kOwn / 4];
+#pragma unroll
+          for (int g = 0; g < kOwn / 8; ++g) {
+            const int head = h0 + 8 * g;
+            float2 ref = make_float2(0.f, 0.f);
+            if (!zero) ref = *reinterpret_cast<const float2*>(&sm.ref[head]);
+            float e[4];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // log2-scaled scores over the reference, -inf where there is no entry
+              float t0 = fmaf(__uint_as_float(x[4 * g + c]), c2, c ? -ref.y : -ref.x);
+              float t1 = fmaf(__uint_as_float(x[4 * g + 2 + c]), c2, c ? -ref.y : -ref.x);
+              if (!in0) t0 = -INFINITY;
+              if (!in1) t1 = -INFINITY;
+              const float higher = head + c < heads ? fmaxf(t0, t1) : 0.f;
+              top = fmaxf(top, higher);
+              if (any) off |= (__ballot_sync(0xffffffffu, higher > -kSlack) & (0x11111111u << (lane & 3))) == 0;
+              e[c] = ex2_approx(t0);
+              e[2 + c] = ex2_approx(t1);
+              sums[2 * g + c] = e[c] + e[2 + c];
             }
+            packed[2 * g] = pack_bf16x2(e[0], e[1]);
+            packed[2 * g + 1] = pack_bf16x2(e[2], e[3]);
+          }
+#pragma unroll
+          for (int g = 0; g < kOwn / 8; ++g) {
+            const uint32_t at = p_at + ((16u * (own / 8 + g)) ^ swz);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(packed[2 * g]) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(packed[2 * g + 1]) : "memory");
           }
         }
-#pragma unroll
-        for (int g = 0; g < kGroup / 4; ++g) l[g] = 0.f;
-        if (soft_vote(dead)) {
-          soft_vote(true);
-          break;
-        }
-      }
-      {
-#pragma unroll 1
-        for (int h = 0; h < heads16; h += 16) {
-          uint32_t x[8];
-          scores(h, x);
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float2 m = *reinterpret_cast<const float2*>(&sm.ref[h + 8 * g + h0]);
-            const bool real0 = h + 8 * g + h0 < heads, real1 = h + 8 * g + h0 + 1 < heads;
-            raise |= real0 && fmaxf(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 2])) > m.x + kSlack;
-            raise |= real1 && fmaxf(__uint_as_float(x[4 * g + 1]), __uint_as_float(x[4 * g + 3])) > m.y + kSlack;
-          }
-        }
-      }
-      if (soft_vote(raise)) {
+        off |= top > kSlack;
+        if (!soft_vote(off)) break;
+        left = soft_vote(dead);
+        if (left) break;
         // New references: the maxima so far of all heads. O and the sums are rescaled to them.
         if (soft_vote(dead)) break;
-#pragma unroll 1
-        for (int h = 0; h < heads16; h += 16) {
-          uint32_t x[8];
-          scores(h, x);
+        if (own < heads16) {
+          uint32_t x[kOwn / 2];
+          tmem_ld_scores<kOwn>(s_at + own, x);
+          tmem_wait_ld();
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
+          for (int g = 0; g < kOwn / 8; ++g) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(__uint_as_float(x[4 * g + e]), __uint_as_float(x[4 * g + 2 + e]));
+            for (int c = 0; c < 2; ++c) {
+              float top = fmaxf(in0 ? __uint_as_float(x[4 * g + c]) * c2 : -INFINITY,
+                                in1 ? __uint_as_float(x[4 * g + 2 + c]) * c2 : -INFINITY);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              if (lane < 4) sm.by_warp[w][h + 8 * g + h0 + e] = top;
+              if (lane < 4) sm.by_warp[w][h0 + 8 * g + c] = top;
             }
           }
         }
@@ -887,30 +935,31 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
         for (int a = 0; a < kGroup / 32; ++a) {
           const int h = 32 * a + lane;
-          const float was = sm.ref[h];
-          to[a] = fmaxf(fmaxf(fmaxf(sm.by_warp[0][h], sm.by_warp[1][h]), fmaxf(sm.by_warp[2][h], sm.by_warp[3][h])), was);
-          f[a] = to[a] == -INFINITY ? 1.f : ex2_approx(was - to[a]);
+          const float top = fmaxf(fmaxf(sm.by_warp[0][h], sm.by_warp[1][h]), fmaxf(sm.by_warp[2][h], sm.by_warp[3][h]));
+          const float was = zero ? 0.f : sm.ref[h];
+          // without an entry so far sums and O are 0; a head of which all scores are -inf keeps its reference
+          to[a] = top == -INFINITY ? was : fresh ? top : fmaxf(top, was);
+          f[a] = fresh ? 1.f : ex2_approx(was - to[a]);
         }
         soft_vote(false);  // all have read the old ones
-        if (w == 0) {
+        if (lead && w == 0) {
 #pragma unroll
           for (int a = 0; a < kGroup / 32; ++a) sm.ref[32 * a + lane] = to[a], sm.factor[32 * a + lane] = f[a];
         }
         if (!first) wait(&sm.k_free[(i - 1) & 1][kQuarters - 1], ((i - 1) / 2) & 1);
-        if (soft_vote(dead)) break;
+        left = soft_vote(dead);
+        if (left) break;
 #pragma unroll
-        for (int g = 0; g < kGroup / 8; ++g) {
-          if (8 * g < heads16) {
-            l[2 * g] *= sm.factor[8 * g + h0];
-            l[2 * g + 1] *= sm.factor[8 * g + h0 + 1];
-          }
+        for (int g = 0; g < kOwn / 8; ++g) {
+          l[2 * g] *= sm.factor[h0 + 8 * g];
+          l[2 * g + 1] *= sm.factor[h0 + 8 * g + 1];
         }
         if (!first) {
           tmem_fence_after();
 #pragma unroll 1
           for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll 1
-            for (int h = 0; h < heads16; h += 16) {
+            for (int h = lead ? 0 : 16; h < heads16; h += 32) {
               uint32_t o[16];
               const uint32_t at = tmem + lanes + mt * kGroup + h;
               tmem_ld_32x16(at, o);
@@ -923,43 +972,19 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           tmem_wait_st();
           tmem_fence_before();
         }
+        zero = fresh = off = false;
       }
-      // the P of two tiles ago has been used
-      if (i >= 2) wait(&sm.k_free[buf][kQuarters - 1], (i / 2 - 1) & 1);
-      {
-        const uint32_t p_at = smem_addr(sm.p[buf]) + key0 * 128 + 2 * h0;
-        const uint32_t swz = static_cast<uint32_t>(key0 & 7) << 4;  // key1 & 7 is the same
+      if (left) break;
+      fresh = fresh && mask == 0;
 #pragma unroll
-        for (int b = 0; b < kGroup / 16; ++b) {
-          if (16 * b < heads16) {
-            uint32_t x[8];
-            scores(16 * b, x);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              float2 m = *reinterpret_cast<const float2*>(&sm.ref[16 * b + 8 * g + h0]);
-              m.x = m.x == -INFINITY ? 0.f : m.x;
-              m.y = m.y == -INFINITY ? 0.f : m.y;
-              float e[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                e[k] = ex2_approx(__uint_as_float(x[4 * g + k]) - (k & 1 ? m.y : m.x));
-                l[4 * b + 2 * g + (k & 1)] += e[k];
-              }
-              const uint32_t at = p_at + ((16u * (2 * b + g)) ^ swz);
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack_bf16x2(e[0], e[1])) : "memory");
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(pack_bf16x2(e[2], e[3])) : "memory");
-            }
-          }
-        }
-        tmem_fence_before();
-        async_proxy_fence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.s_free[buf]);
-      }
+      for (int g = 0; g < kOwn / 4; ++g) l[g] += sums[g];  // of absent heads: unused
+      tmem_fence_before();
+      async_proxy_fence();
       const int request = sm.ring[slot].request, part = sm.ring[slot].part;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&sm.p_full[buf]);
+        mbar_arrive(&sm.s_free[buf]);
         mbar_arrive(&sm.ring_free[slot]);
       }
       if (!(flags & kLast)) continue;
@@ -968,31 +993,29 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const bool whole = part < 0;
       const int group0 = sm.group * sm.group_heads;  // the first head of this CTA
 #pragma unroll
-      for (int g = 0; g < kGroup / 8; ++g) {
-        if (8 * g < heads16) {
+      for (int g = 0; g < kOwn / 8; ++g) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float sum = l[2 * g + e];
+        for (int e = 0; e < 2; ++e) {
+          float sum = l[2 * g + e];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if (lane < 4) sm.by_warp[w][8 * g + h0 + e] = sum;
-          }
+          for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          if (lane < 4) sm.by_warp[w][h0 + 8 * g + e] = sum;
         }
       }
       // O is done; with it the last run's results have been stored, and `inv` is free
       wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
       if (soft_vote(dead)) break;
-      if (w < 2 && 32 * w + lane < heads) {
+      if (lead && w < 2 && 32 * w + lane < heads) {
         const int h = 32 * w + lane;
         const int64_t head = group0 + h;
-        const float own = (sm.by_warp[0][h] + sm.by_warp[1][h]) + (sm.by_warp[2][h] + sm.by_warp[3][h]), ref = sm.ref[h];
-        float sum = own, to = ref == -INFINITY ? 0.f : ref, f = 1.f;
+        const float own = (sm.by_warp[0][h] + sm.by_warp[1][h]) + (sm.by_warp[2][h] + sm.by_warp[3][h]), ref = zero ? 0.f : sm.ref[h];
+        float sum = own, to = ref, f = 1.f;
         if (whole && p.sink != nullptr) {  // one more score, with a value of zero
           const float s = __ldg(p.sink + head) * kLog2e;
-          const float top = fmaxf(ref, s), shift = top == -INFINITY ? 0.f : top;
-          f = ex2_approx(to - shift);
-          sum = own == 0.f ? ex2_approx(s - shift) : own * f + ex2_approx(s - shift);
-          to = shift;
+          // (with nothing else in the sum, or if it is far above the rest, the result is 0 and lse the sink's)
+          to = own == 0.f ? (s == -INFINITY ? 0.f : s) : fmaxf(ref, s);
+          f = ex2_approx(ref - to);
+          sum = (own == 0.f ? 0.f : own * f) + ex2_approx(s - to);
         }
         sm.inv[h] = own == 0.f ? 0.f : f / sum;
         const float lse2 = sum == 0.f ? -INFINITY : to + log2f(sum);
@@ -1001,11 +1024,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         else if (p.lse != nullptr)
           p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
       }
-      if (w == 0 && lane == 0) sm.done_request = request, sm.done_part = part;
+      if (lead && w == 0 && lane == 0) sm.done_request = request, sm.done_part = part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.inv_full);
       soft_vote(false);
-      store_results(0, request, part);
+      store_results(sm, p, heads, lead ? 0 : 1);
     }
   }
   tmem_fence_before();
@@ -1022,12 +1045,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 constexpr int kJoinThreads = 256;
 constexpr int kMaxCtas = 1024;
 
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p, const int sms, const int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p, const __grid_constant__ Layouts layouts) {
   __shared__ int16_t s_owner[kMaxCtas];
   __shared__ int s_count;
   launch_dependents();
   grid_dependency_wait();
   const Task* tasks = reinterpret_cast<const Task*>(p.workspace);
+  const int ctas = layouts.of[2].ctas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {  // the CTAs that start a cut request, in order
     int count = 0;
@@ -1047,7 +1071,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p
     const int cols32 = static_cast<int>(item & 15);
     const int head = static_cast<int>((item >> 4) % heads4) * 4;
     const Task t = tasks[s_owner[(item >> 4) / heads4]];
-    const Layout lay(p.heads, sms, t.group_heads);
+    const Layout& lay = layouts.of[t.group_heads >> 5];  // 16, 32, 64 -> 0, 1, 2
     const int group = head / t.group_heads, h = head % t.group_heads;
     const float* lse = reinterpret_cast<const float*>(p.workspace + lay.lse_at());
     const float* part = reinterpret_cast<const float*>(p.workspace + lay.out_at());
@@ -1129,10 +1153,24 @@ bool encode_query_map(const DecodeParams& p, CUtensorMap* map) {
 
 }  // namespace
 
+namespace {
+// The kernel for caches whose records start on 16 or 8 bytes, and for all heads in one group of 16 or
+// 32 (which frees registers) or in groups of up to 64.
+const void* decode_kernel_for(bool align16, int heads) {
+  if (heads <= 16) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 16> : decode_kernel<false, 16>);
+  if (heads <= 32) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 32> : decode_kernel<false, 32>);
+  return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 64> : decode_kernel<false, 64>);
+}
+}  // namespace
+
 cudaError_t prepare_decode() {
-  const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const cudaError_t e = cudaFuncSetAttribute(decode_kernel<true>, a, kDecodeSmemBytes);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(decode_kernel<false>, a, kDecodeSmemBytes);
+  cudaError_t e = cudaSuccess;
+  for (int heads = 16; heads <= 64; heads *= 2)
+    for (int align16 = 0; align16 < 2; ++align16)
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_kernel_for(align16 != 0, heads), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kDecodeSmemBytes);
+  return e;
 }
 
 int64_t decode_workspace_bytes(int heads, int sm_count) { return Layout(heads, sm_count, kGroup).bytes(); }
@@ -1140,7 +1178,10 @@ int64_t decode_workspace_bytes(int heads, int sm_count) { return Layout(heads, s
 cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stream) {
   CUtensorMap map;
   if (!encode_query_map(p, &map)) return cudaErrorInvalidValue;
-  const int ctas = Layout(p.heads, sm_count, kGroup).ctas;
+  Layouts layouts;
+  for (int i = 0; i < 3; ++i) layouts.of[i] = Layout(p.heads, sm_count, 16 << i);
+  layouts.sms = sm_count;
+  const int ctas = layouts.of[2].ctas;
   if (ctas > kMaxCtas) return cudaErrorInvalidValue;
   const bool align16 = p.kc_stride0 % 16 == 0;  // records then start on 16 bytes, else on 8
   cudaLaunchConfig_t lc = {};
@@ -1153,15 +1194,15 @@ cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  const cudaError_t e = align16 ? cudaLaunchKernelEx(&lc, decode_kernel<true>, p, map, sm_count)
-                                : cudaLaunchKernelEx(&lc, decode_kernel<false>, p, map, sm_count);
+  void* args[] = {const_cast<DecodeParams*>(&p), &map, &layouts};
+  const cudaError_t e = cudaLaunchKernelExC(&lc, decode_kernel_for(align16, p.heads), args);
   if (e != cudaSuccess) return e;
   const int64_t cut = p.requests < ctas ? p.requests : ctas;  // requests that can be cut
   const int64_t join_ctas = (cut * ((p.heads + 3) / 4) * 16 + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   lc.gridDim = dim3(static_cast<unsigned>(join_ctas < 8 * sm_count ? join_ctas : 8 * sm_count));
   lc.blockDim = dim3(kJoinThreads);
   lc.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&lc, join_kernel, p, sm_count, ctas);
+  return cudaLaunchKernelEx(&lc, join_kernel, p, layouts);
 }
 
 }  // namespace c128
