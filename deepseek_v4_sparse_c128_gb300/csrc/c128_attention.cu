@@ -53,14 +53,18 @@ constexpr int kChunks = kHead / 64; // 64-column chunks of 128 bytes (bf16): one
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kTileBytes = kChunks * kChunkBytes;  // a decoded tile: 64 KiB
 constexpr int kQuarters = 4;        // of a tile's columns: 128 each, an M of the second product
-constexpr int kFillWarps = 8, kSoftWarps = 8;
-constexpr int kSoftWarp = kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
+#ifndef C128_SETS
+#define C128_SETS 1
+#endif
+constexpr int kSets = C128_SETS;
+constexpr int kFillWarps = 8, kSoftWarps = 8;  // fill warps of a tile
+constexpr int kSoftWarp = kSets * kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
 constexpr int kRing = 4;            // tiles the index warp may be ahead
 constexpr float kSlack = 32.f;      // log2 units a score may be from the reference
 constexpr int kTmemCols = 512, kTmemS = 256;  // O in columns 0..255, two S tiles behind it
 
-enum : int { kFirst = 1, kLast = 2, kEnd = 4 };  // first or last of its run of one request's tiles
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kOdd = 8 };  // of its run of one request's tiles; kOdd: an odd run
 
 struct Task {  // a request that a CTA starts and leaves to the columns behind it, if parts > 0
   int32_t request, parts, column, group_heads;
@@ -545,17 +549,18 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         id[h] = key < nn ? __ldg(p.table + rr * p.table_stride + static_cast<uint32_t>(key) / bs) : -1;
       }
     };
+    int odd = 0;
     if (left > 0) load_ids(r, tile, n);
-    for (int i = 0; left >= 0; ++i, --left) {
+    for (int i = 0; left > -kSets; ++i, --left) {
       const int slot = i % kRing;
       if (i >= kRing && !warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1)) break;
       TileDesc& d = sm.ring[slot];
-      if (left == 0) {
+      if (left <= 0) {  // the end, once for each set of decoding warps
         if (lane == 0) {
           d.flags = kEnd;
           mbar_arrive(&sm.ring_full[slot]);
         }
-        break;
+        continue;
       }
       const int64_t tiles = tiles_of(n);
       uint64_t mask = 0;
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const bool last_of_request = tile + 1 == tiles;
       if (lane == 0) {
         d.mask = mask;
-        d.flags = (tile == started ? kFirst : 0) | (last_of_request || left == 1 ? kLast : 0);
+        d.flags = (tile == started ? kFirst : 0) | (last_of_request || left == 1 ? kLast : 0) | odd;
         d.request = static_cast<int32_t>(r);
         d.part = started == 0 && last_of_request ? -1 : 2 * column + (started == 0 ? 1 : 0);
       }
@@ -594,6 +599,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
       }
       if (last_of_request) {
+        odd ^= kOdd;
         ++r;
         tile = started = 0;
         if (r - window >= 32) {
@@ -607,69 +613,66 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (left > 1) load_ids(r, tile, n);
     }
     if (err) atomicOr(p.err, err);
-  } else if (warp < kFillWarps) {
+  } else if (warp < kSoftWarp) {
     // ------------------------------------------------------------------------ decode the entries
     // Four threads per entry; thread `sub` of an entry takes the 16 bytes sub, sub + 4, ...: of the
     // codes a quarter of each 64-column chunk, so load j belongs to scale j.
-    const int key = 8 * warp + (lane >> 2), sub = lane & 3;
+    const int set = warp / kFillWarps, key = 8 * (warp % kFillWarps) + (lane >> 2), sub = lane & 3;
     // where its first 16 bytes go: decoded codes to two places of a chunk, rope values to one
     const uint32_t row = smem_addr(sm.k[0]) + key * 128, swz = static_cast<uint32_t>(key & 7) << 4;
     const uint32_t dst0 = row + ((32u * sub) ^ swz), dst1 = row + ((32u * sub + 16u) ^ swz);
     const uint32_t dst_rope = row + 7 * kChunkBytes + ((16u * sub) ^ swz);
-    uint4 raw[9];
+    uint4 raw[5];  // loads on their way: half a tile ahead
     uint2 sc;
     const uint8_t* src = nullptr;
     const uint8_t* ssrc = nullptr;
-    bool more = false;
-    int flags = 0;
-    auto load = [&](int j) {
-      if (src == nullptr) raw[j] = make_uint4(0, 0, 0, 0);
-      else raw[j] = ALIGN16 ? ld16(src + 64 * j) : ld8x2(src + 64 * j);
+    int flags = kEnd;
+    auto load = [&](int k, int j) {
+      if (src == nullptr) raw[k] = make_uint4(0, 0, 0, 0);
+      else raw[k] = ALIGN16 ? ld16(src + 64 * j) : ld8x2(src + 64 * j);
     };
     auto load_scales = [&] { sc = src == nullptr ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : ld8(ssrc); };
     // take tile i's addresses out of the ring
     auto fetch = [&](int i) -> bool {
       const int slot = i % kRing;
-      more = false;
+      flags = kEnd;
       if (!warp_wait(&sm.ring_full[slot], (i / kRing) & 1)) return false;
       flags = sm.ring[slot].flags;
-      more = (flags & kEnd) == 0;
-      if (more) {
-        src = sm.ring[slot].data[key];
-        if (src != nullptr) src += 16 * sub;
-        ssrc = sm.ring[slot].scales[key];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
-      }
+      src = sm.ring[slot].data[key];
+      ssrc = sm.ring[slot].scales[key];
+      if (flags & kEnd) src = nullptr;
+      if (src != nullptr) src += 16 * sub;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
       return true;
     };
     // the results of the run that tile i ended
-    int runs = 0;
-    auto results = [&](int i) {
+    auto results = [&](int i, int run) {
       // O being done, the runs before this one are finished with, and the parity means this run
-      const bool ok = warp_wait(&sm.k_free[i & 1][kQuarters - 1], (i / 2) & 1) && warp_wait(&sm.inv_full, runs & 1);
-      ++runs;
-      if (ok) store_results(sm, p, heads, 2 + warp / 4);
-      return ok;
+      if (!warp_wait(&sm.k_free[i & 1][kQuarters - 1], (i / 2) & 1) || !warp_wait(&sm.inv_full, run & kOdd ? 1 : 0)) return false;
+      store_results(sm, p, heads, 2 + (warp % kFillWarps) / 4);
+      return true;
     };
-    bool ok = fetch(0);
-    if (more) {
-      load_scales();
+    bool ok = fetch(set);
+    load_scales();
 #pragma unroll
-      for (int j = 0; j < 9; ++j) load(j);
-    }
-    bool last1 = false, last2 = false;  // the tile before and the one before it ended a run
-    int i = 0;
-    for (; ok && more; ++i) {
-      if (last2 && !(ok = results(i - 2))) break;
+    for (int j = 0; j < 4; ++j) load(j, j);
+    int done1 = 0, done2 = 0;  // flags of the set's last tiles, of the latest and the one before
+    int i = set;
+    for (; ok && !(flags & kEnd); i += kSets) {
+      // a tile's buffer is free when O has taken the tile two before; if that ended a run, its results come first
+      const int before = kSets == 2 ? done1 : done2;
+      if ((before & kLast) && !(ok = results(i - 2, before))) break;
       const int buf = i & 1;
-      const bool last = flags & kLast;
+      done2 = done1;
+      done1 = flags;
       const uint2 now = sc;
       const bool fits = scales_fit_f16(now.x) && scales_fit_f16(now.y | 127u << 24);  // the eighth is padding
       auto decode = [&](int j, uint32_t (&o)[8]) {
         const float scale = scale_of(((j < 4 ? now.x : now.y) >> (8 * (j & 3))) & 0xffu);
         const uint16_t half = fits ? to_f16(scale) : 0x3c00;  // one
-        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+        const uint4 r = raw[j & 3];
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
         float2 v[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(v[k].x, v[k].y);
-        if (more) load(j);  // of the next tile
+        load(j & 3, j < 4 ? j + 4 : j - 4);  // of this tile's second half, of the next tile's first
       };
       auto store = [&](int j, const uint32_t (&o)[8]) {
         const uint32_t at = buf * kTileBytes + j * kChunkBytes;
@@ -695,37 +698,30 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.k_full[buf][half]);
       };
-      if (!(ok = fetch(i + 1))) break;
-      if (more) load_scales();
       // As much as there are registers for is decoded before its room in the buffer is free.
       uint32_t o[4][8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) decode(j, o[j]);
-      if (!(ok = taken(0))) break;
-      store(0, o[0]);
-      store(1, o[1]);
+      load(4, 8);
       if (!(ok = taken(1))) break;
-      store(2, o[2]);
-      store(3, o[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) store(j, o[j]);
       publish(0);
+      if (!(ok = fetch(i + kSets))) break;
+      load_scales();
 #pragma unroll
       for (int j = 4; j < 7; ++j) decode(j, o[j - 4]);
-      if (!(ok = taken(2))) break;
-      store(4, o[0]);
-      store(5, o[1]);
       if (!(ok = taken(3))) break;
-      store(6, o[2]);
 #pragma unroll
-      for (int j = 7; j < 9; ++j) {  // the rope columns are bf16 already
-        sts16((dst_rope + buf * kTileBytes) ^ (64u * (j - 7)), raw[j].x, raw[j].y, raw[j].z, raw[j].w);
-        if (more) load(j);
-      }
+      for (int j = 4; j < 7; ++j) store(j, o[j - 4]);
+#pragma unroll
+      for (int j = 7; j < 9; ++j)  // the rope columns are bf16 already
+        sts16((dst_rope + buf * kTileBytes) ^ (64u * (j - 7)), raw[j - 4].x, raw[j - 4].y, raw[j - 4].z, raw[j - 4].w);
+      load(3, 3);
       publish(1);
-      last2 = last1;
-      last1 = last;
     }
-    if (ok && last2) ok = results(i - 2);
-    if (ok && last1) results(i - 1);
+    if (kSets == 1 && ok && (done2 & kLast)) ok = results(i - 2, done2);
+    if (ok && (done1 & kLast)) results(i - kSets, done1);
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ------------------------------------------------------------------------ issue the products
     // One elected thread in one branch: the compiler then keeps descriptors in uniform registers, and
@@ -864,10 +860,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       // the P of two tiles ago has been used
       if (i >= 2) wait(&sm.k_free[buf][kQuarters - 1], (i / 2 - 1) & 1);
-      // P with the references as they are, and whether any is off; if so once more with new ones.
+      // P with the references as they are, and whether any is off; if so once more, and only once, with
+      // new ones.
       float sums[kOwn / 4];
       bool off = dead, left = false;
-      for (;;) {
+      for (bool again = false;; again = true) {
         const bool any = fresh && __any_sync(0xffffffffu, in0 || in1);  // else no entry here speaks for a head
         const uint32_t p_at = smem_addr(sm.p[buf]) + key0 * 128 + 4 * (lane & 3);
         const uint32_t swz = static_cast<uint32_t>(key0 & 7) << 4;  // key1 & 7 is the same
@@ -886,8 +883,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               // log2-scaled scores over the reference, -inf where there is no entry
-              float t0 = fmaf(__uint_as_float(x[4 * g + c]), c2, c ? -ref.y : -ref.x);
-              float t1 = fmaf(__uint_as_float(x[4 * g + 2 + c]), c2, c ? -ref.y : -ref.x);
+              // (rounded before the difference, as a reference is: the highest is then 0 exactly)
+              float t0 = __fmul_rn(__uint_as_float(x[4 * g + c]), c2) - (c ? ref.y : ref.x);
+              float t1 = __fmul_rn(__uint_as_float(x[4 * g + 2 + c]), c2) - (c ? ref.y : ref.x);
               if (!in0) t0 = -INFINITY;
               if (!in1) t1 = -INFINITY;
               const float higher = head + c < heads ? fmaxf(t0, t1) : 0.f;
@@ -908,11 +906,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           }
         }
         off |= top > kSlack;
-        if (!soft_vote(off)) break;
+        if (!soft_vote(again ? dead : off)) break;
         left = soft_vote(dead);
         if (left) break;
         // New references: the maxima so far of all heads. O and the sums are rescaled to them.
-        if (soft_vote(dead)) break;
         if (own < heads16) {
           uint32_t x[kOwn / 2];
           tmem_ld_scores<kOwn>(s_at + own, x);
@@ -921,8 +918,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           for (int g = 0; g < kOwn / 8; ++g) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float top = fmaxf(in0 ? __uint_as_float(x[4 * g + c]) * c2 : -INFINITY,
-                                in1 ? __uint_as_float(x[4 * g + 2 + c]) * c2 : -INFINITY);
+              float top = fmaxf(in0 ? __fmul_rn(__uint_as_float(x[4 * g + c]), c2) : -INFINITY,
+                                in1 ? __fmul_rn(__uint_as_float(x[4 * g + 2 + c]), c2) : -INFINITY);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
               if (lane < 4) sm.by_warp[w][h0 + 8 * g + c] = top;

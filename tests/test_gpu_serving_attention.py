@@ -225,6 +225,35 @@ def test_decode_growing_scores(binding):
     _check(c, out, lse)
 
 
+@pytest.mark.parametrize("scale", [1e20, -1e20, 3e35, 1e-30])
+def test_decode_huge_and_tiny_scores(binding, scale):
+    """Scores whose steps in fp32 are wider than any reference's slack (all weight goes to the highest), and all equal."""
+    import torch
+    rng = np.random.default_rng(16)
+    n = 400
+    c = _case(rng, [n, 70], 17, 64)
+    rank = rng.permutation(n)
+    for r in range(2):
+        for j in range(n if r == 0 else 70):        # entry j's rope column 0 holds rank[j] - 200, exact in bf16
+            rec = c["cache"][c["table"][r, j // 64]].reshape(-1)[(j % 64) * RECORD:][:RECORD]
+            x = np.array([np.float32(rank[j] - 200)]).view(np.uint32)[0]
+            assert x & 0xffff == 0
+            rec[NOPE:NOPE + 2] = np.array([x >> 16], np.uint16).view(np.uint8)
+    c["q"][:] = 0
+    c["q"][:, :, NOPE] = 1
+    c["scale"] = scale
+    out, lse = _run(binding, c)
+    if abs(scale) < 1:
+        _check(c, out, lse)
+        return
+    for r, m in ((0, n), (1, 70)):
+        best = int(np.argmax(rank[:m]) if scale > 0 else np.argmin(rank[:m]))
+        want = entries(c["cache"], 64, c["table"][r], m)[best]
+        assert np.array_equal(out[r].double().cpu().numpy(), np.broadcast_to(want, (17, HEAD)))
+        top = abs(scale) * abs(rank[best] - 200)
+        assert np.allclose(lse[r].double().cpu().numpy(), top, rtol=2.0 ** -21, atol=0)
+
+
 def test_decode_far_pages(binding):
     """A cache of more than 4 GiB whose used pages sit behind that."""
     import torch
