@@ -55,6 +55,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 template <bool PART_F32, bool OUT_F32>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams p) {
   const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeThreads / 32) + (threadIdx.x >> 5);
   if (row >= p.requests * p.heads) return;
   const int64_t r = row / p.heads, h = row % p.heads;
@@ -62,34 +64,42 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
   const float* lse_in = p.part_lse + r * p.lse_in_r + h * p.lse_in_h;
   const char* part = static_cast<const char*>(p.part) + (r * p.part_stride_r + h * p.part_stride_h) * kPartBytes;
 
-  float top = -INFINITY;
-  for (int64_t i = 0; i < p.parts; ++i) {
-    const float l = lse_in[i * p.lse_in_p];
-    top = l > top || l != l ? l : top;  // a NaN stays
-  }
-  const float shift = top == -INFINITY ? 0.f : top;
-  float acc[2][8] = {};
-  float sum = 0.f;
   constexpr int kFlight = 4;
-  for (int64_t i0 = 0; i0 < p.parts; i0 += kFlight) {
-    Piece<PART_F32> v[kFlight][2];
-    float w[kFlight];
+  Piece<PART_F32> v[kFlight][2];
+  auto load = [&](int64_t i0) {
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
-      w[k] = 0.f;
       if (i0 + k < p.parts) {
-        w[k] = expf(lse_in[(i0 + k) * p.lse_in_p] - shift);
         const char* src = part + (i0 + k) * p.part_stride_p * kPartBytes;
         v[k][0].load(src, 8 * lane);
         v[k][1].load(src, 256 + 8 * lane);
       }
     }
+  };
+  load(0);  // on its way while the weights are made, a part's by each lane
+  float top = -INFINITY;
+  bool nan = false;
+  for (int64_t i = lane; i < p.parts; i += 32) {
+    const float l = lse_in[i * p.lse_in_p];
+    top = fmaxf(top, l);
+    nan |= l != l;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (__any_sync(0xffffffffu, nan)) top = NAN;
+  const float shift = top == -INFINITY ? 0.f : top;
+  float acc[2][8] = {};
+  float sum = 0.f, own = 0.f;
+  for (int64_t i0 = 0; i0 < p.parts; i0 += kFlight) {
+    if (i0 % 32 == 0) own = i0 + lane < p.parts ? expf(lse_in[(i0 + lane) * p.lse_in_p] - shift) : 0.f;
+    if (i0 > 0) load(i0);
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
-      if (i0 + k < p.parts && w[k] != 0.f) {  // a part without weight may hold anything
-        sum += w[k];
-        v[k][0].add(w[k], acc[0]);
-        v[k][1].add(w[k], acc[1]);
+      const float w = __shfl_sync(0xffffffffu, own, static_cast<int>(i0 % 32) + k);
+      if (w != 0.f) {  // a part without weight may hold anything (and one behind the last has none)
+        sum += w;
+        v[k][0].add(w, acc[0]);
+        v[k][1].add(w, acc[1]);
       }
     }
   }
@@ -117,15 +127,17 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const MergeParams 
 
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream) {
   constexpr int kRows = kMergeThreads / 32;
-  const unsigned grid = static_cast<unsigned>((p.requests * p.heads + kRows - 1) / kRows);
-  if (p.part_f32) {
-    if (p.out_f32) merge_kernel<true, true><<<grid, kMergeThreads, 0, stream>>>(p);
-    else merge_kernel<true, false><<<grid, kMergeThreads, 0, stream>>>(p);
-  } else {
-    if (p.out_f32) merge_kernel<false, true><<<grid, kMergeThreads, 0, stream>>>(p);
-    else merge_kernel<false, false><<<grid, kMergeThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(static_cast<unsigned>((p.requests * p.heads + kRows - 1) / kRows));
+  lc.blockDim = dim3(kMergeThreads);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (p.part_f32) return p.out_f32 ? cudaLaunchKernelEx(&lc, merge_kernel<true, true>, p) : cudaLaunchKernelEx(&lc, merge_kernel<true, false>, p);
+  return p.out_f32 ? cudaLaunchKernelEx(&lc, merge_kernel<false, true>, p) : cudaLaunchKernelEx(&lc, merge_kernel<false, false>, p);
 }
 
 }  // namespace c128
