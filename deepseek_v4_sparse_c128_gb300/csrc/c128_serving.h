@@ -10,6 +10,16 @@ namespace c128 {
 
 constexpr int kMaxDecodeHeads = 1024;
 
+struct Divisor {
+  uint32_t value;
+  int32_t shift;  // log2(value), -1 if that is none
+  Divisor() = default;
+  explicit Divisor(int64_t v) : value(static_cast<uint32_t>(v)), shift(-1) {
+    for (int i = 0; i < 32; ++i)
+      if (value == 1u << i) shift = i;
+  }
+};
+
 struct ExtendParams {
   const int32_t* seq_lens;
   const int32_t* held;
@@ -20,7 +30,7 @@ struct ExtendParams {
   int64_t num_free;
   const int64_t* taken;
   int64_t* taken_out;
-  int64_t ratio, block;
+  Divisor ratio, block;
   unsigned int* err;
 };
 cudaError_t launch_extend(const ExtendParams& p, int sm_count, cudaStream_t stream);
@@ -30,10 +40,11 @@ struct SlotMapParams {
   const int32_t* query_lens;
   int64_t requests;
   const int32_t* state_table;
-  int64_t state_cols, state_stride, state_block;
+  int64_t state_cols, state_stride;
+  Divisor state_block;
   const int32_t* kv_table;
-  int64_t kv_cols, kv_stride, kv_block;
-  int32_t ratio;
+  int64_t kv_cols, kv_stride;
+  Divisor kv_block, ratio;
   int32_t* query_start;
   int32_t* token_to_req;
   int64_t* positions;

@@ -99,7 +99,7 @@ int c128_extend_block_tables(const c128_tensor_t* seq_lens, const c128_tensor_t*
   c128::ExtendParams p{};
   C128_TRY(check_table(block_table, R, &p.stride));
   C128_TRY(check_desc(free_blocks, C128_I32, 1));
-  if (free_blocks->shape[0] > kMaxCount) return C128_ERR_ARG;
+  if (free_blocks->shape[0] >= kMaxCount) return C128_ERR_ARG;
   C128_TRY(check_array(free_blocks, C128_I32, free_blocks->shape[0]));
   C128_TRY(check_array(taken, C128_I64, 1));
   C128_TRY(check_array(taken_out, C128_I64, 1));
@@ -115,8 +115,8 @@ int c128_extend_block_tables(const c128_tensor_t* seq_lens, const c128_tensor_t*
   p.num_free = free_blocks->shape[0];
   p.taken = static_cast<const int64_t*>(taken->data);
   p.taken_out = static_cast<int64_t*>(taken_out->data);
-  p.ratio = compress_ratio;
-  p.block = block_size;
+  p.ratio = c128::Divisor(compress_ratio);
+  p.block = c128::Divisor(block_size);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int sms = 0;
   C128_TRY(c128::stream_errors(s, &p.err, &sms));
@@ -137,7 +137,7 @@ int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* que
   C128_TRY(check_array(query_start, C128_I32, R + 1));
   C128_TRY(check_desc(positions, C128_I64, 1));
   const int64_t T = positions->shape[0];
-  if (T > kMaxCount) return C128_ERR_ARG;
+  if (T >= kMaxCount) return C128_ERR_ARG;
   C128_TRY(check_array(positions, C128_I64, T));
   C128_TRY(check_array(token_to_req_indices, C128_I32, T));
   C128_TRY(check_array(slot_mapping, C128_I64, T));
@@ -152,11 +152,11 @@ int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* que
   p.requests = R;
   p.state_table = static_cast<const int32_t*>(state_table->data);
   p.state_cols = state_table->shape[1];
-  p.state_block = state_block;
+  p.state_block = c128::Divisor(state_block);
   p.kv_table = static_cast<const int32_t*>(kv_table->data);
   p.kv_cols = kv_table->shape[1];
-  p.kv_block = kv_block_size;
-  p.ratio = compress_ratio;
+  p.kv_block = c128::Divisor(kv_block_size);
+  p.ratio = c128::Divisor(compress_ratio);
   p.query_start = static_cast<int32_t*>(query_start->data);
   p.token_to_req = static_cast<int32_t*>(token_to_req_indices->data);
   p.positions = static_cast<int64_t*>(positions->data);

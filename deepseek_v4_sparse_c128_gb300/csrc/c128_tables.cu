@@ -19,28 +19,41 @@ namespace {
 
 constexpr int kChunk = 2048;  // requests per round of the prefix sum
 
+// Sums stop at INT_MAX (blocks and tokens are fewer, so a sum that large is an error anyhow): 32-bit
+// words, and the order of additions does not matter.
+__device__ __forceinline__ uint32_t add_clipped(uint32_t a, uint32_t b) { return min(a + b, static_cast<uint32_t>(INT_MAX)); }
+
 // Exclusive prefix sum of one value per thread over the CTA, and the total. `warp_sums` holds one
 // value per warp and may be used again after the next __syncthreads.
 template <int THREADS>
-__device__ __forceinline__ int64_t block_exclusive_sum(int64_t v, int64_t* warp_sums, int64_t* total) {
+__device__ __forceinline__ uint32_t block_exclusive_sum(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = v;
+  uint32_t incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
+    const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl = add_clipped(incl, u);
   }
+  const uint32_t before = __shfl_up_sync(0xffffffffu, incl, 1);
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  int64_t before = 0, all = 0;
+  uint32_t w = lane < THREADS / 32 ? warp_sums[lane] : 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const int64_t s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
+  for (int o = 1; o < THREADS / 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w = add_clipped(w, u);
   }
-  *total = all;
-  return before + incl - v;
+  *total = __shfl_sync(0xffffffffu, w, THREADS / 32 - 1);
+  const uint32_t warps_before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return add_clipped(warp > 0 ? warps_before : 0, lane > 0 ? before : 0);
+}
+
+// x / d, with a shift where d is a power of two (shift >= 0): block sizes and ratios mostly are.
+__device__ __forceinline__ uint32_t divide(uint32_t x, const Divisor d) { return d.shift >= 0 ? x >> d.shift : x / d.value; }
+
+__device__ __forceinline__ void wait_for_inputs() {
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The last index in [0, n) whose start is <= x (starts ascend, starts[0] <= x).
@@ -70,8 +83,9 @@ __device__ __forceinline__ void load_run(const int32_t* v, int64_t r, int64_t n,
 
 // ------------------------------------------------------------------------------- block tables
 constexpr int kExtendThreads = 512;
-constexpr int kPerThread = kChunk / kExtendThreads;  // requests of a round, blocks of a tile
-constexpr int kExtendTile = kExtendThreads * kPerThread;
+constexpr int kPerThread = kChunk / kExtendThreads;  // requests of a round
+constexpr int kTileBlocks = 8;                       // blocks of a tile per thread, their loads in flight together
+constexpr int kExtendTile = kExtendThreads * kTileBlocks;
 
 // Every CTA sums all requests; the given blocks are dealt out in tiles of kExtendTile. With
 // `write_counts` the CTAs also write held_out (a round each) and CTA 0 taken_out, which must then not
@@ -79,65 +93,67 @@ constexpr int kExtendTile = kExtendThreads * kPerThread;
 __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendParams p, bool write_table, bool write_counts) {
   __shared__ int s_start[kChunk];  // first block of each request of the round, counted from the round's first
   __shared__ int s_held[kChunk];
-  __shared__ int64_t s_warp[kExtendThreads / 32];
-  __shared__ unsigned long long s_fail;
+  __shared__ uint32_t s_warp[kExtendThreads / 32];
+  __shared__ uint32_t s_fail;
 
+  wait_for_inputs();
   const int64_t taken = *p.taken;
   unsigned int err = 0;
   const bool bad_taken = taken < 0 || taken > p.num_free;
   if (bad_taken) err |= C128_DEV_BAD_LENGTH;
-  const int64_t avail = bad_taken ? 0 : p.num_free - taken;
-  int64_t base = 0;  // blocks needed by the requests of earlier rounds
-  int64_t given = 0;
-  bool failed = false;
-  const uint32_t ratio = static_cast<uint32_t>(p.ratio), block = static_cast<uint32_t>(p.block);
+  const uint32_t avail = bad_taken ? 0 : static_cast<uint32_t>(p.num_free - taken);
+  uint32_t base = 0;   // blocks needed by the requests of earlier rounds
+  uint32_t given = 0;
   const int64_t rounds = (p.requests + kChunk - 1) / kChunk;
 
   for (int64_t c = 0; c < rounds; ++c) {
-    if (threadIdx.x == 0) s_fail = ULLONG_MAX;
+    if (threadIdx.x == 0) s_fail = UINT_MAX;
     const int64_t r = c * kChunk + threadIdx.x * kPerThread;
-    int len[kPerThread], held[kPerThread], need[kPerThread];
+    int len[kPerThread], held[kPerThread];
+    uint32_t need[kPerThread], sum = 0;
     load_run(p.seq_lens, r, p.requests, len);
     load_run(p.held, r, p.requests, held);
-    int64_t sum = 0;
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
       if (len[k] < 0) err |= C128_DEV_BAD_LENGTH;
-      const uint32_t entries = static_cast<uint32_t>(max(len[k], 0)) / ratio;
-      const uint32_t needed = entries / block + (entries % block != 0);  // <= 2^31 - 1
+      const uint32_t entries = divide(static_cast<uint32_t>(max(len[k], 0)), p.ratio);
+      const uint32_t full = divide(entries, p.block), needed = full + (full * p.block.value != entries);  // <= INT_MAX
       need[k] = 0;
       if (held[k] < 0) {
         err |= C128_DEV_BAD_LENGTH;
       } else if (needed > static_cast<uint32_t>(held[k])) {
         if (needed > p.columns) err |= C128_DEV_BAD_BT_COL;
-        else need[k] = static_cast<int>(needed) - held[k];
+        else need[k] = needed - static_cast<uint32_t>(held[k]);
       }
-      sum += need[k];
+      sum = add_clipped(sum, need[k]);
     }
-    int64_t total;
-    int64_t off = base + block_exclusive_sum<kExtendThreads>(sum, s_warp, &total);  // a barrier, also for s_fail
-    int64_t first = off;
+    uint32_t total;
+    // (a barrier, also for s_fail)
+    uint32_t off = add_clipped(base, block_exclusive_sum<kExtendThreads>(sum, s_warp, &total));
+    uint32_t first = off;
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-      if (need[k] > 0 && first + need[k] > avail) {
+      const uint32_t next = add_clipped(first, need[k]);
+      if (need[k] > 0 && next > avail) {  // avail < INT_MAX
         err |= C128_DEV_NO_FREE_BLOCK;
-        atomicMin(&s_fail, static_cast<unsigned long long>(first));
+        atomicMin(&s_fail, first);
         break;
       }
-      first += need[k];
+      first = next;
     }
     __syncthreads();
-    // blocks are given up to the first request that the list cannot serve; none after it
-    const int64_t end = s_fail == ULLONG_MAX ? base + total : min(static_cast<int64_t>(s_fail), base + total);
-    const int64_t round_given = failed ? 0 : end - base;  // <= num_free < 2^31
+    // Blocks are given up to the first request that the list cannot serve, and none after it: the sum
+    // only grows, so later rounds find nothing left either.
+    const uint32_t end = min(s_fail, add_clipped(base, total));
+    const uint32_t round_given = base <= avail ? end - base : 0;
     int out[kPerThread];
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
       const int i = threadIdx.x * kPerThread + k;
       s_start[i] = static_cast<int>(min(off - base, round_given));
       s_held[i] = held[k];
-      out[k] = held[k] + (off - base + need[k] <= round_given ? need[k] : 0);
-      off += need[k];
+      out[k] = held[k] + (need[k] <= round_given && off - base <= round_given - need[k] ? static_cast<int>(need[k]) : 0);
+      off = add_clipped(off, need[k]);
     }
     if (write_counts && c % gridDim.x == blockIdx.x) {
 #pragma unroll
@@ -148,22 +164,25 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendPara
     if (write_table) {
       const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), p.requests - c * kChunk));
       const int32_t* from = p.free_blocks + taken + base;
-      for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kExtendTile; i0 < round_given;
-           i0 += static_cast<int64_t>(gridDim.x) * kExtendTile) {
+      for (uint32_t i0 = blockIdx.x * kExtendTile; i0 < round_given; i0 += gridDim.x * kExtendTile) {
+        int id[kTileBlocks];
 #pragma unroll
-        for (int k = 0; k < kPerThread; ++k) {
-          const int64_t i = i0 + k * kExtendThreads + threadIdx.x;
-          if (i < round_given) {
-            const int id = from[i];
-            const int q = last_at_or_before(s_start, n, static_cast<int>(i));
-            p.table[(c * kChunk + q) * p.stride + s_held[q] + (static_cast<int>(i) - s_start[q])] = id;
-          }
+        for (int k = 0; k < kTileBlocks; ++k) {
+          const uint32_t i = i0 + k * kExtendThreads + threadIdx.x;
+          id[k] = i < round_given ? from[i] : 0;
+        }
+        int q = -1;
+#pragma unroll
+        for (int k = 0; k < kTileBlocks; ++k) {
+          const uint32_t i = i0 + k * kExtendThreads + threadIdx.x;
+          if (i >= round_given) break;
+          if (q < 0 || (q + 1 < n && static_cast<uint32_t>(s_start[q + 1]) <= i)) q = last_at_or_before(s_start, n, static_cast<int>(i));
+          p.table[(c * kChunk + q) * p.stride + s_held[q] + (static_cast<int>(i) - s_start[q])] = id[k];
         }
       }
     }
-    failed = failed || s_fail != ULLONG_MAX;
     given += round_given;
-    base += total;
+    base = add_clipped(base, total);
     __syncthreads();  // s_start, s_held, s_warp and s_fail are written again
   }
   if (write_counts && blockIdx.x == 0 && threadIdx.x == 0) *p.taken_out = taken + given;
@@ -171,66 +190,33 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendPara
 }
 
 // ----------------------------------------------------------------------------------- slot maps
-constexpr int kMapThreads = 256;
+constexpr int kMapThreads = 512;                    // a token each
 constexpr int kMapRequests = kChunk / kMapThreads;  // requests per thread and round
-constexpr int kMapTokens = 4;                       // consecutive tokens per thread
-constexpr int kMapTile = kMapThreads * kMapTokens;
 
-// Slot of `index` in row r of a block table, -1 with an error bit if the table has none.
-__device__ __forceinline__ int64_t slot_of(const int32_t* table, int64_t stride, int64_t cols, uint32_t block, int r,
-                                           uint32_t index, unsigned int* err) {
-  const uint32_t col = index / block;
-  if (col >= cols) {
-    *err |= C128_DEV_BAD_BT_COL;
-    return -1;
-  }
-  const int id = table[r * stride + col];
-  if (id < 0) {
-    *err |= C128_DEV_BAD_BLOCK;
-    return -1;
-  }
-  return static_cast<int64_t>(id) * block + index % block;
-}
-
-template <class T, int N>
-__device__ __forceinline__ void store_run(T* v, int64_t t, int64_t n, const T (&x)[N]) {
-  constexpr int kPer16 = 16 / sizeof(T);
-  if (t + N <= n && (reinterpret_cast<uintptr_t>(v) & 15) == 0) {
-#pragma unroll
-    for (int k = 0; k < N; k += kPer16) *reinterpret_cast<int4*>(v + t + k) = *reinterpret_cast<const int4*>(&x[k]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (t + k < n) v[t + k] = x[k];
-  }
-}
-
-// CTA b makes the arrays of tokens [b * kMapTile, (b + 1) * kMapTile) and the per-request outputs of
-// rounds b, b + grid, ...; it sums requests until it has passed both.
+// CTA b makes the arrays of tokens [b * kMapThreads, (b + 1) * kMapThreads) and the per-request outputs
+// of rounds b, b + grid, ...; it sums requests until it has passed both. A token per thread, not
+// several: a decode step has a few hundred, and what counts is the chain of dependent steps of one.
 __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotMapParams p) {
   __shared__ int s_start[kChunk];  // first token of each request of the round
   __shared__ int s_pos[kChunk];    // and its position
-  __shared__ int64_t s_warp[kMapThreads / 32];
+  __shared__ uint32_t s_warp[kMapThreads / 32];
 
-  const int64_t tile = static_cast<int64_t>(blockIdx.x) * kMapTile;
-  const int64_t tile_end = min(tile + kMapTile, p.tokens);
-  const int64_t t0 = tile + threadIdx.x * kMapTokens;
+  wait_for_inputs();
+  const uint32_t t = blockIdx.x * kMapThreads + threadIdx.x;
+  const uint32_t tile_end = static_cast<uint32_t>(min(static_cast<int64_t>(blockIdx.x + 1) * kMapThreads, p.tokens));
   unsigned int err = 0;
-  alignas(16) int32_t req[kMapTokens];
-  alignas(16) int64_t pos[kMapTokens], slot[kMapTokens], kv_slot[kMapTokens];
-#pragma unroll
-  for (int k = 0; k < kMapTokens; ++k) req[k] = 0, pos[k] = 0, slot[k] = kv_slot[k] = -1;
+  int req = 0, pos = 0;
+  int64_t slot = -1, kv_slot = -1;
 
-  const uint32_t ratio = static_cast<uint32_t>(p.ratio);
   const int64_t rounds = max(static_cast<int64_t>(1), (p.requests + kChunk - 1) / kChunk);
-  int64_t base = 0;
+  uint32_t base = 0;
   int64_t duty = blockIdx.x;  // the next round whose per-request outputs are this CTA's
   for (int64_t c = 0; c < rounds && (base < tile_end || duty < rounds); ++c) {
     const int64_t r = c * kChunk + threadIdx.x * kMapRequests;
     int len[kMapRequests], query[kMapRequests];
     load_run(p.seq_lens, r, p.requests, len);
     load_run(p.query_lens, r, p.requests, query);
-    int64_t sum = 0;
+    uint32_t sum = 0;
     unsigned int bad = 0;
 #pragma unroll
     for (int k = 0; k < kMapRequests; ++k) {
@@ -238,58 +224,79 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotMapPara
       len[k] = max(len[k], 0);
       query[k] = max(query[k], 0);
       if (query[k] > len[k]) bad = C128_DEV_BAD_LENGTH;
-      sum += query[k];
+      sum = add_clipped(sum, static_cast<uint32_t>(query[k]));
     }
-    int64_t total;
-    int64_t start = base + block_exclusive_sum<kMapThreads>(sum, s_warp, &total);
+    uint32_t total;
+    uint32_t start = add_clipped(base, block_exclusive_sum<kMapThreads>(sum, s_warp, &total));
 #pragma unroll
     for (int k = 0; k < kMapRequests; ++k) {
       const int i = threadIdx.x * kMapRequests + k;
-      const int clipped = static_cast<int>(min(start, static_cast<int64_t>(INT_MAX)));
-      s_start[i] = clipped;
+      s_start[i] = static_cast<int>(start);
       s_pos[i] = len[k] - query[k];
       if (c == duty && r + k < p.requests) {
-        p.query_start[r + k] = clipped;
-        p.kv_lens[r + k] = static_cast<int32_t>(static_cast<uint32_t>(len[k]) / ratio);
+        p.query_start[r + k] = static_cast<int>(start);
+        p.kv_lens[r + k] = static_cast<int32_t>(divide(static_cast<uint32_t>(len[k]), p.ratio));
       }
-      start += query[k];
+      start = add_clipped(start, static_cast<uint32_t>(query[k]));
     }
+    const uint32_t end = add_clipped(base, total);
     if (c == duty) {
       err |= bad;
       if (c == rounds - 1 && threadIdx.x == 0) {
-        p.query_start[p.requests] = static_cast<int>(min(base + total, static_cast<int64_t>(INT_MAX)));
-        if (base + total > p.tokens) err |= C128_DEV_BAD_LENGTH;
+        p.query_start[p.requests] = static_cast<int>(end);
+        if (end > p.tokens) err |= C128_DEV_BAD_LENGTH;
       }
       duty += gridDim.x;
     }
     __syncthreads();
-    const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), p.requests - c * kChunk));
-    int q = -1;
-#pragma unroll
-    for (int k = 0; k < kMapTokens; ++k) {
-      const int64_t t = t0 + k;
-      if (t < base || t >= base + total || t >= tile_end) continue;
-      if (q < 0 || (q + 1 < n && s_start[q + 1] <= t)) q = last_at_or_before(s_start, n, static_cast<int>(t));
-      const int rq = static_cast<int>(c * kChunk) + q;
-      const int64_t at = static_cast<int64_t>(s_pos[q]) + (t - s_start[q]);
-      req[k] = rq;
-      pos[k] = at;
-      if (at < 0) continue;
-      const uint32_t u = static_cast<uint32_t>(at);
-      slot[k] = slot_of(p.state_table, p.state_stride, p.state_cols, static_cast<uint32_t>(p.state_block), rq, u, &err);
-      if ((u + 1) % ratio == 0)
-        kv_slot[k] = slot_of(p.kv_table, p.kv_stride, p.kv_cols, static_cast<uint32_t>(p.kv_block), rq, u / ratio, &err);
+    if (t >= base && t < end && t < tile_end) {
+      const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), p.requests - c * kChunk));
+      const int q = last_at_or_before(s_start, n, static_cast<int>(t));
+      req = static_cast<int>(c * kChunk) + q;
+      pos = s_pos[q] + (static_cast<int>(t) - s_start[q]);
+      if (pos >= 0) {
+        // both tables are read before either is looked at
+        const uint32_t u = static_cast<uint32_t>(pos), entry = divide(u, p.ratio);
+        const bool ends = u + 1 == (entry + 1) * p.ratio.value;
+        const uint32_t col = divide(u, p.state_block), kv_col = divide(entry, p.kv_block);
+        const bool in = col < p.state_cols, kv_in = ends && kv_col < p.kv_cols;
+        const int id = in ? p.state_table[req * p.state_stride + col] : 0;
+        const int kv_id = kv_in ? p.kv_table[req * p.kv_stride + kv_col] : 0;
+        if (!in || (ends && !kv_in)) err |= C128_DEV_BAD_BT_COL;
+        if (id < 0 || kv_id < 0) err |= C128_DEV_BAD_BLOCK;
+        if (in && id >= 0) slot = static_cast<int64_t>(id) * p.state_block.value + (u - col * p.state_block.value);
+        if (kv_in && kv_id >= 0) kv_slot = static_cast<int64_t>(kv_id) * p.kv_block.value + (entry - kv_col * p.kv_block.value);
+      }
     }
-    base += total;
+    base = end;
     __syncthreads();  // s_start, s_pos and s_warp are written again
   }
-  store_run(p.token_to_req, t0, tile_end, req);
-  store_run(p.positions, t0, tile_end, pos);
-  store_run(p.slots, t0, tile_end, slot);
-  store_run(p.kv_slots, t0, tile_end, kv_slot);
+  if (t < tile_end) {
+    p.token_to_req[t] = req;
+    p.positions[t] = pos;
+    p.slots[t] = slot;
+    p.kv_slots[t] = kv_slot;
+  }
   if (err) atomicOr(p.err, err);
 }
 
+}  // namespace
+
+namespace {
+// Launched so that its start overlaps the end of the kernel before it (it waits for that one's writes).
+template <class P, class... A>
+cudaError_t launch_early(void (*kernel)(P, A...), unsigned grid, unsigned threads, cudaStream_t stream, const P& p, A... args) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid);
+  lc.blockDim = dim3(threads);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, p, args...);
+}
 }  // namespace
 
 // One launch where held_out and taken_out are other memory than held and taken. In place, a CTA
@@ -299,22 +306,15 @@ cudaError_t launch_extend(const ExtendParams& p, int sm_count, cudaStream_t stre
   const bool in_place = p.held_out == p.held || p.taken_out == p.taken;
   const int64_t most = p.columns > 0 && p.requests > p.num_free / p.columns ? p.num_free : p.requests * p.columns;
   const int64_t tiles = (most + kExtendTile - 1) / kExtendTile;
-  const int grid = static_cast<int>(tiles < 1 ? 1 : tiles < sm_count ? tiles : sm_count);
-  if (!in_place || grid == 1) {
-    extend_kernel<<<grid, kExtendThreads, 0, stream>>>(p, true, true);
-    return cudaGetLastError();
-  }
-  extend_kernel<<<grid, kExtendThreads, 0, stream>>>(p, true, false);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  extend_kernel<<<1, kExtendThreads, 0, stream>>>(p, false, true);
-  return cudaGetLastError();
+  const unsigned grid = static_cast<unsigned>(tiles < 1 ? 1 : tiles < 2 * sm_count ? tiles : 2 * sm_count);
+  if (!in_place || grid == 1) return launch_early(extend_kernel, grid, kExtendThreads, stream, p, true, true);
+  const cudaError_t e = launch_early(extend_kernel, grid, kExtendThreads, stream, p, true, false);
+  return e != cudaSuccess ? e : launch_early(extend_kernel, 1u, kExtendThreads, stream, p, false, true);
 }
 
 cudaError_t launch_slot_maps(const SlotMapParams& p, cudaStream_t stream) {
-  const int64_t tiles = (p.tokens + kMapTile - 1) / kMapTile;
-  slot_map_kernel<<<static_cast<unsigned>(tiles < 1 ? 1 : tiles), kMapThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const int64_t tiles = (p.tokens + kMapThreads - 1) / kMapThreads;
+  return launch_early(slot_map_kernel, static_cast<unsigned>(tiles < 1 ? 1 : tiles), kMapThreads, stream, p);
 }
 
 }  // namespace c128

@@ -347,7 +347,7 @@ int c128_debug_stall_first_window_ex(const c128_config_t* config,
  *   held        [R]      int32   blocks it holds already
  *   block_table [R, MB]  int32   in place; stride[1] == 1, stride[0] >= MB. Entries other than the
  *                                ones given are left as they were
- *   free_blocks [F]      int32   block ids, F < 2^31
+ *   free_blocks [F]      int32   block ids, F < 2^31 - 1
  *   taken       [1]      int64   ids of free_blocks given away already
  *   held_out    [R]      int32   may be `held` itself (else: no overlap)
  *   taken_out   [1]      int64   may be `taken` itself
@@ -380,7 +380,7 @@ int c128_extend_block_tables(const c128_tensor_t* seq_lens, const c128_tensor_t*
  *   padded); query_start [R + 1] int32: the index of each request's first token, and their number;
  *   token_to_req_indices [T] int32; positions, slot_mapping, kv_slot_mapping [T] int64; kv_lens [R]
  *   int32: floor(seq_lens[r] / compress_ratio), the entries of the request's cache once the step's
- *   windows are stored. T < 2^31.
+ *   windows are stored. T < 2^31 - 1.
  *
  * Device error bits: C128_DEV_BAD_LENGTH - a negative length (counts as 0), query_lens[r] >
  * seq_lens[r] (tokens at negative positions get slots -1), or more tokens than T (those behind are
