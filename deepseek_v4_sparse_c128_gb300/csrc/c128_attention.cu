@@ -53,15 +53,13 @@ constexpr int kChunks = kHead / 64; // 64-column chunks of 128 bytes (bf16): one
 constexpr int kChunkBytes = kTile * 128;
 constexpr int kTileBytes = kChunks * kChunkBytes;  // a decoded tile: 64 KiB
 constexpr int kQuarters = 4;        // of a tile's columns: 128 each, an M of the second product
-#ifndef C128_SETS
-#define C128_SETS 1
-#endif
-constexpr int kSets = C128_SETS;
-#ifndef AHEAD
-#define AHEAD 3
-#endif
-constexpr int kFillWarps = 8, kSoftWarps = 8;  // fill warps of a tile
-constexpr int kSoftWarp = kSets * kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
+constexpr int kFillWarps = 8;       // decode a tile
+constexpr int kAhead = 3;           // of a tile's 7 chunks of codes, decoded before the buffer has room for them
+// Eight softmax warps, half the heads each: with four, which left 128
+// registers to all, a tile took 0.25 us (16 heads) or 0.5 us (64) longer; a second set of decoding warps
+// for alternate tiles took more than it gave, since with 72 registers they spill.
+constexpr int kSoftWarps = 8;
+constexpr int kSoftWarp = kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
 constexpr int kRing = 4;            // tiles the index warp may be ahead
 constexpr float kSlack = 32.f;      // log2 units a score may be from the reference
@@ -131,9 +129,9 @@ struct DecodeSmem {
   uint64_t q_full, q_free, o_free, drained;
   uint64_t inv_full;             // `inv` and `done` of a finished run are there
   int32_t done_request, done_part;
-  int64_t warp_sums[kDecodeThreads / 32];
-  int64_t begin, end;            // the column's tiles
-  int64_t first_tile;            // of the first request: its tiles before the column's
+  int warp_sums[32];
+  int32_t begin, end;            // the column's tiles
+  int32_t first_tile, first_entries;  // of the first request: its tiles before the column's, its entries
   int32_t first_request;
   Layout lay;                    // read back where results are written, to keep registers free
   int32_t group, group_heads;
@@ -315,47 +313,36 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ int64_t entries_of(const DecodeParams& p, int64_t r, unsigned int* err) {
-  int64_t n = p.kv_lens[r];
-  if (n < 0) {
-    *err |= C128_DEV_BAD_LENGTH;
-    n = 0;
-  }
-  if (n > p.columns * p.kv_bs) {
-    *err |= C128_DEV_BAD_BT_COL;
-    n = p.columns * p.kv_bs;
-  }
-  return n;
+// Entries of request r (p.most: what its table row holds, at most INT_MAX).
+__device__ __forceinline__ int entries_of(const DecodeParams& p, int64_t r, unsigned int* err) {
+  const int n = p.kv_lens[r];
+  if (n < 0) *err |= C128_DEV_BAD_LENGTH;
+  if (n > p.most) *err |= C128_DEV_BAD_BT_COL;
+  return max(min(n, p.most), 0);
 }
-// A request without entries still takes a (masked) tile: its results are written like any other's.
-__device__ __forceinline__ int64_t tiles_of(int64_t entries) { return entries > 0 ? (entries + kTile - 1) / kTile : 1; }
+// A request without entries still takes a (masked) tile: its results are written like any other's. The
+// tiles of all requests are less than 2^31.
+__device__ __forceinline__ int tiles_of(int entries) { return max((entries >> 6) + ((entries & 63) != 0), 1); }
+static_assert(kTile == 64, "tiles_of");
 
 // `total` tiles dealt to `columns` CTA columns, the first `extra` of them one tile more than the rest.
 // A cut that would fall within `snap` tiles of a request's begin or end is moved there: a cut request
 // costs its partial results (2 KB per head and part, written and read again), about what a tile or
 // two take.
-#ifndef C128_SNAP
-#define C128_SNAP 2
-#endif
-constexpr int kSnap = C128_SNAP;
+constexpr int kSnap = 2;
 struct Deal {
-  int64_t share, extra;
-  int snap;
-  __device__ Deal(int64_t total, int columns) {
-    if (total < (1ll << 32)) {  // a 64-bit division is a hundred instructions
-      share = static_cast<uint32_t>(total) / static_cast<uint32_t>(columns);
-    } else {
-      share = total / columns;
-    }
+  int share, extra, snap;
+  __device__ Deal(int total, int columns) {
+    share = static_cast<unsigned>(total) / static_cast<unsigned>(columns);
     extra = total - share * columns;
-    snap = static_cast<int>(min(share / 2, static_cast<int64_t>(kSnap)));
+    snap = min(share / 2, kSnap);
   }
-  __device__ int64_t begin(int column) const { return share * column + min(static_cast<int64_t>(column), extra); }
-  __device__ int column_of(int64_t tile) const {
-    const int64_t longer = extra * (share + 1);
-    const int64_t t = tile < longer ? tile : tile - longer, d = tile < longer ? share + 1 : share;
-    const int64_t q = t < (1ll << 32) ? static_cast<uint32_t>(t) / static_cast<uint32_t>(d) : t / d;
-    return static_cast<int>(tile < longer ? q : extra + q);
+  __device__ int begin(int column) const { return share * column + min(column, extra); }
+  __device__ int column_of(int tile) const {
+    const int longer = extra * (share + 1);
+    const int t = tile < longer ? tile : tile - longer, d = tile < longer ? share + 1 : share;
+    const int q = static_cast<unsigned>(t) / static_cast<unsigned>(d);
+    return tile < longer ? q : extra + q;
   }
 };
 
@@ -418,6 +405,7 @@ constexpr int kBoxHeads = 16;  // heads of a TMA load of queries
 template <bool ALIGN16, int HEADS>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
     decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ Layouts layouts) {
+  constexpr int kOwn = HEADS / 2;  // heads of four softmax warps
   extern __shared__ uint8_t smem_raw[];
   DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -454,39 +442,39 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // Sum the requests' tiles (each thread a stretch of requests)...
   const int64_t per = (p.requests + kDecodeThreads - 1) / kDecodeThreads;
   const int64_t r_begin = min(threadIdx.x * per, p.requests), r_end = min(r_begin + per, p.requests);
-  int64_t mine = 0;
+  int mine = 0;
   for (int64_t r = r_begin; r < r_end; ++r) mine += tiles_of(entries_of(p, r, &err));
-  int64_t incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += u;
   }
   if (lane == 31) sm.warp_sums[warp] = incl;
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  int64_t warps = lane < kDecodeThreads / 32 ? sm.warp_sums[lane] : 0;
+  int warps = lane < kDecodeThreads / 32 ? sm.warp_sums[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, warps, o);
+    const int u = __shfl_up_sync(0xffffffffu, warps, o);
     if (lane >= o) warps += u;
   }
-  const int64_t total = __shfl_sync(0xffffffffu, warps, 31);
-  const int64_t base = __shfl_sync(0xffffffffu, warps, warp) - __shfl_sync(0xffffffffu, incl, 31) + incl - mine;
+  const int total = __shfl_sync(0xffffffffu, warps, 31);
+  const int base = __shfl_sync(0xffffffffu, warps, warp) - __shfl_sync(0xffffffffu, incl, 31) + incl - mine;
   // ...choose the head groups: smaller ones while there are CTAs for a tile each, since the fewer
   // heads a CTA has, the sooner it has loaded their queries and stored their results...
-  const int size = HEADS == 16 || total * layouts.of[0].groups <= layouts.sms ? 0 : HEADS == 32 || total * layouts.of[1].groups <= layouts.sms ? 1 : 2;
+  const int size = HEADS == 16 || total <= layouts.of[0].columns ? 0 : HEADS == 32 || total <= layouts.of[1].columns ? 1 : 2;
   const Layout& lay = layouts.of[size];
   const int group_heads = 16 << size;
   const int column = static_cast<int>(blockIdx.x / static_cast<unsigned>(lay.groups)), group = blockIdx.x - column * lay.groups;
   const int heads = min(group_heads, p.heads - group * group_heads);
   const int heads16 = (heads + 15) & ~15;
   // ...and find this column's run: its first request, and whether its last one goes on behind it.
-  const int columns = static_cast<int>(min(static_cast<int64_t>(lay.columns), total));
+  const int columns = min(lay.columns, total);
   const bool idle = column >= columns;
   const Deal deal(total, columns);
-  const int64_t cut0 = idle ? 0 : deal.begin(column), cut1 = idle ? 0 : deal.begin(column + 1);
+  const int cut0 = idle ? 0 : deal.begin(column), cut1 = idle ? 0 : deal.begin(column + 1);
   Task* const task = reinterpret_cast<Task*>(p.workspace) + blockIdx.x;
   if (threadIdx.x == 0) {
     sm.lay = lay;
@@ -495,15 +483,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (idle) *task = Task{0, 0, 0, 0};
   }
   if (!idle && mine > 0 && base < cut1 && base + mine > cut0) {
-    for (int64_t r = r_begin, at = base; r < r_end && at < cut1; ++r) {
+    int at = base;
+    for (int64_t r = r_begin; r < r_end && at < cut1; ++r) {
       unsigned int ignore = 0;
-      const int64_t n = tiles_of(entries_of(p, r, &ignore)), next = at + n;
+      const int entries = entries_of(p, r, &ignore), next = at + tiles_of(entries);
       const bool holds0 = cut0 >= at && cut0 < next, holds1 = cut1 > at && cut1 <= next;
       if (holds0) {  // cut0 is this request's begin, or inside it, where it may move
         const bool back = cut0 - at <= deal.snap, on = !back && next - cut0 <= deal.snap;
         sm.first_request = static_cast<int32_t>(on ? r + 1 : r);
         sm.first_tile = back || on ? 0 : cut0 - at;
         sm.begin = back ? at : on ? next : cut0;
+        sm.first_entries = !on ? entries : r + 1 < p.requests ? entries_of(p, r + 1, &ignore) : 0;
       }
       if (holds1) {
         const bool on = next - cut1 <= deal.snap && cut1 - at > deal.snap || cut1 == next, back = !on && cut1 - at <= deal.snap;
@@ -537,46 +527,47 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // no tiles
   } else if (warp == kIndexWarp) {
     // -------------------------------------------------------------------------- walk the run
-    int64_t r = sm.first_request, tile = sm.first_tile;
-    int64_t left = sm.end - sm.begin;
-    int64_t started = tile;  // the request's tile at which this run takes it up
+    int64_t r = sm.first_request;
+    int tile = sm.first_tile, n = sm.first_entries;
+    int left = sm.end - sm.begin;
+    int started = tile;  // the request's tile at which this run takes it up
     const uint32_t bs = static_cast<uint32_t>(p.kv_bs);
     int64_t window = r;      // lanes hold the lengths of requests window .. window + 31
     unsigned int ignore = 0;
-    int64_t lens = window + lane < p.requests ? entries_of(p, window + lane, &ignore) : 0;
-    int64_t n = __shfl_sync(0xffffffffu, lens, 0);
     int id[2];
-    auto load_ids = [&](int64_t rr, int64_t tt, int64_t nn) {
+    // entries are fewer than 2^31, so an index past them does not wrap in 32 unsigned bits
+    auto load_ids = [&] {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t key = tt * kTile + 32 * h + lane;
-        id[h] = key < nn ? __ldg(p.table + rr * p.table_stride + static_cast<uint32_t>(key) / bs) : -1;
+        const uint32_t key = static_cast<uint32_t>(tile) * kTile + 32 * h + lane;
+        id[h] = key < static_cast<uint32_t>(n) ? __ldg(p.table + r * p.table_stride + key / bs) : -1;
       }
     };
     int odd = 0;
-    if (left > 0) load_ids(r, tile, n);
-    for (int i = 0; left > -kSets; ++i, --left) {
+    if (left > 0) load_ids();
+    int lens = window + lane < p.requests ? entries_of(p, window + lane, &ignore) : 0;
+    for (int i = 0; left >= 0; ++i, --left) {
       const int slot = i % kRing;
       if (i >= kRing && !warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1)) break;
       TileDesc& d = sm.ring[slot];
-      if (left <= 0) {  // the end, once for each set of decoding warps
+      if (left == 0) {
         if (lane == 0) {
           d.flags = kEnd;
           mbar_arrive(&sm.ring_full[slot]);
         }
-        continue;
+        break;
       }
-      const int64_t tiles = tiles_of(n);
+      const int tiles = tiles_of(n);
       uint64_t mask = 0;
       const uint8_t* from[2];
       const uint8_t* sc[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t key = tile * kTile + 32 * h + lane;
-        const bool in = key < n;
+        const uint32_t key = static_cast<uint32_t>(tile) * kTile + 32 * h + lane;
+        const bool in = key < static_cast<uint32_t>(n);
         const bool ok = in && id[h] >= 0 && id[h] < p.nkb;
         if (in && !ok) err |= C128_DEV_BAD_BLOCK;
-        const uint32_t off = static_cast<uint32_t>(key) % bs;
+        const uint32_t off = key % bs;
         const uint8_t* blk = p.kc + static_cast<int64_t>(ok ? id[h] : 0) * p.kc_stride0;
         from[h] = ok ? blk + static_cast<int64_t>(off) * kTokenStride : nullptr;
         sc[h] = blk + p.kv_bs * kTokenStride + static_cast<int64_t>(off) * kScaleDim;
@@ -614,14 +605,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       } else {
         ++tile;
       }
-      if (left > 1) load_ids(r, tile, n);
+      if (left > 1) load_ids();
     }
     if (err) atomicOr(p.err, err);
   } else if (warp < kSoftWarp) {
     // ------------------------------------------------------------------------ decode the entries
     // Four threads per entry; thread `sub` of an entry takes the 16 bytes sub, sub + 4, ...: of the
     // codes a quarter of each 64-column chunk, so load j belongs to scale j.
-    const int set = warp / kFillWarps, key = 8 * (warp % kFillWarps) + (lane >> 2), sub = lane & 3;
+    const int key = 8 * warp + (lane >> 2), sub = lane & 3;
     // where its first 16 bytes go: decoded codes to two places of a chunk, rope values to one
     const uint32_t row = smem_addr(sm.k[0]) + key * 128, swz = static_cast<uint32_t>(key & 7) << 4;
     const uint32_t dst0 = row + ((32u * sub) ^ swz), dst1 = row + ((32u * sub + 16u) ^ swz);
@@ -654,19 +645,18 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     auto results = [&](int i, int run) {
       // O being done, the runs before this one are finished with, and the parity means this run
       if (!warp_wait(&sm.k_free[i & 1][kQuarters - 1], (i / 2) & 1) || !warp_wait(&sm.inv_full, run & kOdd ? 1 : 0)) return false;
-      store_results(sm, p, heads, 2 + (warp % kFillWarps) / 4);
+      store_results(sm, p, heads, 2 + warp / 4);
       return true;
     };
-    bool ok = fetch(set);
+    bool ok = fetch(0);
     load_scales();
 #pragma unroll
     for (int j = 0; j < 9; ++j) load(j);
-    int done1 = 0, done2 = 0;  // flags of the set's last tiles, of the latest and the one before
-    int i = set;
-    for (; ok && !(flags & kEnd); i += kSets) {
-      // a tile's buffer is free when O has taken the tile two before; if that ended a run, its results come first
-      const int before = kSets == 2 ? done1 : done2;
-      if ((before & kLast) && !(ok = results(i - 2, before))) break;
+    int done1 = 0, done2 = 0;  // flags of the tile before this one, and of the one before it
+    int i = 0;
+    for (; ok && !(flags & kEnd); ++i) {
+      // the buffer is free when O has taken the tile two before; if that ended a run, its results come first
+      if ((done2 & kLast) && !(ok = results(i - 2, done2))) break;
       const int buf = i & 1;
       done2 = done1;
       done1 = flags;
@@ -702,26 +692,27 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.k_full[buf][half]);
       };
-      if (!(ok = fetch(i + kSets))) break;
+      if (!(ok = fetch(i + 1))) break;
       load_scales();
       // As much as there are registers for is decoded before its room in the buffer is free.
-      uint32_t o[AHEAD][8];
+      uint32_t o[kAhead][8];
+      constexpr auto at = [](int j) { return (j & 3) % kAhead; };
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j) decode(j, o[j]);
+      for (int j = 0; j < kAhead; ++j) decode(j, o[j]);
       if (!(ok = taken(1))) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j >= AHEAD) decode(j, o[j % AHEAD]);
-        store(j, o[j % AHEAD]);
+        if (j >= kAhead) decode(j, o[at(j)]);
+        store(j, o[at(j)]);
       }
       publish(0);
 #pragma unroll
-      for (int j = 4; j < min(7, 4 + AHEAD); ++j) decode(j, o[(j - 4) % AHEAD]);
+      for (int j = 4; j < 4 + kAhead; ++j) decode(j, o[at(j)]);
       if (!(ok = taken(3))) break;
 #pragma unroll
       for (int j = 4; j < 7; ++j) {
-        if (j >= 4 + AHEAD) decode(j, o[(j - 4) % AHEAD]);
-        store(j, o[(j - 4) % AHEAD]);
+        if (j >= 4 + kAhead) decode(j, o[at(j)]);
+        store(j, o[at(j)]);
       }
 #pragma unroll
       for (int j = 7; j < 9; ++j) {  // the rope columns are bf16 already
@@ -730,8 +721,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       publish(1);
     }
-    if (kSets == 1 && ok && (done2 & kLast)) ok = results(i - 2, done2);
-    if (ok && (done1 & kLast)) results(i - kSets, done1);
+    if (ok && (done2 & kLast)) ok = results(i - 2, done2);
+    if (ok && (done1 & kLast)) results(i - 1, done1);
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ------------------------------------------------------------------------ issue the products
     // One elected thread in one branch: the compiler then keeps descriptors in uniform registers, and
@@ -831,7 +822,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------------------------------ softmax
-    constexpr int kOwn = HEADS / 2;                  // heads of four warps
     const int w = warp & 3;                          // TMEM lanes 32w .. 32w + 31
     const int own = (warp - kSoftWarp) / 4 * kOwn;   // this warp's first head
     const bool lead = own == 0;
@@ -1054,25 +1044,45 @@ constexpr int kMaxCtas = 1024;
 
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p, const __grid_constant__ Layouts layouts) {
   __shared__ int16_t s_owner[kMaxCtas];
-  __shared__ int s_count;
+  __shared__ unsigned s_votes[32];
+  static_assert(4 * kJoinThreads / 32 == 32, "a word of votes for each lane");
   launch_dependents();
   grid_dependency_wait();
   const Task* tasks = reinterpret_cast<const Task*>(p.workspace);
-  const int ctas = layouts.of[2].ctas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {  // the CTAs that start a cut request, in order
-    int count = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const bool has = c0 + lane < ctas && tasks[c0 + lane].parts > 0;
-      const unsigned vote = __ballot_sync(0xffffffffu, has);
-      if (has) s_owner[count + __popc(vote & ((1u << lane) - 1))] = static_cast<int16_t>(c0 + lane);
-      count += __popc(vote);
-    }
-    if (lane == 0) s_count = count;
+  // the CTAs that start a cut request, in order
+  static_assert(kMaxCtas <= 4 * kJoinThreads, "a thread looks at four CTAs");
+  bool has[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = k * kJoinThreads + threadIdx.x;
+    has[k] = c < layouts.of[2].ctas && tasks[c].parts > 0;
+  }
+  unsigned vote[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    vote[k] = __ballot_sync(0xffffffffu, has[k]);
+    if (lane == 0) s_votes[k * (kJoinThreads / 32) + warp] = vote[k];
+  }
+  __syncthreads();
+  // (lane w: how many of the 32 CTAs of word w are before)
+  int before = __popc(s_votes[lane]);
+  const int own = before;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += u;
+  }
+  const int count = __shfl_sync(0xffffffffu, before, 31);
+  before -= own;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int at = __shfl_sync(0xffffffffu, before, k * (kJoinThreads / 32) + warp) + __popc(vote[k] & ((1u << lane) - 1));
+    if (has[k]) s_owner[at] = static_cast<int16_t>(k * kJoinThreads + threadIdx.x);
   }
   __syncthreads();
   const int heads4 = (p.heads + 3) / 4;
-  const int64_t items = static_cast<int64_t>(s_count) * heads4 * 16;
+  const int64_t items = static_cast<int64_t>(count) * heads4 * 16;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + warp; item < items;
        item += static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32)) {
     const int cols32 = static_cast<int>(item & 15);

@@ -63,6 +63,7 @@ struct DecodeParams {
   int64_t nkb, kv_bs, kc_stride0;
   const int32_t* table;
   int64_t requests, columns, table_stride;
+  int32_t most;                  // entries that a row of the table holds, at most 2^31 - 1
   const int32_t* kv_lens;
   int32_t heads;
   float scale;
