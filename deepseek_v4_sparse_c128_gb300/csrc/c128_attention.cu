@@ -62,7 +62,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kSoftWarp = kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
 constexpr int kRing = 4;            // tiles the index warp may be ahead
-constexpr float kSlack = 32.f;      // log2 units a score may be from the reference
+constexpr float kHigh = 0x1p32f, kLow = 0x1p-32f;  // weights may be up to, and one in the first tile has to be over
 constexpr int kTmemCols = 512, kTmemS = 256;  // O in columns 0..255, two S tiles behind it
 
 enum : int { kFirst = 1, kLast = 2, kEnd = 4, kOdd = 8 };  // of its run of one request's tiles; kOdd: an odd run
@@ -267,31 +267,39 @@ __device__ __forceinline__ bool soft_vote(bool pred) {
 }
 
 // ------------------------------------------------------------------------------------- decoding
-// Two e4m3 codes to fp32, times an fp16 scale: to fp16 (exact, NaN stays NaN), then a product of fp16
-// operands in fp32. With the packing to bf16 50 cycles of a scheduler per 16 codes and warp; moving the
-// bits into bf16 fields and multiplying there took 85, most of it half-rate integer operations.
-__device__ __forceinline__ float2 codes_to_f32(uint16_t two, uint16_t scale) {
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// Two e4m3 codes times a power of two to bf16x2, by way of fp16 (exact, NaN stays NaN) and fp32. About
+// 50 cycles of a scheduler per 16 codes and warp; moving the bits into bf16 fields and multiplying
+// there took 85, most of it half-rate integer operations, NaN codes aside.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint16_t two, float scale) {
+  uint32_t h;
   float2 v;
-  asm("{\n\t.reg .b32 h;\n\t.reg .b16 lo, hi;\n\t"
-      "cvt.rn.f16x2.e4m3x2 h, %2;\n\t"
-      "mov.b32 {lo, hi}, h;\n\t"
-      "fma.rn.f32.f16 %0, lo, %3, 0f00000000;\n\t"
-      "fma.rn.f32.f16 %1, hi, %3, 0f00000000;\n}"
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.f32.f16 %0, lo;\n\t"
+      "cvt.f32.f16 %1, hi;\n}"
       : "=f"(v.x), "=f"(v.y)
-      : "h"(two), "h"(scale));
-  return v;
+      : "r"(h));
+  v = mul2(v, make_float2(scale, scale));
+  return pack_bf16x2(v.x, v.y);
 }
-// 2^(byte - 127): the byte is the float's exponent field (0: the subnormal 2^-127). Between 2^-24 and
-// 2^15 it is an fp16 too.
+// 2^(byte - 127): the byte is the float's exponent field (0: the subnormal 2^-127).
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
-__device__ __forceinline__ bool scales_fit_f16(uint32_t w) {
-  return (__vcmpltu4(w, 0x01010101u * 103) | __vcmpgtu4(w, 0x01010101u * 142)) == 0;
-}
-__device__ __forceinline__ uint16_t to_f16(float x) {
-  uint16_t h;
-  asm("cvt.rn.f16.f32 %0, %1;" : "=h"(h) : "f"(x));
-  return h;
-}
 
 // Read once and past L1, whose memory the tiles and the products use (0.2 us a tile less than with
 // L1::no_allocate).
@@ -661,24 +669,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       done2 = done1;
       done1 = flags;
       const uint2 now = sc;
-      const bool fits = scales_fit_f16(now.x) && scales_fit_f16(now.y | 127u << 24);  // the eighth is padding
       auto decode = [&](int j, uint32_t (&o)[8]) {
         const float scale = scale_of(((j < 4 ? now.x : now.y) >> (8 * (j & 3))) & 0xffu);
-        const uint16_t half = fits ? to_f16(scale) : 0x3c00;  // one
         const uint4 r = raw[j];
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-        float2 v[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          v[2 * k] = codes_to_f32(static_cast<uint16_t>(w[k]), half);
-          v[2 * k + 1] = codes_to_f32(static_cast<uint16_t>(w[k] >> 16), half);
+          o[2 * k] = codes_to_bf16(static_cast<uint16_t>(w[k]), scale);
+          o[2 * k + 1] = codes_to_bf16(static_cast<uint16_t>(w[k] >> 16), scale);
         }
-        if (!fits) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k].x *= scale, v[k].y *= scale;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = pack_bf16x2(v[k].x, v[k].y);
         load(j);  // of the next tile
       };
       auto store = [&](int j, const uint32_t (&o)[8]) {
@@ -829,7 +828,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int key0 = 16 * w + (lane >> 2), key1 = key0 + 8;  // this thread's two entries of a tile
     const int h0 = own + 2 * (lane & 3);  // and its heads: h0 and h0 + 1, and on in steps of 8
     const float c2 = p.scale * kLog2e;
-    float l[kOwn / 4];             // its sums: of heads h0 + 8g and + 1 in l[2g], l[2g + 1]
+    float2 l[kOwn / 8];            // its sums: of heads h0 + 8g and + 1 in l[g]
     // Barriers of the eight warps, on a hardware barrier, which has no time limit. So a warp whose wait
     // ran out does not leave: it says so at the next barrier, which it reaches as the others do, and
     // all of them leave there.
@@ -856,47 +855,56 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (first) {
         fresh = zero = true;
 #pragma unroll
-        for (int g = 0; g < kOwn / 4; ++g) l[g] = 0.f;
+        for (int g = 0; g < kOwn / 8; ++g) l[g] = make_float2(0.f, 0.f);
       }
       wait(&sm.s_full[buf], (i / 2) & 1);
       tmem_fence_after();
       // P with the references as they are, and whether any is off; if so once more, and only once, with
       // new ones.
-      float sums[kOwn / 4];
+      float2 sums[kOwn / 8];
       bool off = dead, left = false;
       for (bool again = false;; again = true) {
         const bool any = fresh && __any_sync(0xffffffffu, in0 || in1);  // else no entry here speaks for a head
         const uint32_t p_at = smem_addr(sm.p[buf]) + key0 * 128 + 4 * (lane & 3);
         const uint32_t swz = static_cast<uint32_t>(key0 & 7) << 4;  // key1 & 7 is the same
-        float top = -INFINITY;  // the highest score over its reference
+        // The sums of a thread's two weights stand for the higher of the two in these checks.
+        float high = 0.f;
         if (own < heads16) {
           uint32_t x[kOwn / 2];
           tmem_ld_scores<kOwn>(s_at + own, x);  // scores of absent heads are there, and not used
           tmem_wait_ld();
           uint32_t packed[kOwn / 4];
+          const float2 scale = make_float2(c2, c2);
 #pragma unroll
           for (int g = 0; g < kOwn / 8; ++g) {
-            const int head = h0 + 8 * g;
-            float2 ref = make_float2(0.f, 0.f);
-            if (!zero) ref = *reinterpret_cast<const float2*>(&sm.ref[head]);
-            float e[4];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              // log2-scaled scores over the reference, -inf where there is no entry
-              // (rounded before the difference, as a reference is: the highest is then 0 exactly)
-              float t0 = __fmul_rn(__uint_as_float(x[4 * g + c]), c2) - (c ? ref.y : ref.x);
-              float t1 = __fmul_rn(__uint_as_float(x[4 * g + 2 + c]), c2) - (c ? ref.y : ref.x);
-              if (!in0) t0 = -INFINITY;
-              if (!in1) t1 = -INFINITY;
-              const float higher = head + c < heads ? fmaxf(t0, t1) : 0.f;
-              top = fmaxf(top, higher);
-              if (any) off |= (__ballot_sync(0xffffffffu, higher > -kSlack) & (0x11111111u << (lane & 3))) == 0;
-              e[c] = ex2_approx(t0);
-              e[2 + c] = ex2_approx(t1);
-              sums[2 * g + c] = e[c] + e[2 + c];
+            // log2-scaled scores over the reference, -inf where there is no entry
+            const uint32_t* y = x + 4 * g;
+            float2 t0 = mul2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), scale);
+            float2 t1 = mul2(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), scale);
+            if (!zero) {
+              // the product is rounded before the difference, as a reference is: the highest is then 0 exactly
+              const float2 ref = *reinterpret_cast<const float2*>(&sm.ref[h0 + 8 * g]);
+              t0 = make_float2(__fsub_rn(t0.x, ref.x), __fsub_rn(t0.y, ref.y));
+              t1 = make_float2(__fsub_rn(t1.x, ref.x), __fsub_rn(t1.y, ref.y));
             }
-            packed[2 * g] = pack_bf16x2(e[0], e[1]);
-            packed[2 * g + 1] = pack_bf16x2(e[2], e[3]);
+            if (!in0) t0 = make_float2(-INFINITY, -INFINITY);
+            if (!in1) t1 = make_float2(-INFINITY, -INFINITY);
+            const float2 e0 = make_float2(ex2_approx(t0.x), ex2_approx(t0.y));
+            const float2 e1 = make_float2(ex2_approx(t1.x), ex2_approx(t1.y));
+            sums[g] = add2(e0, e1);
+            packed[2 * g] = pack_bf16x2(e0.x, e0.y);
+            packed[2 * g + 1] = pack_bf16x2(e1.x, e1.y);
+            float2 s = sums[g];
+            if (heads < own + kOwn) {  // absent heads pass any check
+              if (h0 + 8 * g >= heads) s.x = 1.f;
+              if (h0 + 8 * g + 1 >= heads) s.y = 1.f;
+            }
+            high = fmaxf(high, fmaxf(s.x, s.y));
+            if (any) {
+              const unsigned four = 0x11111111u << (lane & 3);  // the lanes that hold these heads
+              off |= (__ballot_sync(0xffffffffu, s.x > kLow) & four) == 0;
+              off |= (__ballot_sync(0xffffffffu, s.y > kLow) & four) == 0;
+            }
           }
 #pragma unroll
           for (int g = 0; g < kOwn / 8; ++g) {
@@ -905,7 +913,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(packed[2 * g + 1]) : "memory");
           }
         }
-        off |= top > kSlack;
+        off |= high > kHigh;
         if (!soft_vote(again ? dead : off)) break;
         left = soft_vote(dead);
         if (left) break;
@@ -948,8 +956,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         if (left) break;
 #pragma unroll
         for (int g = 0; g < kOwn / 8; ++g) {
-          l[2 * g] *= sm.factor[h0 + 8 * g];
-          l[2 * g + 1] *= sm.factor[h0 + 8 * g + 1];
+          l[g].x *= sm.factor[h0 + 8 * g];
+          l[g].y *= sm.factor[h0 + 8 * g + 1];
         }
         if (!first) {
           tmem_fence_after();
@@ -974,7 +982,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (left) break;
       fresh = fresh && mask == 0;
 #pragma unroll
-      for (int g = 0; g < kOwn / 4; ++g) l[g] += sums[g];  // of absent heads: unused
+      for (int g = 0; g < kOwn / 8; ++g) l[g] = add2(l[g], sums[g]);  // of absent heads: unused
       tmem_fence_before();
       async_proxy_fence();
       const int request = sm.ring[slot].request, part = sm.ring[slot].part;
@@ -993,7 +1001,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       for (int g = 0; g < kOwn / 8; ++g) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float sum = l[2 * g + e];
+          float sum = e ? l[g].y : l[g].x;
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
           if (lane < 4) sm.by_warp[w][h0 + 8 * g + e] = sum;
