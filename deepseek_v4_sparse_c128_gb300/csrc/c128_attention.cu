@@ -141,13 +141,14 @@ struct DecodeSmem {
 static_assert(sizeof(DecodeSmem) <= 232448, "shared memory of one SM");
 
 // The bounded wait of this kernel, inline and on the SM's clock: a call would have to keep the many
-// values that live across it out of registers, and the global timer takes longer than most waits.
+// values that live across it out of registers, and the global timer takes longer than most waits. (Tries
+// without a time hint: a tile takes 4 % less.)
 constexpr uint32_t kWaitCycles = 2000000000u;  // about a second; the 32-bit clock wraps after two
 __device__ __forceinline__ bool decode_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag) {
-  if (mbar_try_wait_suspend(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint32_t t0 = clock();
   for (;;) {
-    if (mbar_try_wait_suspend(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (abort_flag != nullptr && *abort_flag) return false;
     if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) return false;
   }
@@ -521,14 +522,21 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   __syncthreads();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);  // known to be the same in the whole warp
   volatile int* const abort_flag = &sm.abort;
-  // A wait of a whole warp, with one answer for all its lanes; false: give up (the CTA ends).
+  // A wait of a whole warp. One that runs out sets the abort flag, and with that set every wait returns
+  // at once: the warps then run on as ever, on whatever they find, to the end that `tile_flags` shows them,
+  // and no result is stored. So no lane or warp leaves a path that others count on it for, without asking
+  // all lanes after every wait whether to go on (that took 6 % of a tile's time).
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, decode_wait(bar, parity, abort_flag));
-    if (!ok && lane == 0) {
+    if (!decode_wait(bar, parity, abort_flag)) {
       *abort_flag = 1;
       atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
     }
-    return ok;
+    __syncwarp();
+  };
+  auto tile_flags = [&](int i) {
+    warp_wait(&sm.ring_full[i % kRing], (i / kRing) & 1);
+    const int flags = sm.ring[i % kRing].flags;
+    return *abort_flag ? kEnd : flags;
   };
 
   if (idle) {
@@ -556,7 +564,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     int lens = window + lane < p.requests ? entries_of(p, window + lane, &ignore) : 0;
     for (int i = 0; left >= 0; ++i, --left) {
       const int slot = i % kRing;
-      if (i >= kRing && !warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1)) break;
+      if (i >= kRing) warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1);
       TileDesc& d = sm.ring[slot];
       if (left == 0) {
         if (lane == 0) {
@@ -636,35 +644,32 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     };
     auto load_scales = [&] { sc = src == nullptr ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : ld8(ssrc); };
     // take tile i's addresses out of the ring
-    auto fetch = [&](int i) -> bool {
+    auto fetch = [&](int i) {
       const int slot = i % kRing;
-      flags = kEnd;
-      if (!warp_wait(&sm.ring_full[slot], (i / kRing) & 1)) return false;
-      flags = sm.ring[slot].flags;
+      flags = tile_flags(i);
       src = sm.ring[slot].data[key];
       ssrc = sm.ring[slot].scales[key];
       if (flags & kEnd) src = nullptr;
       if (src != nullptr) src += 16 * sub;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
-      return true;
     };
     // the results of the run that tile i ended
     auto results = [&](int i, int run) {
       // O being done, the runs before this one are finished with, and the parity means this run
-      if (!warp_wait(&sm.k_free[i & 1][kQuarters - 1], (i / 2) & 1) || !warp_wait(&sm.inv_full, run & kOdd ? 1 : 0)) return false;
-      store_results(sm, p, heads, 2 + warp / 4);
-      return true;
+      warp_wait(&sm.k_free[i & 1][kQuarters - 1], (i / 2) & 1);
+      warp_wait(&sm.inv_full, run & kOdd ? 1 : 0);
+      if (!*abort_flag) store_results(sm, p, heads, 2 + warp / 4);
     };
-    bool ok = fetch(0);
+    fetch(0);
     load_scales();
 #pragma unroll
     for (int j = 0; j < 9; ++j) load(j);
     int done1 = 0, done2 = 0;  // flags of the tile before this one, and of the one before it
     int i = 0;
-    for (; ok && !(flags & kEnd); ++i) {
+    for (; !(flags & kEnd); ++i) {
       // the buffer is free when O has taken the tile two before; if that ended a run, its results come first
-      if ((done2 & kLast) && !(ok = results(i - 2, done2))) break;
+      if (done2 & kLast) results(i - 2, done2);
       const int buf = i & 1;
       done2 = done1;
       done1 = flags;
@@ -685,20 +690,22 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         sts16(dst0 + at, o[0], o[1], o[2], o[3]);
         sts16(dst1 + at, o[4], o[5], o[6], o[7]);
       };
-      auto taken = [&](int quarter) { return i < 2 || warp_wait(&sm.k_free[buf][quarter], (i / 2 - 1) & 1); };
+      auto await_room = [&](int quarter) {
+        if (i >= 2) warp_wait(&sm.k_free[buf][quarter], (i / 2 - 1) & 1);
+      };
       auto publish = [&](int half) {
         async_proxy_fence();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.k_full[buf][half]);
       };
-      if (!(ok = fetch(i + 1))) break;
+      fetch(i + 1);
       load_scales();
       // As much as there are registers for is decoded before its room in the buffer is free.
       uint32_t o[kAhead][8];
       constexpr auto at = [](int j) { return (j & 3) % kAhead; };
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) decode(j, o[j]);
-      if (!(ok = taken(1))) break;
+      await_room(1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j >= kAhead) decode(j, o[at(j)]);
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       publish(0);
 #pragma unroll
       for (int j = 4; j < 4 + kAhead; ++j) decode(j, o[at(j)]);
-      if (!(ok = taken(3))) break;
+      await_room(3);
 #pragma unroll
       for (int j = 4; j < 7; ++j) {
         if (j >= 4 + kAhead) decode(j, o[at(j)]);
@@ -720,8 +727,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       publish(1);
     }
-    if (ok && (done2 & kLast)) ok = results(i - 2, done2);
-    if (ok && (done1 & kLast)) results(i - 1, done1);
+    if (done2 & kLast) results(i - 2, done2);
+    if (done1 & kLast) results(i - 1, done1);
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ------------------------------------------------------------------------ issue the products
     // One elected thread in one branch: the compiler then keeps descriptors in uniform registers, and
@@ -829,26 +836,20 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int h0 = own + 2 * (lane & 3);  // and its heads: h0 and h0 + 1, and on in steps of 8
     const float c2 = p.scale * kLog2e;
     float2 l[kOwn / 8];            // its sums: of heads h0 + 8g and + 1 in l[g]
-    // Barriers of the eight warps, on a hardware barrier, which has no time limit. So a warp whose wait
-    // ran out does not leave: it says so at the next barrier, which it reaches as the others do, and
-    // all of them leave there.
-    bool dead = false;
+    // (The votes are a hardware barrier, which has no time limit: see warp_wait for why all eight warps
+    // come to each.)
     bool zero = true, fresh = true;  // the references are 0; the run has had no entry yet
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!dead) dead = !warp_wait(bar, parity);
-    };
     for (int i = 0;; ++i) {
       const int slot = i % kRing, buf = i & 1;
-      wait(&sm.ring_full[slot], (i / kRing) & 1);
-      const int flags = dead ? 0 : sm.ring[slot].flags;
+      const int flags = tile_flags(i);
       const uint64_t mask = sm.ring[slot].mask;
-      if (flags & kEnd) {  // the two votes that a warp whose wait ran out here takes part in
+      if (flags & kEnd) {  // two votes, so that warps that do not see it yet, after a wait that ran out, leave too
         soft_vote(true);
         soft_vote(true);
         break;
       }
       // the P of two tiles ago has been used
-      if (i >= 2) wait(&sm.k_free[buf][kQuarters - 1], (i / 2 - 1) & 1);
+      if (i >= 2) warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2 - 1) & 1);
       const bool in0 = mask >> key0 & 1, in1 = mask >> key1 & 1;
       const bool first = flags & kFirst;
       const uint32_t s_at = tmem + lanes + kTmemS + buf * kGroup;
@@ -857,12 +858,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
         for (int g = 0; g < kOwn / 8; ++g) l[g] = make_float2(0.f, 0.f);
       }
-      wait(&sm.s_full[buf], (i / 2) & 1);
+      warp_wait(&sm.s_full[buf], (i / 2) & 1);
       tmem_fence_after();
       // P with the references as they are, and whether any is off; if so once more, and only once, with
       // new ones.
       float2 sums[kOwn / 8];
-      bool off = dead, left = false;
+      bool off = false, left = false;
       for (bool again = false;; again = true) {
         const bool any = fresh && __any_sync(0xffffffffu, in0 || in1);  // else no entry here speaks for a head
         const uint32_t p_at = smem_addr(sm.p[buf]) + key0 * 128 + 4 * (lane & 3);
@@ -914,8 +915,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           }
         }
         off |= high > kHigh;
-        if (!soft_vote(again ? dead : off)) break;
-        left = soft_vote(dead);
+        if (!soft_vote(off && !again)) break;
+        left = soft_vote(false);
         if (left) break;
         // New references: the maxima so far of all heads. O and the sums are rescaled to them.
         if (own < heads16) {
@@ -951,9 +952,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
           for (int a = 0; a < kGroup / 32; ++a) sm.ref[32 * a + lane] = to[a], sm.factor[32 * a + lane] = f[a];
         }
-        if (!first) wait(&sm.k_free[(i - 1) & 1][kQuarters - 1], ((i - 1) / 2) & 1);
-        left = soft_vote(dead);
-        if (left) break;
+        if (!first) warp_wait(&sm.k_free[(i - 1) & 1][kQuarters - 1], ((i - 1) / 2) & 1);
+        soft_vote(false);
 #pragma unroll
         for (int g = 0; g < kOwn / 8; ++g) {
           l[g].x *= sm.factor[h0 + 8 * g];
@@ -1008,8 +1008,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
       }
       // O is done; with it the last run's results have been stored, and `inv` is free
-      wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
-      if (soft_vote(dead)) break;
+      warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
+      soft_vote(false);
       if (lead && w < 2 && 32 * w + lane < heads) {
         const int h = 32 * w + lane;
         const int64_t head = group0 + h;
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.inv_full);
       soft_vote(false);
-      store_results(sm, p, heads, lead ? 0 : 1);
+      if (!*abort_flag) store_results(sm, p, heads, lead ? 0 : 1);
     }
   }
   tmem_fence_before();
