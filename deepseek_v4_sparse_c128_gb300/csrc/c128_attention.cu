@@ -128,6 +128,8 @@ struct DecodeSmem {
   uint64_t s_full[2], s_free[2], p_full[2];
   uint64_t q_full, q_free, o_free, drained;
   uint64_t inv_full;             // `inv` and `done` of a finished run are there
+  uint64_t soft;                 // barrier of the softmax warps
+  volatile int32_t off[2];       // 1 + the tile whose P in this buffer was made with a reference that is off
   int32_t done_request, done_part;
   int warp_sums[32];
   int32_t begin, end;            // the column's tiles
@@ -251,20 +253,6 @@ __device__ __forceinline__ void load_query_box(void* dst, const CUtensorMap* map
           smem_addr(dst)),
       "l"(map), "r"(col), "r"(head), "r"(request), "r"(smem_addr(bar))
       : "memory");
-}
-
-// Barrier of the softmax warps with the OR of `pred` over them.
-__device__ __forceinline__ bool soft_vote(bool pred) {
-  uint32_t out;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, 1, %2, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(out)
-      : "r"(static_cast<uint32_t>(pred)), "n"(32 * kSoftWarps)
-      : "memory");
-  return out != 0;
 }
 
 // ------------------------------------------------------------------------------------- decoding
@@ -436,6 +424,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     mbar_init(&sm.q_free, 1);
     mbar_init(&sm.o_free, kSoftWarps + kFillWarps);
     mbar_init(&sm.inv_full, kSoftWarps);
+    mbar_init(&sm.soft, kSoftWarps);
+    sm.off[0] = sm.off[1] = 0;
     mbar_init(&sm.drained, 2);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -810,13 +800,19 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           }
         };
         int seg = -1;
+        uint32_t phase = 0;  // of p_full, bit b of buffer b
         for (int i = 0;; ++i) {
           const int slot = i % kRing, buf = i & 1;
           if (!wait(&sm.ring_full[slot], (i / kRing) & 1)) break;
           const int flags = sm.ring[slot].flags;
           if (flags & kEnd) break;
           mbar_arrive(&sm.ring_free[slot]);
-          if (!wait(&sm.p_full[buf], (i / 2) & 1)) break;
+          if (!wait(&sm.p_full[buf], phase >> buf & 1)) break;
+          phase ^= 1u << buf;
+          if (sm.off[buf] == i + 1) {  // that was made with references that are off: another comes
+            if (!wait(&sm.p_full[buf], phase >> buf & 1)) break;
+            phase ^= 1u << buf;
+          }
           // the results of the run before are out of O
           if ((flags & kFirst) && ++seg > 0 && !wait(&sm.o_free, (seg - 1) & 1)) break;
           if (buf) product_o(Const<1>(), flags & kFirst); else product_o(Const<0>(), flags & kFirst);
@@ -836,18 +832,19 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int h0 = own + 2 * (lane & 3);  // and its heads: h0 and h0 + 1, and on in steps of 8
     const float c2 = p.scale * kLog2e;
     float2 l[kOwn / 8];            // its sums: of heads h0 + 8g and + 1 in l[g]
-    // (The votes are a hardware barrier, which has no time limit: see warp_wait for why all eight warps
-    // come to each.)
     bool zero = true, fresh = true;  // the references are 0; the run has had no entry yet
+    uint32_t soft_phase = 0, p_phase = 0;  // p_phase: bit b of buffer b
+    auto soft_sync = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.soft);
+      warp_wait(&sm.soft, soft_phase);
+      soft_phase ^= 1;
+    };
     for (int i = 0;; ++i) {
       const int slot = i % kRing, buf = i & 1;
       const int flags = tile_flags(i);
       const uint64_t mask = sm.ring[slot].mask;
-      if (flags & kEnd) {  // two votes, so that warps that do not see it yet, after a wait that ran out, leave too
-        soft_vote(true);
-        soft_vote(true);
-        break;
-      }
+      if (flags & kEnd) break;
       // the P of two tiles ago has been used
       if (i >= 2) warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2 - 1) & 1);
       const bool in0 = mask >> key0 & 1, in1 = mask >> key1 & 1;
@@ -860,11 +857,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       warp_wait(&sm.s_full[buf], (i / 2) & 1);
       tmem_fence_after();
-      // P with the references as they are, and whether any is off; if so once more, and only once, with
-      // new ones.
+      // P with the references as they are; a warp that finds one off leaves word before it arrives. The
+      // second product looks there when all have arrived, and so do the warps: then once more, and only
+      // once, with new references. (A vote before the arrival took 5 % of a tile's time.)
       float2 sums[kOwn / 8];
-      bool off = false, left = false;
       for (bool again = false;; again = true) {
+        bool off = false;
         const bool any = fresh && __any_sync(0xffffffffu, in0 || in1);  // else no entry here speaks for a head
         const uint32_t p_at = smem_addr(sm.p[buf]) + key0 * 128 + 4 * (lane & 3);
         const uint32_t swz = static_cast<uint32_t>(key0 & 7) << 4;  // key1 & 7 is the same
@@ -915,9 +913,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           }
         }
         off |= high > kHigh;
-        if (!soft_vote(off && !again)) break;
-        left = soft_vote(false);
-        if (left) break;
+        if (off && !again) sm.off[buf] = i + 1;
+        tmem_fence_before();
+        async_proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[buf]);
+        warp_wait(&sm.p_full[buf], p_phase >> buf & 1);
+        p_phase ^= 1u << buf;
+        if (again || sm.off[buf] != i + 1) break;
+        tmem_fence_after();
         // New references: the maxima so far of all heads. O and the sums are rescaled to them.
         if (own < heads16) {
           uint32_t x[kOwn / 2];
@@ -935,7 +939,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             }
           }
         }
-        soft_vote(false);
+        soft_sync();
         float to[kGroup / 32];  // two heads per lane of every warp
         float f[kGroup / 32];
 #pragma unroll
@@ -947,13 +951,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           to[a] = top == -INFINITY ? was : fresh ? top : fmaxf(top, was);
           f[a] = fresh ? 1.f : ex2_approx(was - to[a]);
         }
-        soft_vote(false);  // all have read the old ones
+        soft_sync();  // all have read the old ones
         if (lead && w == 0) {
 #pragma unroll
           for (int a = 0; a < kGroup / 32; ++a) sm.ref[32 * a + lane] = to[a], sm.factor[32 * a + lane] = f[a];
         }
         if (!first) warp_wait(&sm.k_free[(i - 1) & 1][kQuarters - 1], ((i - 1) / 2) & 1);
-        soft_vote(false);
+        soft_sync();
 #pragma unroll
         for (int g = 0; g < kOwn / 8; ++g) {
           l[g].x *= sm.factor[h0 + 8 * g];
@@ -977,18 +981,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           tmem_wait_st();
           tmem_fence_before();
         }
-        zero = fresh = off = false;
+        zero = fresh = false;
       }
-      if (left) break;
       fresh = fresh && mask == 0;
 #pragma unroll
       for (int g = 0; g < kOwn / 8; ++g) l[g] = add2(l[g], sums[g]);  // of absent heads: unused
-      tmem_fence_before();
-      async_proxy_fence();
       const int request = sm.ring[slot].request, part = sm.ring[slot].part;
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&sm.p_full[buf]);
         mbar_arrive(&sm.s_free[buf]);
         mbar_arrive(&sm.ring_free[slot]);
       }
@@ -1009,7 +1009,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       // O is done; with it the last run's results have been stored, and `inv` is free
       warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
-      soft_vote(false);
+      soft_sync();
       if (lead && w < 2 && 32 * w + lane < heads) {
         const int h = 32 * w + lane;
         const int64_t head = group0 + h;
@@ -1032,7 +1032,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (lead && w == 0 && lane == 0) sm.done_request = request, sm.done_part = part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.inv_full);
-      soft_vote(false);
+      soft_sync();
       if (!*abort_flag) store_results(sm, p, heads, lead ? 0 : 1);
     }
   }
