@@ -44,6 +44,7 @@ EXPORTS = (
     "c128_build_slot_maps",
     "c128_decode_attention",
     "c128_decode_attention_workspace",
+    "c128_debug_stall_decode_attention",
     "c128_merge_attention",
 )
 
@@ -120,6 +121,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     L.c128_extend_block_tables.argtypes = [T, T, T, T, T, i32, i64, T, T, vp]
     L.c128_build_slot_maps.argtypes = [T, T, T, i64, T, i64, i32, T, T, T, T, T, T, vp]
     L.c128_decode_attention.argtypes = [T, T, i64, T, T, ctypes.c_float, T, T, T, T, vp]
+    L.c128_debug_stall_decode_attention.argtypes = L.c128_decode_attention.argtypes
     L.c128_decode_attention_workspace.argtypes = [i64, ctypes.POINTER(i64)]
     L.c128_merge_attention.argtypes = [T, T, T, T, vp]
     for name in EXPORTS:
@@ -403,6 +405,13 @@ def decode_attention(q, k_cache, kv_block_size: int, block_table, kv_lens, scale
             workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
     PreparedOp("decode_attention", q, k_cache, kv_block_size, block_table, kv_lens, scale, out, lse=lse, sink=sink,
                workspace=workspace, stream=stream)()
+
+
+def debug_stall_decode_attention(*args, **kw) -> None:
+    """Test of decode_attention's bounded waits (tests only): CTA 0 never learns of its tiles and gives up
+    with C128_DEV_TIMEOUT (read it with device_errors). Arguments as for decode_attention."""
+    op = PreparedOp("decode_attention", *args, **kw)
+    _check(lib().c128_debug_stall_decode_attention(*op._args), "c128_debug_stall_decode_attention")
 
 
 def merge_attention(part_out, part_lse, out, lse=None, stream=None) -> None:

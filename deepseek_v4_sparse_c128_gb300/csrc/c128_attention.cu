@@ -55,9 +55,9 @@ constexpr int kTileBytes = kChunks * kChunkBytes;  // a decoded tile: 64 KiB
 constexpr int kQuarters = 4;        // of a tile's columns: 128 each, an M of the second product
 constexpr int kFillWarps = 8;       // decode a tile
 constexpr int kAhead = 3;           // of a tile's 7 chunks of codes, decoded before the buffer has room for them
-// Eight softmax warps, half the heads each: with four, which left 128
-// registers to all, a tile took 0.25 us (16 heads) or 0.5 us (64) longer; a second set of decoding warps
-// for alternate tiles took more than it gave, since with 72 registers they spill.
+// Eight softmax warps, half the heads each: with four, which left 128 registers to all, a tile took 0.25 us
+// (16 heads) or 0.5 us (64) longer. Sixteen decoding warps, a set for alternate tiles or for either half
+// of the columns, took 0.1 to 0.6 us longer: seven warps to a scheduler have 72 registers, and spill.
 constexpr int kSoftWarps = 8;
 constexpr int kSoftWarp = kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
@@ -552,6 +552,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     int odd = 0;
     if (left > 0) load_ids();
     int lens = window + lane < p.requests ? entries_of(p, window + lane, &ignore) : 0;
+    if (p.stall && blockIdx.x == 0) left = -1;
     for (int i = 0; left >= 0; ++i, --left) {
       const int slot = i % kRing;
       if (i >= kRing) warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1);

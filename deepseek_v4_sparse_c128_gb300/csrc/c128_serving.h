@@ -74,6 +74,7 @@ struct DecodeParams {
   float* lse;                    // nullable
   int64_t lse_stride_r, lse_stride_h;
   uint8_t* workspace;
+  int32_t stall;                 // test only: CTA 0 never learns of its tiles, and its waits run out
   unsigned int* err;
 };
 cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stream);

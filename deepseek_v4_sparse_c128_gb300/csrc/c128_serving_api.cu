@@ -82,6 +82,72 @@ bool partly_overlap(const void* a, const void* b, int64_t bytes) {
   return x != y && (x < y ? y - x : x - y) < static_cast<uintptr_t>(bytes);
 }
 
+// c128_decode_attention; `stall`: the test of its waits.
+int decode(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
+           const c128_tensor_t* block_table, const c128_tensor_t* kv_lens, float scale,
+           const c128_tensor_t* sink, const c128_tensor_t* out, const c128_tensor_t* lse,
+           const c128_tensor_t* workspace, c128_stream_t stream, bool stall) {
+  c128::DecodeParams p{};
+  C128_TRY(check_rows(q, 3, nullptr));
+  const int64_t R = q->shape[0], H = q->shape[1];
+  if (R > kMaxCount) return C128_ERR_ARG;
+  if (H > c128::kMaxDecodeHeads) return C128_ERR_UNSUPPORTED;
+  C128_TRY(check_rows(out, 3, &p.out_f32));
+  if (out->shape[0] != R || out->shape[1] != H) return C128_ERR_SHAPE;
+  // the cache as the compressor takes it (slots of 584 bytes or more, a block a flat byte range)
+  C128_TRY(check_desc(k_cache, C128_U8, 3));
+  if (kv_block_size < 1 || kv_block_size > kMaxCount || k_cache->shape[1] != kv_block_size) return C128_ERR_ARG;
+  if (k_cache->shape[0] > kMaxCount) return C128_ERR_ARG;
+  if (k_cache->shape[2] < c128::kSlotBytes) return C128_ERR_SHAPE;
+  if (k_cache->stride[2] != 1 || k_cache->stride[1] != k_cache->shape[2]) return C128_ERR_STRIDE;
+  if (k_cache->shape[0] > 1 && k_cache->stride[0] < k_cache->shape[1] * k_cache->shape[2]) return C128_ERR_STRIDE;
+  if ((k_cache->shape[0] > 1 && k_cache->stride[0] % 8 != 0) || !aligned(k_cache->data, 16)) return C128_ERR_ALIGN;
+  C128_TRY(check_data(k_cache));
+  C128_TRY(check_table(block_table, R, &p.table_stride));
+  C128_TRY(check_array(kv_lens, C128_I32, R));
+  if (!std::isfinite(scale)) return C128_ERR_ARG;
+  if (sink != nullptr) C128_TRY(check_array(sink, C128_F32, H));
+  if (lse != nullptr) {
+    C128_TRY(check_lse(lse, 2));
+    if (lse->shape[0] != R || lse->shape[1] != H) return C128_ERR_SHAPE;
+  }
+  C128_TRY(check_desc(workspace, C128_U8, 1));
+  C128_TRY(check_array(workspace, C128_U8, workspace->shape[0]));
+  if (!aligned(workspace->data, 256)) return C128_ERR_ALIGN;
+  if (R == 0 || H == 0) return C128_OK;
+  // what the table can hold, in tiles of 64 entries: the kernel counts those in 32 bits
+  const int64_t most = block_table->shape[1] > kMaxCount / kv_block_size ? kMaxCount : block_table->shape[1] * kv_block_size;
+  if (R * (most / 64 + 1) > kMaxCount) return C128_ERR_ARG;
+  p.most = static_cast<int32_t>(most);
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.q_stride_r = step(q, 0);
+  p.q_stride_h = step(q, 1);
+  p.kc = static_cast<const uint8_t*>(k_cache->data);
+  p.nkb = k_cache->shape[0];
+  p.kv_bs = kv_block_size;
+  p.kc_stride0 = step(k_cache, 0);
+  p.table = static_cast<const int32_t*>(block_table->data);
+  p.requests = R;
+  p.columns = block_table->shape[1];
+  p.kv_lens = static_cast<const int32_t*>(kv_lens->data);
+  p.heads = static_cast<int32_t>(H);
+  p.scale = scale;
+  p.sink = sink != nullptr ? static_cast<const float*>(sink->data) : nullptr;
+  p.out = out->data;
+  p.out_stride_r = step(out, 0);
+  p.out_stride_h = step(out, 1);
+  p.lse = lse != nullptr ? static_cast<float*>(lse->data) : nullptr;
+  p.lse_stride_r = lse != nullptr ? step(lse, 0) : 0;
+  p.lse_stride_h = lse != nullptr ? step(lse, 1) : 0;
+  p.workspace = static_cast<uint8_t*>(workspace->data);
+  p.stall = stall ? 1 : 0;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  C128_TRY(c128::stream_errors(s, &p.err, &sms));
+  if (workspace->shape[0] < c128::decode_workspace_bytes(p.heads, sms)) return C128_ERR_ARG;
+  return done(c128::launch_decode(p, sms, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -185,64 +251,14 @@ int c128_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, 
                           const c128_tensor_t* block_table, const c128_tensor_t* kv_lens, float scale,
                           const c128_tensor_t* sink, const c128_tensor_t* out, const c128_tensor_t* lse,
                           const c128_tensor_t* workspace, c128_stream_t stream) {
-  c128::DecodeParams p{};
-  C128_TRY(check_rows(q, 3, nullptr));
-  const int64_t R = q->shape[0], H = q->shape[1];
-  if (R > kMaxCount) return C128_ERR_ARG;
-  if (H > c128::kMaxDecodeHeads) return C128_ERR_UNSUPPORTED;
-  C128_TRY(check_rows(out, 3, &p.out_f32));
-  if (out->shape[0] != R || out->shape[1] != H) return C128_ERR_SHAPE;
-  // the cache as the compressor takes it (slots of 584 bytes or more, a block a flat byte range)
-  C128_TRY(check_desc(k_cache, C128_U8, 3));
-  if (kv_block_size < 1 || kv_block_size > kMaxCount || k_cache->shape[1] != kv_block_size) return C128_ERR_ARG;
-  if (k_cache->shape[0] > kMaxCount) return C128_ERR_ARG;
-  if (k_cache->shape[2] < c128::kSlotBytes) return C128_ERR_SHAPE;
-  if (k_cache->stride[2] != 1 || k_cache->stride[1] != k_cache->shape[2]) return C128_ERR_STRIDE;
-  if (k_cache->shape[0] > 1 && k_cache->stride[0] < k_cache->shape[1] * k_cache->shape[2]) return C128_ERR_STRIDE;
-  if ((k_cache->shape[0] > 1 && k_cache->stride[0] % 8 != 0) || !aligned(k_cache->data, 16)) return C128_ERR_ALIGN;
-  C128_TRY(check_data(k_cache));
-  C128_TRY(check_table(block_table, R, &p.table_stride));
-  C128_TRY(check_array(kv_lens, C128_I32, R));
-  if (!std::isfinite(scale)) return C128_ERR_ARG;
-  if (sink != nullptr) C128_TRY(check_array(sink, C128_F32, H));
-  if (lse != nullptr) {
-    C128_TRY(check_lse(lse, 2));
-    if (lse->shape[0] != R || lse->shape[1] != H) return C128_ERR_SHAPE;
-  }
-  C128_TRY(check_desc(workspace, C128_U8, 1));
-  C128_TRY(check_array(workspace, C128_U8, workspace->shape[0]));
-  if (!aligned(workspace->data, 256)) return C128_ERR_ALIGN;
-  if (R == 0 || H == 0) return C128_OK;
-  // what the table can hold, in tiles of 64 entries: the kernel counts those in 32 bits
-  const int64_t most = block_table->shape[1] > kMaxCount / kv_block_size ? kMaxCount : block_table->shape[1] * kv_block_size;
-  if (R * (most / 64 + 1) > kMaxCount) return C128_ERR_ARG;
-  p.most = static_cast<int32_t>(most);
-  p.q = static_cast<const uint16_t*>(q->data);
-  p.q_stride_r = step(q, 0);
-  p.q_stride_h = step(q, 1);
-  p.kc = static_cast<const uint8_t*>(k_cache->data);
-  p.nkb = k_cache->shape[0];
-  p.kv_bs = kv_block_size;
-  p.kc_stride0 = step(k_cache, 0);
-  p.table = static_cast<const int32_t*>(block_table->data);
-  p.requests = R;
-  p.columns = block_table->shape[1];
-  p.kv_lens = static_cast<const int32_t*>(kv_lens->data);
-  p.heads = static_cast<int32_t>(H);
-  p.scale = scale;
-  p.sink = sink != nullptr ? static_cast<const float*>(sink->data) : nullptr;
-  p.out = out->data;
-  p.out_stride_r = step(out, 0);
-  p.out_stride_h = step(out, 1);
-  p.lse = lse != nullptr ? static_cast<float*>(lse->data) : nullptr;
-  p.lse_stride_r = lse != nullptr ? step(lse, 0) : 0;
-  p.lse_stride_h = lse != nullptr ? step(lse, 1) : 0;
-  p.workspace = static_cast<uint8_t*>(workspace->data);
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int sms = 0;
-  C128_TRY(c128::stream_errors(s, &p.err, &sms));
-  if (workspace->shape[0] < c128::decode_workspace_bytes(p.heads, sms)) return C128_ERR_ARG;
-  return done(c128::launch_decode(p, sms, s));
+  return decode(q, k_cache, kv_block_size, block_table, kv_lens, scale, sink, out, lse, workspace, stream, false);
+}
+
+int c128_debug_stall_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
+                                      const c128_tensor_t* block_table, const c128_tensor_t* kv_lens, float scale,
+                                      const c128_tensor_t* sink, const c128_tensor_t* out, const c128_tensor_t* lse,
+                                      const c128_tensor_t* workspace, c128_stream_t stream) {
+  return decode(q, k_cache, kv_block_size, block_table, kv_lens, scale, sink, out, lse, workspace, stream, true);
 }
 
 int c128_merge_attention(const c128_tensor_t* part_out, const c128_tensor_t* part_lse, const c128_tensor_t* out,

@@ -429,6 +429,18 @@ int c128_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, 
                           const c128_tensor_t* sink, const c128_tensor_t* out, const c128_tensor_t* lse,
                           const c128_tensor_t* workspace, c128_stream_t stream);
 
+/*
+ * Test of the failure handling, for tests only: c128_decode_attention, except that CTA 0 never learns of
+ * its tiles. Every wait of that kernel is bounded (about 1 s), so CTA 0 gives up and ends with
+ * C128_DEV_TIMEOUT in the device error bits, and stores nothing; the requests (or heads, or parts of
+ * requests) of other CTAs are computed as usual. The context stays usable.
+ */
+int c128_debug_stall_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache,
+                                      int64_t kv_block_size, const c128_tensor_t* block_table,
+                                      const c128_tensor_t* kv_lens, float scale, const c128_tensor_t* sink,
+                                      const c128_tensor_t* out, const c128_tensor_t* lse,
+                                      const c128_tensor_t* workspace, c128_stream_t stream);
+
 /* Bytes of workspace that c128_decode_attention needs on the current device for `num_heads` heads,
  * whatever the requests and their lengths. */
 int c128_decode_attention_workspace(int64_t num_heads, int64_t* bytes);

@@ -330,6 +330,26 @@ def test_decode_refuses_a_small_workspace(binding):
     assert e.value.status == 7
 
 
+def test_decode_gives_up_after_a_wait_that_runs_out(binding):
+    """CTA 0 never learns of its tiles: the call ends with the TIMEOUT bit, the other CTAs' requests are there, what
+    CTA 0 had to store is as it was, and the next call is right."""
+    import torch
+    rng = np.random.default_rng(17)
+    c = _case(rng, [64] * 400, 16, 64)               # one tile each, whole requests only
+    args = (c["q"], _cuda(c["cache"]), 64, _cuda(c["table"]), _cuda(c["lens"]), c["scale"])
+    out = torch.full((400, 16, HEAD), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((400, 16), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    binding.debug_stall_decode_attention(*args, out, lse=lse)
+    assert binding.device_errors(clear=True) == 32
+    untouched = (out == 7).all(-1).all(-1)
+    n = int(untouched.sum())
+    assert 1 <= n <= 5 and bool(untouched[:n].all())  # the first column's run
+    _check(c, out, lse, list(range(n, 400, 13)))
+    out, lse = _run(binding, c)
+    _check(c, out, lse, list(range(0, 400, 13)))
+
+
 # ------------------------------------------------------------------------------------------ merge
 @pytest.mark.parametrize("part_f32", [False, True])
 @pytest.mark.parametrize("out_f32", [False, True])
