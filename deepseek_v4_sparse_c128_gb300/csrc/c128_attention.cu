@@ -37,7 +37,6 @@
 //          to L2 a few tiles ahead
 #include <cuda_runtime.h>
 
-#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -79,7 +78,8 @@ struct Layout {
   Layout() = default;
   Layout(int all_heads, int sms, int group) {
     groups = (all_heads + group - 1) / group;
-    columns = sms / groups > 0 ? sms / groups : 1;
+    columns = sms / groups;  // 0: no such groups on this GPU, but for the largest
+    if (columns == 0 && group == kGroup) columns = 1;
     heads = groups > 1 ? group : (all_heads + 15) / 16 * 16;
     ctas = sms > columns * groups ? sms : columns * groups;
   }
@@ -100,8 +100,7 @@ struct Layout {
 };
 
 struct Layouts {  // made on the host: their divisions would stand in front of the kernel's work
-  Layout of[3];   // for groups of 16, 32 and 64 heads
-  int sms;
+  Layout of[3];  // for groups of 16, 32 and 64 heads
 };
 
 struct TileDesc {
@@ -154,17 +153,6 @@ __device__ __forceinline__ bool decode_wait(uint64_t* bar, uint32_t parity, cons
     if (abort_flag != nullptr && *abort_flag) return false;
     if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) return false;
   }
-}
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, P;\n}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 
 // ------------------------------------------------------------------------------------ tcgen05
@@ -1206,7 +1194,6 @@ cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stre
   if (!encode_query_map(p, &map)) return cudaErrorInvalidValue;
   Layouts layouts;
   for (int i = 0; i < 3; ++i) layouts.of[i] = Layout(p.heads, sm_count, 16 << i);
-  layouts.sms = sm_count;
   const int ctas = layouts.of[2].ctas;
   if (ctas > kMaxCtas) return cudaErrorInvalidValue;
   const bool align16 = p.kc_stride0 % 16 == 0;  // records then start on 16 bytes, else on 8

@@ -105,7 +105,7 @@ int decode(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_bloc
   C128_TRY(check_data(k_cache));
   C128_TRY(check_table(block_table, R, &p.table_stride));
   C128_TRY(check_array(kv_lens, C128_I32, R));
-  if (!std::isfinite(scale)) return C128_ERR_ARG;
+  if (!std::isfinite(scale * 1.44269504f)) return C128_ERR_ARG;  // times log2(e), the kernel's factor
   if (sink != nullptr) C128_TRY(check_array(sink, C128_F32, H));
   if (lse != nullptr) {
     C128_TRY(check_lse(lse, 2));

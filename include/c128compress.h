@@ -410,7 +410,7 @@ int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* que
  *   k_cache     [NKB, bs, W]  uint8  as for compress_norm_rope_store; kv_block_size == bs
  *   block_table [R, MB]       int32  k_cache block of entries b*bs .. b*bs + bs - 1 of request r
  *   kv_lens     [R]           int32  entries of each request; bytes behind them are never used
- *   scale                     fp32   finite
+ *   scale                     fp32   finite, times log2(e) too
  *   sink        [H]           fp32   may be NULL
  *   out         [R, H, 512]   bf16 or fp32, strides as for q (fp32: multiples of 4)
  *   lse         [R, H]        fp32   positive strides; may be NULL
@@ -422,7 +422,8 @@ int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* que
  * weights are rounded to bf16) and add up in fp32; the softmax statistics are fp32.
  * Device error bits: C128_DEV_BAD_BT_COL - kv_lens[r] > MB*bs (the entries behind are left out);
  * C128_DEV_BAD_BLOCK - a block id outside [0, NKB) (its entries are left out); C128_DEV_BAD_LENGTH
- * - a negative kv_lens[r] (counts as 0); C128_DEV_TIMEOUT.
+ * - a negative kv_lens[r] (counts as 0); C128_DEV_TIMEOUT - a wait inside the kernel ran out: some of
+ * the results are not there. R * (MB*bs / 64 + 1) < 2^31, else C128_ERR_ARG.
  */
 int c128_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
                           const c128_tensor_t* block_table, const c128_tensor_t* kv_lens, float scale,
