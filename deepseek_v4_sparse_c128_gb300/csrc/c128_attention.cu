@@ -1034,116 +1034,150 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 }
 
 // ------------------------------------------------------------------- join the partial results
-// out = sum_k 2^(lse_k - L) part_k. One warp per cut request, 4 heads and 32 columns: 16 bytes per lane
-// and part, as the parts are laid out.
-constexpr int kJoinThreads = 256;
+// out = sum_k 2^(lse_k - L) part_k, in the layout of the parts: a warp takes four heads and 32 or 128
+// columns of a cut request, 16 bytes per lane, part and 32 columns. What it takes is the trips to L2 one
+// behind the other: who has been cut, that task, and then the parts' statistics and values at once.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinPerSm = 4;  // CTAs that fit (registers)
 constexpr int kMaxCtas = 1024;
 
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const DecodeParams p, const __grid_constant__ Layouts layouts) {
-  __shared__ int16_t s_owner[kMaxCtas];
-  __shared__ unsigned s_votes[32];
-  static_assert(4 * kJoinThreads / 32 == 32, "a word of votes for each lane");
+__device__ __forceinline__ float4 ld16_if(bool p, const float* from) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t@p ld.global.v4.f32 {%0, %1, %2, %3}, [%5];\n}"
+               : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)
+               : "r"(static_cast<uint32_t>(p)), "l"(from));
+  return v;
+}
+
+// Heads head .. head + 3, columns 32 * block .. of BLOCKS blocks.
+template <int BLOCKS>
+__device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout& lay, const Task t, int head, int block) {
+  constexpr int kFlight = 16 / BLOCKS;  // parts whose values are on their way at once
+  const int lane = threadIdx.x & 31;
+  const int size = t.group_heads >> 5, group = head >> (4 + size), h = head & (t.group_heads - 1);
+  // (at most 2 * 1024 * 64 rows of 512 floats: in 32 bits)
+  const int first = ((2 * t.column + 1) * lay.groups + group) * lay.heads, step = 2 * lay.groups * lay.heads;
+  auto row = [&](int k) { return first + k * step - (k > 0 ? lay.groups * lay.heads : 0); };  // slots 2c + 1, 2c + 2, 2c + 4, ...
+  const float* lse = reinterpret_cast<const float*>(p.workspace + lay.lse_at());
+  const float* part = reinterpret_cast<const float*>(p.workspace + lay.out_at()) + (block * (lay.heads / 4) + h / 4) * 128 + 4 * lane;
+  float4 v[kFlight][BLOCKS];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+#pragma unroll
+      for (int b = 0; b < BLOCKS; ++b) v[u][b] = ld16_if(k0 + u < t.parts, part + row(k0 + u) * kHead + b * (lay.heads * 32));
+  };
+  load(0);
+  // the parts' statistics: lane = 4 * part + head within eight parts, reduced over the parts
+  const int hh = lane & 3;
+  const bool real = head + hh < p.heads;
+  auto lse_of = [&](int k) { return k < t.parts && real ? lse[row(k) + h + hh] : -INFINITY; };
+  const float sink = p.sink != nullptr && real ? __ldg(p.sink + head + hh) * kLog2e : -INFINITY;
+  float top = sink;
+  bool nan = false;
+  for (int k = lane >> 2; k < t.parts; k += 8) {
+    const float x = lse_of(k);
+    nan |= x != x;
+    top = fmaxf(top, x);
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), o) != 0;
+  }
+  const float shift = nan ? NAN : top == -INFINITY ? 0.f : top;
+  float acc[BLOCKS][4] = {};
+  float sum = lane < 4 ? ex2_approx(sink - shift) : 0.f;  // lane 4k + hh: of head hh, some of the parts
+#pragma unroll 1
+  for (int k0 = 0; k0 < t.parts; k0 += kFlight) {
+    if (k0 > 0) load(k0);
+    float w[(kFlight + 7) / 8];
+#pragma unroll
+    for (int j = 0; j < (kFlight + 7) / 8; ++j) {
+      w[j] = ex2_approx(lse_of(k0 + 8 * j + (lane >> 2)) - shift);
+      if (kFlight >= 8 || (lane >> 2) < kFlight) sum += w[j];
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = __shfl_sync(0xffffffffu, w[u / 8], 4 * (u % 8) + e);
+#pragma unroll
+      for (int b = 0; b < BLOCKS; ++b) {
+        acc[b][0] = fmaf(f[0], v[u][b].x, acc[b][0]), acc[b][1] = fmaf(f[1], v[u][b].y, acc[b][1]);
+        acc[b][2] = fmaf(f[2], v[u][b].z, acc[b][2]), acc[b][3] = fmaf(f[3], v[u][b].w, acc[b][3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float f = __shfl_sync(0xffffffffu, inv, e);
+    if (head + e >= p.heads) break;
+    const int64_t at = t.request * p.out_stride_r + (head + e) * p.out_stride_h + 32 * block + lane;
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b) {
+      const float x = acc[b][e] * f;
+      if (p.out_f32) static_cast<float*>(p.out)[at + 32 * b] = x;
+      else static_cast<uint16_t*>(p.out)[at + 32 * b] = static_cast<uint16_t>(pack_bf16x2(x, 0.f));
+    }
+  }
+  if (p.lse != nullptr && block == 0 && lane < 4 && real)
+    p.lse[t.request * p.lse_stride_r + (head + lane) * p.lse_stride_h] =
+        sum == 0.f ? -INFINITY : (shift + log2f(sum)) * 0.69314718055994531f;
+}
+
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) join_kernel(const DecodeParams p, const __grid_constant__ Layouts layouts) {
   launch_dependents();
   grid_dependency_wait();
   const Task* tasks = reinterpret_cast<const Task*>(p.workspace);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the CTAs that start a cut request, in order
-  static_assert(kMaxCtas <= 4 * kJoinThreads, "a thread looks at four CTAs");
-  bool has[4];
+  const int lane = threadIdx.x & 31;
+  // The CTAs that start a cut request: lane w has those of 32 w .. 32 w + 31, and how many come before.
+  const int ctas = layouts.of[2].ctas;
+  unsigned votes = 0;
+  static_assert(kMaxCtas <= 32 * 32, "a word of votes for each lane");
+#pragma unroll 1
+  for (int w0 = 0; 32 * w0 < ctas; w0 += 5) {  // 160 CTAs at once
+    bool has[5];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = k * kJoinThreads + threadIdx.x;
-    has[k] = c < layouts.of[2].ctas && tasks[c].parts > 0;
-  }
-  unsigned vote[4];
+    for (int k = 0; k < 5; ++k) {
+      const int c = 32 * (w0 + k) + lane;
+      has[k] = c < ctas && tasks[c].parts > 0;
+    }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    vote[k] = __ballot_sync(0xffffffffu, has[k]);
-    if (lane == 0) s_votes[k * (kJoinThreads / 32) + warp] = vote[k];
+    for (int k = 0; k < 5; ++k) {
+      const unsigned vote = __ballot_sync(0xffffffffu, has[k]);
+      if (lane == w0 + k) votes = vote;
+    }
   }
-  __syncthreads();
-  // (lane w: how many of the 32 CTAs of word w are before)
-  int before = __popc(s_votes[lane]);
-  const int own = before;
+  int behind = __popc(votes);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += u;
+    const int u = __shfl_up_sync(0xffffffffu, behind, o);
+    if (lane >= o) behind += u;
   }
-  const int count = __shfl_sync(0xffffffffu, before, 31);
-  before -= own;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int at = __shfl_sync(0xffffffffu, before, k * (kJoinThreads / 32) + warp) + __popc(vote[k] & ((1u << lane) - 1));
-    if (has[k]) s_owner[at] = static_cast<int16_t>(k * kJoinThreads + threadIdx.x);
-  }
-  __syncthreads();
+  const int count = __shfl_sync(0xffffffffu, behind, 31), before = behind - __popc(votes);
   const int heads4 = (p.heads + 3) / 4;
-  const int64_t items = static_cast<int64_t>(count) * heads4 * 16;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + warp; item < items;
-       item += static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32)) {
-    const int cols32 = static_cast<int>(item & 15);
-    const int head = static_cast<int>((item >> 4) % heads4) * 4;
-    const Task t = tasks[s_owner[(item >> 4) / heads4]];
+  const int warps = gridDim.x * (kJoinThreads / 32);
+  // Few: a warp for each 32 columns. Many: 128 columns, so that with the few parts of each there is enough on
+  // its way, and a request's statistics are made less often.
+  const bool many = count * heads4 * 16 > warps;
+  const unsigned per_head4 = many ? 4 : 16, items = count * heads4 * per_head4;
+#pragma unroll 1
+  for (unsigned item = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); item < items; item += warps) {
+    const unsigned rest = item / per_head4, block = item - rest * per_head4;
+    const int n = rest / static_cast<unsigned>(heads4), head4 = rest - n * heads4;
+    // the n-th of those CTAs
+    const int word = __ffs(__ballot_sync(0xffffffffu, before <= n && n < behind)) - 1;
+    const unsigned bits = __shfl_sync(0xffffffffu, votes, word);
+    const int rank = n - __shfl_sync(0xffffffffu, before, word);
+    const int bit = __ffs(__ballot_sync(0xffffffffu, (bits >> lane & 1) && __popc(bits & ((1u << lane) - 1)) == rank)) - 1;
+    const Task t = tasks[32 * word + bit];
     const Layout& lay = layouts.of[t.group_heads >> 5];  // 16, 32, 64 -> 0, 1, 2
-    const int group = head / t.group_heads, h = head % t.group_heads;
-    const float* lse = reinterpret_cast<const float*>(p.workspace + lay.lse_at());
-    const float* part = reinterpret_cast<const float*>(p.workspace + lay.out_at());
-    auto slot = [&](int k) { return k == 0 ? 2 * t.column + 1 : 2 * (t.column + k); };
-    // the parts' statistics: lane = 4 * part + head within eight parts, reduced over the parts
-    const int hh = lane & 3;
-    const bool real = head + hh < p.heads;
-    float top = -INFINITY;
-    bool nan = false;
-    for (int k = lane >> 2; k < t.parts; k += 8) {
-      const float v = real ? lse[lay.row(slot(k), group, h + hh)] : -INFINITY;
-      nan |= v != v;
-      top = fmaxf(top, v);
-    }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), o) != 0;
-    }
-    const float sink = p.sink != nullptr && real ? __ldg(p.sink + head + hh) * kLog2e : -INFINITY;
-    top = fmaxf(top, sink);
-    const float shift = nan ? NAN : top == -INFINITY ? 0.f : top;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    float sum = lane < 4 ? ex2_approx(sink - shift) : 0.f;  // lane 4k + hh: of head hh, parts k, k + 8, ...
-    for (int k0 = 0; k0 < t.parts; k0 += 8) {
-      const int k = k0 + (lane >> 2);
-      const float w = k < t.parts && real ? ex2_approx(lse[lay.row(slot(k), group, h + hh)] - shift) : 0.f;
-      sum += w;
-      float4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (k0 + u < t.parts)
-          v[u] = *(reinterpret_cast<const float4*>(part + lay.block(slot(k0 + u), group, cols32, h / 4)) + lane);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float w0 = __shfl_sync(0xffffffffu, w, 4 * u), w1 = __shfl_sync(0xffffffffu, w, 4 * u + 1);
-        const float w2 = __shfl_sync(0xffffffffu, w, 4 * u + 2), w3 = __shfl_sync(0xffffffffu, w, 4 * u + 3);
-        if (k0 + u < t.parts) {
-          acc[0] = fmaf(w0, v[u].x, acc[0]), acc[1] = fmaf(w1, v[u].y, acc[1]);
-          acc[2] = fmaf(w2, v[u].z, acc[2]), acc[3] = fmaf(w3, v[u].w, acc[3]);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float v = acc[k] * __shfl_sync(0xffffffffu, inv, k);
-      const int64_t at = t.request * p.out_stride_r + (head + k) * p.out_stride_h + 32 * cols32 + lane;
-      if (head + k < p.heads) {
-        if (p.out_f32) static_cast<float*>(p.out)[at] = v;
-        else static_cast<uint16_t*>(p.out)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-      }
-    }
-    if (p.lse != nullptr && cols32 == 0 && lane < 4 && real)
-      p.lse[t.request * p.lse_stride_r + (head + lane) * p.lse_stride_h] =
-          sum == 0.f ? -INFINITY : (shift + log2f(sum)) * 0.69314718055994531f;
+    if (many) join_columns<4>(p, lay, t, 4 * head4, 4 * block);
+    else join_columns<1>(p, lay, t, 4 * head4, block);
   }
 }
 
@@ -1212,7 +1246,7 @@ cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stre
   if (e != cudaSuccess) return e;
   const int64_t cut = p.requests < ctas ? p.requests : ctas;  // requests that can be cut
   const int64_t join_ctas = (cut * ((p.heads + 3) / 4) * 16 + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
-  lc.gridDim = dim3(static_cast<unsigned>(join_ctas < 8 * sm_count ? join_ctas : 8 * sm_count));
+  lc.gridDim = dim3(static_cast<unsigned>(join_ctas < kJoinPerSm * sm_count ? join_ctas : kJoinPerSm * sm_count));
   lc.blockDim = dim3(kJoinThreads);
   lc.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&lc, join_kernel, p, layouts);
