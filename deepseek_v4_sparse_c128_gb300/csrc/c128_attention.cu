@@ -131,9 +131,8 @@ struct DecodeSmem {
   volatile int32_t off[2];       // 1 + the tile whose P in this buffer was made with a reference that is off
   int32_t done_request, done_part;
   int warp_sums[32];
-  int32_t begin, end;            // the column's tiles
-  int32_t first_tile, first_entries;  // of the first request: its tiles before the column's, its entries
-  int32_t first_request;
+  int32_t first_request, first_tile, first_entries;  // where the column's run begins, and that request's entries
+  int32_t end_request, end_tile;  // and the tile behind its end
   Layout lay;                    // read back where results are written, to keep registers free
   int32_t group, group_heads;
   uint32_t tmem;
@@ -305,15 +304,17 @@ __device__ __forceinline__ int entries_of(const DecodeParams& p, int64_t r, unsi
   if (n > p.most) *err |= C128_DEV_BAD_BT_COL;
   return max(min(n, p.most), 0);
 }
-// A request without entries still takes a (masked) tile: its results are written like any other's. The
-// tiles of all requests are less than 2^31.
+// A request without entries still takes a (masked) tile: its results are written like any other's.
 __device__ __forceinline__ int tiles_of(int entries) { return max((entries >> 6) + ((entries & 63) != 0), 1); }
 static_assert(kTile == 64, "tiles_of");
 
-// `total` tiles dealt to `columns` CTA columns, the first `extra` of them one tile more than the rest.
-// A cut that would fall within `snap` tiles of a request's begin or end is moved there: a cut request
-// costs its partial results (2 KB per head and part, written and read again), about what a tile or
-// two take.
+// The requests' tiles one after the other, kRunCost units between two requests, are dealt to the CTA
+// columns in equal runs: storing the results of a request takes a CTA about as long as a tile (2.2 us of
+// 64 heads, a tile 1.9), and every run ends with that. (The units of all requests are less than 2^31.)
+// `total` units go to `columns`, the first `extra` of them one more than the rest. A cut that falls between
+// requests, or would fall within `snap` tiles of a request's begin or end, is made there: a cut request
+// costs its partial results (2 KB per head and part, written and read again), about what a tile or two take.
+constexpr int kRunCost = 1;
 constexpr int kSnap = 2;
 struct Deal {
   int share, extra, snap;
@@ -426,11 +427,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   }
   launch_dependents();
   grid_dependency_wait();  // what the kernels before this one wrote is read from here on
-  // Sum the requests' tiles (each thread a stretch of requests)...
+  // Sum the requests' units (each thread a stretch of requests)...
   const int64_t per = (p.requests + kDecodeThreads - 1) / kDecodeThreads;
   const int64_t r_begin = min(threadIdx.x * per, p.requests), r_end = min(r_begin + per, p.requests);
   int mine = 0;
-  for (int64_t r = r_begin; r < r_end; ++r) mine += tiles_of(entries_of(p, r, &err));
+  for (int64_t r = r_begin; r < r_end; ++r) mine += tiles_of(entries_of(p, r, &err)) + kRunCost;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -447,11 +448,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int u = __shfl_up_sync(0xffffffffu, warps, o);
     if (lane >= o) warps += u;
   }
-  const int total = __shfl_sync(0xffffffffu, warps, 31);
+  const int total = __shfl_sync(0xffffffffu, warps, 31) - kRunCost;  // none behind the last request
+  const int64_t tiles = total - (p.requests - 1) * kRunCost;
   const int base = __shfl_sync(0xffffffffu, warps, warp) - __shfl_sync(0xffffffffu, incl, 31) + incl - mine;
   // ...choose the head groups: smaller ones while there are CTAs for a tile each, since the fewer
   // heads a CTA has, the sooner it has loaded their queries and stored their results...
-  const int size = HEADS == 16 || total <= layouts.of[0].columns ? 0 : HEADS == 32 || total <= layouts.of[1].columns ? 1 : 2;
+  const int size = HEADS == 16 || tiles <= layouts.of[0].columns ? 0 : HEADS == 32 || tiles <= layouts.of[1].columns ? 1 : 2;
   const Layout& lay = layouts.of[size];
   const int group_heads = 16 << size;
   const int column = static_cast<int>(blockIdx.x / static_cast<unsigned>(lay.groups)), group = blockIdx.x - column * lay.groups;
@@ -469,28 +471,28 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     sm.group_heads = group_heads;
     if (idle) *task = Task{0, 0, 0, 0};
   }
-  if (!idle && mine > 0 && base < cut1 && base + mine > cut0) {
+  if (!idle && mine > 0 && base <= cut1 && base + mine > cut0) {
     int at = base;
-    for (int64_t r = r_begin; r < r_end && at < cut1; ++r) {
+    for (int64_t r = r_begin; r < r_end && at <= cut1; ++r) {
       unsigned int ignore = 0;
-      const int entries = entries_of(p, r, &ignore), next = at + tiles_of(entries);
-      const bool holds0 = cut0 >= at && cut0 < next, holds1 = cut1 > at && cut1 <= next;
-      if (holds0) {  // cut0 is this request's begin, or inside it, where it may move
-        const bool back = cut0 - at <= deal.snap, on = !back && next - cut0 <= deal.snap;
-        sm.first_request = static_cast<int32_t>(on ? r + 1 : r);
-        sm.first_tile = back || on ? 0 : cut0 - at;
-        sm.begin = back ? at : on ? next : cut0;
-        sm.first_entries = !on ? entries : r + 1 < p.requests ? entries_of(p, r + 1, &ignore) : 0;
+      const int entries = entries_of(p, r, &ignore), end = at + tiles_of(entries), next = end + kRunCost;
+      const bool holds0 = cut0 >= at && cut0 < next, holds1 = cut1 >= at && cut1 < next;
+      auto on = [&](int cut) { return cut >= end || (cut - at > deal.snap && end - cut <= deal.snap); };
+      auto back = [&](int cut) { return cut < end && cut - at <= deal.snap; };
+      if (holds0) {
+        const bool begins = on(cut0);  // with the next request
+        sm.first_request = static_cast<int32_t>(begins ? r + 1 : r);
+        sm.first_tile = begins || back(cut0) ? 0 : cut0 - at;
+        sm.first_entries = !begins ? entries : r + 1 < p.requests ? entries_of(p, r + 1, &ignore) : 0;
       }
       if (holds1) {
-        const bool on = next - cut1 <= deal.snap && cut1 - at > deal.snap || cut1 == next, back = !on && cut1 - at <= deal.snap;
-        sm.end = on ? next : back ? at : cut1;
         // cut inside: does the request begin in this column? Then this column's task is to join it,
         // with every column that has a cut of it as its begin
-        const bool inside = !on && !back;
-        const bool begins_here = at > cut0 || cut0 - at <= deal.snap;
+        const bool inside = !on(cut1) && !back(cut1);
+        sm.end_request = static_cast<int32_t>(on(cut1) ? r + 1 : r);
+        sm.end_tile = inside ? cut1 - at : 0;
         *task = Task{static_cast<int32_t>(r),
-                     inside && begins_here && group == 0 ? deal.column_of(next - deal.snap - 1) - column + 1 : 0, column, group_heads};
+                     inside && back(cut0) && group == 0 ? deal.column_of(end - deal.snap - 1) - column + 1 : 0, column, group_heads};
       }
       at = next;
     }
@@ -523,7 +525,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // -------------------------------------------------------------------------- walk the run
     int64_t r = sm.first_request;
     int tile = sm.first_tile, n = sm.first_entries;
-    int left = sm.end - sm.begin;
+    const int end_tile = sm.end_tile;
+    const int64_t end_request = sm.end_request;
+    bool ends = r == end_request && tile == end_tile;  // the run, here
     int started = tile;  // the request's tile at which this run takes it up
     const uint32_t bs = static_cast<uint32_t>(p.kv_bs);
     int64_t window = r;      // lanes hold the lengths of requests window .. window + 31
@@ -538,14 +542,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
     };
     int odd = 0;
-    if (left > 0) load_ids();
+    if (!ends) load_ids();
     int lens = window + lane < p.requests ? entries_of(p, window + lane, &ignore) : 0;
-    if (p.stall && blockIdx.x == 0) left = -1;
-    for (int i = 0; left >= 0; ++i, --left) {
+    for (int i = 0; !(p.stall && blockIdx.x == 0); ++i) {
       const int slot = i % kRing;
       if (i >= kRing) warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1);
       TileDesc& d = sm.ring[slot];
-      if (left == 0) {
+      if (ends) {
         if (lane == 0) {
           d.flags = kEnd;
           mbar_arrive(&sm.ring_full[slot]);
@@ -573,7 +576,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const bool last_of_request = tile + 1 == tiles;
       if (lane == 0) {
         d.mask = mask;
-        d.flags = (tile == started ? kFirst : 0) | (last_of_request || left == 1 ? kLast : 0) | odd;
+        d.flags = (tile == started ? kFirst : 0) | (last_of_request || (r == end_request && tile + 1 == end_tile) ? kLast : 0) | odd;
         d.request = static_cast<int32_t>(r);
         d.part = started == 0 && last_of_request ? -1 : 2 * column + (started == 0 ? 1 : 0);
       }
@@ -600,7 +603,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       } else {
         ++tile;
       }
-      if (left > 1) load_ids();
+      ends = r == end_request && tile == end_tile;
+      if (!ends) load_ids();
     }
     if (err) atomicOr(p.err, err);
   } else if (warp < kSoftWarp) {

@@ -115,9 +115,9 @@ int decode(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_bloc
   C128_TRY(check_array(workspace, C128_U8, workspace->shape[0]));
   if (!aligned(workspace->data, 256)) return C128_ERR_ALIGN;
   if (R == 0 || H == 0) return C128_OK;
-  // what the table can hold, in tiles of 64 entries: the kernel counts those in 32 bits
+  // what the table can hold, in tiles of 64 entries: the kernel counts those, and the requests, in 32 bits
   const int64_t most = block_table->shape[1] > kMaxCount / kv_block_size ? kMaxCount : block_table->shape[1] * kv_block_size;
-  if (R * (most / 64 + 1) > kMaxCount) return C128_ERR_ARG;
+  if (R * (most / 64 + 2) > kMaxCount) return C128_ERR_ARG;
   p.most = static_cast<int32_t>(most);
   p.q = static_cast<const uint16_t*>(q->data);
   p.q_stride_r = step(q, 0);

@@ -423,7 +423,7 @@ int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* que
  * Device error bits: C128_DEV_BAD_BT_COL - kv_lens[r] > MB*bs (the entries behind are left out);
  * C128_DEV_BAD_BLOCK - a block id outside [0, NKB) (its entries are left out); C128_DEV_BAD_LENGTH
  * - a negative kv_lens[r] (counts as 0); C128_DEV_TIMEOUT - a wait inside the kernel ran out: some of
- * the results are not there. R * (MB*bs / 64 + 1) < 2^31, else C128_ERR_ARG.
+ * the results are not there. R * (MB*bs / 64 + 2) < 2^31, else C128_ERR_ARG.
  */
 int c128_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
                           const c128_tensor_t* block_table, const c128_tensor_t* kv_lens, float scale,
