@@ -64,7 +64,7 @@ constexpr int kRing = 4;            // tiles the index warp may be ahead
 constexpr float kHigh = 0x1p32f, kLow = 0x1p-32f;  // weights may be up to, and one in the first tile has to be over
 constexpr int kTmemCols = 512, kTmemS = 256;  // O in columns 0..255, two S tiles behind it
 
-enum : int { kFirst = 1, kLast = 2, kEnd = 4, kOdd = 8 };  // of its run of one request's tiles; kOdd: an odd run
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kRunShift = 3 };  // of its stretch of one request's tiles; above, the stretch's number mod 4
 
 struct Task {  // a request that a CTA starts and leaves to the columns behind it, if parts > 0
   int32_t request, parts, column, group_heads;
@@ -119,17 +119,17 @@ struct DecodeSmem {
   TileDesc ring[kRing];
   alignas(16) float ref[kGroup];      // the running references m
   alignas(16) float factor[kGroup];   // what O is rescaled by
-  alignas(16) float inv[kGroup];      // 1 / sum
+  alignas(16) float inv[2][kGroup];   // 1 / sum, of even and odd stretches
   float by_warp[4][kGroup];           // maxima or sums of 16 entries each
   uint64_t ring_full[kRing], ring_free[kRing];
   uint64_t k_full[2][2];              // half of a tile's columns decoded
   uint64_t k_free[2][kQuarters];      // O has taken the quarter (the last: O is done)
   uint64_t s_full[2], s_free[2], p_full[2];
   uint64_t q_full, q_free, o_free, drained;
-  uint64_t inv_full;             // `inv` and `done` of a finished run are there
+  uint64_t inv_full[2];          // `inv` and `done` of a stretch are there
   uint64_t soft;                 // barrier of the softmax warps
   volatile int32_t off[2];       // 1 + the tile whose P in this buffer was made with a reference that is off
-  int32_t done_request, done_part;
+  int32_t done_request[2], done_part[2];
   int warp_sums[32];
   int32_t first_request, first_tile, first_entries;  // where the column's run begins, and that request's entries
   int32_t end_request, end_tile;  // and the tile behind its end
@@ -314,7 +314,7 @@ static_assert(kTile == 64, "tiles_of");
 // `total` units go to `columns`, the first `extra` of them one more than the rest. A cut that falls between
 // requests, or would fall within `snap` tiles of a request's begin or end, is made there: a cut request
 // costs its partial results (2 KB per head and part, written and read again), about what a tile or two take.
-constexpr int kRunCost = 1;
+constexpr int kRunCost = 1;  // not 0: a cut at the end of one request would be in none
 constexpr int kSnap = 2;
 struct Deal {
   int share, extra, snap;
@@ -332,14 +332,14 @@ struct Deal {
   }
 };
 
-// A run's results: O of all heads times 1 / sum, to the output or the workspace. The softmax and the
+// A stretch's results: O of all heads times 1 / sum, to the output or the workspace. The softmax and the
 // decoding warps share the work, four warps (`rank`) to each quarter of the TMEM lanes.
-__device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams& p, int heads, int rank) {
+__device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams& p, int heads, int rank, int odd) {
   int tid = threadIdx.x;
   asm volatile("" : "+r"(tid));  // keeps what follows from being computed ahead, and in registers, in the callers' loops
   const int warp = tid >> 5, lane = tid & 31, heads16 = (heads + 15) & ~15;
-  const int64_t request = sm.done_request;
-  const int part = sm.done_part;
+  const int64_t request = sm.done_request[odd];
+  const int part = sm.done_part[odd];
   tmem_fence_after();
   const int quarter = warp & 3, group0 = sm.group * sm.group_heads;
   const uint32_t o_at = sm.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
@@ -352,7 +352,7 @@ __device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams
     tmem_wait_ld();
 #pragma unroll
     for (int k = 0; k < 16; k += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(&sm.inv[h + k]);
+      const float4 f = *reinterpret_cast<const float4*>(&sm.inv[odd][h + k]);
       o[k] = __float_as_uint(__uint_as_float(o[k]) * f.x), o[k + 1] = __float_as_uint(__uint_as_float(o[k + 1]) * f.y);
       o[k + 2] = __float_as_uint(__uint_as_float(o[k + 2]) * f.z), o[k + 3] = __float_as_uint(__uint_as_float(o[k + 3]) * f.w);
     }
@@ -372,12 +372,12 @@ __device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams
     } else {
       // neighbouring lanes swap halves of a pair of heads, so that each stores two columns of one
       uint16_t* dst = static_cast<uint16_t*>(p.out) + row + (lane & 1) * p.out_stride_h + (col & ~1);
+      const uint32_t halves = lane & 1 ? 0x3276 : 0x5410;
 #pragma unroll
       for (int k = 0; k < 16; k += 2, dst += 2 * p.out_stride_h) {
-        const float mine_ = __uint_as_float(lane & 1 ? o[k + 1] : o[k]);
-        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(lane & 1 ? o[k] : o[k + 1]), 1);
-        if (h + k + (lane & 1) < heads)
-          *reinterpret_cast<uint32_t*>(dst) = lane & 1 ? pack_bf16x2(other, mine_) : pack_bf16x2(mine_, other);
+        const uint32_t two = pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1]));
+        const uint32_t both = __byte_perm(two, __shfl_xor_sync(0xffffffffu, two, 1), halves);
+        if (h + k + (lane & 1) < heads) *reinterpret_cast<uint32_t*>(dst) = both;
       }
     }
   }
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_free, 1);
     mbar_init(&sm.o_free, kSoftWarps + kFillWarps);
-    mbar_init(&sm.inv_full, kSoftWarps);
+    mbar_init(&sm.inv_full[0], kSoftWarps);
+    mbar_init(&sm.inv_full[1], kSoftWarps);
     mbar_init(&sm.soft, kSoftWarps);
     sm.off[0] = sm.off[1] = 0;
     mbar_init(&sm.drained, 2);
@@ -426,12 +427,24 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   launch_dependents();
+  // This CTA's place for each size of head groups: its division is done before there is anything to read.
+  constexpr int kSizes = HEADS == 16 ? 1 : HEADS == 32 ? 2 : 3;
+  int most_columns[kSizes], column_for[kSizes], group_for[kSizes];
+#pragma unroll
+  for (int k = 0; k < kSizes; ++k) {
+    const unsigned groups = layouts.of[k].groups;
+    most_columns[k] = layouts.of[k].columns;
+    column_for[k] = static_cast<int>(blockIdx.x / groups);
+    group_for[k] = static_cast<int>(blockIdx.x - column_for[k] * groups);
+  }
+  const int requests = static_cast<int>(p.requests);
   grid_dependency_wait();  // what the kernels before this one wrote is read from here on
   // Sum the requests' units (each thread a stretch of requests)...
-  const int64_t per = (p.requests + kDecodeThreads - 1) / kDecodeThreads;
-  const int64_t r_begin = min(threadIdx.x * per, p.requests), r_end = min(r_begin + per, p.requests);
-  int mine = 0;
-  for (int64_t r = r_begin; r < r_end; ++r) mine += tiles_of(entries_of(p, r, &err)) + kRunCost;
+  const unsigned per = (static_cast<unsigned>(requests) + kDecodeThreads - 1) / kDecodeThreads;
+  const int r_begin = min(threadIdx.x * per, static_cast<unsigned>(requests)), r_end = min(r_begin + per, static_cast<unsigned>(requests));
+  const int n_begin = r_begin < r_end ? entries_of(p, r_begin, &err) : 0;
+  int mine = r_begin < r_end ? tiles_of(n_begin) + kRunCost : 0;
+  for (int r = r_begin + 1; r < r_end; ++r) mine += tiles_of(entries_of(p, r, &err)) + kRunCost;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -449,49 +462,50 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (lane >= o) warps += u;
   }
   const int total = __shfl_sync(0xffffffffu, warps, 31) - kRunCost;  // none behind the last request
-  const int64_t tiles = total - (p.requests - 1) * kRunCost;
+  const int tiles = total - (requests - 1) * kRunCost;
   const int base = __shfl_sync(0xffffffffu, warps, warp) - __shfl_sync(0xffffffffu, incl, 31) + incl - mine;
   // ...choose the head groups: smaller ones while there are CTAs for a tile each, since the fewer
   // heads a CTA has, the sooner it has loaded their queries and stored their results...
-  const int size = HEADS == 16 || tiles <= layouts.of[0].columns ? 0 : HEADS == 32 || tiles <= layouts.of[1].columns ? 1 : 2;
-  const Layout& lay = layouts.of[size];
+  int size = kSizes - 1, most = most_columns[kSizes - 1], column = column_for[kSizes - 1], group = group_for[kSizes - 1];
+#pragma unroll
+  for (int k = kSizes - 2; k >= 0; --k)
+    if (tiles <= most_columns[k]) size = k, most = most_columns[k], column = column_for[k], group = group_for[k];
   const int group_heads = 16 << size;
-  const int column = static_cast<int>(blockIdx.x / static_cast<unsigned>(lay.groups)), group = blockIdx.x - column * lay.groups;
   const int heads = min(group_heads, p.heads - group * group_heads);
   const int heads16 = (heads + 15) & ~15;
   // ...and find this column's run: its first request, and whether its last one goes on behind it.
-  const int columns = min(lay.columns, total);
+  const int columns = min(most, total);
   const bool idle = column >= columns;
   const Deal deal(total, columns);
   const int cut0 = idle ? 0 : deal.begin(column), cut1 = idle ? 0 : deal.begin(column + 1);
   Task* const task = reinterpret_cast<Task*>(p.workspace) + blockIdx.x;
-  if (threadIdx.x == 0) {
-    sm.lay = lay;
+  if (threadIdx.x == 32 * kMmaWarp) {
+    sm.lay = layouts.of[size];
     sm.group = group;
     sm.group_heads = group_heads;
     if (idle) *task = Task{0, 0, 0, 0};
   }
   if (!idle && mine > 0 && base <= cut1 && base + mine > cut0) {
     int at = base;
-    for (int64_t r = r_begin; r < r_end && at <= cut1; ++r) {
+    for (int r = r_begin; r < r_end && at <= cut1; ++r) {
       unsigned int ignore = 0;
-      const int entries = entries_of(p, r, &ignore), end = at + tiles_of(entries), next = end + kRunCost;
+      const int entries = r == r_begin ? n_begin : entries_of(p, r, &ignore), end = at + tiles_of(entries), next = end + kRunCost;
       const bool holds0 = cut0 >= at && cut0 < next, holds1 = cut1 >= at && cut1 < next;
       auto on = [&](int cut) { return cut >= end || (cut - at > deal.snap && end - cut <= deal.snap); };
       auto back = [&](int cut) { return cut < end && cut - at <= deal.snap; };
       if (holds0) {
         const bool begins = on(cut0);  // with the next request
-        sm.first_request = static_cast<int32_t>(begins ? r + 1 : r);
+        sm.first_request = begins ? r + 1 : r;
         sm.first_tile = begins || back(cut0) ? 0 : cut0 - at;
-        sm.first_entries = !begins ? entries : r + 1 < p.requests ? entries_of(p, r + 1, &ignore) : 0;
+        sm.first_entries = !begins ? entries : r + 1 < requests ? entries_of(p, r + 1, &ignore) : 0;
       }
       if (holds1) {
         // cut inside: does the request begin in this column? Then this column's task is to join it,
         // with every column that has a cut of it as its begin
         const bool inside = !on(cut1) && !back(cut1);
-        sm.end_request = static_cast<int32_t>(on(cut1) ? r + 1 : r);
+        sm.end_request = on(cut1) ? r + 1 : r;
         sm.end_tile = inside ? cut1 - at : 0;
-        *task = Task{static_cast<int32_t>(r),
+        *task = Task{r,
                      inside && back(cut0) && group == 0 ? deal.column_of(end - deal.snap - 1) - column + 1 : 0, column, group_heads};
       }
       at = next;
@@ -529,7 +543,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int64_t end_request = sm.end_request;
     bool ends = r == end_request && tile == end_tile;  // the run, here
     int started = tile;  // the request's tile at which this run takes it up
-    const uint32_t bs = static_cast<uint32_t>(p.kv_bs);
+    const Divisor bs = p.kv_div;
     int64_t window = r;      // lanes hold the lengths of requests window .. window + 31
     unsigned int ignore = 0;
     int id[2];
@@ -538,10 +552,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t key = static_cast<uint32_t>(tile) * kTile + 32 * h + lane;
-        id[h] = key < static_cast<uint32_t>(n) ? __ldg(p.table + r * p.table_stride + key / bs) : -1;
+        id[h] = key < static_cast<uint32_t>(n) ? __ldg(p.table + r * p.table_stride + divide(key, bs)) : -1;
       }
     };
-    int odd = 0;
+    int stretch = 0;
     if (!ends) load_ids();
     int lens = window + lane < p.requests ? entries_of(p, window + lane, &ignore) : 0;
     for (int i = 0; !(p.stall && blockIdx.x == 0); ++i) {
@@ -565,7 +579,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const bool in = key < static_cast<uint32_t>(n);
         const bool ok = in && id[h] >= 0 && id[h] < p.nkb;
         if (in && !ok) err |= C128_DEV_BAD_BLOCK;
-        const uint32_t off = key % bs;
+        const uint32_t off = key - divide(key, bs) * bs.value;
         const uint8_t* blk = p.kc + static_cast<int64_t>(ok ? id[h] : 0) * p.kc_stride0;
         from[h] = ok ? blk + static_cast<int64_t>(off) * kTokenStride : nullptr;
         sc[h] = blk + p.kv_bs * kTokenStride + static_cast<int64_t>(off) * kScaleDim;
@@ -576,7 +590,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const bool last_of_request = tile + 1 == tiles;
       if (lane == 0) {
         d.mask = mask;
-        d.flags = (tile == started ? kFirst : 0) | (last_of_request || (r == end_request && tile + 1 == end_tile) ? kLast : 0) | odd;
+        d.flags = (tile == started ? kFirst : 0) | (last_of_request || (r == end_request && tile + 1 == end_tile) ? kLast : 0) | (stretch & 3) << kRunShift;
         d.request = static_cast<int32_t>(r);
         d.part = started == 0 && last_of_request ? -1 : 2 * column + (started == 0 ? 1 : 0);
       }
@@ -592,7 +606,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
       }
       if (last_of_request) {
-        odd ^= kOdd;
+        ++stretch;
         ++r;
         tile = started = 0;
         if (r - window >= 32) {
@@ -637,12 +651,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ring_free[slot]);
     };
-    // the results of the run that tile i ended
-    auto results = [&](int i, int run) {
-      // O being done, the runs before this one are finished with, and the parity means this run
+    // the results of the stretch that tile i ended
+    auto results = [&](int i, int flags_i) {
+      const int stretch = flags_i >> kRunShift;
       warp_wait(&sm.k_free[i & 1][kQuarters - 1], (i / 2) & 1);
-      warp_wait(&sm.inv_full, run & kOdd ? 1 : 0);
-      if (!*abort_flag) store_results(sm, p, heads, 2 + warp / 4);
+      // (that of the stretch after next needs a tile of these warps, so the parity means this one)
+      warp_wait(&sm.inv_full[stretch & 1], stretch >> 1 & 1);
+      if (!*abort_flag) store_results(sm, p, heads, 2 + warp / 4, stretch & 1);
     };
     fetch(0);
     load_scales();
@@ -1000,9 +1015,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           if (lane < 4) sm.by_warp[w][h0 + 8 * g + e] = sum;
         }
       }
-      // O is done; with it the last run's results have been stored, and `inv` is free
-      warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
       soft_sync();
+      // 1 / sum while the last product runs. (The results of the stretch before the last have been stored, since
+      // the last one's O was done when these warps stored it.)
+      const int stretch = flags >> kRunShift, odd = stretch & 1;
       if (lead && w < 2 && 32 * w + lane < heads) {
         const int h = 32 * w + lane;
         const int64_t head = group0 + h;
@@ -1015,18 +1031,19 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           f = ex2_approx(ref - to);
           sum = (own == 0.f ? 0.f : own * f) + ex2_approx(s - to);
         }
-        sm.inv[h] = own == 0.f ? 0.f : f / sum;
+        sm.inv[odd][h] = own == 0.f ? 0.f : f / sum;
         const float lse2 = sum == 0.f ? -INFINITY : to + log2f(sum);
         if (!whole)
           reinterpret_cast<float*>(p.workspace + sm.lay.lse_at())[sm.lay.row(part, sm.group, h)] = lse2;
         else if (p.lse != nullptr)
           p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
       }
-      if (lead && w == 0 && lane == 0) sm.done_request = request, sm.done_part = part;
+      if (lead && w == 0 && lane == 0) sm.done_request[odd] = request, sm.done_part[odd] = part;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.inv_full);
-      soft_sync();
-      if (!*abort_flag) store_results(sm, p, heads, lead ? 0 : 1);
+      if (lane == 0) mbar_arrive(&sm.inv_full[odd]);
+      warp_wait(&sm.inv_full[odd], stretch >> 1 & 1);
+      warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
+      if (!*abort_flag) store_results(sm, p, heads, lead ? 0 : 1, odd);
     }
   }
   tmem_fence_before();

@@ -19,6 +19,8 @@ struct Divisor {
       if (value == 1u << i) shift = i;
   }
 };
+// x / d, with a shift where d is a power of two (shift >= 0): block sizes and ratios mostly are.
+__device__ __forceinline__ uint32_t divide(uint32_t x, const Divisor d) { return d.shift >= 0 ? x >> d.shift : x / d.value; }
 
 struct ExtendParams {
   const int32_t* seq_lens;
@@ -61,8 +63,9 @@ struct DecodeParams {
   int64_t q_stride_r, q_stride_h;
   const uint8_t* kc;
   int64_t nkb, kv_bs, kc_stride0;
+  Divisor kv_div;                // kv_bs
   const int32_t* table;
-  int64_t requests, columns, table_stride;
+  int64_t requests, table_stride;
   int32_t most;                  // entries that a row of the table holds, at most 2^31 - 1
   const int32_t* kv_lens;
   int32_t heads;

@@ -125,10 +125,10 @@ int decode(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_bloc
   p.kc = static_cast<const uint8_t*>(k_cache->data);
   p.nkb = k_cache->shape[0];
   p.kv_bs = kv_block_size;
+  p.kv_div = c128::Divisor(kv_block_size);
   p.kc_stride0 = step(k_cache, 0);
   p.table = static_cast<const int32_t*>(block_table->data);
   p.requests = R;
-  p.columns = block_table->shape[1];
   p.kv_lens = static_cast<const int32_t*>(kv_lens->data);
   p.heads = static_cast<int32_t>(H);
   p.scale = scale;

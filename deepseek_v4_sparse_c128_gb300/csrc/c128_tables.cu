@@ -48,9 +48,6 @@ __device__ __forceinline__ uint32_t block_exclusive_sum(uint32_t v, uint32_t* wa
   return add_clipped(warp > 0 ? warps_before : 0, lane > 0 ? before : 0);
 }
 
-// x / d, with a shift where d is a power of two (shift >= 0): block sizes and ratios mostly are.
-__device__ __forceinline__ uint32_t divide(uint32_t x, const Divisor d) { return d.shift >= 0 ? x >> d.shift : x / d.value; }
-
 __device__ __forceinline__ void wait_for_inputs() {
   asm volatile("griddepcontrol.launch_dependents;" :::);
   asm volatile("griddepcontrol.wait;" ::: "memory");
