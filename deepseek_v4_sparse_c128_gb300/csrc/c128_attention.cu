@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (err) atomicOr(p.err, err);
   } else if (warp < kSoftWarp) {
     // ------------------------------------------------------------------------ decode the entries
+    // (Results are stored in two places of this code, not three, for the sake of the instruction cache.)
     // Four threads per entry; thread `sub` of an entry takes the 16 bytes sub, sub + 4, ...: of the
     // codes a quarter of each 64-column chunk, so load j belongs to scale j.
     const int key = 8 * warp + (lane >> 2), sub = lane & 3;
@@ -725,14 +726,18 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       publish(1);
     }
-    if (done2 & kLast) results(i - 2, done2);
-    if (done1 & kLast) results(i - 1, done1);
+#pragma unroll 1
+    for (int k = 2; k > 0; --k) {  // the last two tiles'
+      if (done2 & kLast) results(i - k, done2);
+      done2 = done1;
+    }
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // ------------------------------------------------------------------------ issue the products
     // One elected thread in one branch: the compiler then keeps descriptors in uniform registers, and
     // a product issues faster than it runs (23 to 32 cycles for S, 39 to 48 for O, bound by the reads of
     // the operands from shared memory). Behind a test of the lane each took 66 to 75 cycles to issue.
-    // The buffer is a constant of the lambdas for the same reason.
+    // The loops are short, and the same for both buffers: five warps with five programs share a scheduler's
+    // instruction cache, and with this code unrolled and twice a tile took 5 % longer.
     if (elect_one()) {
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (decode_wait(bar, parity, abort_flag)) return true;
@@ -746,10 +751,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const uint32_t desc = mma_desc(kTile, heads16, false);
         const int boxes = heads16 / kBoxHeads;
         const uint32_t box_bytes = static_cast<uint32_t>(min(p.heads, kBoxHeads)) * 128;
-        auto half_of_s = [&](auto buffer, auto which) {
-          constexpr int buf = decltype(buffer)::value, half = decltype(which)::value;
+        auto half_of_s = [&](int buf, auto which) {
+          constexpr int half = decltype(which)::value;
           tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < kChunks / 2; ++k) {
             constexpr int c0 = half * (kChunks / 2);
 #pragma unroll
@@ -783,9 +788,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             loading = false;
           }
           if (!wait(&sm.k_full[buf][0], (i / 2) & 1)) break;
-          if (buf) half_of_s(Const<1>(), Const<0>()); else half_of_s(Const<0>(), Const<0>());
+          half_of_s(buf, Const<0>());
           if (!wait(&sm.k_full[buf][1], (i / 2) & 1)) break;
-          if (buf) half_of_s(Const<1>(), Const<1>()); else half_of_s(Const<0>(), Const<1>());
+          half_of_s(buf, Const<1>());
           mma_commit(&sm.s_full[buf]);
           if (flags & kLast) mma_commit(&sm.q_free);
         }
@@ -793,8 +798,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       } else {
         const uint32_t kv_at = desc_low(k_at, kChunkBytes), p_at = desc_low(smem_addr(sm.p[0]), 16);
         const uint32_t desc = mma_desc(128, heads16, true);
-        auto product_o = [&](auto buffer, bool first) {
-          constexpr int buf = decltype(buffer)::value;
+        auto product_o = [&](int buf, bool first) {
           tmem_fence_after();
 #pragma unroll
           for (int mt = 0; mt < kQuarters; ++mt) {
@@ -823,7 +827,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           }
           // the results of the run before are out of O
           if ((flags & kFirst) && ++seg > 0 && !wait(&sm.o_free, (seg - 1) & 1)) break;
-          if (buf) product_o(Const<1>(), flags & kFirst); else product_o(Const<0>(), flags & kFirst);
+          product_o(buf, flags & kFirst);
         }
       }
       mma_commit(&sm.drained);
