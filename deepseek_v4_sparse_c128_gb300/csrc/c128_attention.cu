@@ -521,10 +521,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // and no result is stored. So no lane or warp leaves a path that others count on it for, without asking
   // all lanes after every wait whether to go on (that took 6 % of a tile's time).
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!decode_wait(bar, parity, abort_flag)) {
-      *abort_flag = 1;
-      atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
-    }
+    if (!decode_wait(bar, parity, abort_flag)) *abort_flag = 1;
     __syncwarp();
   };
   auto tile_flags = [&](int i) {
@@ -742,7 +739,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (decode_wait(bar, parity, abort_flag)) return true;
         *abort_flag = 1;
-        atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
         return false;
       };
       const uint32_t k_at = smem_addr(sm.k[0]);
@@ -1052,6 +1048,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   }
   tmem_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
   if (warp == kMmaWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
