@@ -708,18 +708,18 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         store(j, o[at(j)]);
       }
       publish(0);
+      await_room(3);
+#pragma unroll
+      for (int j = 7; j < 9; ++j) {  // the rope columns are bf16 already; the sooner the next ones are on their way, the better
+        sts16((dst_rope + buf * kTileBytes) ^ (64u * (j - 7)), raw[j].x, raw[j].y, raw[j].z, raw[j].w);
+        load(j);
+      }
 #pragma unroll
       for (int j = 4; j < 4 + kAhead; ++j) decode(j, o[at(j)]);
-      await_room(3);
 #pragma unroll
       for (int j = 4; j < 7; ++j) {
         if (j >= 4 + kAhead) decode(j, o[at(j)]);
         store(j, o[at(j)]);
-      }
-#pragma unroll
-      for (int j = 7; j < 9; ++j) {  // the rope columns are bf16 already
-        sts16((dst_rope + buf * kTileBytes) ^ (64u * (j - 7)), raw[j].x, raw[j].y, raw[j].z, raw[j].w);
-        load(j);
       }
       publish(1);
     }
