@@ -4,7 +4,8 @@
 //   S^T = K Q^T            per tile of 64 entries: M = 64 entries, N = heads, K = 512
 //   P^T = exp2(c S^T - m)  c = scale * log2(e), m a running reference per head
 //   O^T += K^T P^T         M = 128 columns (4 times), N = heads, K = 64 entries
-//   out = O / sum P
+//   L += 1 P^T             the sums of P as the products see it, rounded to bf16: M = 64 rows of ones
+//   out = O / L
 //
 // An entry is key and value, so a tile is decoded once, to bf16 in shared memory (exact: an e4m3 code
 // has 4 significant bits and its scale is a power of two), and both products read it from there as
@@ -14,6 +15,10 @@
 // softmax next to nothing to exchange: a thread holds two entries and some heads, and keeps its own
 // sums to the end. Heads are dealt out in groups of 64; a group decodes the cache for itself (the
 // second group's reads hit L2).
+//
+// P is rounded to bf16 (2^-9), and O is divided by the sums of the rounded weights: then a weight's
+// rounding is felt only against the other entries', not at all with a single one. lse is of the exact
+// sums, in fp32. (Two sums in the softmax warps' registers took 10 % longer than the product with ones.)
 //
 // The running reference m need not be the maximum: P, its sums and O are floating point, so a common
 // factor costs no precision. So m is 0 where that does, that is where every head has a score within
@@ -62,7 +67,7 @@ constexpr int kSoftWarp = kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexW
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
 constexpr int kRing = 4;            // tiles the index warp may be ahead
 constexpr float kHigh = 0x1p32f, kLow = 0x1p-32f;  // weights may be up to, and one in the first tile has to be over
-constexpr int kTmemCols = 512, kTmemS = 256;  // O in columns 0..255, two S tiles behind it
+constexpr int kTmemCols = 512, kTmemS = 256, kTmemL = 384;  // O in columns 0..255, two S tiles and L behind it
 
 enum : int { kFirst = 1, kLast = 2, kEnd = 4, kRunShift = 3 };  // of its stretch of one request's tiles; above, the stretch's number mod 4
 
@@ -116,10 +121,12 @@ struct DecodeSmem {
   alignas(1024) uint8_t q[kGroup * kHead * 2];
   alignas(1024) uint8_t k[2][kTileBytes];
   alignas(1024) uint8_t p[2][kGroup * kTile * 2];
+  alignas(128) uint32_t ones[512];    // 64 x 16 of bf16, in any order
   TileDesc ring[kRing];
   alignas(16) float ref[kGroup];      // the running references m
   alignas(16) float factor[kGroup];   // what O is rescaled by
-  alignas(16) float inv[2][kGroup];   // 1 / sum, of even and odd stretches
+  alignas(16) float sums[kGroup];     // L
+  alignas(16) float inv[2][kGroup];   // 1 / L (with a sink: the entries' share / L), of even and odd stretches
   float by_warp[4][kGroup];           // maxima or sums of 16 entries each
   uint64_t ring_full[kRing], ring_free[kRing];
   uint64_t k_full[2][2];              // half of a tile's columns decoded
@@ -180,11 +187,18 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
   return e != 0;
 }
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t desc, bool add) {
+// An unswizzled K-major operand of 16 columns: 8 rows of 16 bytes, the same 128 bytes on for the other 8 columns, 256
+// bytes on for the next 8 rows.
+__device__ __forceinline__ uint64_t desc_plain(uint32_t addr) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"((addr & 0x3ffff) >> 4 | 128u >> 4 << 16), "r"(256u >> 4 | 1u << 14));
+  return d;
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(desc64(a_low)), "l"(desc64(b_low)), "r"(desc),
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(desc),
       "r"(static_cast<uint32_t>(add))
       : "memory");
 }
@@ -420,6 +434,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x < 512) sm.ones[threadIdx.x] = 0x3f803f80u;
+  async_proxy_fence();  // (to the products, behind the barriers below)
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)),
                  "n"(kTmemCols)
@@ -757,7 +773,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             for (int ks = 0; ks < 4; ++ks) {
               const uint32_t a = ks_at + ((buf * kTileBytes + (c0 + k) * kChunkBytes + ks * 32) >> 4);
               const uint32_t b = q_at + (((c0 + k) * (kGroup * 128) + ks * 32) >> 4);
-              mma(tmem + kTmemS + buf * kGroup, a, b, desc, half + k + ks > 0);
+              mma(tmem + kTmemS + buf * kGroup, desc64(a), desc64(b), desc, half + k + ks > 0);
             }
           }
         };
@@ -793,7 +809,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         if (loading) decode_wait(&sm.q_full, seg & 1, nullptr);  // nothing may be in flight when the CTA ends
       } else {
         const uint32_t kv_at = desc_low(k_at, kChunkBytes), p_at = desc_low(smem_addr(sm.p[0]), 16);
-        const uint32_t desc = mma_desc(128, heads16, true);
+        const uint32_t desc = mma_desc(128, heads16, true), desc_ones = mma_desc(64, heads16, false) | 1u << 16;  // (of P the other way around)
+        const uint64_t ones = desc_plain(smem_addr(sm.ones));
         auto product_o = [&](int buf, bool first) {
           tmem_fence_after();
 #pragma unroll
@@ -802,7 +819,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             for (int ks = 0; ks < kTile / 16; ++ks) {
               const uint32_t a = kv_at + ((buf * kTileBytes + 2 * mt * kChunkBytes + ks * 2048) >> 4);
               const uint32_t b = p_at + ((buf * (kGroup * kTile * 2) + ks * 2048) >> 4);
-              mma(tmem + mt * kGroup, a, b, desc, !first || ks > 0);
+              mma(tmem + mt * kGroup, desc64(a), desc64(b), desc, !first || ks > 0);
+            }
+            if (mt == kQuarters - 1) {
+#pragma unroll
+                  for (int ks = 0; ks < kTile / 16; ++ks)
+                mma(tmem + kTmemL, ones, desc64(p_at + ((buf * (kGroup * kTile * 2) + ks * 2048) >> 4)), desc_ones, !first || ks > 0);
             }
             mma_commit(&sm.k_free[buf][mt]);
           }
@@ -974,11 +996,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         if (!first) {
           tmem_fence_after();
 #pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int mt = 0; mt < 5; ++mt) {  // O and L
 #pragma unroll 1
             for (int h = lead ? 0 : 16; h < heads16; h += 32) {
               uint32_t o[16];
-              const uint32_t at = tmem + lanes + mt * kGroup + h;
+              const uint32_t at = tmem + lanes + (mt < 4 ? mt * kGroup : kTmemL) + h;
               tmem_ld_32x16(at, o);
               tmem_wait_ld();
 #pragma unroll
@@ -1016,22 +1038,23 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
       }
       soft_sync();
-      // 1 / sum while the last product runs. (The results of the stretch before the last have been stored, since
-      // the last one's O was done when these warps stored it.)
+      // lse, while the last product runs, and what the entries have of all weight (the sink's too) into `inv`: the
+      // stretch before the last, which had this one, is stored, since the last one's O was done when these warps stored it
       const int stretch = flags >> kRunShift, odd = stretch & 1;
       if (lead && w < 2 && 32 * w + lane < heads) {
         const int h = 32 * w + lane;
         const int64_t head = group0 + h;
         const float own = (sm.by_warp[0][h] + sm.by_warp[1][h]) + (sm.by_warp[2][h] + sm.by_warp[3][h]), ref = zero ? 0.f : sm.ref[h];
-        float sum = own, to = ref, f = 1.f;
+        float sum = own, to = ref, share = own == 0.f ? 0.f : 1.f;
         if (whole && p.sink != nullptr) {  // one more score, with a value of zero
           const float s = __ldg(p.sink + head) * kLog2e;
           // (with nothing else in the sum, or if it is far above the rest, the result is 0 and lse the sink's)
           to = own == 0.f ? (s == -INFINITY ? 0.f : s) : fmaxf(ref, s);
-          f = ex2_approx(ref - to);
-          sum = (own == 0.f ? 0.f : own * f) + ex2_approx(s - to);
+          const float entries = own == 0.f ? 0.f : own * ex2_approx(ref - to);
+          sum = entries + ex2_approx(s - to);
+          if (own != 0.f) share = entries / sum;
         }
-        sm.inv[odd][h] = own == 0.f ? 0.f : f / sum;
+        sm.inv[odd][h] = share;
         const float lse2 = sum == 0.f ? -INFINITY : to + log2f(sum);
         if (!whole)
           reinterpret_cast<float*>(p.workspace + sm.lay.lse_at())[sm.lay.row(part, sm.group, h)] = lse2;
@@ -1039,10 +1062,25 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
       }
       if (lead && w == 0 && lane == 0) sm.done_request[odd] = request, sm.done_part[odd] = part;
+      warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
+      if (lead && w < 2 && 32 * w < heads16) {
+        tmem_fence_after();
+#pragma unroll 1
+        for (int h = 32 * w; h < min(heads16, 32 * w + 32); h += 16) {  // every row of L is the same
+          uint32_t x[16];
+          tmem_ld_32x16(tmem + lanes + kTmemL + h, x);
+          tmem_wait_ld();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) *reinterpret_cast<uint4*>(&sm.sums[h + k]) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+          }
+        }
+        __syncwarp();
+        if (32 * w + lane < heads && sm.inv[odd][32 * w + lane] != 0.f) sm.inv[odd][32 * w + lane] /= sm.sums[32 * w + lane];
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.inv_full[odd]);
       warp_wait(&sm.inv_full[odd], stretch >> 1 & 1);
-      warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
       if (!*abort_flag) store_results(sm, p, heads, lead ? 0 : 1, odd);
     }
   }

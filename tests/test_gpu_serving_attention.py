@@ -204,6 +204,30 @@ def test_decode_bad_pages_and_lengths(binding):
     _check(c, out, lse)
 
 
+@pytest.mark.parametrize("heads", [5, 32, 100])
+@pytest.mark.parametrize("sink", [False, True])
+def test_decode_of_one_entry_is_that_entry(binding, heads, sink):
+    """The weights' rounding cancels: with one entry the result is the entry, to the bit, and without rounding in lse;
+    with a sink it is the entry times its share, rounded once."""
+    rng = np.random.default_rng([18, heads])
+    c = _case(rng, [1] * 40, heads, 64, size=4.0, sink=sink)
+    out, lse = _run(binding, c)
+    out, lse, q = out.double().cpu().numpy(), lse.double().cpu().numpy(), c["q"].double().cpu().numpy()
+    for r in range(40):
+        k = entries(c["cache"], 64, c["table"][r], 1)[0]
+        s = c["scale"] * (q[r] @ k)
+        if not sink:
+            assert np.array_equal(out[r], np.broadcast_to(k, out[r].shape))
+            # the score: 512 products in fp32, then log2 and back
+            assert (np.abs(lse[r] - s) <= 600 * HALF_F32 * (c["scale"] * (np.abs(q[r]) @ np.abs(k)) + 1)).all()
+        else:
+            share = 1 / (1 + np.exp(c["sink"].astype(np.float64) - s))
+            # half a step of bf16, and the score's error and three operations of 2^-22 in the share
+            off = 600 * HALF_F32 * (c["scale"] * (np.abs(q[r]) @ np.abs(k)) + 1) + 2.0 ** -20
+            want = share[:, None] * k[None]
+            assert (np.abs(out[r] - want) <= np.abs(want) * (HALF_BF16 * (1 + 2.0 ** -8) + off[:, None])).all()
+
+
 def test_decode_growing_scores(binding):
     """Scores that climb from tile to tile by far more than an exponential holds, and ones that fall."""
     import torch
