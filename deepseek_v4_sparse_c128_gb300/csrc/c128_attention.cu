@@ -65,6 +65,8 @@ constexpr int kAhead = 3;           // of a tile's 7 chunks of codes, decoded be
 constexpr int kSoftWarps = 8;
 constexpr int kSoftWarp = kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
+constexpr int kStaged = 2;          // of the 9 16-byte pieces that a decoding thread has on their way: the rope values
+constexpr int kStageBytes = kFillWarps * 32 * 16;
 constexpr int kRing = 4;            // tiles the index warp may be ahead
 constexpr float kHigh = 0x1p32f, kLow = 0x1p-32f;  // weights may be up to, and one in the first tile has to be over
 constexpr int kTmemCols = 512, kTmemS = 256, kTmemL = 384;  // O in columns 0..255, two S tiles and L behind it
@@ -122,6 +124,7 @@ struct DecodeSmem {
   alignas(1024) uint8_t k[2][kTileBytes];
   alignas(1024) uint8_t p[2][kGroup * kTile * 2];
   alignas(128) uint32_t ones[512];    // 64 x 16 of bf16, in any order
+  alignas(16) uint8_t stage[kStaged][kStageBytes];
   TileDesc ring[kRing];
   alignas(16) float ref[kGroup];      // the running references m
   alignas(16) float factor[kGroup];   // what O is rescaled by
@@ -644,14 +647,40 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const uint32_t row = smem_addr(sm.k[0]) + key * 128, swz = static_cast<uint32_t>(key & 7) << 4;
     const uint32_t dst0 = row + ((32u * sub) ^ swz), dst1 = row + ((32u * sub + 16u) ^ swz);
     const uint32_t dst_rope = row + 7 * kChunkBytes + ((16u * sub) ^ swz);
-    uint4 raw[9];  // loads on their way: a tile ahead
+    // Loads on their way, a tile ahead: codes to registers; rope values, which are only moved, by way of shared
+    // memory, as far as there is room (with all nine in registers, which spilled, a tile took 5 % longer; with all nine
+    // in shared memory, where fewer heads leave room, 3 %).
+    constexpr int kInRegs = 9 - kStaged;
+    uint4 raw[kInRegs];
+    const uint32_t stage = smem_addr(sm.stage[0]) + threadIdx.x * 16;
+    auto stage_at = [&](int j) { return stage + (j - kInRegs) * kStageBytes; };
     uint2 sc;
     const uint8_t* src = nullptr;
     const uint8_t* ssrc = nullptr;
     int flags = kEnd;
     auto load = [&](int j) {
-      if (src == nullptr) raw[j] = make_uint4(0, 0, 0, 0);
-      else raw[j] = ALIGN16 ? ld16(src + 64 * j) : ld8x2(src + 64 * j);
+      if (j >= kInRegs) {
+        const uint8_t* from = src == nullptr ? p.workspace : src + 64 * j;
+        const uint32_t bytes = src == nullptr ? 0 : ALIGN16 ? 16 : 8;  // 0: zeros, and nothing is read
+        if constexpr (ALIGN16) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(stage_at(j)), "l"(from), "r"(bytes) : "memory");
+        } else {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(stage_at(j)), "l"(from), "r"(bytes) : "memory");
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(stage_at(j) + 8), "l"(from + (bytes ? 8 : 0)), "r"(bytes) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      } else if (src == nullptr) {
+        raw[j] = make_uint4(0, 0, 0, 0);
+      } else {
+        raw[j] = ALIGN16 ? ld16(src + 64 * j) : ld8x2(src + 64 * j);
+      }
+    };
+    auto take = [&](int j) {
+      if (j < kInRegs) return raw[j];
+      uint4 v;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStaged - 1) : "memory");  // the oldest, of this thread's own
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(stage_at(j)) : "memory");
+      return v;
     };
     auto load_scales = [&] { sc = src == nullptr ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : ld8(ssrc); };
     // take tile i's addresses out of the ring
@@ -675,8 +704,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     };
     fetch(0);
     load_scales();
+    // in the order of their use, as the loop has them
 #pragma unroll
-    for (int j = 0; j < 9; ++j) load(j);
+    for (int j = 0; j < 4; ++j) load(j);
+    load(7);
+    load(8);
+#pragma unroll
+    for (int j = 4; j < 7; ++j) load(j);
     int done1 = 0, done2 = 0;  // flags of the tile before this one, and of the one before it
     int i = 0;
     for (; !(flags & kEnd); ++i) {
@@ -688,7 +722,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const uint2 now = sc;
       auto decode = [&](int j, uint32_t (&o)[8]) {
         const float scale = scale_of(((j < 4 ? now.x : now.y) >> (8 * (j & 3))) & 0xffu);
-        const uint4 r = raw[j];
+        const uint4 r = take(j);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -727,7 +761,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       await_room(3);
 #pragma unroll
       for (int j = 7; j < 9; ++j) {  // the rope columns are bf16 already; the sooner the next ones are on their way, the better
-        sts16((dst_rope + buf * kTileBytes) ^ (64u * (j - 7)), raw[j].x, raw[j].y, raw[j].z, raw[j].w);
+        const uint4 r = take(j);
+        sts16((dst_rope + buf * kTileBytes) ^ (64u * (j - 7)), r.x, r.y, r.z, r.w);
         load(j);
       }
 #pragma unroll
@@ -739,6 +774,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       publish(1);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may be in flight when the CTA ends
 #pragma unroll 1
     for (int k = 2; k > 0; --k) {  // the last two tiles'
       if (done2 & kLast) results(i - k, done2);

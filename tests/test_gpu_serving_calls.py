@@ -161,3 +161,23 @@ def test_tables_into_views_and_free_lists_behind_an_offset(binding):
     assert binding.device_errors(clear=True) == want[3]
     assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(h.cpu().numpy(), want[1]) and int(k) == want[2]
     assert bool((wide[:, :2] == -7).all()) and bool((wide[:, 2 + MB:] == -7).all())
+
+
+def test_decode_over_an_empty_cache(binding):
+    """No block at all: zeros and -inf (the sink), and a request that claims entries has them left out."""
+    import torch
+    q = torch.ones(3, 20, HEAD, dtype=torch.bfloat16, device="cuda")
+    cache = torch.empty(0, 64, 584, dtype=torch.uint8, device="cuda")
+    table = torch.zeros(3, 4, dtype=torch.int32, device="cuda")
+    sink = torch.linspace(-3, 3, 20, device="cuda")
+    for lens, bits in (([0, 0, 0], 0), ([0, 200, 64], 4)):
+        for with_sink in (None, sink):
+            out, lse = torch.full_like(q, 7), torch.full((3, 20), 7.0, device="cuda")
+            binding.decode_attention(q, cache, 64, table, _cuda(np.array(lens, np.int32)), 0.05, out, lse=lse, sink=with_sink)
+            assert binding.device_errors(clear=True) == bits
+            assert bool((out == 0).all())
+            if with_sink is None:
+                assert bool((lse == -np.inf).all())
+            else:
+                # log2 and back of the sink: a few roundings of a value of 3
+                assert bool(((lse - sink).abs() <= 2.0 ** -20).all())
