@@ -3,14 +3,14 @@
 // (or tokens) that finds each one's request in the sums.
 //
 // Decode steps make a few kilobytes of either, so what counts there is the number of dependent trips
-// to memory: one launch, in which every CTA sums the requests for itself (2048 per round, a few KB
+// to memory: one launch, in which every CTA sums the requests for itself (thousands per round, a few KB
 // that all CTAs read from L2) instead of a scan kernel and a second one behind it, then looks its
 // own blocks or tokens up in shared memory. Nothing is accumulated across CTAs: no atomics but the
 // error bits, and no scratch.
 //
-// Measured, device time per call back to back: tables of 256 requests that each grow by one token 2.2 us, of
-// 16 requests that get all blocks of up to a million tokens (1.1 M blocks, 9 MB) 6.3 us; maps of 256 rows
-// 2.7 us, of 32 thousand tokens 3.3, of 215 thousand (6 MB) 4.4. A launch that does nothing takes about 2 us
+// Measured, device time per call back to back: tables of 256 requests that each grow by one token 2.1 us, of
+// 16 requests that get all blocks of up to a million tokens (1.1 M blocks, 9 MB) 4.0 us; maps of 256 rows
+// 2.4 us, of 32 thousand tokens 2.6, of 215 thousand (6 MB) 4.1. A launch that does nothing takes about 2 us
 // this way, and what is left is the chain of loads, sum, search and loads. (Sums in 64 bits, divisions
 // and several tokens to a thread took 7 to 8 us for the maps.)
 #include <cuda_runtime.h>
@@ -22,8 +22,6 @@
 
 namespace c128 {
 namespace {
-
-constexpr int kChunk = 2048;  // requests per round of the prefix sum
 
 // Sums stop at INT_MAX (blocks and tokens are fewer, so a sum that large is an error anyhow): 32-bit
 // words, and the order of additions does not matter.
@@ -69,12 +67,12 @@ __device__ __forceinline__ int last_at_or_before(const int* starts, int n, int x
   return lo;
 }
 
-// N values v[r .. r + N - 1] of a vector of n, zero behind its end; 16-byte loads where they fit.
+// N values v[r .. r + N - 1] of a vector of n, zero behind its end; in 16-byte loads where those fit.
 template <int N>
 __device__ __forceinline__ void load_run(const int32_t* v, int64_t r, int64_t n, int (&out)[N]) {
-  if (r + N <= n && (reinterpret_cast<uintptr_t>(v) & 15) == 0) {
+  if (N % 4 == 0 && r + N <= n && (reinterpret_cast<uintptr_t>(v) & 15) == 0) {
 #pragma unroll
-    for (int k = 0; k < N; k += 4) {
+    for (int k = 0; k + 3 < N; k += 4) {
       const int4 x = *reinterpret_cast<const int4*>(v + r + k);
       out[k] = x.x, out[k + 1] = x.y, out[k + 2] = x.z, out[k + 3] = x.w;
     }
@@ -85,8 +83,11 @@ __device__ __forceinline__ void load_run(const int32_t* v, int64_t r, int64_t n,
 }
 
 // ------------------------------------------------------------------------------- block tables
-constexpr int kExtendThreads = 512;
-constexpr int kPerThread = kChunk / kExtendThreads;  // requests of a round
+// One CTA to an SM, and a request to a thread: with 512 threads, two CTAs to an SM and four requests 1.1 M blocks took
+// 6.3 us, not 4.0, and a step of 256 requests 2.2, not 2.1.
+constexpr int kExtendThreads = 1024;
+constexpr int kPerThread = 1;  // requests of a round
+constexpr int kExtendChunk = kPerThread * kExtendThreads;
 constexpr int kTileBlocks = 8;                       // blocks of a tile per thread, their loads in flight together
 constexpr int kExtendTile = kExtendThreads * kTileBlocks;
 
@@ -94,8 +95,8 @@ constexpr int kExtendTile = kExtendThreads * kTileBlocks;
 // `write_counts` the CTAs also write held_out (a round each) and CTA 0 taken_out, which must then not
 // be `held` and `taken` themselves unless the grid is one CTA.
 __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendParams p, bool write_table, bool write_counts) {
-  __shared__ int s_start[kChunk];  // first block of each request of the round, counted from the round's first
-  __shared__ int s_held[kChunk];
+  __shared__ int s_start[kExtendChunk];  // first block of each request of the round, counted from the round's first
+  __shared__ int s_held[kExtendChunk];
   __shared__ uint32_t s_warp[kExtendThreads / 32];
   __shared__ uint32_t s_fail;
 
@@ -107,11 +108,11 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendPara
   const uint32_t avail = bad_taken ? 0 : static_cast<uint32_t>(p.num_free - taken);
   uint32_t base = 0;   // blocks needed by the requests of earlier rounds
   uint32_t given = 0;
-  const int64_t rounds = (p.requests + kChunk - 1) / kChunk;
+  const int64_t rounds = (p.requests + kExtendChunk - 1) / kExtendChunk;
 
   for (int64_t c = 0; c < rounds; ++c) {
     if (threadIdx.x == 0) s_fail = UINT_MAX;
-    const int64_t r = c * kChunk + threadIdx.x * kPerThread;
+    const int64_t r = c * kExtendChunk + threadIdx.x * kPerThread;
     int len[kPerThread], held[kPerThread];
     uint32_t need[kPerThread], sum = 0;
     load_run(p.seq_lens, r, p.requests, len);
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendPara
     }
     __syncthreads();
     if (write_table) {
-      const int n = static_cast<int>(min(static_cast<int64_t>(kChunk), p.requests - c * kChunk));
+      const int n = static_cast<int>(min(static_cast<int64_t>(kExtendChunk), p.requests - c * kExtendChunk));
       const int32_t* from = p.free_blocks + taken + base;
       for (uint32_t i0 = blockIdx.x * kExtendTile; i0 < round_given; i0 += gridDim.x * kExtendTile) {
         int id[kTileBlocks];
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendPara
           const uint32_t i = i0 + k * kExtendThreads + threadIdx.x;
           if (i >= round_given) break;
           if (q < 0 || (q + 1 < n && static_cast<uint32_t>(s_start[q + 1]) <= i)) q = last_at_or_before(s_start, n, static_cast<int>(i));
-          p.table[(c * kChunk + q) * p.stride + s_held[q] + (static_cast<int>(i) - s_start[q])] = id[k];
+          p.table[(c * kExtendChunk + q) * p.stride + s_held[q] + (static_cast<int>(i) - s_start[q])] = id[k];
         }
       }
     }
@@ -193,20 +194,19 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendPara
 }
 
 // ----------------------------------------------------------------------------------- slot maps
-constexpr int kMapThreads = 512;                    // a token each
-constexpr int kMapRequests = kChunk / kMapThreads;  // requests per thread and round
-
-// CTA b makes the arrays of tokens [b * kMapThreads, (b + 1) * kMapThreads) and the per-request outputs
+// CTA b makes the arrays of tokens [b * THREADS, (b + 1) * THREADS) and the per-request outputs
 // of rounds b, b + grid, ...; it sums requests until it has passed both. A token per thread, not
 // several: a decode step has a few hundred, and what counts is the chain of dependent steps of one.
-__global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotMapParams p) {
+template <int THREADS, int PER>  // requests per thread and round
+__global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p) {
+  constexpr int kChunk = PER * THREADS;
   __shared__ int s_start[kChunk];  // first token of each request of the round
   __shared__ int s_pos[kChunk];    // and its position
-  __shared__ uint32_t s_warp[kMapThreads / 32];
+  __shared__ uint32_t s_warp[THREADS / 32];
 
   wait_for_inputs();
-  const uint32_t t = blockIdx.x * kMapThreads + threadIdx.x;
-  const uint32_t tile_end = static_cast<uint32_t>(min(static_cast<int64_t>(blockIdx.x + 1) * kMapThreads, p.tokens));
+  const uint32_t t = blockIdx.x * THREADS + threadIdx.x;
+  const uint32_t tile_end = static_cast<uint32_t>(min(static_cast<int64_t>(blockIdx.x + 1) * THREADS, p.tokens));
   unsigned int err = 0;
   int req = 0, pos = 0;
   int64_t slot = -1, kv_slot = -1;
@@ -215,14 +215,14 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotMapPara
   uint32_t base = 0;
   int64_t duty = blockIdx.x;  // the next round whose per-request outputs are this CTA's
   for (int64_t c = 0; c < rounds && (base < tile_end || duty < rounds); ++c) {
-    const int64_t r = c * kChunk + threadIdx.x * kMapRequests;
-    int len[kMapRequests], query[kMapRequests];
+    const int64_t r = c * kChunk + threadIdx.x * PER;
+    int len[PER], query[PER];
     load_run(p.seq_lens, r, p.requests, len);
     load_run(p.query_lens, r, p.requests, query);
     uint32_t sum = 0;
     unsigned int bad = 0;
 #pragma unroll
-    for (int k = 0; k < kMapRequests; ++k) {
+    for (int k = 0; k < PER; ++k) {
       if (len[k] < 0 || query[k] < 0) bad = C128_DEV_BAD_LENGTH;
       len[k] = max(len[k], 0);
       query[k] = max(query[k], 0);
@@ -230,10 +230,10 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotMapPara
       sum = add_clipped(sum, static_cast<uint32_t>(query[k]));
     }
     uint32_t total;
-    uint32_t start = add_clipped(base, block_exclusive_sum<kMapThreads>(sum, s_warp, &total));
+    uint32_t start = add_clipped(base, block_exclusive_sum<THREADS>(sum, s_warp, &total));
 #pragma unroll
-    for (int k = 0; k < kMapRequests; ++k) {
-      const int i = threadIdx.x * kMapRequests + k;
+    for (int k = 0; k < PER; ++k) {
+      const int i = threadIdx.x * PER + k;
       s_start[i] = static_cast<int>(start);
       s_pos[i] = len[k] - query[k];
       if (c == duty && r + k < p.requests) {
@@ -309,15 +309,21 @@ cudaError_t launch_extend(const ExtendParams& p, int sm_count, cudaStream_t stre
   const bool in_place = p.held_out == p.held || p.taken_out == p.taken;
   const int64_t most = p.columns > 0 && p.requests > p.num_free / p.columns ? p.num_free : p.requests * p.columns;
   const int64_t tiles = (most + kExtendTile - 1) / kExtendTile;
-  const unsigned grid = static_cast<unsigned>(tiles < 1 ? 1 : tiles < 2 * sm_count ? tiles : 2 * sm_count);
+  const unsigned grid = static_cast<unsigned>(tiles < 1 ? 1 : tiles < sm_count ? tiles : sm_count);
   if (!in_place || grid == 1) return launch_early(extend_kernel, grid, kExtendThreads, stream, p, true, true);
   const cudaError_t e = launch_early(extend_kernel, grid, kExtendThreads, stream, p, true, false);
   return e != cudaSuccess ? e : launch_early(extend_kernel, 1u, kExtendThreads, stream, p, false, true);
 }
 
+// A request to a thread while one round takes them all; else four, and the rounds are fewer: 200 requests 2.4 us and
+// 2.5, 333 with 32 thousand tokens 2.6 and 3.2; 2048 4.5 and 3.4, 1000 with 100 thousand tokens 5.2 and 4.4.
 cudaError_t launch_slot_maps(const SlotMapParams& p, cudaStream_t stream) {
-  const int64_t tiles = (p.tokens + kMapThreads - 1) / kMapThreads;
-  return launch_early(slot_map_kernel, static_cast<unsigned>(tiles < 1 ? 1 : tiles), kMapThreads, stream, p);
+  const bool one_round = p.requests <= 512;
+  const int threads = one_round ? 512 : 256;  // a token each
+  const int64_t tiles = (p.tokens + threads - 1) / threads;
+  const unsigned grid = static_cast<unsigned>(tiles < 1 ? 1 : tiles);
+  if (one_round) return launch_early(slot_map_kernel<512, 1>, grid, 512, stream, p);
+  return launch_early(slot_map_kernel<256, 4>, grid, 256, stream, p);
 }
 
 }  // namespace c128

@@ -1,5 +1,5 @@
 """c128_extend_block_tables and c128_build_slot_maps against plain loops (whole numbers, so equal), at the sizes
-where a prefix sum over rounds of 2048 requests and tiles of blocks or tokens can go wrong."""
+where a prefix sum over rounds of 512 or 1024 requests and tiles of blocks or tokens can go wrong."""
 import numpy as np
 import pytest
 
@@ -51,7 +51,8 @@ def _check_extend(binding, lens, held, table, free, taken, ratio, block, **kw):
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("requests,longest,ratio,block", [
     (1, 1, 1, 8), (1, 100000, 1, 8), (3, 7, 1, 8), (256, 900, 1, 8), (513, 300, 4, 2), (2047, 50, 1, 3),
-    (2048, 40, 1, 1), (2049, 64, 128, 1), (5000, 33, 1, 8), (7, 20001, 1, 1),
+    (2048, 40, 1, 1), (2049, 64, 128, 1), (5000, 33, 1, 8), (7, 20001, 1, 1), (1023, 9, 1, 8), (1024, 20, 1, 8),
+    (1025, 20, 1, 8), (9000, 300, 1, 1),
 ])
 def test_extend_matches_loops(binding, requests, longest, ratio, block, in_place):
     rng = np.random.default_rng([requests, longest, ratio, block])
@@ -147,6 +148,8 @@ def _check_maps(binding, lens, new, st, sb, kt, kb, ratio, tokens, **kw):
     (1, 1, 1, 0, 128, 8, 64, 0), (1, 1, 1, 5, 1, 8, 1, 1), (1, 5000, 5000, 0, 4, 8, 2, 0), (3, 700, 1, 2, 128, 8, 64, 1),
     (200, 3000, 1, 56, 128, 8, 64, 0), (333, 900, 40, 7, 4, 8, 2, 0), (2048, 60, 3, 0, 4, 8, 1, 0),
     (2049, 60, 3, 1000, 8, 3, 7, 3), (5000, 20, 1, 1, 2, 8, 64, 0), (64, 4000, 900, 1025, 128, 8, 64, 0),
+    (511, 60, 3, 3, 4, 8, 2, 0), (512, 60, 3, 0, 128, 8, 1, 1), (513, 60, 3, 9, 4, 8, 2, 0), (1024, 90, 2, 0, 8, 8, 2, 2),
+    (1025, 90, 2, 0, 8, 8, 2, 0),
 ])
 def test_maps_match_loops(binding, requests, longest, most_new, pad, ratio, sb, kb, offset):
     rng = np.random.default_rng([requests, longest, most_new, pad])
