@@ -26,8 +26,14 @@
 // the range). Else it is raised or lowered to the maximum so far, O in TMEM rescaled with it.
 //
 // Work is dealt out in tiles: the requests' tiles, one after the other, are cut into as many equal
-// runs as there are CTAs, so a long request is shared by many CTAs and a CTA takes many short ones. A
-// request that is cut leaves fp32 partial results in the workspace, joined by a second kernel.
+// runs as there are CTAs, so a long request is shared by many CTAs and a CTA takes many short ones. (What
+// a run has of one request is called a stretch here.) A request that is cut leaves fp32 partial results in
+// the workspace, joined by a second kernel.
+//
+// Measured, device time per call with the join: 8 requests of up to 65,536 entries, 16 heads (173 MB) 62.7 us,
+// 2.75 TB/s; 48 of up to 8,192, 128 heads 59.7 us; 64 of up to 1,024, 64 heads 27.3 us; one of 1,024 12.3 us. A
+// tile takes an SM 1.48 us (16 heads) or 1.85 (64). Decoding is the longest link, on a shared memory of which the
+// products' operands take half the bandwidth and come first.
 //
 // Roles of the 19 warps (each wait is bounded; five warps to a scheduler leave them 96 registers, and a
 // spill would be a trip to L2, beside the little L1 that the tiles leave):
@@ -326,11 +332,12 @@ __device__ __forceinline__ int tiles_of(int entries) { return max((entries >> 6)
 static_assert(kTile == 64, "tiles_of");
 
 // The requests' tiles one after the other, kRunCost units between two requests, are dealt to the CTA
-// columns in equal runs: storing the results of a request takes a CTA about as long as a tile (2.2 us of
-// 64 heads, a tile 1.9), and every run ends with that. (The units of all requests are less than 2^31.)
+// columns in equal runs: storing the results of a request takes a CTA about as long as a tile (2 us of
+// 64 heads), and every run ends with that. (The units of all requests are less than 2^31.)
 // `total` units go to `columns`, the first `extra` of them one more than the rest. A cut that falls between
 // requests, or would fall within `snap` tiles of a request's begin or end, is made there: a cut request
 // costs its partial results (2 KB per head and part, written and read again), about what a tile or two take.
+// (A cost of 2: 64 x 1,024 entries 4 % slower, 48 x 8,192 4 % faster; snap of 1 or 3: up to 6 % slower.)
 constexpr int kRunCost = 1;  // not 0: a cut at the end of one request would be in none
 constexpr int kSnap = 2;
 struct Deal {
@@ -1132,7 +1139,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 // ------------------------------------------------------------------- join the partial results
 // out = sum_k 2^(lse_k - L) part_k, in the layout of the parts: a warp takes four heads and 32 or 128
 // columns of a cut request, 16 bytes per lane, part and 32 columns. What it takes is the trips to L2 one
-// behind the other: who has been cut, that task, and then the parts' statistics and values at once.
+// behind the other: who has been cut, that task, and then the parts' statistics and values at once. One
+// request in 16 parts takes 3.4 us, 64 requests in about 200 parts of 64 heads (26 MB) 6.
 constexpr int kJoinThreads = 128;
 constexpr int kJoinPerSm = 4;  // CTAs that fit (registers)
 constexpr int kMaxCtas = 1024;
