@@ -67,7 +67,8 @@ constexpr int kFillWarps = 8;       // decode a tile
 constexpr int kAhead = 3;           // of a tile's 7 chunks of codes, decoded before the buffer has room for them
 // Eight softmax warps, half the heads each: with four, which left 128 registers to all, a tile took 0.25 us
 // (16 heads) or 0.5 us (64) longer. Sixteen decoding warps, a set for alternate tiles or for either half
-// of the columns, took 0.1 to 0.6 us longer: seven warps to a scheduler have 72 registers, and spill.
+// of the columns, took 0.1 to 0.6 us longer: seven warps to a scheduler have 72 registers, and spill. (With
+// four softmax warps and the registers dealt out so that nothing spilled: 0.2 us longer.)
 constexpr int kSoftWarps = 8;
 constexpr int kSoftWarp = kFillWarps, kMmaWarp = kSoftWarp + kSoftWarps, kIndexWarp = kMmaWarp + 2;
 constexpr int kDecodeThreads = 32 * (kIndexWarp + 1);
@@ -570,12 +571,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     int64_t window = r;      // lanes hold the lengths of requests window .. window + 31
     unsigned int ignore = 0;
     int id[2];
-    // entries are fewer than 2^31, so an index past them does not wrap in 32 unsigned bits
+    // Entries are fewer than 2^31, so an index past them does not wrap in 32 unsigned bits. (Not as read-only data: this
+    // kernel may have started before the one that writes the table has ended.)
     auto load_ids = [&] {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t key = static_cast<uint32_t>(tile) * kTile + 32 * h + lane;
-        id[h] = key < static_cast<uint32_t>(n) ? __ldg(p.table + r * p.table_stride + divide(key, bs)) : -1;
+        id[h] = key < static_cast<uint32_t>(n) ? __ldcg(p.table + r * p.table_stride + divide(key, bs)) : -1;
       }
     };
     int stretch = 0;
@@ -1090,7 +1092,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const float own = (sm.by_warp[0][h] + sm.by_warp[1][h]) + (sm.by_warp[2][h] + sm.by_warp[3][h]), ref = zero ? 0.f : sm.ref[h];
         float sum = own, to = ref, share = own == 0.f ? 0.f : 1.f;
         if (whole && p.sink != nullptr) {  // one more score, with a value of zero
-          const float s = __ldg(p.sink + head) * kLog2e;
+          const float s = __ldcg(p.sink + head) * kLog2e;
           // (with nothing else in the sum, or if it is far above the rest, the result is 0 and lse the sink's)
           to = own == 0.f ? (s == -INFINITY ? 0.f : s) : fmaxf(ref, s);
           const float entries = own == 0.f ? 0.f : own * ex2_approx(ref - to);
@@ -1176,7 +1178,7 @@ __device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout
   const int hh = lane & 3;
   const bool real = head + hh < p.heads;
   auto lse_of = [&](int k) { return k < t.parts && real ? lse[row(k) + h + hh] : -INFINITY; };
-  const float sink = p.sink != nullptr && real ? __ldg(p.sink + head + hh) * kLog2e : -INFINITY;
+  const float sink = p.sink != nullptr && real ? __ldcg(p.sink + head + hh) * kLog2e : -INFINITY;
   float top = sink;
   bool nan = false;
   for (int k = lane >> 2; k < t.parts; k += 8) {

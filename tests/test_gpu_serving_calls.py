@@ -181,3 +181,39 @@ def test_decode_over_an_empty_cache(binding):
             else:
                 # log2 and back of the sink: a few roundings of a value of 3
                 assert bool(((lse - sink).abs() <= 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("lens,heads", [([64], 16), ([300, 64, 5, 700], 40)])
+def test_calls_follow_one_another_without_gaps(binding, lens, heads):
+    """Tables rewritten between attention calls that are launched back to back (each launch starts before the one before
+    it has ended): every call sees the table that was written right before it, one of two sets of pages."""
+    import torch
+    rng = np.random.default_rng([45, heads])
+    block, R = 64, len(lens)
+    need = [cdiv(n, block) for n in lens]
+    cache = make_cache(rng, 2 * sum(need), block)
+    pages = rng.permutation(2 * sum(need)).astype(np.int32).reshape(2, -1)
+    q = torch.from_numpy(rng.standard_normal((R, heads, HEAD)).astype(np.float32)).to(torch.bfloat16).cuda()
+    lens_gpu, held, taken = _cuda(np.array(lens, np.int32)), _cuda(np.zeros(R, np.int32)), torch.zeros(1, dtype=torch.int64, device="cuda")
+    table = torch.full((R, max(need)), -1, dtype=torch.int32, device="cuda")
+    held_out, taken_out = torch.empty_like(held), torch.empty_like(taken)
+    fill = [binding.PreparedOp("extend_block_tables", lens_gpu, held, table, _cuda(pages[k]), taken, 1, block, held_out=held_out,
+                               taken_out=taken_out) for k in range(2)]
+    cache_gpu = _cuda(cache)
+    outs = [(torch.zeros_like(q), torch.zeros(R, heads, device="cuda")) for _ in range(40)]
+    calls = [binding.PreparedOp("decode_attention", q, cache_gpu, block, table, lens_gpu, HEAD ** -0.5, o, lse=l) for o, l in outs]
+    torch.cuda.synchronize()
+    for k, call in enumerate(calls):
+        fill[k % 2]()
+        call()
+    torch.cuda.synchronize()
+    assert binding.device_errors(clear=True) == 0
+    for k in range(2):
+        rows = np.full((R, max(need)), -1, np.int32)
+        at = 0
+        for r, n in enumerate(need):
+            rows[r, :n] = pages[k][at:at + n]
+            at += n
+        _check_decode(cache, rows, (q, None, block, None, lens_gpu, HEAD ** -0.5), *outs[k])
+        for o, l in outs[k::2]:
+            assert torch.equal(o, outs[k][0]) and torch.equal(l, outs[k][1])
