@@ -5,8 +5,9 @@
 // 512 values, 16 per lane in two 16-byte pieces (bf16), so that each load of a warp covers 512
 // consecutive bytes and the loads of four parts are in flight before the first is used.
 //
-// Measured: 256 requests x 128 heads, 4 bf16 parts (168 MB) 28.2 us, 6.0 TB/s, 0.88 of the measured copy; one
-// request, 64 heads, 2 parts 1.9 us, which is a launch. (Weights first and values behind them: 34.2 us.)
+// Measured: 256 requests x 128 heads, 4 bf16 parts (168 MB) 26.0 us, 6.5 TB/s, 0.96 of the measured copy; one
+// request, 64 heads, 2 parts 1.8 us, which is a launch. (Weights first and values behind them 34.2 us;
+// CTAs of 256 threads, whose rows end together, 28.2, of 512 38.9, of 32 33.4; streaming loads 26.7.)
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -17,7 +18,7 @@
 namespace c128 {
 namespace {
 
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 64;
 
 // Values [c, c + 8) of a row.
 template <bool F32>
@@ -26,8 +27,8 @@ template <>
 struct Piece<true> {
   float4 a, b;
   __device__ __forceinline__ void load(const void* row, int c) {
-    a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(row) + c));
-    b = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(row) + c) + 1);
+    a = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + c));
+    b = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + c) + 1);
   }
   __device__ __forceinline__ void add(float w, float (&acc)[8]) const {
     acc[0] = fmaf(w, a.x, acc[0]), acc[1] = fmaf(w, a.y, acc[1]), acc[2] = fmaf(w, a.z, acc[2]), acc[3] = fmaf(w, a.w, acc[3]);
@@ -38,7 +39,7 @@ template <>
 struct Piece<false> {
   uint4 a;
   __device__ __forceinline__ void load(const void* row, int c) {
-    a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c));
+    a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c));
   }
   __device__ __forceinline__ void add(float w, float (&acc)[8]) const {
     const uint32_t v[4] = {a.x, a.y, a.z, a.w};

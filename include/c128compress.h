@@ -419,7 +419,8 @@ int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* que
  *                                    GPU need one each (so do graphs that are replayed at once)
  *
  * Products take bf16 operands (the entries are exact in bf16 for scale bytes 8 .. 246; the softmax
- * weights are rounded to bf16) and add up in fp32; the softmax statistics are fp32.
+ * weights are rounded to bf16) and add up in fp32. out is divided by the sums of the rounded weights, so
+ * that of one entry is that entry; lse is of the exact ones, in fp32.
  * Device error bits: C128_DEV_BAD_BT_COL - kv_lens[r] > MB*bs (the entries behind are left out);
  * C128_DEV_BAD_BLOCK - a block id outside [0, NKB) (its entries are left out); C128_DEV_BAD_LENGTH
  * - a negative kv_lens[r] (counts as 0); C128_DEV_TIMEOUT - a wait inside the kernel ran out: some of
