@@ -356,8 +356,12 @@ class PreparedOp:
     def __init__(self, op: str, *args, stream=None, **kw):
         self._name, c_args, owned = _OPS[op](*args, **kw)
         self._keep = (args, kw, owned)
-        self._fn = getattr(lib(), self._name)
-        self._args = (*c_args, _stream_handle(stream))
+        # A function object of its own, without argument types, and arguments that are converted here: with types
+        # ctypes checks every argument again in every call, more than half of what a call costs on the host.
+        types = getattr(lib(), self._name).argtypes
+        self._fn = lib()[self._name]
+        self._args = tuple(t(a) if isinstance(a, (int, float)) else a
+                           for t, a in zip(types, (*c_args, _stream_handle(stream)), strict=True))
 
     def __call__(self) -> None:
         rc = self._fn(*self._args)
