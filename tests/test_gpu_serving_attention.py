@@ -78,7 +78,7 @@ def test_decode_lengths_and_blocks(binding, heads, block):
     _check(c, out, lse)
 
 
-@pytest.mark.parametrize("heads", [2, 15, 17, 31, 48, 63, 65, 128, 130, 200])
+@pytest.mark.parametrize("heads", [2, 15, 17, 31, 48, 63, 65, 128, 130, 200, 1000, 1024])
 def test_decode_heads(binding, heads):
     rng = np.random.default_rng(heads)
     c = _case(rng, [70, 3, 0, 150], heads, 16, sink=heads % 2 == 0)
@@ -87,7 +87,8 @@ def test_decode_heads(binding, heads):
 
 
 @pytest.mark.parametrize("requests,heads,longest", [(1, 64, 5000), (1, 8, 20000), (3, 128, 2000), (2, 16, 1), (1, 1, 64),
-                                                    (1, 128, 129), (40, 4, 700), (170, 20, 130), (700, 3, 90)])
+                                                    (1, 128, 129), (40, 4, 700), (170, 20, 130), (700, 3, 90),
+                                                    (9000, 3, 2)])
 def test_decode_split_over_the_cache(binding, requests, heads, longest):
     """Requests split over many CTAs, and many requests to a CTA."""
     rng = np.random.default_rng([requests, heads, longest])
@@ -95,7 +96,7 @@ def test_decode_split_over_the_cache(binding, requests, heads, longest):
     lens[0] = longest
     c = _case(rng, lens, heads, 64 if longest > 1000 else 7)
     out, lse = _run(binding, c)
-    _check(c, out, lse, None if requests < 50 else list(range(0, requests, 7)))
+    _check(c, out, lse, None if requests < 50 else list(range(0, requests, 7 if requests < 1000 else 90)))
 
 
 def test_decode_is_deterministic(binding):
