@@ -313,8 +313,10 @@ def _refs(*tensors):
     return [None if t is None else ctypes.byref(describe(t)) for t in tensors]
 
 
+# Each operator's arguments to its C entry, name, C arguments and what the call keeps alive. `stream` is the one that the call
+# will run on.
 def _extend_block_tables(seq_lens, held, block_table, free_blocks, taken, compress_ratio: int, block_size: int,
-                         held_out=None, taken_out=None):
+                         held_out=None, taken_out=None, stream=None):
     held_out = held if held_out is None else held_out
     taken_out = taken if taken_out is None else taken_out
     a = _refs(seq_lens, held, block_table, free_blocks, taken, held_out, taken_out)
@@ -323,22 +325,31 @@ def _extend_block_tables(seq_lens, held, block_table, free_blocks, taken, compre
 
 def _build_slot_maps(seq_lens, query_lens, state_table, state_block: int, kv_table, kv_block_size: int,
                      compress_ratio: int, query_start, token_to_req_indices, positions, slot_mapping, kv_slot_mapping,
-                     kv_lens):
+                     kv_lens, stream=None):
     a = _refs(seq_lens, query_lens, state_table, kv_table, query_start, token_to_req_indices, positions, slot_mapping,
               kv_slot_mapping, kv_lens)
     return "c128_build_slot_maps", (*a[:3], int(state_block), a[3], int(kv_block_size), int(compress_ratio), *a[4:]), ()
 
 
-def _decode_attention(q, k_cache, kv_block_size: int, block_table, kv_lens, scale: float, out, lse=None, sink=None,
-                      workspace=None):
+def _scratch(num_heads: int, device, stream):
+    """A workspace of decode_attention out of torch's pool of the stream that will use it: what the pool hands out may still
+    be in use by calls on its own stream that have not run yet, and goes back to calls on that stream."""
     import torch
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):  # None: the current stream
+        return torch.empty(decode_attention_workspace(num_heads), dtype=torch.uint8, device=device)
+
+
+def _decode_attention(q, k_cache, kv_block_size: int, block_table, kv_lens, scale: float, out, lse=None, sink=None,
+                      workspace=None, stream=None):
     if workspace is None:
-        workspace = torch.empty(decode_attention_workspace(q.shape[1]), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(q.shape[1], q.device, stream)
     a = _refs(q, k_cache, block_table, kv_lens, sink, out, lse, workspace)
     return "c128_decode_attention", (*a[:2], int(kv_block_size), *a[2:4], float(scale), *a[4:]), (workspace,)
 
 
-def _merge_attention(part_out, part_lse, out, lse=None):
+def _merge_attention(part_out, part_lse, out, lse=None, stream=None):
     return "c128_merge_attention", (*_refs(part_out, part_lse, out, lse),), ()
 
 
@@ -354,7 +365,7 @@ class PreparedOp:
     A ``decode_attention`` without a ``workspace`` gets one of its own, kept with the object."""
 
     def __init__(self, op: str, *args, stream=None, **kw):
-        self._name, c_args, owned = _OPS[op](*args, **kw)
+        self._name, c_args, owned = _OPS[op](*args, stream=stream, **kw)
         self._keep = (args, kw, owned)
         # A function object of its own, without argument types, and arguments that are converted here: with types
         # ctypes checks every argument again in every call, more than half of what a call costs on the host.
@@ -401,12 +412,7 @@ def decode_attention(q, k_cache, kv_block_size: int, block_table, kv_lens, scale
     """Attention of one new token per request over its entries of the paged FP8 ``k_cache``
     (c128_decode_attention in include/c128compress.h); ``out`` and ``lse`` are written. ``workspace``
     (uint8, decode_attention_workspace bytes) is scratch; without one the call takes one from torch's
-    allocator."""
-    if workspace is None:
-        import torch
-        workspace = torch.empty(decode_attention_workspace(q.shape[1]), dtype=torch.uint8, device=q.device)
-        if stream is not None:  # the allocator must not hand it out again before that stream is done with it
-            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    pool of the stream it runs on."""
     PreparedOp("decode_attention", q, k_cache, kv_block_size, block_table, kv_lens, scale, out, lse=lse, sink=sink,
                workspace=workspace, stream=stream)()
 

@@ -1,0 +1,99 @@
+"""The binding of the operators around the compressor without a GPU: which stream its own allocations belong to."""
+import contextlib
+
+import pytest
+
+from deepseek_v4_sparse_c128_gb300 import binding, build
+
+
+class FakeTensor:
+    """As much of a CUDA tensor as the binding looks at."""
+
+    def __init__(self, shape, dtype, index=0):
+        import torch
+        self.shape, self.dtype = tuple(shape), dtype
+        self.device = torch.device("cuda", index)
+        self._stride = [1] * len(self.shape)
+        for i in range(len(self.shape) - 2, -1, -1):
+            self._stride[i] = self._stride[i + 1] * self.shape[i + 1]
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i):
+        return self._stride[i]
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+class FakeStream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+class FakeLibrary:
+    """The library's signatures; a call is noted and nothing else, so no address here is ever used."""
+
+    def __init__(self, real, calls):
+        self._real, self._calls = real, calls
+
+    def __getattr__(self, name):
+        return getattr(self._real, name)
+
+    def __getitem__(self, name):
+        return lambda *args: self._calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def cuda(monkeypatch):
+    """A current stream and device without CUDA, and what torch.empty was asked for on which stream."""
+    import torch
+    build.build()
+    real = binding.load()
+    state = {"stream": FakeStream(11), "device": 0, "empty": [], "calls": []}
+
+    @contextlib.contextmanager
+    def on(stream):
+        before = state["stream"]
+        state["stream"] = before if stream is None else stream
+        yield
+        state["stream"] = before
+
+    def empty(n, dtype=None, device=None):
+        state["empty"].append((n, state["stream"].cuda_stream))
+        return FakeTensor([n], dtype)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: state["stream"])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state["device"])
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(binding, "decode_attention_workspace", lambda heads: 1000 * heads)
+    monkeypatch.setattr(binding, "lib", lambda: FakeLibrary(real, state["calls"]))
+    return state
+
+
+def _decode_args():
+    import torch
+    return (FakeTensor([3, 5, 512], torch.bfloat16), FakeTensor([4, 2, 584], torch.uint8), 2,
+            FakeTensor([3, 9], torch.int32), FakeTensor([3], torch.int32), 0.1, FakeTensor([3, 5, 512], torch.bfloat16))
+
+
+@pytest.mark.parametrize("stream,owner", [(None, 11), (FakeStream(22), 22), (33, 33)])
+def test_own_workspace_belongs_to_the_stream_of_the_call(cuda, stream, owner):
+    """torch's allocator orders a block's uses on the stream it was allocated on: another stream's kernel would write into
+    memory that queued work still uses, and its own block could be handed out again under it."""
+    op = binding.PreparedOp("decode_attention", *_decode_args(), stream=stream)
+    op()
+    assert cuda["empty"] == [(5000, owner)] and cuda["calls"][0][1][-1].value == owner
+    cuda["empty"].clear()
+    binding.decode_attention(*_decode_args(), stream=stream)
+    assert cuda["empty"] == [(5000, owner)]
+    assert cuda["stream"].cuda_stream == 11
