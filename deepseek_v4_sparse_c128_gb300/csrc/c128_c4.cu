@@ -222,7 +222,7 @@ __device__ void small_scheduler(const Params& p, SmallSmem<HEAD>& S, int lane, b
       next_t += 32ll * gridDim.x;
       live = false;
       if (t < p.T) {
-        const int64_t sl = __ldg(p.slot + t), ps = __ldg(p.pos + t), kv = __ldg(p.kvslot + t);
+        const int64_t sl = p.slot[t], ps = p.pos[t], kv = p.kvslot[t];
         live = (sl >= 0) & (ps >= 0) & (((ps + 1) & (p.ratio - 1)) == 0) & (kv >= 0);
       }
     } else {
@@ -233,9 +233,9 @@ __device__ void small_scheduler(const Params& p, SmallSmem<HEAD>& S, int lane, b
     int blk0 = 0, row0 = 0, half0 = 0, blk1 = 0, row1 = 0, half1 = 0;
     uint32_t err = 0;
     if (live) {
-      req = __ldg(p.ttr + t);
-      pos = __ldg(p.pos + t);
-      kvs = __ldg(p.kvslot + t);
+      req = p.ttr[t];
+      pos = p.pos[t];
+      kvs = p.kvslot[t];
       cp = pos & ~static_cast<int64_t>(p.ratio - 1);  // (p / ratio) * ratio; ratio is a power of two
       if (req < 0 || req >= p.bt_rows) err |= C128_DEV_BAD_REQ;
       if (pos / p.sblk >= p.bt_cols) err |= C128_DEV_BAD_BT_COL;
@@ -252,13 +252,13 @@ __device__ void small_scheduler(const Params& p, SmallSmem<HEAD>& S, int lane, b
       // and (state block a multiple of ratio) lies in one state block
       const int64_t q0 = start, q1 = start + p.ratio;
       if (q0 >= 0) {
-        blk0 = __ldg(bt_row + q0 / p.sblk);
+        blk0 = bt_row[q0 / p.sblk];
         row0 = static_cast<int>(q0 % p.sblk);
         half0 = 0;
         ngroups = 1;
       }
       if (p.overlap) {
-        const int b1 = __ldg(bt_row + q1 / p.sblk);
+        const int b1 = bt_row[q1 / p.sblk];
         const int r1 = static_cast<int>(q1 % p.sblk);
         if (ngroups == 0) {
           blk0 = b1;
@@ -304,7 +304,7 @@ __device__ void small_scheduler(const Params& p, SmallSmem<HEAD>& S, int lane, b
           const float* r = nullptr;
           if (i < nvalid) {
             const int64_t q = first + i;
-            const int b = __ldg(bt_row + q / p.sblk);
+            const int b = bt_row[q / p.sblk];
             if (b < 0 || b >= p.nb) {
               bad = true;
             } else {

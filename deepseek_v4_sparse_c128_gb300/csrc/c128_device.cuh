@@ -131,6 +131,10 @@ __device__ __forceinline__ bool consumer_bar_or(bool pred) {
       : "memory");
   return out != 0;
 }
+// Behind the wait, what earlier kernels on the stream have written is there: the per-token arrays and block tables of a call
+// may come from one that let this kernel start while it was still running. So they are read by plain loads. A read-only load
+// (__ldg) is defined, and kept behind the wait, only for memory that nobody writes while the kernel is resident: the norm's
+// weight and the rotation table.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 

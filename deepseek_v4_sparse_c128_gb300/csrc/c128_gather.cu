@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(256, 3) gather_kernel(Params p) {
   for (int64_t a = blockIdx.x; a < A; a += gridDim.x) {
     __syncthreads();  // the previous window's epilogue is done with the shared scratch
     const int64_t t = plan_token(p, chunk_prefix, static_cast<uint32_t>(a));
-    const int req = __ldg(p.ttr + t);
-    const int64_t pos = __ldg(p.pos + t), kvs = __ldg(p.kvslot + t);
+    const int req = p.ttr[t];
+    const int64_t pos = p.pos[t], kvs = p.kvslot[t];
     uint32_t err = 0;
     if (req < 0 || req >= p.bt_rows) err |= C128_DEV_BAD_REQ;
     if (pos / p.sblk >= p.bt_cols) err |= C128_DEV_BAD_BT_COL;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(256, 3) gather_kernel(Params p) {
       for (int i = rg; i < nrows; i += G::kRowGroups) {
         const int64_t q = start + i;
         if (q < 0) continue;
-        const int b = __ldg(p.bt + static_cast<int64_t>(req) * p.bt_stride + q / p.sblk);
+        const int b = p.bt[static_cast<int64_t>(req) * p.bt_stride + q / p.sblk];
         bad |= b < 0 || b >= p.nb;
       }
     }
@@ -248,11 +248,11 @@ __global__ void __launch_bounds__(256, 3) gather_kernel(Params p) {
         kv[r] = make_float4(0.f, 0.f, 0.f, 0.f);
         sc[r] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (i < nrows && q >= 0) {
-          const int b = __ldg(p.bt + static_cast<int64_t>(req) * p.bt_stride + q / p.sblk);
+          const int b = p.bt[static_cast<int64_t>(req) * p.bt_stride + q / p.sblk];
           const float* row = p.state + static_cast<int64_t>(b) * p.s0 + (q % p.sblk) * p.s1 +
                              (i >= p.ratio ? HEAD : 0) + col;
-          kv[r] = __ldg(reinterpret_cast<const float4*>(row));
-          sc[r] = __ldg(reinterpret_cast<const float4*>(row + p.sw));
+          kv[r] = *reinterpret_cast<const float4*>(row);
+          sc[r] = *reinterpret_cast<const float4*>(row + p.sw);
         }
       }
 #pragma unroll

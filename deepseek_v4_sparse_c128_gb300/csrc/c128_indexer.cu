@@ -127,7 +127,7 @@ __device__ void ix_scheduler(const Params& p, IxSmem& S, int lane) {
         const int64_t c = next_t + static_cast<int64_t>(lane) * gridDim.x;
         bool act = false;
         if (c < p.T) {
-          const int64_t sl = __ldg(p.slot + c), ps = __ldg(p.pos + c), kv = __ldg(p.kvslot + c);
+          const int64_t sl = p.slot[c], ps = p.pos[c], kv = p.kvslot[c];
           act = (sl >= 0) & (ps >= 0) & (((ps + 1) & (p.ratio - 1)) == 0) & (kv >= 0);
         }
         const uint32_t m = __ballot_sync(0xffffffffu, act);
@@ -153,9 +153,9 @@ __device__ void ix_scheduler(const Params& p, IxSmem& S, int lane) {
     uint32_t err = 0;
     if (!end) {
       if (lane == 0) {
-        req = __ldg(p.ttr + t);
-        pos = __ldg(p.pos + t);
-        kvs = __ldg(p.kvslot + t);
+        req = p.ttr[t];
+        pos = p.pos[t];
+        kvs = p.kvslot[t];
         if (req < 0 || req >= p.bt_rows) err |= C128_DEV_BAD_REQ;
         if (pos / p.sblk >= p.bt_cols) err |= C128_DEV_BAD_BT_COL;
         if ((pos & ~static_cast<long long>(p.ratio - 1)) >= p.cs_rows) err |= C128_DEV_BAD_COS_ROW;
@@ -175,7 +175,7 @@ __device__ void ix_scheduler(const Params& p, IxSmem& S, int lane) {
       bool bad = false;
       if (lane < nch) {
         const long long q0 = first + static_cast<long long>(kIxChunk) * lane;
-        blk = __ldg(p.bt + static_cast<int64_t>(req) * p.bt_stride + q0 / p.sblk);
+        blk = p.bt[static_cast<int64_t>(req) * p.bt_stride + q0 / p.sblk];
         row = static_cast<int>(q0 % p.sblk);
         half = (p.overlap && q0 - start >= p.ratio) ? 1 : 0;
         bad = blk < 0 || blk >= p.nb;

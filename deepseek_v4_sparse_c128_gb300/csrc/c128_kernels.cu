@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params p) {
   for (int i = 0; i < kPlanTokensPerThread; ++i) {
     const int64_t t = base + i * kPlanThreads + tid;
     if (t < p.T) {
-      const int64_t s = __ldg(p.slot + t), pos = __ldg(p.pos + t), kv = __ldg(p.kvslot + t);
+      const int64_t s = p.slot[t], pos = p.pos[t], kv = p.kvslot[t];
       const bool active = (s >= 0) & (pos >= 0) & (((pos + 1) & (p.ratio - 1)) == 0) & (kv >= 0);
       flags |= static_cast<uint32_t>(active) << i;
     }
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(THREADS) plan_chunks_kernel(Params p) {
   for (int i = 0; i < kTok; ++i) {
     const int64_t t = base + static_cast<int64_t>(tid) * kTok + i;
     if (t < p.T) {
-      const int64_t s = __ldg(p.slot + t), pos = __ldg(p.pos + t), kv = __ldg(p.kvslot + t);
+      const int64_t s = p.slot[t], pos = p.pos[t], kv = p.kvslot[t];
       const bool active = (s >= 0) & (pos >= 0) & (((pos + 1) & (p.ratio - 1)) == 0) & (kv >= 0);
       flags |= static_cast<uint32_t>(active) << i;
     }
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(THREADS) plan_chunks_kernel(Params p) {
 __device__ __forceinline__ int chunk_block(const Params& p, int req, long long start, int j, int64_t* off) {
   const long long q0 = start + static_cast<long long>(kStateBlock) * j;
   const long long col = q0 / p.sblk, row = q0 - col * p.sblk;
-  const int blk = __ldg(p.bt + static_cast<int64_t>(req) * p.bt_stride + col);
+  const int blk = p.bt[static_cast<int64_t>(req) * p.bt_stride + col];
   *off = static_cast<int64_t>(blk) * p.s0 + row * p.s1;
   return blk;
 }
@@ -181,9 +181,9 @@ __device__ void scheduler_warp(const Params& p, Smem& S, int lane) {
     if (!end && lane == 0) t = plan_token(p, S.chunk_prefix, a);
     if (!end) {
       if (lane == 0) {
-        req = __ldg(p.ttr + t);
-        pos = __ldg(p.pos + t);
-        kvs = __ldg(p.kvslot + t);
+        req = p.ttr[t];
+        pos = p.pos[t];
+        kvs = p.kvslot[t];
         if (req < 0 || req >= p.bt_rows) err |= C128_DEV_BAD_REQ;
         if ((ANY ? pos / p.sblk : pos / kStateBlock) >= p.bt_cols) err |= C128_DEV_BAD_BT_COL;
         if (pos - (kRatio - 1) >= p.cs_rows) err |= C128_DEV_BAD_COS_ROW;  // (p/128)*128 == p-127
@@ -202,7 +202,7 @@ __device__ void scheduler_warp(const Params& p, Smem& S, int lane) {
         if (lane < kWindowBlocks) blk = chunk_block(p, req, pos - (kRatio - 1), lane, &choff);
       } else {
         if (lane < kWindowBlocks)
-          blk = __ldg(p.bt + static_cast<int64_t>(req) * p.bt_stride + (pos - (kRatio - 1)) / kStateBlock + lane);
+          blk = p.bt[static_cast<int64_t>(req) * p.bt_stride + (pos - (kRatio - 1)) / kStateBlock + lane];
       }
       const bool bad = lane < kWindowBlocks && (blk < 0 || blk >= p.nb);
       if (__any_sync(0xffffffffu, bad)) err |= C128_DEV_BAD_BLOCK;
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, R > 0 ? 2 : 1) direct_kernel(Params 
   grid_dependency_wait();
   // the token (every thread; broadcast loads), issued before the barrier set-up so that their
   // latency overlaps it
-  const int64_t slot = __ldg(p.slot + t), pos = __ldg(p.pos + t), kvs = __ldg(p.kvslot + t);
-  const int req = __ldg(p.ttr + t);
+  const int64_t slot = p.slot[t], pos = p.pos[t], kvs = p.kvslot[t];
+  const int req = p.ttr[t];
   // an inactive token's CTAs leave at once (uniformly: every CTA of a cluster reads the same token)
   if (!((slot >= 0) & (pos >= 0) & ((pos & (kRatio - 1)) == kRatio - 1) & (kvs >= 0))) return;
   if (tid == 0) {
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, R > 0 ? 2 : 1) direct_kernel(Params 
       if (lane < kWindowBlocks) blk = chunk_block(p, req, pos - (kRatio - 1), lane, &unused);
     } else {
       if (lane < kWindowBlocks)
-        blk = __ldg(p.bt + static_cast<int64_t>(req) * p.bt_stride + (pos - (kRatio - 1)) / kStateBlock + lane);
+        blk = p.bt[static_cast<int64_t>(req) * p.bt_stride + (pos - (kRatio - 1)) / kStateBlock + lane];
     }
     if (__any_sync(0xffffffffu, lane < kWindowBlocks && (blk < 0 || blk >= p.nb))) err |= C128_DEV_BAD_BLOCK;
   }
