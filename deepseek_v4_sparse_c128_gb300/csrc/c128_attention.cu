@@ -80,6 +80,9 @@ constexpr int kTmemCols = 512, kTmemS = 256, kTmemL = 384;  // O in columns 0..2
 
 enum : int { kFirst = 1, kLast = 2, kEnd = 4, kRunShift = 3 };  // of its stretch of one request's tiles; above, the stretch's number mod 4
 
+// In the place of a part's log-sum-exp: the part's CTA gave up. (None comes out so: a reference or a sum that is infinite makes NaN.)
+constexpr float kNotThere = INFINITY;
+
 struct Task {  // a request that a CTA starts and leaves to the columns behind it, if parts > 0
   int32_t request, parts, column, group_heads;
 };
@@ -411,6 +414,16 @@ __device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams
   if (lane == 0) mbar_arrive(&sm.o_free);
 }
 
+// The end of a CTA whose wait ran out. What it has in the workspace may be of any call: its parts are marked, and the
+// requests that they are of are not joined.
+__device__ __noinline__ void give_up(const DecodeSmem& sm, uint8_t* workspace, int all_heads, unsigned int* err) {
+  if (threadIdx.x == 0) atomicOr(err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
+  const int column = blockIdx.x / sm.lay.groups, heads = min(sm.group_heads, all_heads - sm.group * sm.group_heads);
+  float* lse = reinterpret_cast<float*>(workspace + sm.lay.lse_at());
+  for (int i = threadIdx.x; i < 2 * heads; i += kDecodeThreads)
+    lse[sm.lay.row(2 * column + (i >= heads), sm.group, i >= heads ? i - heads : i)] = kNotThere;
+}
+
 constexpr int kBoxHeads = 16;  // heads of a TMA load of queries
 
 template <bool ALIGN16, int HEADS>
@@ -545,8 +558,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   volatile int* const abort_flag = &sm.abort;
   // A wait of a whole warp. One that runs out sets the abort flag, and with that set every wait returns
   // at once: the warps then run on as ever, on whatever they find, to the end that `tile_flags` shows them,
-  // and no result is stored. So no lane or warp leaves a path that others count on it for, without asking
-  // all lanes after every wait whether to go on (that took 6 % of a tile's time).
+  // and no result is stored: the flag is looked at behind the last wait that a result depends on. So no lane or warp
+  // leaves a path that others count on it for, without asking all lanes after every wait whether to go on (that took 6 %
+  // of a tile's time).
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     if (!decode_wait(bar, parity, abort_flag)) *abort_flag = 1;
     __syncwarp();
@@ -1101,10 +1115,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         }
         sm.inv[odd][h] = share;
         const float lse2 = sum == 0.f ? -INFINITY : to + log2f(sum);
-        if (!whole)
-          reinterpret_cast<float*>(p.workspace + sm.lay.lse_at())[sm.lay.row(part, sm.group, h)] = lse2;
-        else if (p.lse != nullptr)
-          p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
+        if (!*abort_flag) {
+          if (!whole)
+            reinterpret_cast<float*>(p.workspace + sm.lay.lse_at())[sm.lay.row(part, sm.group, h)] = lse2;
+          else if (p.lse != nullptr)
+            p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
+        }
       }
       if (lead && w == 0 && lane == 0) sm.done_request[odd] = request, sm.done_part[odd] = part;
       warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
@@ -1131,7 +1147,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   }
   tmem_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
+  if (*abort_flag) give_up(sm, p.workspace, p.heads, p.err);
   if (warp == kMmaWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
@@ -1179,7 +1195,7 @@ __device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout
   const bool real = head + hh < p.heads;
   auto lse_of = [&](int k) { return k < t.parts && real ? lse[row(k) + h + hh] : -INFINITY; };
   const float sink = p.sink != nullptr && real ? __ldcg(p.sink + head + hh) * kLog2e : -INFINITY;
-  float top = sink;
+  float top = -INFINITY;
   bool nan = false;
   for (int k = lane >> 2; k < t.parts; k += 8) {
     const float x = lse_of(k);
@@ -1191,6 +1207,8 @@ __device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), o) != 0;
   }
+  const unsigned gone = __ballot_sync(0xffffffffu, top == kNotThere);  // bit e: of head e, and on in steps of 4
+  top = fmaxf(top, sink);
   const float shift = nan ? NAN : top == -INFINITY ? 0.f : top;
   float acc[BLOCKS][4] = {};
   float sum = lane < 4 ? ex2_approx(sink - shift) : 0.f;  // lane 4k + hh: of head hh, some of the parts
@@ -1222,6 +1240,7 @@ __device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout
   for (int e = 0; e < 4; ++e) {
     const float f = __shfl_sync(0xffffffffu, inv, e);
     if (head + e >= p.heads) break;
+    if (gone >> e & 1) continue;
     const int64_t at = t.request * p.out_stride_r + (head + e) * p.out_stride_h + 32 * block + lane;
 #pragma unroll
     for (int b = 0; b < BLOCKS; ++b) {
@@ -1230,7 +1249,7 @@ __device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout
       else static_cast<uint16_t*>(p.out)[at + 32 * b] = static_cast<uint16_t>(pack_bf16x2(x, 0.f));
     }
   }
-  if (p.lse != nullptr && block == 0 && lane < 4 && real)
+  if (p.lse != nullptr && block == 0 && lane < 4 && real && !(gone >> lane & 1))
     p.lse[t.request * p.lse_stride_r + (head + lane) * p.lse_stride_h] =
         sum == 0.f ? -INFINITY : (shift + log2f(sum)) * 0.69314718055994531f;
 }

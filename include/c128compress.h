@@ -424,7 +424,8 @@ int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* que
  * Device error bits: C128_DEV_BAD_BT_COL - kv_lens[r] > MB*bs (the entries behind are left out);
  * C128_DEV_BAD_BLOCK - a block id outside [0, NKB) (its entries are left out); C128_DEV_BAD_LENGTH
  * - a negative kv_lens[r] (counts as 0); C128_DEV_TIMEOUT - a wait inside the kernel ran out: some of
- * the results are not there. R * (MB*bs / 64 + 2) < 2^31, else C128_ERR_ARG.
+ * the results are not there, and each value of out and lse is the result or what it was before.
+ * R * (MB*bs / 64 + 2) < 2^31, else C128_ERR_ARG.
  */
 int c128_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
                           const c128_tensor_t* block_table, const c128_tensor_t* kv_lens, float scale,
@@ -434,8 +435,8 @@ int c128_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, 
 /*
  * Test of the failure handling, for tests only: c128_decode_attention, except that CTA 0 never learns of
  * its tiles. Every wait of that kernel is bounded (about 1 s), so CTA 0 gives up and ends with
- * C128_DEV_TIMEOUT in the device error bits, and stores nothing; the requests (or heads, or parts of
- * requests) of other CTAs are computed as usual. The context stays usable.
+ * C128_DEV_TIMEOUT in the device error bits, and stores nothing; requests (or heads) that it shares with
+ * other CTAs are left as they were too, all others are computed as usual. The context stays usable.
  */
 int c128_debug_stall_decode_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache,
                                       int64_t kv_block_size, const c128_tensor_t* block_table,
