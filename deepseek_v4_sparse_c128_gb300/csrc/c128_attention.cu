@@ -21,9 +21,12 @@
 // sums, in fp32. (Two sums in the softmax warps' registers took 10 % longer than the product with ones.)
 //
 // The running reference m need not be the maximum: P, its sums and O are floating point, so a common
-// factor costs no precision. So m is 0 where that does, that is where every head has a score within
-// 2^+-32 of 1 in the first tile, and none above it (2^32 times 2^25 entries of 2^70 is still inside
-// the range). Else it is raised or lowered to the maximum so far, O in TMEM rescaled with it.
+// factor costs no precision while the products stay inside the range. So m is 0 where that does, that is where
+// every head has a weight within 2^+-32 of 1 in the first tile, none passes 2^32, and no value passes 2^64 (2^31
+// entries of that are 2^127). Else it is raised or lowered to the maximum so far, O in TMEM rescaled with it: then
+// no weight of this tile is above 1. Values that large are looked for where they pass through registers, in the scale
+// bytes and the rope columns. (At the other end a head's weights reach down to 2^-32, and values below 2^-92 can get
+// lost: a look for those as well took 3 % of a tile's time, and is not worth it.)
 //
 // Work is dealt out in tiles: the requests' tiles, one after the other, are cut into as many equal
 // runs as there are CTAs, so a long request is shared by many CTAs and a CTA takes many short ones. (What
@@ -148,7 +151,7 @@ struct DecodeSmem {
   uint64_t q_full, q_free, o_free, drained;
   uint64_t inv_full[2];          // `inv` and `done` of a stretch are there
   uint64_t soft;                 // barrier of the softmax warps
-  volatile int32_t off[2];       // 1 + the tile whose P in this buffer was made with a reference that is off
+  volatile int32_t off[2];       // 1 + the tile whose P in this buffer was made with a reference that is off, or will be
   int32_t done_request[2], done_part[2];
   int warp_sums[32];
   int32_t first_request, first_tile, first_entries;  // where the column's run begins, and that request's entries
@@ -300,6 +303,19 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint16_t two, float scale) {
       : "r"(h));
   v = mul2(v, make_float2(scale, scale));
   return pack_bf16x2(v.x, v.y);
+}
+// The larger magnitudes of two pairs of bf16 (under either sign).
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Whether a value is beyond what a reference of 0 allows: one of 7 scale bytes at 176 (the largest code gives 2^57.8) or
+// above, or one of two bf16 magnitudes at 2^64. The low bits of a field plus a constant carry into its highest.
+__device__ __forceinline__ bool too_large(uint2 scales, uint32_t values) {
+  const uint32_t a = ((scales.x & 0x7f7f7f7fu) + 0x50505050u) & scales.x, b = ((scales.y & 0x007f7f7fu) + 0x00505050u) & scales.y & 0x00ffffffu;
+  const uint32_t v = (values & 0x7fff7fffu) + (0x80008000u - 0x5f805f80u);
+  return (((a | b) & 0x80808080u) | (v & 0x80008000u)) != 0;
 }
 // 2^(byte - 127): the byte is the float's exponent field (0: the subnormal 2^-127).
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
@@ -782,12 +798,16 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       publish(0);
       await_room(3);
+      uint32_t large = 0;
 #pragma unroll
       for (int j = 7; j < 9; ++j) {  // the rope columns are bf16 already; the sooner the next ones are on their way, the better
         const uint4 r = take(j);
         sts16((dst_rope + buf * kTileBytes) ^ (64u * (j - 7)), r.x, r.y, r.z, r.w);
         load(j);
+        large = larger2(larger2(large, larger2(r.x, r.y)), larger2(r.z, r.w));
       }
+      // (What stands there is of tile i - 2, whose last P has been used.)
+      if (too_large(now, large)) sm.off[buf] = i + 1;
 #pragma unroll
       for (int j = 4; j < 4 + kAhead; ++j) decode(j, o[at(j)]);
 #pragma unroll

@@ -420,7 +420,9 @@ int c128_build_slot_maps(const c128_tensor_t* seq_lens, const c128_tensor_t* que
  *
  * Products take bf16 operands (the entries are exact in bf16 for scale bytes 8 .. 246; the softmax
  * weights are rounded to bf16) and add up in fp32. out is divided by the sums of the rounded weights, so
- * that of one entry is that entry; lse is of the exact ones, in fp32.
+ * that of one entry is that entry; lse is of the exact ones, in fp32. The sums are relative to the largest
+ * weight where they have to be: an entry may be of any magnitude, as long as the largest times the
+ * number of entries stays below 2^128, but values below 2^-92 can count as 0.
  * Device error bits: C128_DEV_BAD_BT_COL - kv_lens[r] > MB*bs (the entries behind are left out);
  * C128_DEV_BAD_BLOCK - a block id outside [0, NKB) (its entries are left out); C128_DEV_BAD_LENGTH
  * - a negative kv_lens[r] (counts as 0); C128_DEV_TIMEOUT - a wait inside the kernel ran out: some of
