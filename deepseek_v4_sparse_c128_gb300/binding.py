@@ -313,6 +313,14 @@ def _refs(*tensors):
     return [None if t is None else ctypes.byref(describe(t)) for t in tensors]
 
 
+def _whole(x, bits: int, what: str) -> int:
+    """x as a C integer of that many bits; ctypes would cut off what does not fit."""
+    n = int(x)
+    if n != x or not -(1 << (bits - 1)) <= n < 1 << (bits - 1):
+        raise ValueError(f"{what}: {x} is not a whole number of {bits} bits")
+    return n
+
+
 # Each operator's arguments to its C entry, name, C arguments and what the call keeps alive. `stream` is the one that the call
 # will run on.
 def _extend_block_tables(seq_lens, held, block_table, free_blocks, taken, compress_ratio: int, block_size: int,
@@ -320,7 +328,8 @@ def _extend_block_tables(seq_lens, held, block_table, free_blocks, taken, compre
     held_out = held if held_out is None else held_out
     taken_out = taken if taken_out is None else taken_out
     a = _refs(seq_lens, held, block_table, free_blocks, taken, held_out, taken_out)
-    return "c128_extend_block_tables", (*a[:5], int(compress_ratio), int(block_size), *a[5:]), ()
+    return "c128_extend_block_tables", (*a[:5], _whole(compress_ratio, 32, "compress_ratio"),
+                                        _whole(block_size, 64, "block_size"), *a[5:]), ()
 
 
 def _build_slot_maps(seq_lens, query_lens, state_table, state_block: int, kv_table, kv_block_size: int,
@@ -328,7 +337,8 @@ def _build_slot_maps(seq_lens, query_lens, state_table, state_block: int, kv_tab
                      kv_lens, stream=None):
     a = _refs(seq_lens, query_lens, state_table, kv_table, query_start, token_to_req_indices, positions, slot_mapping,
               kv_slot_mapping, kv_lens)
-    return "c128_build_slot_maps", (*a[:3], int(state_block), a[3], int(kv_block_size), int(compress_ratio), *a[4:]), ()
+    return "c128_build_slot_maps", (*a[:3], _whole(state_block, 64, "state_block"), a[3], _whole(kv_block_size, 64, "kv_block_size"),
+                                    _whole(compress_ratio, 32, "compress_ratio"), *a[4:]), ()
 
 
 def _scratch(num_heads: int, device, stream):
@@ -346,7 +356,8 @@ def _decode_attention(q, k_cache, kv_block_size: int, block_table, kv_lens, scal
     if workspace is None:
         workspace = _scratch(q.shape[1], q.device, stream)
     a = _refs(q, k_cache, block_table, kv_lens, sink, out, lse, workspace)
-    return "c128_decode_attention", (*a[:2], int(kv_block_size), *a[2:4], float(scale), *a[4:]), (workspace,)
+    return "c128_decode_attention", (*a[:2], _whole(kv_block_size, 64, "kv_block_size"), *a[2:4], float(scale),
+                                     *a[4:]), (workspace,)
 
 
 def _merge_attention(part_out, part_lse, out, lse=None, stream=None):
@@ -361,8 +372,9 @@ class PreparedOp:
     """One of the operators below with its descriptors built once, for repeated calls on the same
     tensors: ``PreparedOp("decode_attention", q, k_cache, ...)`` takes the arguments of the function
     of that name, and calling the object is a single C-ABI call. The tensors must stay alive and keep
-    their storage; the stream is fixed when the object is built (default: the current torch stream).
-    A ``decode_attention`` without a ``workspace`` gets one of its own, kept with the object."""
+    their storage; the stream is fixed when the object is built (default: the current torch stream),
+    and the device that was current then has to be current in every call. A ``decode_attention``
+    without a ``workspace`` gets one of its own, kept with the object."""
 
     def __init__(self, op: str, *args, stream=None, **kw):
         self._name, c_args, owned = _OPS[op](*args, stream=stream, **kw)
@@ -403,7 +415,7 @@ def build_slot_maps(seq_lens, query_lens, state_table, state_block: int, kv_tabl
 def decode_attention_workspace(num_heads: int) -> int:
     """Bytes of workspace a decode_attention call with ``num_heads`` heads needs."""
     n = ctypes.c_int64(0)
-    _check(lib().c128_decode_attention_workspace(int(num_heads), ctypes.byref(n)), "c128_decode_attention_workspace")
+    _check(lib().c128_decode_attention_workspace(_whole(num_heads, 64, "num_heads"), ctypes.byref(n)), "c128_decode_attention_workspace")
     return n.value
 
 

@@ -97,3 +97,27 @@ def test_own_workspace_belongs_to_the_stream_of_the_call(cuda, stream, owner):
     binding.decode_attention(*_decode_args(), stream=stream)
     assert cuda["empty"] == [(5000, owner)]
     assert cuda["stream"].cuda_stream == 11
+
+
+def test_numbers_that_a_c_integer_does_not_hold_are_refused(cuda):
+    """They would reach the library cut to 32 or 64 bits, or to a whole number, as another ratio or block size."""
+    import torch
+    i32 = lambda *s: FakeTensor(s, torch.int32)
+    i64 = lambda *s: FakeTensor(s, torch.int64)
+    extend = lambda ratio, block: binding.extend_block_tables(i32(5), i32(5), i32(5, 9), i32(40), i64(1), ratio, block)
+    maps = lambda sb, kb, ratio: binding.build_slot_maps(i32(5), i32(5), i32(5, 9), sb, i32(5, 9), kb, ratio, i32(6), i32(7), i64(7),
+                                                         i64(7), i64(7), i32(5))
+    for ratio, block in [((1 << 32) + 4, 8), (4, (1 << 64) + 8), (4, 8.5), (4.5, 8), (-(1 << 31) - 1, 8)]:
+        with pytest.raises(ValueError, match="whole number"):
+            extend(ratio, block)
+    for sb, kb, ratio in [((1 << 64) + 8, 64, 128), (8, 63.5, 128), (8, 64, (1 << 32) + 128)]:
+        with pytest.raises(ValueError, match="whole number"):
+            maps(sb, kb, ratio)
+    a = list(_decode_args())
+    a[2] = (1 << 64) + 2
+    with pytest.raises(ValueError, match="whole number"):
+        binding.decode_attention(*a)
+    assert cuda["calls"] == []
+    extend(4, 8.0), maps(8, 64, 128)
+    assert [c[0] for c in cuda["calls"]] == ["c128_extend_block_tables", "c128_build_slot_maps"]
+    assert [x.value for x in cuda["calls"][0][1][5:7]] == [4, 8]
