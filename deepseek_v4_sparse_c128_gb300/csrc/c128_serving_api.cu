@@ -72,6 +72,14 @@ int check_rows(const c128_tensor_t* t, int ndim, int32_t* f32) {
   C128_TRY(check_data(t));
   return aligned(t->data, 16) ? C128_OK : C128_ERR_ALIGN;
 }
+// The results [R, H, width] (width 1: [R, H]) are stored by many CTAs at once, so no two rows may share an element: the
+// rows of one of the two dimensions have to lie between two neighbours of the other.
+int check_apart(const c128_tensor_t* t, int64_t width) {
+  int64_t inner = t->shape[1], at = t->stride[1], outer = t->stride[0];
+  if (t->shape[0] <= 1 || t->shape[1] <= 1) return C128_OK;
+  if (at > outer) at = t->stride[0], outer = t->stride[1], inner = t->shape[0];
+  return (outer - width) / at >= inner - 1 ? C128_OK : C128_ERR_STRIDE;
+}
 // Stride of dimension i, 0 where it has a single index (whatever the descriptor says there).
 int64_t step(const c128_tensor_t* t, int i) { return t->shape[i] > 1 ? t->stride[i] : 0; }
 
@@ -94,6 +102,7 @@ int decode(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_bloc
   if (H > c128::kMaxDecodeHeads) return C128_ERR_UNSUPPORTED;
   C128_TRY(check_rows(out, 3, &p.out_f32));
   if (out->shape[0] != R || out->shape[1] != H) return C128_ERR_SHAPE;
+  if (R > 0 && H > 0) C128_TRY(check_apart(out, c128::kHead));
   // the cache as the compressor takes it (slots of 584 bytes or more, a block a flat byte range)
   C128_TRY(check_desc(k_cache, C128_U8, 3));
   if (kv_block_size < 1 || kv_block_size > kMaxCount || k_cache->shape[1] != kv_block_size) return C128_ERR_ARG;
@@ -110,6 +119,7 @@ int decode(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_bloc
   if (lse != nullptr) {
     C128_TRY(check_lse(lse, 2));
     if (lse->shape[0] != R || lse->shape[1] != H) return C128_ERR_SHAPE;
+    if (R > 0 && H > 0) C128_TRY(check_apart(lse, 1));
   }
   C128_TRY(check_desc(workspace, C128_U8, 1));
   C128_TRY(check_array(workspace, C128_U8, workspace->shape[0]));
@@ -272,9 +282,11 @@ int c128_merge_attention(const c128_tensor_t* part_out, const c128_tensor_t* par
   if (part_lse->shape[0] != P || part_lse->shape[1] != R || part_lse->shape[2] != H) return C128_ERR_SHAPE;
   C128_TRY(check_rows(out, 3, &p.out_f32));
   if (out->shape[0] != R || out->shape[1] != H) return C128_ERR_SHAPE;
+  if (R > 0 && H > 0) C128_TRY(check_apart(out, c128::kHead));
   if (lse != nullptr) {
     C128_TRY(check_lse(lse, 2));
     if (lse->shape[0] != R || lse->shape[1] != H) return C128_ERR_SHAPE;
+    if (R > 0 && H > 0) C128_TRY(check_apart(lse, 1));
   }
   if (R == 0 || H == 0) return C128_OK;
   p.part = part_out->data;

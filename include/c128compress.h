@@ -332,7 +332,8 @@ int c128_debug_stall_first_window_ex(const c128_config_t* config,
  * (read with c128_device_errors; a stream without a workspace gets one, so the first call on a
  * stream that is being captured returns C128_ERR_CAPTURE unless c128_reserve_workspace came before).
  * All tensors live on the current device. Unless a call says otherwise, an output overlaps no input
- * and no other output.
+ * and no other output, and (C128_ERR_STRIDE) the rows of an output do not overlap one another: those of
+ * one dimension lie between two neighbours of the other.
  */
 
 /*
