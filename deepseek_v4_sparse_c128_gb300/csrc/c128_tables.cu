@@ -3,10 +3,11 @@
 // (or tokens) that finds each one's request in the sums.
 //
 // Decode steps make a few kilobytes of either, so what counts there is the number of dependent trips
-// to memory: one launch, in which every CTA sums the requests for itself (thousands per round, a few KB
+// to memory: one launch, in which every CTA sums the requests for itself (512 or 1024 in a round, a few KB
 // that all CTAs read from L2) instead of a scan kernel and a second one behind it, then looks its
-// own blocks or tokens up in shared memory. Nothing is accumulated across CTAs: no atomics but the
-// error bits, and no scratch.
+// own blocks or tokens up in shared memory. Nothing is accumulated across CTAs, and there is no scratch. The
+// only atomics are the error bits and, within a CTA, the minimum that finds the first request that the list cannot
+// serve: the order of neither matters.
 //
 // Measured, device time per call back to back: tables of 256 requests that each grow by one token 2.1 us, of
 // 16 requests that get all blocks of up to a million tokens (1.1 M blocks, 9 MB) 4.0 us; maps of 256 rows
@@ -86,8 +87,7 @@ __device__ __forceinline__ void load_run(const int32_t* v, int64_t r, int64_t n,
 // One CTA to an SM, and a request to a thread: with 512 threads, two CTAs to an SM and four requests 1.1 M blocks took
 // 6.3 us, not 4.0, and a step of 256 requests 2.2, not 2.1.
 constexpr int kExtendThreads = 1024;
-constexpr int kPerThread = 1;  // requests of a round
-constexpr int kExtendChunk = kPerThread * kExtendThreads;
+constexpr int kExtendChunk = kExtendThreads;         // requests of a round
 constexpr int kTileBlocks = 8;                       // blocks of a tile per thread, their loads in flight together
 constexpr int kExtendTile = kExtendThreads * kTileBlocks;
 
@@ -112,58 +112,34 @@ __global__ void __launch_bounds__(kExtendThreads) extend_kernel(const ExtendPara
 
   for (int64_t c = 0; c < rounds; ++c) {
     if (threadIdx.x == 0) s_fail = UINT_MAX;
-    const int64_t r = c * kExtendChunk + threadIdx.x * kPerThread;
-    int len[kPerThread], held[kPerThread];
-    uint32_t need[kPerThread], sum = 0;
-    load_run(p.seq_lens, r, p.requests, len);
-    load_run(p.held, r, p.requests, held);
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      if (len[k] < 0) err |= C128_DEV_BAD_LENGTH;
-      const uint32_t entries = divide(static_cast<uint32_t>(max(len[k], 0)), p.ratio);
-      const uint32_t full = divide(entries, p.block), needed = full + (full * p.block.value != entries);  // <= INT_MAX
-      need[k] = 0;
-      if (held[k] < 0) {
-        err |= C128_DEV_BAD_LENGTH;
-      } else if (needed > static_cast<uint32_t>(held[k])) {
-        if (needed > p.columns) err |= C128_DEV_BAD_BT_COL;
-        else need[k] = needed - static_cast<uint32_t>(held[k]);
-      }
-      sum = add_clipped(sum, need[k]);
+    const int64_t r = c * kExtendChunk + threadIdx.x;
+    const int len = r < p.requests ? p.seq_lens[r] : 0, held = r < p.requests ? p.held[r] : 0;
+    if (len < 0) err |= C128_DEV_BAD_LENGTH;
+    const uint32_t entries = divide(static_cast<uint32_t>(max(len, 0)), p.ratio);
+    const uint32_t full = divide(entries, p.block), needed = full + (full * p.block.value != entries);  // <= INT_MAX
+    uint32_t need = 0;
+    if (held < 0) {
+      err |= C128_DEV_BAD_LENGTH;
+    } else if (needed > static_cast<uint32_t>(held)) {
+      if (needed > p.columns) err |= C128_DEV_BAD_BT_COL;
+      else need = needed - static_cast<uint32_t>(held);
     }
     uint32_t total;
     // (a barrier, also for s_fail)
-    uint32_t off = add_clipped(base, block_exclusive_sum<kExtendThreads>(sum, s_warp, &total));
-    uint32_t first = off;
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      const uint32_t next = add_clipped(first, need[k]);
-      if (need[k] > 0 && next > avail) {  // avail < INT_MAX
-        err |= C128_DEV_NO_FREE_BLOCK;
-        atomicMin(&s_fail, first);
-        break;
-      }
-      first = next;
+    const uint32_t off = add_clipped(base, block_exclusive_sum<kExtendThreads>(need, s_warp, &total));
+    if (need > 0 && add_clipped(off, need) > avail) {  // avail < INT_MAX
+      err |= C128_DEV_NO_FREE_BLOCK;
+      atomicMin(&s_fail, off);
     }
     __syncthreads();
     // Blocks are given up to the first request that the list cannot serve, and none after it: the sum
     // only grows, so later rounds find nothing left either.
     const uint32_t end = min(s_fail, add_clipped(base, total));
     const uint32_t round_given = base <= avail ? end - base : 0;
-    int out[kPerThread];
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      const int i = threadIdx.x * kPerThread + k;
-      s_start[i] = static_cast<int>(min(off - base, round_given));
-      s_held[i] = held[k];
-      out[k] = held[k] + (need[k] <= round_given && off - base <= round_given - need[k] ? static_cast<int>(need[k]) : 0);
-      off = add_clipped(off, need[k]);
-    }
-    if (write_counts && c % gridDim.x == blockIdx.x) {
-#pragma unroll
-      for (int k = 0; k < kPerThread; ++k)
-        if (r + k < p.requests) p.held_out[r + k] = out[k];
-    }
+    s_start[threadIdx.x] = static_cast<int>(min(off - base, round_given));
+    s_held[threadIdx.x] = held;
+    if (write_counts && c % gridDim.x == blockIdx.x && r < p.requests)
+      p.held_out[r] = held + (need <= round_given && off - base <= round_given - need ? static_cast<int>(need) : 0);
     __syncthreads();
     if (write_table) {
       const int n = static_cast<int>(min(static_cast<int64_t>(kExtendChunk), p.requests - c * kExtendChunk));

@@ -358,7 +358,7 @@ int c128_debug_stall_first_window_ex(const c128_config_t* config,
  * C128_DEV_BAD_BT_COL - a request needs more than MB blocks (it gets none, the others are served);
  * C128_DEV_BAD_LENGTH - a negative length (counts as 0) or held count (the request gets none), or
  * taken outside [0, F] (nobody gets any).
- * Results do not depend on scheduling: no atomics, the same inputs give the same tables.
+ * Results do not depend on scheduling: the same inputs give the same tables.
  */
 int c128_extend_block_tables(const c128_tensor_t* seq_lens, const c128_tensor_t* held,
                              const c128_tensor_t* block_table, const c128_tensor_t* free_blocks,
