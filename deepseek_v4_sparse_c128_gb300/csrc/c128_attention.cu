@@ -16,7 +16,7 @@
 // sums to the end. Heads are dealt out in groups of 64; a group decodes the cache for itself (the
 // second group's reads hit L2).
 //
-// P is rounded to bf16 (2^-9), and O is divided by the sums of the rounded weights: then a weight's
+// P is rounded to bf16 (2^-8), and O is divided by the sums of the rounded weights: then a weight's
 // rounding is felt only against the other entries', not at all with a single one. lse is of the exact
 // sums, in fp32. (Two sums in the softmax warps' registers took 10 % longer than the product with ones.)
 //
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             }
             if (mt == kQuarters - 1) {
 #pragma unroll
-                  for (int ks = 0; ks < kTile / 16; ++ks)
+              for (int ks = 0; ks < kTile / 16; ++ks)
                 mma(tmem + kTmemL, ones, desc64(p_at + ((buf * (kGroup * kTile * 2) + ks * 2048) >> 4)), desc_ones, !first || ks > 0);
             }
             mma_commit(&sm.k_free[buf][mt]);

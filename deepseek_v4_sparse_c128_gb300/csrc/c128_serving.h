@@ -1,5 +1,5 @@
 // Parameters and launchers of the operators around the compressor (c128_serving_api.cu checks the
-// arguments; c128_tables.cu and c128_attention.cu hold the kernels).
+// arguments; c128_tables.cu, c128_attention.cu and c128_merge.cu hold the kernels).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
