@@ -346,7 +346,8 @@ def _scratch(num_heads: int, device, stream):
     be in use by calls on its own stream that have not run yet, and goes back to calls on that stream."""
     import torch
     if stream is not None and not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # (torch takes a handle of 0 for none given, and makes a stream of its own)
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     with torch.cuda.stream(stream):  # None: the current stream
         return torch.empty(decode_attention_workspace(num_heads), dtype=torch.uint8, device=device)
 

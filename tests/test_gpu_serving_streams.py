@@ -85,3 +85,29 @@ def test_scratch_of_a_call_in_flight_is_not_handed_out(binding, how):
     assert all(bool((t == 9).all()) for t in others)
     assert binding.device_errors(s, clear=True) == 0
     check(out, lse)
+
+
+def test_a_handle_of_0_is_the_default_stream(binding):
+    """The call runs on the default stream while another is current: its scratch is the default stream's."""
+    import torch
+    args, out, lse, check = _case()
+    n = binding.decode_attention_workspace(64)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        binding.decode_attention(*args, out, lse=lse, stream=0)
+        torch.cuda.synchronize()
+        out.fill_(7)
+        mine = torch.full((n,), 5, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(SLEEP)
+        copy = mine.clone()
+        del mine
+        op = binding.PreparedOp("decode_attention", *args, out, lse=lse, stream=0)
+        op()
+        del op
+        others = [torch.full((n,), 9, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert bool((copy == 5).all()) and all(bool((t == 9).all()) for t in others)
+    assert binding.device_errors(0, clear=True) == 0
+    check(out, lse)

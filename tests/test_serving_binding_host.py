@@ -71,7 +71,8 @@ def cuda(monkeypatch):
         return FakeTensor([n], dtype)
 
     monkeypatch.setattr(torch.cuda, "stream", on)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: FakeStream(handle or 99))  # 0: one out of torch's pool
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: FakeStream(0))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: state["stream"])
     monkeypatch.setattr(torch.cuda, "current_device", lambda: state["device"])
     monkeypatch.setattr(torch, "empty", empty)
@@ -86,13 +87,13 @@ def _decode_args():
             FakeTensor([3, 9], torch.int32), FakeTensor([3], torch.int32), 0.1, FakeTensor([3, 5, 512], torch.bfloat16))
 
 
-@pytest.mark.parametrize("stream,owner", [(None, 11), (FakeStream(22), 22), (33, 33)])
+@pytest.mark.parametrize("stream,owner", [(None, 11), (FakeStream(22), 22), (33, 33), (0, 0), (FakeStream(0), 0)])
 def test_own_workspace_belongs_to_the_stream_of_the_call(cuda, stream, owner):
     """torch's allocator orders a block's uses on the stream it was allocated on: another stream's kernel would write into
     memory that queued work still uses, and its own block could be handed out again under it."""
     op = binding.PreparedOp("decode_attention", *_decode_args(), stream=stream)
     op()
-    assert cuda["empty"] == [(5000, owner)] and cuda["calls"][0][1][-1].value == owner
+    assert cuda["empty"] == [(5000, owner)] and (cuda["calls"][0][1][-1].value or 0) == owner
     cuda["empty"].clear()
     binding.decode_attention(*_decode_args(), stream=stream)
     assert cuda["empty"] == [(5000, owner)]
