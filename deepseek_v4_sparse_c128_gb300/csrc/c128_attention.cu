@@ -33,10 +33,11 @@
 // a run has of one request is called a stretch here.) A request that is cut leaves fp32 partial results in
 // the workspace, joined by a second kernel.
 //
-// Measured, device time per call with the join: 8 requests of up to 65,536 entries, 16 heads (173 MB) 62.7 us,
-// 2.75 TB/s; 48 of up to 8,192, 128 heads 59.7 us; 64 of up to 1,024, 64 heads 27.3 us; one of 1,024 12.3 us. A
-// tile takes an SM 1.48 us (16 heads) or 1.85 (64). Decoding is the longest link, on a shared memory of which the
-// products' operands take half the bandwidth and come first.
+// Measured, device time per call with the join: 8 requests of up to 65,536 entries, 16 heads (173 MB) 64.0 us,
+// 2.70 TB/s; 48 of up to 8,192, 128 heads 60.2 us; 64 of up to 1,024, 64 heads 27.7 us; one of 1,024 12.4 us. A
+// tile takes an SM 1.47 us (16 heads) or 1.87 (64). Its stages wait for one another over two buffers; decoding is the
+// longest of them, on a shared memory of which the products' operands take half the bandwidth and come first. With
+// references other than 0 (scores of a deviation of 20) 69.6, 82.0, 36.1 and 13.5 us.
 //
 // Roles of the 19 warps (each wait is bounded; five warps to a scheduler leave them 96 registers, and a
 // spill would be a trip to L2, beside the little L1 that the tiles leave):

@@ -5,7 +5,7 @@
 // 512 values, 16 per lane in two 16-byte pieces (bf16), so that each load of a warp covers 512
 // consecutive bytes and the loads of four parts are in flight before the first is used.
 //
-// Measured: 256 requests x 128 heads, 4 bf16 parts (168 MB) 25.7 us, 6.55 TB/s, 0.97 of the measured copy; one
+// Measured in a graph: 256 requests x 128 heads, 4 bf16 parts (168 MB) 25.6 us, 6.56 TB/s, 0.97 of the measured copy; one
 // request, 64 heads, 2 parts 1.8 us, which is a launch. (Weights first and values behind them 34.2 us;
 // CTAs of 256 threads, whose rows end together, 28.2, of 512 38.9, of 32 33.4; streaming loads 26.7.)
 #include <cuda_runtime.h>

@@ -9,9 +9,9 @@
 // only atomics are the error bits and, within a CTA, the minimum that finds the first request that the list cannot
 // serve: the order of neither matters.
 //
-// Measured, device time per call back to back: tables of 256 requests that each grow by one token 2.1 us, of
-// 16 requests that get all blocks of up to a million tokens (1.1 M blocks, 9 MB) 4.0 us; maps of 256 rows
-// 2.4 us, of 32 thousand tokens 2.6, of 215 thousand (6 MB) 4.1. A launch that does nothing takes about 2 us
+// Measured, device time per call in a graph: tables of 256 requests that each grow by one token 2.0 us (in place, with
+// two launches, 4.0), of 16 requests that get all blocks of up to a million tokens (1.1 M blocks, 9 MB) 3.8 us; maps of
+// 256 rows 2.3 us, of 32 thousand tokens 2.6, of 215 thousand (6 MB) 4.0. A launch that does nothing takes about 2 us
 // this way, and what is left is the chain of loads, sum, search and loads. (Sums in 64 bits, divisions
 // and several tokens to a thread took 7 to 8 us for the maps.)
 #include <cuda_runtime.h>
