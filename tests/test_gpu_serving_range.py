@@ -127,7 +127,10 @@ def test_one_far_entry_among_others(binding, where, big, reach):
     for r, n in enumerate(lens):
         k = entries(cache, block, table[r], n)
         want, want_lse, tol, tol_lse = attention(q64[r], k, 1.0, out_half=2.0 ** -24)
-        # a weight below 2^-126 of the highest is 0 in fp32
-        off = np.abs(out[r] - want) - (tol + LOST + 2.0 ** -126 * np.abs(k).sum(0))
+        # out = sum_j w_j (1 + e_j) k_j / sum_j w_j (1 + e_j), |e_j| <= 2^-8: off by up to 2^-8 sum_j p_j |k_j| for the e_j
+        # above (in tol) and 2^-8 |out| for those below, which one entry that outweighs a column's others can feel in
+        # full; 1 / (1 + e) leaves 2^-6 of that. A weight below 2^-126 of the highest is 0 in fp32.
+        rounded = 2.0 ** -8 * (1 + 2.0 ** -6) * np.abs(want)
+        off = np.abs(out[r] - want) - (tol + rounded + LOST + 2.0 ** -126 * np.abs(k).sum(0))
         assert np.isfinite(out[r]).all() and (off <= 0).all(), (r, np.unravel_index(off.argmax(), off.shape), off.max())
         assert (np.abs(lse[r] - want_lse) <= tol_lse).all(), r
