@@ -20,26 +20,35 @@ namespace {
 
 constexpr int kMergeThreads = 64;
 
+// 16 bytes past L1, and never ahead of the wait for the kernels before this one, which may be writing them. (__ldcg does
+// not say that it keeps that order.)
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // Values [c, c + 8) of a row.
 template <bool F32>
 struct Piece;
 template <>
 struct Piece<true> {
-  float4 a, b;
+  uint4 a, b;
   __device__ __forceinline__ void load(const void* row, int c) {
-    a = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + c));
-    b = __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(row) + c) + 1);
+    a = ld16(static_cast<const float*>(row) + c);
+    b = ld16(static_cast<const float*>(row) + c + 4);
   }
   __device__ __forceinline__ void add(float w, float (&acc)[8]) const {
-    acc[0] = fmaf(w, a.x, acc[0]), acc[1] = fmaf(w, a.y, acc[1]), acc[2] = fmaf(w, a.z, acc[2]), acc[3] = fmaf(w, a.w, acc[3]);
-    acc[4] = fmaf(w, b.x, acc[4]), acc[5] = fmaf(w, b.y, acc[5]), acc[6] = fmaf(w, b.z, acc[6]), acc[7] = fmaf(w, b.w, acc[7]);
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, __uint_as_float(v[i]), acc[i]);
   }
 };
 template <>
 struct Piece<false> {
   uint4 a;
   __device__ __forceinline__ void load(const void* row, int c) {
-    a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c));
+    a = ld16(static_cast<const uint16_t*>(row) + c);
   }
   __device__ __forceinline__ void add(float w, float (&acc)[8]) const {
     const uint32_t v[4] = {a.x, a.y, a.z, a.w};

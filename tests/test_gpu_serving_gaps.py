@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from deepseek_v4_sparse_c128_gb300 import inputs
-from serving_ref import cdiv
+from serving_ref import cdiv, make_cache, make_tables
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,47 @@ def test_steps_follow_one_another_without_gaps(binding, head, ratio, overlap, fm
     assert binding.device_errors(clear=True) == 0
     for rep in range(2, 18):
         assert torch.equal(caches[rep], caches[rep % 2]), rep
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("requests,heads", [(1, 16), (5, 40), (60, 8)])
+def test_attention_and_merge_follow_one_another_without_gaps(binding, requests, heads, f32):
+    """Two queries in turn through attention over two caches and the merge, the partial results in the same tensors:
+    every merge joins what was written right before it, out of place and in place."""
+    import torch
+    rng = np.random.default_rng([82, requests, heads])
+    block, lens = 64, rng.integers(1, 700, (2, requests)).astype(np.int32)
+    cuda = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    caches, tables = [], []
+    for k in range(2):
+        pages = sum(cdiv(int(n), block) for n in lens[k])
+        caches.append(cuda(make_cache(rng, pages, block)))
+        tables.append(cuda(make_tables(rng, lens[k], block, pages)))
+    q = [torch.from_numpy((2 * rng.standard_normal((requests, heads, 512))).astype(np.float32)).to(torch.bfloat16).cuda()
+         for _ in range(2)]
+    kind = torch.float32 if f32 else torch.bfloat16
+    part = torch.zeros(2, requests, heads, 512, dtype=kind, device="cuda")
+    part_lse = torch.zeros(2, requests, heads, device="cuda")
+    lens_gpu = [cuda(n) for n in lens]
+    P = binding.PreparedOp
+    attend = [[P("decode_attention", q[i], caches[k], block, tables[k], lens_gpu[k], 512 ** -0.5, part[k], lse=part_lse[k])
+               for k in range(2)] for i in range(2)]
+    reps = 24
+    outs = torch.zeros(reps, requests, heads, 512, dtype=kind, device="cuda")
+    lses = torch.zeros(reps, requests, heads, device="cuda")
+    merges = [P("merge_attention", part, part_lse, outs[r], lse=lses[r]) for r in range(reps)]
+    in_place = P("merge_attention", part, part_lse, part[1], lse=part_lse[1])
+    for r in range(2):                                       # each by itself
+        for call in (*attend[r], merges[r]):
+            call()
+            torch.cuda.synchronize()
+    assert not torch.equal(outs[0], outs[1])
+    for r in range(2, reps):
+        for call in (*attend[r % 2], merges[r]):
+            call()
+        in_place()
+        outs[r][0, 0].copy_(part[1][0, 0])                   # a row of the merge in place
+    torch.cuda.synchronize()
+    assert binding.device_errors(clear=True) == 0
+    for r in range(2, reps):
+        assert torch.equal(outs[r], outs[r % 2]) and torch.equal(lses[r], lses[r % 2]), r
