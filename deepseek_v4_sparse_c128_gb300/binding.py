@@ -46,6 +46,9 @@ EXPORTS = (
     "c128_decode_attention_workspace",
     "c128_debug_stall_decode_attention",
     "c128_merge_attention",
+    "c128_build_cos_sin",
+    "c128_rotate",
+    "c128_norm_rope_store",
 )
 
 
@@ -66,6 +69,26 @@ class Config(ctypes.Structure):
 def config(head_dim=512, compress_ratio=128, overlap=0, state_width=None, cache_format=0, rope_head_dim=64) -> Config:
     sw = state_width if state_width is not None else head_dim * (1 + overlap)
     return Config(head_dim, rope_head_dim, compress_ratio, overlap, sw, cache_format)
+
+
+ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN = 0, 1, 2   # scalings of c128_rope_t
+ROPE_PAIRS, ROPE_HALVES = 0, 1                 # layouts of c128_rotate
+_SCALINGS = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "yarn": ROPE_YARN}
+
+
+class Rope(ctypes.Structure):
+    """c128_rope_t: theta, factor, original_positions, beta_fast, beta_slow, magnitude, scaling."""
+    _fields_ = [("theta", ctypes.c_double), ("factor", ctypes.c_double), ("original_positions", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double),
+                ("scaling", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+def rope(theta=10000.0, scaling="none", factor=1.0, original_positions=65536, beta_fast=32.0, beta_slow=1.0,
+         magnitude=1.0) -> Rope:
+    """How positions turn, for build_cos_sin; ``scaling`` is "none", "linear" or "yarn"."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling: {scaling!r} is none of {', '.join(_SCALINGS)}")
+    return Rope(theta, factor, original_positions, beta_fast, beta_slow, magnitude, _SCALINGS[scaling], 0)
 
 
 class Info(ctypes.Structure):
@@ -124,6 +147,9 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     L.c128_debug_stall_decode_attention.argtypes = L.c128_decode_attention.argtypes
     L.c128_decode_attention_workspace.argtypes = [i64, ctypes.POINTER(i64)]
     L.c128_merge_attention.argtypes = [T, T, T, T, vp]
+    L.c128_build_cos_sin.argtypes = [ctypes.POINTER(Rope), i64, T, vp]
+    L.c128_rotate.argtypes = [T, T, T, i64, i32, i32, T, vp]
+    L.c128_norm_rope_store.argtypes = [T, T, ctypes.c_float, T, T, T, T, T, T, T, i64, vp]
     for name in EXPORTS:
         if name != "c128_status_string":
             getattr(L, name).restype = ctypes.c_int
@@ -365,8 +391,26 @@ def _merge_attention(part_out, part_lse, out, lse=None, stream=None):
     return "c128_merge_attention", (*_refs(part_out, part_lse, out, lse),), ()
 
 
+def _build_cos_sin(rope: Rope, first_position: int, cos_sin_cache, stream=None):
+    return "c128_build_cos_sin", (ctypes.byref(rope), _whole(first_position, 64, "first_position"), *_refs(cos_sin_cache)), (rope,)
+
+
+def _rotate(x, positions, cos_sin_cache, out=None, first_column: int = 0, layout: int = ROPE_PAIRS, inverse: bool = False,
+            stream=None):
+    a = _refs(x, positions, cos_sin_cache, x if out is None else out)
+    return "c128_rotate", (*a[:3], _whole(first_column, 64, "first_column"), _whole(layout, 32, "layout"), int(bool(inverse)),
+                           a[3]), ()
+
+
+def _norm_rope_store(positions, slot_mapping, eps: float, cos_sin_cache, q=None, q_w=None, q_out=None, k=None, k_w=None,
+                     k_cache=None, kv_block_size: int = 0, stream=None):
+    a = _refs(positions, slot_mapping, cos_sin_cache, q, q_w, q if q_out is None else q_out, k, k_w, k_cache)
+    return "c128_norm_rope_store", (*a[:2], float(eps), *a[2:], _whole(kv_block_size, 64, "kv_block_size")), ()
+
+
 _OPS = {"extend_block_tables": _extend_block_tables, "build_slot_maps": _build_slot_maps,
-        "decode_attention": _decode_attention, "merge_attention": _merge_attention}
+        "decode_attention": _decode_attention, "merge_attention": _merge_attention,
+        "build_cos_sin": _build_cos_sin, "rotate": _rotate, "norm_rope_store": _norm_rope_store}
 
 
 class PreparedOp:
@@ -441,6 +485,28 @@ def merge_attention(part_out, part_lse, out, lse=None, stream=None) -> None:
     """Join attentions over different sets of entries by their log-sum-exp (c128_merge_attention in
     include/c128compress.h); ``out`` and ``lse`` are written."""
     PreparedOp("merge_attention", part_out, part_lse, out, lse=lse, stream=stream)()
+
+
+def build_cos_sin(rope: Rope, first_position: int, cos_sin_cache, stream=None) -> None:
+    """Cosines and sines of the positions from ``first_position`` on, a row each, into ``cos_sin_cache``
+    (c128_build_cos_sin in include/c128compress.h). ``rope``: see rope()."""
+    PreparedOp("build_cos_sin", rope, first_position, cos_sin_cache, stream=stream)()
+
+
+def rotate(x, positions, cos_sin_cache, out=None, first_column: int = 0, layout: int = ROPE_PAIRS, inverse: bool = False,
+           stream=None) -> None:
+    """Turn part of every head of ``x`` [T, H, D] by its token's position, or back (c128_rotate in
+    include/c128compress.h), into ``out`` or, without one, in place."""
+    PreparedOp("rotate", x, positions, cos_sin_cache, out=out, first_column=first_column, layout=layout, inverse=inverse,
+               stream=stream)()
+
+
+def norm_rope_store(positions, slot_mapping, eps: float, cos_sin_cache, q=None, q_w=None, q_out=None, k=None, k_w=None,
+                    k_cache=None, kv_block_size: int = 0, stream=None) -> None:
+    """Normalise and turn a step's queries ``q`` (into ``q_out`` or, without one, in place) and its keys ``k``, which
+    become entries of ``k_cache`` (c128_norm_rope_store in include/c128compress.h). Either may be left out."""
+    PreparedOp("norm_rope_store", positions, slot_mapping, eps, cos_sin_cache, q=q, q_w=q_w, q_out=q_out, k=k, k_w=k_w,
+               k_cache=k_cache, kv_block_size=kv_block_size, stream=stream)()
 
 
 def call_status(*args, **kw) -> int:

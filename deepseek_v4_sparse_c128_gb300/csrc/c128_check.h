@@ -1,8 +1,16 @@
 // Descriptor checks shared by the entry points (host only, nothing here touches CUDA).
 #pragma once
+#include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "c128_internal.h"
 #include "c128compress.h"
+
+#define C128_TRY(expr)         \
+  do {                         \
+    const int rc_ = (expr);    \
+    if (rc_ != C128_OK) return rc_; \
+  } while (0)
 
 namespace c128 {
 namespace check {
@@ -33,11 +41,93 @@ inline int check_vector(const c128_tensor_t* t, int dtype, int64_t n) {
 }
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+constexpr int64_t kMaxCount = 0x7fffffffLL;
+
+// Element size of a descriptor's type.
+inline uintptr_t item_bytes(const c128_tensor_t* t) {
+  switch (t->dtype) {
+    case C128_I64: return 8;
+    case C128_I32: case C128_F32: return 4;
+    case C128_BF16: return 2;
+    default: return 1;
+  }
+}
+
+// A vector of n elements of one type, aligned to its elements.
+inline int check_array(const c128_tensor_t* t, int dtype, int64_t n) {
+  C128_TRY(check_vector(t, dtype, n));
+  return aligned(t->data, item_bytes(t)) ? C128_OK : C128_ERR_ALIGN;
+}
+
+// A block table [requests, columns] whose rows may be padded; its row stride in *stride.
+inline int check_table(const c128_tensor_t* t, int64_t requests, int64_t* stride) {
+  C128_TRY(check_desc(t, C128_I32, 2));
+  if (t->shape[0] != requests || t->shape[1] > kMaxCount) return C128_ERR_SHAPE;
+  *stride = t->shape[1];
+  if (numel(t) == 0) return C128_OK;
+  if (t->shape[1] > 1 && t->stride[1] != 1) return C128_ERR_STRIDE;
+  if (t->shape[0] > 1 && t->stride[0] < t->shape[1]) return C128_ERR_STRIDE;
+  C128_TRY(check_data(t));
+  if (!aligned(t->data, 4)) return C128_ERR_ALIGN;
+  *stride = t->shape[0] > 1 ? t->stride[0] : t->shape[1];
+  return C128_OK;
+}
+
+// A statistic [.., R, H] fp32 with positive strides of any order.
+inline int check_lse(const c128_tensor_t* t, int ndim) {
+  C128_TRY(check_desc(t, C128_F32, ndim));
+  if (numel(t) == 0) return C128_OK;
+  for (int i = 0; i < ndim; ++i)
+    if (t->shape[i] > 1 && t->stride[i] < 1) return C128_ERR_STRIDE;
+  C128_TRY(check_data(t));
+  return aligned(t->data, 4) ? C128_OK : C128_ERR_ALIGN;
+}
+
+// Rows of 512 values [.., R, H, 512], bf16 or (where `f32` is not NULL) fp32, each row starting on a
+// 16-byte boundary.
+inline int check_rows(const c128_tensor_t* t, int ndim, int32_t* f32) {
+  if (t == nullptr) return C128_ERR_NULL_PTR;
+  const bool is_f32 = t->dtype == C128_F32;
+  C128_TRY(check_desc(t, f32 != nullptr && is_f32 ? C128_F32 : C128_BF16, ndim));
+  if (f32 != nullptr) *f32 = is_f32 ? 1 : 0;
+  if (t->shape[ndim - 1] != kHead) return C128_ERR_UNSUPPORTED;
+  if (numel(t) == 0) return C128_OK;  // its strides say nothing
+  if (t->stride[ndim - 1] != 1) return C128_ERR_STRIDE;
+  for (int i = 0; i + 1 < ndim; ++i) {
+    if (t->shape[i] > 1 && t->stride[i] < kHead) return C128_ERR_STRIDE;
+    if (t->shape[i] > 1 && (t->stride[i] * item_bytes(t)) % 16 != 0) return C128_ERR_ALIGN;
+  }
+  C128_TRY(check_data(t));
+  return aligned(t->data, 16) ? C128_OK : C128_ERR_ALIGN;
+}
+// The results [R, H, width] (width 1: [R, H]) are stored by many CTAs at once, so no two rows may share an element: the
+// rows of one of the two dimensions have to lie between two neighbours of the other.
+inline int check_apart(const c128_tensor_t* t, int64_t width) {
+  int64_t inner = t->shape[1], at = t->stride[1], outer = t->stride[0];
+  if (t->shape[0] <= 1 || t->shape[1] <= 1) return C128_OK;
+  if (at > outer) at = t->stride[0], outer = t->stride[1], inner = t->shape[0];
+  return (outer - width) / at >= inner - 1 ? C128_OK : C128_ERR_STRIDE;
+}
+// The cache as the compressor takes it: slots of 584 bytes or more, a block a flat byte range.
+inline int check_cache(const c128_tensor_t* t, int64_t block_size) {
+  C128_TRY(check_desc(t, C128_U8, 3));
+  if (block_size < 1 || block_size > kMaxCount || t->shape[1] != block_size) return C128_ERR_ARG;
+  if (t->shape[0] > kMaxCount) return C128_ERR_ARG;
+  if (t->shape[2] < kSlotBytes) return C128_ERR_SHAPE;
+  if (t->stride[2] != 1 || t->stride[1] != t->shape[2]) return C128_ERR_STRIDE;
+  if (t->shape[0] > 1 && t->stride[0] < t->shape[1] * t->shape[2]) return C128_ERR_STRIDE;
+  if ((t->shape[0] > 1 && t->stride[0] % 8 != 0) || !aligned(t->data, 16)) return C128_ERR_ALIGN;
+  return check_data(t);
+}
+// Stride of dimension i, 0 where it has a single index (whatever the descriptor says there).
+inline int64_t step(const c128_tensor_t* t, int i) { return t->shape[i] > 1 ? t->stride[i] : 0; }
+
+inline int done(cudaError_t e) { return e == cudaSuccess ? C128_OK : C128_ERR_CUDA; }
+
+inline bool partly_overlap(const void* a, const void* b, int64_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x != y && (x < y ? y - x : x - y) < static_cast<uintptr_t>(bytes);
+}
+
 }  // namespace check
 }  // namespace c128
-
-#define C128_TRY(expr)         \
-  do {                         \
-    const int rc_ = (expr);    \
-    if (rc_ != C128_OK) return rc_; \
-  } while (0)

@@ -468,6 +468,110 @@ int c128_decode_attention_workspace(int64_t num_heads, int64_t* bytes);
 int c128_merge_attention(const c128_tensor_t* part_out, const c128_tensor_t* part_lse,
                          const c128_tensor_t* out, const c128_tensor_t* lse, c128_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Around the attention of recent tokens: what makes a step's queries and the entries of its tokens, the
+ * rotations that carry their positions, and the attention over the last tokens. The rules are those of
+ * the calls above. A token with slot_mapping[t] < 0 or positions[t] < 0 (a batch padded to a captured size)
+ * is skipped: its rows are left as they were. So is a token whose indices do not fit, which is reported.
+ */
+
+/*
+ * c128_rope_t — how far each pair of columns turns with a position. Pair i of the R / 2 has the step
+ * f_i = theta^(-2i/R) radians per position, changed by the scaling:
+ *   C128_ROPE_PLAIN   f_i
+ *   C128_ROPE_LINEAR  f_i / factor
+ *   C128_ROPE_YARN    f_i (1 - g_i) + f_i / factor g_i, as the YaRN paper has it ("NTK by parts"): with
+ *                     pair(b) = R ln(original_positions / (2 pi b)) / (2 ln theta), the pair that turns b
+ *                     times over the original positions, low = max(floor(pair(beta_fast)), 0), high =
+ *                     min(ceil(pair(beta_slow)), R - 1), g_i = (i - low) / max(high - low, 0.001) cut
+ *                     to [0, 1]
+ * `magnitude` multiplies every cosine and sine (YaRN's attention factor; 1 for none).
+ */
+enum {
+    C128_ROPE_PLAIN = 0,
+    C128_ROPE_LINEAR = 1,
+    C128_ROPE_YARN = 2,
+};
+typedef struct c128_rope {
+    double theta;              /* > 1 */
+    double factor;             /* > 0; plain: not used */
+    double original_positions; /* the rest but magnitude: yarn only. > 0 */
+    double beta_fast, beta_slow; /* > 0 */
+    double magnitude;          /* finite */
+    int32_t scaling;           /* C128_ROPE_* */
+    int32_t reserved;          /* 0 */
+} c128_rope_t;
+
+/*
+ * c128_build_cos_sin — the table that the other calls take as cos_sin_cache: row j holds the cosines of
+ * position first_position + j's R / 2 angles, then their sines.
+ *
+ *   cos_sin_cache [MP, R] fp32  stride[1] == 1, stride[0] >= R; R even, 2 .. 512
+ *   first_position        0 <= first_position, first_position + MP <= 2^32
+ *
+ * Angles are kept as 64-bit fractions of a turn, which whole turns drop out of without rounding, so far
+ * positions are as exact as near ones: an angle is within 2^-30 + 2^-48 * (its turns) of position * step,
+ * which is the rounding of the steps to 64 bits, and each value within 2^-22 of its own size for that angle.
+ */
+int c128_build_cos_sin(const c128_rope_t* rope, int64_t first_position, const c128_tensor_t* cos_sin_cache,
+                       c128_stream_t stream);
+
+/*
+ * c128_rotate — turn columns first_column .. first_column + R - 1 of every head by its token's position:
+ *   (u, v) -> (u cos - v sin, v cos + u sin)     inverse: (u cos + v sin, v cos - u sin)
+ * where (u, v) are columns 2i and 2i + 1 of those (C128_ROPE_PAIRS) or i and i + R/2 (C128_ROPE_HALVES).
+ * The other columns are copied, or stay where `out` is `x` itself. The inverse takes the position out of
+ * attention results, which carry it because entries are values too.
+ *
+ *   x             [T, H, D]  bf16 or fp32, stride[2] == 1, other strides >= D
+ *   positions     [T]        int64; < 0: the token is skipped
+ *   cos_sin_cache [MP, R]    fp32, as c128_build_cos_sin makes it; R even, 2 .. D - first_column
+ *   out           [T, H, D]  type as x; x itself (with its strides), else no overlap
+ *
+ * Sums in fp32 (each product rounded), rounded once to the type. H * D < 2^31, T < 2^31.
+ * Device error bits: C128_DEV_BAD_COS_ROW - positions[t] >= MP (the token is skipped).
+ */
+enum {
+    C128_ROPE_PAIRS = 0,
+    C128_ROPE_HALVES = 1,
+};
+int c128_rotate(const c128_tensor_t* x, const c128_tensor_t* positions, const c128_tensor_t* cos_sin_cache,
+                int64_t first_column, int32_t layout, int32_t inverse, const c128_tensor_t* out,
+                c128_stream_t stream);
+
+/*
+ * c128_norm_rope_store — a step's queries and keys: each head of q, and the key, is normalised (RMSNorm
+ * over its 512 values, times a weight if there is one) and its last 64 columns, pairs of neighbours, are
+ * turned by the token's position; the key becomes an entry of the paged cache, in the layout that the
+ * C128_FORMAT_SPARSE_FP8 compressor stores and c128_window_attention reads.
+ *   n = x * rrms * w, rrms = 1 / sqrt(mean(x^2) + eps);  (e, o) -> (e cos - o sin, o cos + e sin)
+ * Queries: the mean of squares in fp32, n and the rotation in fp32, rounded once to q_out's type. Keys:
+ * every step as compress_norm_rope_store has it behind compressed[] (at the top of this file), with k's
+ * row in its place and the position's own row of cos_sin_cache: the bytes are a pure function of the row.
+ * (Of a row with an infinity or NaN, values that are NaN get the code of NaN.)
+ *
+ *   positions     [T]           int64
+ *   slot_mapping  [T]           int64  cache slot (block*bs + offset) of the token; < 0: skipped. Two
+ *                                      tokens with the same slot race
+ *   cos_sin_cache [MP, 64]      fp32   cos in [0, 32), sin in [32, 64) of row positions[t]; stride[1] == 1
+ *   q             [T, H, 512]   bf16 or fp32, stride[2] == 1, other strides >= 512, rows 16-byte aligned;
+ *                               NULL (and q_out): no queries
+ *   q_w           [512]         fp32, 16-byte aligned; NULL: no weight
+ *   q_out         [T, H, 512]   bf16 or fp32, strides as for q; may be q itself (same type and strides)
+ *   k             [T, 512]      bf16 or fp32, stride[1] == 1, rows 16-byte aligned; NULL (and k_cache): no keys
+ *   k_w           [512]         fp32, 16-byte aligned; NULL: no weight
+ *   k_cache       [NKB, bs, W]  uint8  as for compress_norm_rope_store; kv_block_size == bs. Only the 584
+ *                               bytes of a token's slot are written
+ *
+ * T * (ceil(H / 4) + 1) < 2^31. q and k may differ in type.
+ * Device error bits: C128_DEV_BAD_COS_ROW - positions[t] >= MP; C128_DEV_BAD_KV_SLOT - slot_mapping[t] >=
+ * NKB*bs (with keys). The token is skipped, its queries too.
+ */
+int c128_norm_rope_store(const c128_tensor_t* positions, const c128_tensor_t* slot_mapping, float eps,
+                         const c128_tensor_t* cos_sin_cache, const c128_tensor_t* q, const c128_tensor_t* q_w,
+                         const c128_tensor_t* q_out, const c128_tensor_t* k, const c128_tensor_t* k_w,
+                         const c128_tensor_t* k_cache, int64_t kv_block_size, c128_stream_t stream);
+
 /* Human-readable name of a return code (static string, never NULL). */
 const char* c128_status_string(int status);
 
