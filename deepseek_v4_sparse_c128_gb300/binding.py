@@ -49,6 +49,7 @@ EXPORTS = (
     "c128_build_cos_sin",
     "c128_rotate",
     "c128_norm_rope_store",
+    "c128_window_attention",
 )
 
 
@@ -147,6 +148,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     L.c128_debug_stall_decode_attention.argtypes = L.c128_decode_attention.argtypes
     L.c128_decode_attention_workspace.argtypes = [i64, ctypes.POINTER(i64)]
     L.c128_merge_attention.argtypes = [T, T, T, T, vp]
+    L.c128_window_attention.argtypes = [T, T, i64, T, T, T, T, i64, i64, ctypes.c_float, T, T, T, T, vp]
     L.c128_build_cos_sin.argtypes = [ctypes.POINTER(Rope), i64, T, vp]
     L.c128_rotate.argtypes = [T, T, T, i64, i32, i32, T, vp]
     L.c128_norm_rope_store.argtypes = [T, T, ctypes.c_float, T, T, T, T, T, T, T, i64, vp]
@@ -408,9 +410,19 @@ def _norm_rope_store(positions, slot_mapping, eps: float, cos_sin_cache, q=None,
     return "c128_norm_rope_store", (*a[:2], float(eps), *a[2:], _whole(kv_block_size, 64, "kv_block_size")), ()
 
 
+def _window_attention(q, k_cache, kv_block_size: int, block_table, token_to_req_indices, positions, slot_mapping, window: int,
+                      scale: float, out, first: int = 0, lse=None, sink=None, workspace=None, stream=None):
+    if workspace is None:
+        workspace = _scratch(q.shape[1], q.device, stream)
+    a = _refs(q, k_cache, block_table, token_to_req_indices, positions, slot_mapping, sink, out, lse, workspace)
+    return "c128_window_attention", (*a[:2], _whole(kv_block_size, 64, "kv_block_size"), *a[2:6], _whole(window, 64, "window"),
+                                     _whole(first, 64, "first"), float(scale), *a[6:]), (workspace,)
+
+
 _OPS = {"extend_block_tables": _extend_block_tables, "build_slot_maps": _build_slot_maps,
         "decode_attention": _decode_attention, "merge_attention": _merge_attention,
-        "build_cos_sin": _build_cos_sin, "rotate": _rotate, "norm_rope_store": _norm_rope_store}
+        "build_cos_sin": _build_cos_sin, "rotate": _rotate, "norm_rope_store": _norm_rope_store,
+        "window_attention": _window_attention}
 
 
 class PreparedOp:
@@ -418,8 +430,8 @@ class PreparedOp:
     tensors: ``PreparedOp("decode_attention", q, k_cache, ...)`` takes the arguments of the function
     of that name, and calling the object is a single C-ABI call. The tensors must stay alive and keep
     their storage; the stream is fixed when the object is built (default: the current torch stream),
-    and the device that was current then has to be current in every call. A ``decode_attention``
-    without a ``workspace`` gets one of its own, kept with the object."""
+    and the device that was current then has to be current in every call. A ``decode_attention`` or
+    ``window_attention`` without a ``workspace`` gets one of its own, kept with the object."""
 
     def __init__(self, op: str, *args, stream=None, **kw):
         self._name, c_args, owned = _OPS[op](*args, stream=stream, **kw)
@@ -507,6 +519,15 @@ def norm_rope_store(positions, slot_mapping, eps: float, cos_sin_cache, q=None, 
     become entries of ``k_cache`` (c128_norm_rope_store in include/c128compress.h). Either may be left out."""
     PreparedOp("norm_rope_store", positions, slot_mapping, eps, cos_sin_cache, q=q, q_w=q_w, q_out=q_out, k=k, k_w=k_w,
                k_cache=k_cache, kv_block_size=kv_block_size, stream=stream)()
+
+
+def window_attention(q, k_cache, kv_block_size: int, block_table, token_to_req_indices, positions, slot_mapping, window: int,
+                     scale: float, out, first: int = 0, lse=None, sink=None, workspace=None, stream=None) -> None:
+    """Attention of each token to the last ``window`` entries of its request up to its own, and the ``first`` ones
+    (c128_window_attention in include/c128compress.h); ``out`` and ``lse`` are written. ``workspace`` as for
+    decode_attention."""
+    PreparedOp("window_attention", q, k_cache, kv_block_size, block_table, token_to_req_indices, positions, slot_mapping, window,
+               scale, out, first=first, lse=lse, sink=sink, workspace=workspace, stream=stream)()
 
 
 def call_status(*args, **kw) -> int:

@@ -82,6 +82,7 @@ constexpr int kRing = 4;            // tiles the index warp may be ahead
 constexpr float kHigh = 0x1p32f, kLow = 0x1p-32f;  // weights may be up to, and one in the first tile has to be over
 constexpr int kTmemCols = 512, kTmemS = 256, kTmemL = 384;  // O in columns 0..255, two S tiles and L behind it
 
+enum : int { kWhole = -1, kSkipped = -2 };  // parts that are none: a result to `out`; none (a token that is skipped)
 enum : int { kFirst = 1, kLast = 2, kEnd = 4, kRunShift = 3 };  // of its stretch of one request's tiles; above, the stretch's number mod 4
 
 // In the place of a part's log-sum-exp: the part's CTA gave up. (None comes out so: a reference or a sum that is infinite makes NaN.)
@@ -129,7 +130,7 @@ struct TileDesc {
   const uint8_t* scales[kTile];
   uint64_t mask;                 // entries there are
   int32_t flags, request;
-  int32_t part;                  // kLast: slot of the partial result, -1 if the request is whole
+  int32_t part;                  // kLast: slot of the partial result, kWhole, or kSkipped
   int32_t pad;
 };
 
@@ -341,14 +342,40 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Entries of request r (p.most: what its table row holds, at most INT_MAX).
+// The entries that request r attends to (p.most: what its table row holds, at most INT_MAX): `n` of them, the first
+// `lead` are entries 0, 1, .. of table row `row`, the others those from lead + shift on. With a window (WINDOW) r is a
+// token: its row is its request's, and n is -1 if it is skipped.
+struct Seen {
+  int n, lead, shift, row;
+};
+template <bool WINDOW>
+__device__ __forceinline__ Seen seen_by(const DecodeParams& p, int64_t r, unsigned int* err) {
+  if constexpr (!WINDOW) {
+    const int n = p.kv_lens[r];
+    if (n < 0) *err |= C128_DEV_BAD_LENGTH;
+    if (n > p.most) *err |= C128_DEV_BAD_BT_COL;
+    return Seen{max(min(n, p.most), 0), 0, 0, static_cast<int>(r)};
+  } else {
+    const int64_t pos = p.positions[r], slot = p.slots[r];
+    const int row = p.token_req[r];
+    if (pos < 0 || slot < 0) return Seen{-1, 0, 0, 0};
+    if (row < 0 || row >= p.table_rows) {
+      *err |= C128_DEV_BAD_REQ;
+      return Seen{-1, 0, 0, 0};
+    }
+    if (pos >= p.most) *err |= C128_DEV_BAD_BT_COL;
+    const int end = static_cast<int>(min(pos, static_cast<int64_t>(p.most) - 1)) + 1;
+    const int begin = static_cast<int>(min(max(pos + 1 - p.window, static_cast<int64_t>(0)), static_cast<int64_t>(p.most)));
+    const int lead = min(p.first, begin);
+    return Seen{lead + max(end - begin, 0), lead, begin - lead, row};
+  }
+}
+template <bool WINDOW>
 __device__ __forceinline__ int entries_of(const DecodeParams& p, int64_t r, unsigned int* err) {
-  const int n = p.kv_lens[r];
-  if (n < 0) *err |= C128_DEV_BAD_LENGTH;
-  if (n > p.most) *err |= C128_DEV_BAD_BT_COL;
-  return max(min(n, p.most), 0);
+  return seen_by<WINDOW>(p, r, err).n;
 }
 // A request without entries still takes a (masked) tile: its results are written like any other's.
+// (So does a skipped token, whose results are not.)
 __device__ __forceinline__ int tiles_of(int entries) { return max((entries >> 6) + ((entries & 63) != 0), 1); }
 static_assert(kTile == 64, "tiles_of");
 
@@ -389,7 +416,7 @@ __device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams
   const int quarter = warp & 3, group0 = sm.group * sm.group_heads;
   const uint32_t o_at = sm.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
 #pragma unroll 1
-  for (int item = rank; item < heads16 / 4; item += (kFillWarps + kSoftWarps) / 4) {  // 16 heads of 128 columns each
+  for (int item = part == kSkipped ? heads16 : rank; item < heads16 / 4; item += (kFillWarps + kSoftWarps) / 4) {  // 16 heads of 128 columns each
     const int mt = item & 3, h = (item >> 2) * 16;
     const int col = mt * 128 + 32 * quarter + lane;
     uint32_t o[16];
@@ -443,7 +470,7 @@ __device__ __noinline__ void give_up(const DecodeSmem& sm, uint8_t* workspace, i
 
 constexpr int kBoxHeads = 16;  // heads of a TMA load of queries
 
-template <bool ALIGN16, int HEADS>
+template <bool ALIGN16, int HEADS, bool WINDOW>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
     decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ Layouts layouts) {
   constexpr int kOwn = HEADS / 2;  // heads of four softmax warps
@@ -499,9 +526,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // Sum the requests' units (each thread a stretch of requests)...
   const unsigned per = (static_cast<unsigned>(requests) + kDecodeThreads - 1) / kDecodeThreads;
   const int r_begin = min(threadIdx.x * per, static_cast<unsigned>(requests)), r_end = min(r_begin + per, static_cast<unsigned>(requests));
-  const int n_begin = r_begin < r_end ? entries_of(p, r_begin, &err) : 0;
+  const int n_begin = r_begin < r_end ? entries_of<WINDOW>(p, r_begin, &err) : 0;
   int mine = r_begin < r_end ? tiles_of(n_begin) + kRunCost : 0;
-  for (int r = r_begin + 1; r < r_end; ++r) mine += tiles_of(entries_of(p, r, &err)) + kRunCost;
+  for (int r = r_begin + 1; r < r_end; ++r) mine += tiles_of(entries_of<WINDOW>(p, r, &err)) + kRunCost;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -546,7 +573,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     int at = base;
     for (int r = r_begin; r < r_end && at <= cut1; ++r) {
       unsigned int ignore = 0;
-      const int entries = r == r_begin ? n_begin : entries_of(p, r, &ignore), end = at + tiles_of(entries), next = end + kRunCost;
+      const int entries = r == r_begin ? n_begin : entries_of<WINDOW>(p, r, &ignore), end = at + tiles_of(entries), next = end + kRunCost;
       const bool holds0 = cut0 >= at && cut0 < next, holds1 = cut1 >= at && cut1 < next;
       auto on = [&](int cut) { return cut >= end || (cut - at > deal.snap && end - cut <= deal.snap); };
       auto back = [&](int cut) { return cut < end && cut - at <= deal.snap; };
@@ -554,7 +581,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         const bool begins = on(cut0);  // with the next request
         sm.first_request = begins ? r + 1 : r;
         sm.first_tile = begins || back(cut0) ? 0 : cut0 - at;
-        sm.first_entries = !begins ? entries : r + 1 < requests ? entries_of(p, r + 1, &ignore) : 0;
+        sm.first_entries = !begins ? entries : r + 1 < requests ? entries_of<WINDOW>(p, r + 1, &ignore) : 0;
       }
       if (holds1) {
         // cut inside: does the request begin in this column? Then this column's task is to join it,
@@ -599,21 +626,39 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     bool ends = r == end_request && tile == end_tile;  // the run, here
     int started = tile;  // the request's tile at which this run takes it up
     const Divisor bs = p.kv_div;
-    int64_t window = r;      // lanes hold the lengths of requests window .. window + 31
+    int64_t window = r;      // lanes hold what requests window .. window + 31 see
     unsigned int ignore = 0;
     int id[2];
+    int lead = 0, shift = 0;  // of this request, if WINDOW
+    int64_t row = r;
+    auto entry = [&](uint32_t key) { return WINDOW && key >= static_cast<uint32_t>(lead) ? key + shift : key; };
     // Entries are fewer than 2^31, so an index past them does not wrap in 32 unsigned bits. (Not as read-only data: this
     // kernel may have started before the one that writes the table has ended.)
     auto load_ids = [&] {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t key = static_cast<uint32_t>(tile) * kTile + 32 * h + lane;
-        id[h] = key < static_cast<uint32_t>(n) ? __ldcg(p.table + r * p.table_stride + divide(key, bs)) : -1;
+        id[h] = key < static_cast<uint32_t>(WINDOW ? max(n, 0) : n) ? __ldcg(p.table + (WINDOW ? row : r) * p.table_stride + divide(entry(key), bs)) : -1;
       }
     };
     int stretch = 0;
-    if (!ends) load_ids();
-    int lens = window + lane < p.requests ? entries_of(p, window + lane, &ignore) : 0;
+    Seen lens{0, 0, 0, 0};
+    auto load_lens = [&] { lens = window + lane < p.requests ? seen_by<WINDOW>(p, window + lane, &ignore) : Seen{0, 0, 0, 0}; };
+    auto take_request = [&] {
+      if constexpr (WINDOW) {
+        const int from = static_cast<int>(r - window);
+        lead = __shfl_sync(0xffffffffu, lens.lead, from), shift = __shfl_sync(0xffffffffu, lens.shift, from);
+        row = __shfl_sync(0xffffffffu, lens.row, from);
+      }
+    };
+    if constexpr (WINDOW) {
+      load_lens();
+      take_request();
+      if (!ends) load_ids();
+    } else {  // its length and blocks are read at once
+      if (!ends) load_ids();
+      load_lens();
+    }
     for (int i = 0; !(p.stall && blockIdx.x == 0); ++i) {
       const int slot = i % kRing;
       if (i >= kRing) warp_wait(&sm.ring_free[slot], (i / kRing - 1) & 1);
@@ -632,10 +677,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t key = static_cast<uint32_t>(tile) * kTile + 32 * h + lane;
-        const bool in = key < static_cast<uint32_t>(n);
+        const bool in = key < static_cast<uint32_t>(WINDOW ? max(n, 0) : n);
         const bool ok = in && id[h] >= 0 && id[h] < p.nkb;
         if (in && !ok) err |= C128_DEV_BAD_BLOCK;
-        const uint32_t off = key - divide(key, bs) * bs.value;
+        const uint32_t off = entry(key) - divide(entry(key), bs) * bs.value;
         const uint8_t* blk = p.kc + static_cast<int64_t>(ok ? id[h] : 0) * p.kc_stride0;
         from[h] = ok ? blk + static_cast<int64_t>(off) * kTokenStride : nullptr;
         sc[h] = blk + p.kv_bs * kTokenStride + static_cast<int64_t>(off) * kScaleDim;
@@ -648,7 +693,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         d.mask = mask;
         d.flags = (tile == started ? kFirst : 0) | (last_of_request || (r == end_request && tile + 1 == end_tile) ? kLast : 0) | (stretch & 3) << kRunShift;
         d.request = static_cast<int32_t>(r);
-        d.part = started == 0 && last_of_request ? -1 : 2 * column + (started == 0 ? 1 : 0);
+        d.part = WINDOW && n < 0 ? kSkipped : started == 0 && last_of_request ? kWhole : 2 * column + (started == 0 ? 1 : 0);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.ring_full[slot]);
@@ -667,9 +712,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         tile = started = 0;
         if (r - window >= 32) {
           window = r;
-          lens = window + lane < p.requests ? entries_of(p, window + lane, &ignore) : 0;
+          load_lens();
         }
-        n = __shfl_sync(0xffffffffu, lens, static_cast<int>(r - window));
+        n = __shfl_sync(0xffffffffu, lens.n, static_cast<int>(r - window));
+        take_request();
       } else {
         ++tile;
       }
@@ -1139,7 +1185,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         if (!*abort_flag) {
           if (!whole)
             reinterpret_cast<float*>(p.workspace + sm.lay.lse_at())[sm.lay.row(part, sm.group, h)] = lse2;
-          else if (p.lse != nullptr)
+          else if (p.lse != nullptr && part != kSkipped)
             p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
         }
       }
@@ -1350,20 +1396,24 @@ bool encode_query_map(const DecodeParams& p, CUtensorMap* map) {
 namespace {
 // The kernel for caches whose records start on 16 or 8 bytes, and for all heads in one group of 16 or
 // 32 (which frees registers) or in groups of up to 64.
+template <bool WINDOW>
 const void* decode_kernel_for(bool align16, int heads) {
-  if (heads <= 16) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 16> : decode_kernel<false, 16>);
-  if (heads <= 32) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 32> : decode_kernel<false, 32>);
-  return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 64> : decode_kernel<false, 64>);
+  if (heads <= 16) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 16, WINDOW> : decode_kernel<false, 16, WINDOW>);
+  if (heads <= 32) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 32, WINDOW> : decode_kernel<false, 32, WINDOW>);
+  return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 64, WINDOW> : decode_kernel<false, 64, WINDOW>);
+}
+const void* decode_kernel_for(bool align16, int heads, bool window) {
+  return window ? decode_kernel_for<true>(align16, heads) : decode_kernel_for<false>(align16, heads);
 }
 }  // namespace
 
 cudaError_t prepare_decode() {
   cudaError_t e = cudaSuccess;
   for (int heads = 16; heads <= 64; heads *= 2)
-    for (int align16 = 0; align16 < 2; ++align16)
+    for (int variant = 0; variant < 4; ++variant)
       if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel_for(align16 != 0, heads), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kDecodeSmemBytes);
+        e = cudaFuncSetAttribute(decode_kernel_for((variant & 1) != 0, heads, (variant & 2) != 0),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kDecodeSmemBytes);
   return e;
 }
 
@@ -1388,7 +1438,7 @@ cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stre
   lc.attrs = attr;
   lc.numAttrs = 1;
   void* args[] = {const_cast<DecodeParams*>(&p), &map, &layouts};
-  const cudaError_t e = cudaLaunchKernelExC(&lc, decode_kernel_for(align16, p.heads), args);
+  const cudaError_t e = cudaLaunchKernelExC(&lc, decode_kernel_for(align16, p.heads, p.kv_lens == nullptr), args);
   if (e != cudaSuccess) return e;
   const int64_t cut = p.requests < ctas ? p.requests : ctas;  // requests that can be cut
   const int64_t join_ctas = (cut * ((p.heads + 3) / 4) * 16 + kJoinThreads / 32 - 1) / (kJoinThreads / 32);

@@ -3,7 +3,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "c128_internal.h"
+#include "c128_serving.h"
 #include "c128compress.h"
 
 #define C128_TRY(expr)         \
@@ -127,6 +130,51 @@ inline int done(cudaError_t e) { return e == cudaSuccess ? C128_OK : C128_ERR_CU
 inline bool partly_overlap(const void* a, const void* b, int64_t bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x != y && (x < y ? y - x : x - y) < static_cast<uintptr_t>(bytes);
+}
+
+// What the two attentions over a paged cache have in common, into *p: queries [R, H, 512], cache, scale, sink,
+// results and scratch.
+inline int check_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size, float scale,
+                           const c128_tensor_t* sink, const c128_tensor_t* out, const c128_tensor_t* lse,
+                           const c128_tensor_t* workspace, DecodeParams* p) {
+  C128_TRY(check_rows(q, 3, nullptr));
+  const int64_t R = q->shape[0], H = q->shape[1];
+  if (R > kMaxCount) return C128_ERR_ARG;
+  if (H > kMaxDecodeHeads) return C128_ERR_UNSUPPORTED;
+  C128_TRY(check_rows(out, 3, &p->out_f32));
+  if (out->shape[0] != R || out->shape[1] != H) return C128_ERR_SHAPE;
+  if (R > 0 && H > 0) C128_TRY(check_apart(out, kHead));
+  C128_TRY(check_cache(k_cache, kv_block_size));
+  if (!std::isfinite(scale * 1.44269504f)) return C128_ERR_ARG;  // times log2(e), the kernel's factor
+  if (sink != nullptr) C128_TRY(check_array(sink, C128_F32, H));
+  if (lse != nullptr) {
+    C128_TRY(check_lse(lse, 2));
+    if (lse->shape[0] != R || lse->shape[1] != H) return C128_ERR_SHAPE;
+    if (R > 0 && H > 0) C128_TRY(check_apart(lse, 1));
+  }
+  C128_TRY(check_desc(workspace, C128_U8, 1));
+  C128_TRY(check_array(workspace, C128_U8, workspace->shape[0]));
+  if (!aligned(workspace->data, 256)) return C128_ERR_ALIGN;
+  p->q = static_cast<const uint16_t*>(q->data);
+  p->q_stride_r = step(q, 0);
+  p->q_stride_h = step(q, 1);
+  p->kc = static_cast<const uint8_t*>(k_cache->data);
+  p->nkb = k_cache->shape[0];
+  p->kv_bs = kv_block_size;
+  p->kv_div = Divisor(kv_block_size);
+  p->kc_stride0 = step(k_cache, 0);
+  p->requests = R;
+  p->heads = static_cast<int32_t>(H);
+  p->scale = scale;
+  p->sink = sink != nullptr ? static_cast<const float*>(sink->data) : nullptr;
+  p->out = out->data;
+  p->out_stride_r = step(out, 0);
+  p->out_stride_h = step(out, 1);
+  p->lse = lse != nullptr ? static_cast<float*>(lse->data) : nullptr;
+  p->lse_stride_r = lse != nullptr ? step(lse, 0) : 0;
+  p->lse_stride_h = lse != nullptr ? step(lse, 1) : 0;
+  p->workspace = static_cast<uint8_t*>(workspace->data);
+  return C128_OK;
 }
 
 }  // namespace check

@@ -67,7 +67,12 @@ struct DecodeParams {
   const int32_t* table;
   int64_t requests, table_stride;
   int32_t most;                  // entries that a row of the table holds, at most 2^31 - 1
-  const int32_t* kv_lens;
+  const int32_t* kv_lens;        // NULL: c128_window_attention, and `requests` are tokens
+  const int32_t* token_req;      // its arrays: the row of each token's request in the table,
+  const int64_t* positions;      // its position (the entry that is its own),
+  const int64_t* slots;          // and its cache slot (< 0: skipped)
+  int64_t table_rows, window;    // a token sees the last `window` entries and the `first` ones
+  int32_t first;
   int32_t heads;
   float scale;
   const float* sink;             // nullable

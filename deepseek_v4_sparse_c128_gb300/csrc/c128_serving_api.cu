@@ -19,52 +19,17 @@ int decode(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_bloc
            const c128_tensor_t* sink, const c128_tensor_t* out, const c128_tensor_t* lse,
            const c128_tensor_t* workspace, c128_stream_t stream, bool stall) {
   c128::DecodeParams p{};
-  C128_TRY(check_rows(q, 3, nullptr));
-  const int64_t R = q->shape[0], H = q->shape[1];
-  if (R > kMaxCount) return C128_ERR_ARG;
-  if (H > c128::kMaxDecodeHeads) return C128_ERR_UNSUPPORTED;
-  C128_TRY(check_rows(out, 3, &p.out_f32));
-  if (out->shape[0] != R || out->shape[1] != H) return C128_ERR_SHAPE;
-  if (R > 0 && H > 0) C128_TRY(check_apart(out, c128::kHead));
-  C128_TRY(check_cache(k_cache, kv_block_size));
+  C128_TRY(check_attention(q, k_cache, kv_block_size, scale, sink, out, lse, workspace, &p));
+  const int64_t R = q->shape[0];
   C128_TRY(check_table(block_table, R, &p.table_stride));
   C128_TRY(check_array(kv_lens, C128_I32, R));
-  if (!std::isfinite(scale * 1.44269504f)) return C128_ERR_ARG;  // times log2(e), the kernel's factor
-  if (sink != nullptr) C128_TRY(check_array(sink, C128_F32, H));
-  if (lse != nullptr) {
-    C128_TRY(check_lse(lse, 2));
-    if (lse->shape[0] != R || lse->shape[1] != H) return C128_ERR_SHAPE;
-    if (R > 0 && H > 0) C128_TRY(check_apart(lse, 1));
-  }
-  C128_TRY(check_desc(workspace, C128_U8, 1));
-  C128_TRY(check_array(workspace, C128_U8, workspace->shape[0]));
-  if (!aligned(workspace->data, 256)) return C128_ERR_ALIGN;
-  if (R == 0 || H == 0) return C128_OK;
+  if (R == 0 || q->shape[1] == 0) return C128_OK;
   // what the table can hold, in tiles of 64 entries: the kernel counts those, and the requests, in 32 bits
   const int64_t most = block_table->shape[1] > kMaxCount / kv_block_size ? kMaxCount : block_table->shape[1] * kv_block_size;
   if (R * (most / 64 + 2) > kMaxCount) return C128_ERR_ARG;
   p.most = static_cast<int32_t>(most);
-  p.q = static_cast<const uint16_t*>(q->data);
-  p.q_stride_r = step(q, 0);
-  p.q_stride_h = step(q, 1);
-  p.kc = static_cast<const uint8_t*>(k_cache->data);
-  p.nkb = k_cache->shape[0];
-  p.kv_bs = kv_block_size;
-  p.kv_div = c128::Divisor(kv_block_size);
-  p.kc_stride0 = step(k_cache, 0);
   p.table = static_cast<const int32_t*>(block_table->data);
-  p.requests = R;
   p.kv_lens = static_cast<const int32_t*>(kv_lens->data);
-  p.heads = static_cast<int32_t>(H);
-  p.scale = scale;
-  p.sink = sink != nullptr ? static_cast<const float*>(sink->data) : nullptr;
-  p.out = out->data;
-  p.out_stride_r = step(out, 0);
-  p.out_stride_h = step(out, 1);
-  p.lse = lse != nullptr ? static_cast<float*>(lse->data) : nullptr;
-  p.lse_stride_r = lse != nullptr ? step(lse, 0) : 0;
-  p.lse_stride_h = lse != nullptr ? step(lse, 1) : 0;
-  p.workspace = static_cast<uint8_t*>(workspace->data);
   p.stall = stall ? 1 : 0;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int sms = 0;

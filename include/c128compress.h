@@ -572,6 +572,40 @@ int c128_norm_rope_store(const c128_tensor_t* positions, const c128_tensor_t* sl
                          const c128_tensor_t* q_out, const c128_tensor_t* k, const c128_tensor_t* k_w,
                          const c128_tensor_t* k_cache, int64_t kv_block_size, c128_stream_t stream);
 
+/*
+ * c128_window_attention — attention of a step's tokens to the last entries before them and a few first ones,
+ * over the paged cache that c128_norm_rope_store fills (an entry per position). The token at position p of
+ * its request sees entry j of that request where
+ *   j <= p  and  (j > p - window  or  j < first)
+ * and with those, k_j, scale, sink, lse and out are as for c128_decode_attention. A step's tokens may be one of
+ * each request or many, in any order; entries of the step's own tokens have to be in the cache. lse lets the
+ * result be merged with that of c128_decode_attention over the compressed cache (c128_merge_attention; the sink in
+ * one of them only).
+ *
+ *   q                    [T, H, 512]   bf16   as for c128_decode_attention
+ *   k_cache              [NKB, bs, W]  uint8  kv_block_size == bs
+ *   block_table          [R, MB]       int32  k_cache block of entries b*bs .. b*bs + bs - 1 of a request. Blocks
+ *                                             that hold no entry that a token sees are not read (-1, say)
+ *   token_to_req_indices [T]           int32
+ *   positions            [T]           int64
+ *   slot_mapping         [T]           int64  only its sign is used: < 0, the token is skipped
+ *   window                             1 <= window < 2^31
+ *   first                              0 <= first < 2^31
+ *   scale, sink [H], out [T, H, 512], lse [T, H], workspace: as for c128_decode_attention (the workspace is
+ *                                      of c128_decode_attention_workspace bytes)
+ *
+ * The rows of out and lse of skipped tokens are left as they were.
+ * Device error bits: C128_DEV_BAD_REQ - token_to_req_indices[t] outside [0, R) (the token is skipped);
+ * C128_DEV_BAD_BT_COL - positions[t] >= MB*bs (the entries behind are left out); C128_DEV_BAD_BLOCK - a block id
+ * outside [0, NKB) where one is needed (its entries are left out); C128_DEV_TIMEOUT as for c128_decode_attention.
+ * T * (min(MB*bs, window + first) / 64 + 2) < 2^31, else C128_ERR_ARG.
+ */
+int c128_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
+                          const c128_tensor_t* block_table, const c128_tensor_t* token_to_req_indices,
+                          const c128_tensor_t* positions, const c128_tensor_t* slot_mapping, int64_t window,
+                          int64_t first, float scale, const c128_tensor_t* sink, const c128_tensor_t* out,
+                          const c128_tensor_t* lse, const c128_tensor_t* workspace, c128_stream_t stream);
+
 /* Human-readable name of a return code (static string, never NULL). */
 const char* c128_status_string(int status);
 

@@ -67,3 +67,9 @@ def queries(x, w, eps, cs, kind):
     out, mag = rotate(n, cs, NOPE, "pairs", False)
     off = mag * (2.0 ** -20 + 2.0 ** -23)
     return out, off + HALF[kind] * (np.abs(out) + off)
+
+
+def seen(p, window, first, most):
+    """Entries that the token at position p sees, of a table row that holds `most`."""
+    begin = max(0, p + 1 - window)
+    return list(range(min(first, begin, most))) + list(range(begin, min(p + 1, most)))

@@ -104,6 +104,44 @@ def test_norm_rope_store_refuses(L, over, code):
     assert _call(L, "c128_norm_rope_store", NORM, args, over) == code
 
 
+WINDOW = ("q", "cache", "block", "table", "req", "pos", "slot", "window", "first", "scale", "sink", "out", "lse", "ws")
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(q=None), NULL), (dict(ws=None), NULL), (dict(table=None), NULL), (dict(req=None), NULL), (dict(pos=None), NULL),
+    (dict(slot=None), NULL), (dict(out=None), NULL), (dict(cache=_t([4, 2, 584], U8, data=None)), NULL),
+    (dict(q=_t([3, 5, 512], F32)), DTYPE), (dict(out=_t([3, 5, 512], U8)), DTYPE), (dict(req=_t([3], I64)), DTYPE),
+    (dict(pos=_t([3], I32)), DTYPE), (dict(slot=_t([3], I32)), DTYPE), (dict(table=_t([2, 9], I64)), DTYPE),
+    (dict(lse=_t([3, 5], BF16)), DTYPE),
+    (dict(out=_t([3, 4, 512], BF16)), SHAPE), (dict(req=_t([2], I32)), SHAPE), (dict(pos=_t([4], I64)), SHAPE),
+    (dict(slot=_t([2], I64)), SHAPE), (dict(sink=_t([4], F32)), SHAPE), (dict(lse=_t([5, 3], F32)), SHAPE), (dict(table=_t([9], I32)), SHAPE),
+    (dict(q=_t([3, 5, 512], BF16, strides=[512, 0, 1])), STRIDE), (dict(out=_t([3, 5, 512], BF16, strides=[512, 512, 1])), STRIDE),
+    (dict(lse=_t([3, 5], F32, strides=[1, 1])), STRIDE), (dict(table=_t([2, 9], I32, strides=[8, 1])), STRIDE),
+    (dict(pos=_t([3], I64, strides=[2])), STRIDE),
+    (dict(q=_t([3, 5, 512], BF16, data=FAKE + 8)), ALIGN), (dict(pos=_t([3], I64, data=FAKE + 4)), ALIGN),
+    (dict(ws=_t([1 << 30], U8, data=FAKE + 128)), ALIGN), (dict(cache=_t([4, 2, 584], U8, data=FAKE + 8)), ALIGN),
+    (dict(q=_t([3, 5, 256], BF16)), UNSUPPORTED), (dict(q=_t([3, 1025, 512], BF16)), UNSUPPORTED),
+    (dict(block=4), ARG), (dict(window=0), ARG), (dict(window=1 << 31), ARG), (dict(first=-1), ARG), (dict(first=1 << 31), ARG),
+    (dict(scale=float("nan")), ARG), (dict(scale=3e38), ARG),
+    (dict(q=_t([0, 5, 512], BF16), out=_t([0, 5, 512], BF16), req=_t([0], I32), pos=_t([0], I64), slot=_t([0], I64),
+          lse=_t([0, 5], F32)), 0),
+])
+def test_window_attention_refuses(L, over, code):
+    args = dict(q=_t([3, 5, 512], BF16), cache=_t([4, 2, 584], U8), block=2, table=_t([2, 9], I32), req=_t([3], I32), pos=_t([3], I64),
+                slot=_t([3], I64), window=128, first=4, scale=0.1, sink=_t([5], F32), out=_t([3, 5, 512], BF16), lse=_t([3, 5], F32),
+                ws=_t([1 << 30], U8))
+    assert _call(L, "c128_window_attention", WINDOW, args, over) == code
+
+
+def test_window_attention_refuses_more_tiles_than_it_counts(L):
+    """T * (min(MB*bs, window + first) / 64 + 2) has to be below 2^31."""
+    T = 1 << 16
+    args = dict(q=_t([T, 5, 512], BF16), cache=_t([4, 2, 584], U8), block=2, table=_t([2, 1 << 20], I32), req=_t([T], I32),
+                pos=_t([T], I64), slot=_t([T], I64), window=(1 << 31) - 1, first=0, scale=0.1, sink=None, out=_t([T, 5, 512], BF16),
+                lse=None, ws=_t([1 << 30], U8))
+    assert _call(L, "c128_window_attention", WINDOW, args, {}) == ARG  # 2^16 * 32770
+
+
 def test_binding_refuses():
     import torch
     with pytest.raises(ValueError, match="scaling"):
