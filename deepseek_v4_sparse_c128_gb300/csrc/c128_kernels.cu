@@ -26,6 +26,7 @@
 // its own copies in flight and returns.
 #include "c128_device.cuh"
 #include "c128_serving.h"
+#include "c128_step.h"
 
 namespace c128 {
 namespace {
@@ -694,6 +695,7 @@ cudaError_t prepare_device(int /*device*/) {
   if (e == cudaSuccess) e = prepare_small();
   if (e == cudaSuccess) e = prepare_indexer_windows();
   if (e == cudaSuccess) e = prepare_decode();
+  if (e == cudaSuccess) e = prepare_window();
   return e;
 }
 

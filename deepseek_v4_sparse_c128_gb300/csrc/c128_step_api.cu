@@ -245,7 +245,7 @@ int c128_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, 
   int sms = 0;
   C128_TRY(c128::stream_errors(s, &p.err, &sms));
   if (workspace->shape[0] < c128::decode_workspace_bytes(p.heads, sms)) return C128_ERR_ARG;
-  return done(c128::launch_decode(p, sms, s));
+  return done(c128::window_fits(p) ? c128::launch_window(p, sms, s) : c128::launch_decode(p, sms, s));
 }
 
 }  // extern "C"

@@ -228,3 +228,43 @@ def test_graph_and_other_stream(window):
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     binding.release_stream(s)
+
+
+@pytest.mark.parametrize("H", [64, 16, 5])
+def test_entries_that_are_not_finite(H):
+    """An entry with NaN makes the tokens that see it NaN, and no other: not those beside it in one item, nor those that
+    come when it has left the window. The same for infinities. (Codes, rope values, and products without room.)"""
+    tokens = consecutive(0, 0, 60) + consecutive(1, 0, 40)
+    c = Case(40, tokens, [60, 40], H, 12, 2, 8, rubbish=False)
+    flat = c.cache.reshape(c.cache.shape[0], -1)
+
+    def entry(r, j):
+        page, off = c.table[r, j // 8], j % 8
+        return flat[page, off * 576:off * 576 + 576], flat[page, 8 * 576 + off * 8:8 * 576 + off * 8 + 8]
+
+    entry(0, 20)[0][100] = 0xff
+    entry(0, 41)[0][448:].view(np.uint16)[5] = 0x7f80
+    entry(1, 1)[0][448:].view(np.uint16)[63] = 0xffc0   # one of the first entries: seen to the end
+    entry(1, 0)[1][3] = 255
+    out, lse = c.run()
+    bad = [any((r, j) in ((0, 20), (0, 41), (1, 1), (1, 0)) for j in ref.seen(p, 12, 2, 1 << 20)) for r, p in tokens]
+    bad = torch.tensor(bad, device="cuda")
+    assert 0 < bad.sum() < len(tokens)
+    assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
+    c.check(out, lse, tokens=[t for t in range(len(tokens)) if not bad[t]])
+
+
+def test_rows_that_are_not_finite():
+    """A query with NaN makes its own row NaN, and no other."""
+    c = Case(41, consecutive(0, 50, 20), [70], 16, 12, 2, 8)
+    c.q[3, 5, 100] = float("nan")
+    c.q[9, 0, 500] = float("inf")
+    out, lse = c.run()
+    torch.cuda.synchronize()
+    assert torch.isnan(out[3, 5]).all() and torch.isnan(lse[3, 5])
+    c.q[3, 5, 100] = c.q[9, 0, 500] = 0
+    keep = [t for t in range(20) if t not in (3, 9)]
+    c.check(out, lse, tokens=keep)
+    other = [h for h in range(16) if h != 5]
+    ref_out, ref_lse = c.run()
+    assert torch.equal(out[3, other], ref_out[3, other]) and torch.equal(out[9, 1:], ref_out[9, 1:])
