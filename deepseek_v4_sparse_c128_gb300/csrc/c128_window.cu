@@ -4,7 +4,8 @@
 //   S^T = K Q^T            M = 128 entries (and the rest of them), N = rows, K = 512
 //   P^T = exp2(c S^T - m)  c = scale * log2(e), m the row's largest c S^T
 //   O^T = K^T P^T          M = 128 columns (4 times), N = rows, K = entries
-//   out = O / sum(P as the products see it, rounded to bf16); lse = of the exact sums, in fp32
+//   L = 1 P^T              the sums of P as the products see it, rounded to bf16: M = 64 rows of ones
+//   out = O / L; lse is of the exact sums, in fp32
 //
 // An entry is key and value: both products read it as their A, with the 512 columns along K, and with them along M. An
 // item is a token with its heads (up to 64 rows, padded to eights), or as many consecutive tokens as 64 rows hold. Entries
@@ -19,11 +20,14 @@
 // A masked entry has weight 0, and 0 times what stands there has to be 0 for every row: so an entry with a value that is
 // not finite is stored as zeros and marked, and its scores are NaN for the rows that see it, and for no other.
 //
-// Roles of the 18 warps (each wait is bounded):
-//   0..7   softmax, four warps for either half of the rows; results
-//   8..15  decode entries
+// Roles of the 20 warps (five to a scheduler leave them 96 registers; each wait is bounded):
+//   0..7   softmax, four warps for either half of the rows
+//   8..15  results, four warps for either half of the rows
+//          (and these decode entries at the start of a run)
 //   16     one thread issues the products
-//   17     makes the items, reads their queries (TMA)
+//   17     makes the items
+//   18     decodes entries
+//   19     reads the queries (TMA)
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -43,19 +47,21 @@ constexpr int kChunkBytes = kSlots * 128;  // 64 columns of all entries: rows of
 constexpr int kKBytes = kChunks * kChunkBytes;
 constexpr int kQChunkBytes = kRows * 128;
 constexpr int kPBytes = (kSlots + 8) * 128;  // [entry][row]; K steps of 16 entries end at 144
-constexpr int kSoftWarps = 8, kFillWarps = 8;
-constexpr int kMmaWarp = kSoftWarps + kFillWarps, kItemWarp = kMmaWarp + 1;
-constexpr int kWindowThreads = 32 * (kItemWarp + 1);
+constexpr int kSoftWarps = 8, kOutWarps = 8;
+constexpr int kMmaWarp = kSoftWarps + kOutWarps, kItemWarp = kMmaWarp + 1, kDecodeWarp = kMmaWarp + 2, kQueryWarp = kMmaWarp + 3;
+constexpr int kPass = 8 * (kOutWarps + 1);  // entries that are decoded at once at the start of a run
+static_assert(2 * kPass >= kSlots, "two passes");
+constexpr int kWindowThreads = 32 * (kQueryWarp + 1);
 constexpr int kRing = 4;      // items that may be on their way
-constexpr int kTmemCols = 512, kTmemS = 256, kTmemTail = 320;
+constexpr int kTmemCols = 512, kTmemS = 256, kTmemTail = 320, kTmemL = 384;
 
-enum : int { kEnd = 1, kSerial = 2, kTail = 4, kStepShift = 4 };  // flags of an item; above: K steps of O
+enum : int { kEnd = 1, kFresh = 2, kSerial = 4, kTail = 8, kStepShift = 4 };  // flags of an item; above: K steps of O
 enum : uint8_t { kThere = 0, kAbsent = 1, kPoison = 2 };          // what an entry's place holds
 
 struct Item {
   int32_t token, count;     // its first token; tokens
   int32_t row;              // their request's row of the table
-  int32_t lo, hi;           // the first token sees entries lo .. hi (and `first` ones), those behind it one more each
+  int32_t hi, last;         // the first token's position; the last entry that there is for them
   int32_t from, lead, news; // entries to decode: 0 .. lead - 1, and `news` from `from` on
   int32_t ring;             // where on the ring the first of them that goes there goes
   int32_t base, newest;     // the entry at place 0 of the ring when the run began; place of the last entry
@@ -67,7 +73,7 @@ struct WindowPlan {
   int32_t pitch;                // rows of a token: its heads, padded to eights
   int32_t together;             // tokens of an item, at most
   int32_t columns;              // CTAs that share the tokens
-  int32_t lookahead;            // entries of the next item have room beside those of this one
+  int32_t lookahead;            // an item's entries have room beside those of so many items, itself among them
   uint32_t pitch_inv;           // 2^16 / pitch, rounded up
 };
 
@@ -77,15 +83,18 @@ struct WindowSmem {
   alignas(1024) uint8_t q[kRows * kHead * 2];
   alignas(1024) uint8_t p[kPBytes];
   alignas(16) float by_max[2][4][kRows];         // of even and odd items: 32 entries each
-  alignas(16) float sums[2][4][kRows], rounded[2][4][kRows];
+  alignas(16) float sums[2][4][kRows];
+  alignas(128) uint32_t ones[512];               // 64 x 16 of bf16, in any order
   alignas(16) float ref[2][kRows];
-  alignas(16) float inv[kRows];
-  int64_t at[kRows];                  // where a row's results go, -1: nowhere
+  alignas(16) float inv[kRows], weights[kRows];  // 1 / L (with a sink: the entries' share / L); L
   Item ring[kRing];
   uint64_t ring_full[kRing], ring_free[kRing];
-  uint64_t k_full[2], o_full[2];      // of even and odd items
+  uint64_t k_full[kRing], o_full[kRing];
+  uint64_t p_full[2];                 // of even and odd items
+  uint64_t k_help;                    // the first entries of a run
+  uint64_t q_full[2], q_free[2];      // of either half of the columns
   uint64_t set[2];                    // barriers of the softmax warps of either half
-  uint64_t q_full, q_free, s_full, s_free, p_full, o_free, drained;
+  uint64_t s_full, s_free, o_free, drained;
   uint8_t state[kSlots];
   uint32_t tmem;
   volatile int abort;
@@ -122,68 +131,168 @@ __device__ __forceinline__ float reduce_rows(const float (&v)[8], int lane, F op
   return op(hi ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, hi ? b[0] : b[1], 4));
 }
 
-// Four threads per entry; thread `sub` has the 16 bytes sub, sub + 4, ...: of the codes a quarter of each 64-column
-// chunk, so load j belongs to scale j.
-struct Quarter {
-  uint4 raw[9];
-  uint2 scales;
-  template <bool ALIGN16>
-  __device__ __forceinline__ void load(const uint8_t* data, const uint8_t* sc, int sub) {
-#pragma unroll
-    for (int j = 0; j < 9; ++j) {
-      if (data == nullptr) raw[j] = make_uint4(0, 0, 0, 0);
-      else raw[j] = ALIGN16 ? ld16(data + 16 * sub + 64 * j) : ld8x2(data + 16 * sub + 64 * j);
+// A wait of a whole warp; as in the decode attention's kernel, one that runs out sets the abort flag, every wait then
+// returns at once, and the warps run on to the end, which the items' flags show them. No result is stored then.
+__device__ __forceinline__ void warp_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity) {
+  if (!decode_wait(bar, parity, abort_flag)) *abort_flag = 1;
+  __syncwarp();
+}
+
+// Where entry e of those that an item brings is in the cache (NULL: nowhere), and its place.
+struct Source {
+  const uint8_t* data;
+  const uint8_t* scales;
+  int place;
+  __device__ __forceinline__ Source(const DecodeParams& p, const Item& it, int e) : data(nullptr), scales(nullptr) {
+    const Divisor bs = p.kv_div;
+    const int entry = e < it.lead ? e : it.from + e - it.lead, circle = kSlots - p.first;
+    const uint32_t block = divide(entry, bs), off = entry - block * bs.value;
+    const int id = __ldcg(p.table + it.row * p.table_stride + block);
+    if (id >= 0 && id < p.nkb) {
+      const uint8_t* blk = p.kc + id * p.kc_stride0;
+      data = blk + static_cast<int64_t>(off) * kTokenStride;
+      scales = blk + p.kv_bs * kTokenStride + static_cast<int64_t>(off) * kScaleDim;
+    } else {
+      atomicOr(p.err, static_cast<unsigned int>(C128_DEV_BAD_BLOCK));
     }
-    scales = data == nullptr ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : ld8(sc);
-  }
-  __device__ __forceinline__ float scale(int j) const { return scale_of(((j < 4 ? scales.x : scales.y) >> (8 * (j & 3))) & 0xffu); }
-  // Chunk j as bf16
-  __device__ __forceinline__ void decode(int j, uint32_t (&o)[8]) const {
-    const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-    const float s = scale(j);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      o[2 * k] = codes_to_bf16(static_cast<uint16_t>(w[k]), s);
-      o[2 * k + 1] = codes_to_bf16(static_cast<uint16_t>(w[k] >> 16), s);
+    place = entry;
+    if (entry >= p.first) {
+      place = it.ring + entry - max(it.from, p.first);
+      place = p.first + (place >= circle ? place - circle : place);
     }
-  }
-  // Whether a value is not finite: a code of NaN, a bf16 or (scales from 2^120 on) a product without room.
-  __device__ __forceinline__ bool not_finite() const {
-    uint32_t codes = 0, halves = 0, large = 0;
-#pragma unroll
-    for (int j = 0; j < 7; ++j) {
-      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) codes |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
-      large |= (((j < 4 ? scales.x : scales.y) >> (8 * (j & 3))) & 0xffu) >= 247u;
-    }
-#pragma unroll
-    for (int j = 7; j < 9; ++j) {
-      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) halves |= (w[k] & 0x7fff7fffu) + 0x00800080u;
-    }
-    if (large) {
-#pragma unroll 1
-      for (int j = 0; j < 7; ++j) {
-        uint32_t o[8];
-        uint4 r = raw[0];
-#pragma unroll
-        for (int i = 1; i < 7; ++i)
-          if (i == j) r = raw[i];
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[2 * k] = codes_to_bf16(static_cast<uint16_t>(w[k]), scale(j));
-          o[2 * k + 1] = codes_to_bf16(static_cast<uint16_t>(w[k] >> 16), scale(j));
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) halves |= (o[k] & 0x7fff7fffu) + 0x00800080u;
-      }
-    }
-    return ((codes & 0x80808080u) | (halves & 0x80008000u)) != 0;
   }
 };
+// 16 codes to bf16
+__device__ __forceinline__ void decode_codes(uint4 r, uint32_t scale_byte, uint32_t (&o)[8]) {
+  const float s = scale_of(scale_byte);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    o[2 * k] = codes_to_bf16(static_cast<uint16_t>(w[k]), s);
+    o[2 * k + 1] = codes_to_bf16(static_cast<uint16_t>(w[k] >> 16), s);
+  }
+}
+// Whether one of the bf16 is not finite shows in bits 15 and 31.
+__device__ __forceinline__ uint32_t not_finite(const uint32_t (&o)[8]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) most |= (o[k] & 0x7fff7fffu) + 0x00800080u;
+  return most & 0x80008000u;
+}
+
+// The entries that item i brings to its run, one after the other by all lanes of a warp: lanes 0 .. 27 have 16 codes each,
+// lanes 28 .. 31 two times 8 rope values. Stored once O has been through the item `back` items before, which was the last to
+// see what they replace. (O may be on its way through later ones, so what is there has to be finite at any time.)
+template <bool ALIGN16>
+__device__ __forceinline__ void decode_next(const DecodeParams& p, WindowSmem& sm, int i, int back) {
+  const Item& it = sm.ring[i % kRing];
+  const int lane = threadIdx.x & 31, all = it.news;
+  const bool rope = lane >= 28;
+#pragma unroll 1
+  for (int e = 0; e <= all; ++e) {  // (one more, for an item that brings none)
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    uint32_t scale = 127;
+    Source src(p, it, e < all ? e : 0);
+    if (e == all) src.data = nullptr;
+    if (src.data != nullptr) {
+      const uint8_t* from = src.data + 16 * lane;
+      a = ALIGN16 ? ld16(from) : ld8x2(from);
+      if (rope) b = ALIGN16 ? ld16(from + 64) : ld8x2(from + 64);
+      else asm("ld.global.cg.u8 %0, [%1];" : "=r"(scale) : "l"(src.scales + (lane >> 2)));
+    }
+    if (e == 0 && i >= back) warp_wait(&sm.abort, &sm.o_full[(i - back) % kRing], ((i - back) / kRing) & 1);
+    if (e == all) break;
+    uint32_t o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (!rope) decode_codes(a, scale, o);
+    const bool poison = __any_sync(0xffffffffu, not_finite(o) != 0);
+    if (poison) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = 0;
+    }
+    const uint32_t swz = static_cast<uint32_t>(src.place & 7) << 4, unit = rope ? 16u * (lane - 28) : 32u * (lane & 3);
+    const uint32_t at = smem_addr(sm.k) + src.place * 128 + (rope ? 7 : lane >> 2) * kChunkBytes;
+    sts16(at + (unit ^ swz), o[0], o[1], o[2], o[3]);
+    sts16(at + ((unit + (rope ? 64u : 16u)) ^ swz), o[4], o[5], o[6], o[7]);
+    if (lane == 0) sm.state[src.place] = src.data == nullptr ? kAbsent : poison ? kPoison : kThere;
+  }
+  async_proxy_fence();
+  __syncwarp();
+}
+
+// The entries that a run begins with, once O has been through the item before: eight at a time to a warp, each by four
+// threads, which have the 16 bytes sub, sub + 4, ... of it (of the codes a quarter of each 64 columns, so piece j belongs to
+// scale j).
+template <bool ALIGN16>
+__device__ __forceinline__ void decode_first(const DecodeParams& p, WindowSmem& sm, int i, int index) {
+  const Item& it = sm.ring[i % kRing];
+  const int lane = threadIdx.x & 31, sub = lane & 3, all = it.lead + it.news, mine = 8 * index + (lane >> 2);
+  const uint8_t* data = nullptr;  // of this entry, and the next
+  const uint8_t* next = nullptr;
+  const uint8_t* scales_at = nullptr;
+  const uint8_t* scales_next = nullptr;
+  int place = 0, place_next = 0;
+  if (mine < all) {
+    const Source src(p, it, mine);
+    data = src.data, scales_at = src.scales, place = src.place;
+  }
+  if (mine + kPass < all) {
+    const Source src(p, it, mine + kPass);
+    next = src.data, scales_next = src.scales, place_next = src.place;
+    if (next != nullptr) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(next + 128 * sub));
+      if (sub == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + 512));
+      if (sub == 1) asm volatile("prefetch.global.L2 [%0];" ::"l"(scales_next));
+    }
+  }
+  __syncwarp();
+  bool waited = i == 0;
+#pragma unroll 1
+  for (int e = mine; e - (lane >> 2) < all || !waited; e += kPass) {
+    uint4 raw[9];
+    uint2 scales = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll
+    for (int j = 0; j < 9; ++j) {
+      raw[j] = make_uint4(0, 0, 0, 0);
+      if (data != nullptr) raw[j] = ALIGN16 ? ld16(data + 16 * sub + 64 * j) : ld8x2(data + 16 * sub + 64 * j);
+    }
+    if (data != nullptr) scales = ld8(scales_at);
+    if (!waited) {
+      warp_wait(&sm.abort, &sm.o_full[(i - 1) % kRing], ((i - 1) / kRing) & 1);
+      waited = true;
+    }
+    const uint32_t row = smem_addr(sm.k) + place * 128, swz = static_cast<uint32_t>(place & 7) << 4;
+    const bool in = e < all;
+    const uint32_t rope[8] = {raw[7].x, raw[7].y, raw[7].z, raw[7].w, raw[8].x, raw[8].y, raw[8].z, raw[8].w};  // bf16 already
+    if (in) {
+      const uint32_t at = row + 7 * kChunkBytes;
+      sts16(at + ((16u * sub) ^ swz), rope[0], rope[1], rope[2], rope[3]);
+      sts16(at + ((16u * sub + 64u) ^ swz), rope[4], rope[5], rope[6], rope[7]);
+    }
+    uint32_t poison = not_finite(rope);
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+      uint32_t o[8];
+      decode_codes(raw[j], ((j < 4 ? scales.x : scales.y) >> (8 * (j & 3))) & 0xffu, o);
+      if (in) {
+        const uint32_t at = row + j * kChunkBytes;
+        sts16(at + ((32u * sub) ^ swz), o[0], o[1], o[2], o[3]);
+        sts16(at + ((32u * sub + 16u) ^ swz), o[4], o[5], o[6], o[7]);
+      }
+      poison |= not_finite(o);
+    }
+    // An entry with a value that is not finite (a code of NaN, a bf16 that is not, a product without room): zeros.
+    poison |= __shfl_xor_sync(0xffffffffu, poison, 1);
+    poison |= __shfl_xor_sync(0xffffffffu, poison, 2);
+    if (in && poison) {
+#pragma unroll 1
+      for (int j = 0; j < 16; ++j) sts16(row + (j >> 1) * kChunkBytes + 32 * sub + 16 * (j & 1), 0, 0, 0, 0);
+    }
+    if (in && sub == 0) sm.state[place] = data == nullptr ? kAbsent : poison ? kPoison : kThere;
+    data = next, scales_at = scales_next, place = place_next;
+  }
+  async_proxy_fence();
+  __syncwarp();
+}
 
 template <bool ALIGN16>
 __global__ void __launch_bounds__(kWindowThreads, 1)
@@ -200,18 +309,19 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.ring_full[i], 1);
-      mbar_init(&sm.ring_free[i], kSoftWarps + kFillWarps + 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.k_full[i], kFillWarps);
+      mbar_init(&sm.ring_free[i], kSoftWarps + kOutWarps + 3);
+      mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.o_full[i], 1);
     }
-    mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.p_full[i], kSoftWarps);
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_free[i], 1);
+    }
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.s_free, kSoftWarps);
-    mbar_init(&sm.p_full, kSoftWarps);
-    mbar_init(&sm.o_free, kSoftWarps);
+    mbar_init(&sm.o_free, kOutWarps);
+    mbar_init(&sm.k_help, kOutWarps);
     mbar_init(&sm.drained, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.set[i], kSoftWarps / 2);
     sm.abort = 0;
@@ -220,6 +330,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
   // Places without an entry, and weights of those that there never are, have to be finite from the start.
   for (int i = threadIdx.x; i < (kKBytes + 1024) / 16; i += kWindowThreads) reinterpret_cast<uint4*>(sm.k)[i] = make_uint4(0, 0, 0, 0);
   for (int i = threadIdx.x; i < 1024 / 16; i += kWindowThreads) reinterpret_cast<uint4*>(sm.p + kSlots * 128)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < 512) sm.ones[threadIdx.x] = 0x3f803f80u;
   async_proxy_fence();  // (to the products, behind the barrier below)
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "n"(kTmemCols) : "memory");
@@ -232,12 +343,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
   grid_dependency_wait();  // what the kernels before this one wrote is read from here on
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
   volatile int* const abort_flag = &sm.abort;
-  // A wait of a whole warp; as in the decode attention's kernel, one that runs out sets the abort flag, every wait then
-  // returns at once, and the warps run on to the end, which item_flags shows them. No result is stored then.
-  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!decode_wait(bar, parity, abort_flag)) *abort_flag = 1;
-    __syncwarp();
-  };
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) { c128::warp_wait(abort_flag, bar, parity); };
   auto item_flags = [&](int i) {
     warp_wait(&sm.ring_full[i % kRing], (i / kRing) & 1);
     const int flags = sm.ring[i % kRing].flags;
@@ -249,9 +355,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
   };
 
   if (warp == kItemWarp) {
-    // -------------------------------------------------------------------------- items and queries
+    // --------------------------------------------------------------------------------- the items
     const int64_t begin = p.requests * column / plan.columns, end = p.requests * (column + 1) / plan.columns;
-    const uint32_t q_bytes = static_cast<uint32_t>(kChunks * plan.together * plan.pitch * 128);
     unsigned int err = 0;
     int64_t batch = begin;  // lanes hold tokens batch .. batch + 31
     int lo = 0, hi = 0, req = 0;
@@ -270,7 +375,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         if (ok && pos >= p.most) err |= C128_DEV_BAD_BT_COL;
       }
       if (!ok) pos = -1;
-      hi = static_cast<int>(min(pos, static_cast<int64_t>(p.most) - 1));
+      hi = static_cast<int>(min(pos, static_cast<int64_t>(0x7ffff000)));  // (of a position behind the table, which goes alone: enough)
       lo = static_cast<int>(min(max(pos + 1 - window, static_cast<int64_t>(0)), static_cast<int64_t>(p.most)));
       int64_t pos_before = __shfl_up_sync(0xffffffffu, pos, 1);
       int req_before = __shfl_up_sync(0xffffffffu, req, 1);
@@ -283,9 +388,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     if (begin < end) load_batch();
     int base = 0, newest = -1, seen_to = -1;  // the run's
     bool stalled = p.stall && blockIdx.x == 0;
-    int i = 0, loads = 0;
     int64_t t = begin;
-    for (; !stalled; ++i) {
+    for (int i = 0; !stalled; ++i) {
       while (t < end) {  // the next token that is not skipped
         if (t - batch >= 32) {
           batch += 32;
@@ -314,14 +418,15 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       it.token = static_cast<int>(t);
       it.count = count;
       it.row = __shfl_sync(0xffffffffu, req, j);
-      it.lo = __shfl_sync(0xffffffffu, lo, j);
+      const int lo_j = __shfl_sync(0xffffffffu, lo, j);
       it.hi = __shfl_sync(0xffffffffu, hi, j);
-      const int last = it.hi + count - 1;
+      const int last = min(it.hi + count, p.most) - 1;
+      it.last = last;
       const bool fresh = i == 0 || !(goes_on >> j & 1);
       if (fresh) {
-        it.lead = min(first, it.lo);
-        it.from = it.lo;
-        base = max(first, it.lo);
+        it.lead = min(first, lo_j);
+        it.from = lo_j;
+        base = max(first, lo_j);
         it.ring = 0;
         newest = max(last - base, -1);  // (-1: the ring is empty)
       } else {
@@ -336,99 +441,160 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       it.newest = newest;
       seen_to = last;
       const int used = last >= base ? first + min(last - base + 1, circle) : min(first, last + 1);
-      it.flags = (fresh || !plan.lookahead ? kSerial : 0) | (used > kMain ? kTail : 0) | max((used + 15) / 16, 1) << kStepShift;
+      it.flags = (fresh ? kFresh : 0) | (fresh || plan.lookahead < 2 ? kSerial : 0) | (used > kMain ? kTail : 0) | max((used + 15) / 16, 1) << kStepShift;
       if (lane == 0) {
         sm.ring[slot] = it;
         mbar_arrive(&sm.ring_full[slot]);
-        if (i > 0)
-          for (int c = 0; c < kChunks; ++c) prefetch_query_rows(&q_map, 64 * c, head0, it.token);
       }
       __syncwarp();
       t += count;
-      // its queries, when S of the item before has been taken
-      if (i > 0) warp_wait(&sm.q_free, (i - 1) & 1);
-      if (*abort_flag) break;
-      loads = i + 1;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sm.q_full, q_bytes);
-        for (int c = 0; c < kChunks; ++c) load_query_rows(sm.q + c * kQChunkBytes, &q_map, 64 * c, head0, it.token, &sm.q_full);
-      }
-      __syncwarp();
     }
     if (err) atomicOr(p.err, err);
-    if (loads > 0) decode_wait(&sm.q_full, (loads - 1) & 1, nullptr);  // nothing may be in flight when the CTA ends
-    __syncwarp();
-  } else if (warp >= kSoftWarps && warp < kMmaWarp) {
-    // ------------------------------------------------------------------------ decode the entries
-    const int sub = lane & 3, mine = 8 * (warp - kSoftWarps) + (lane >> 2);
-    const uint32_t k_at = smem_addr(sm.k);
-    const Divisor bs = p.kv_div;
-    unsigned int err = 0;
+  } else if (warp == kQueryWarp) {
+    // -------------------------------------------------------------------------------- the queries
+    const uint32_t q_bytes = static_cast<uint32_t>(kChunks / 2 * plan.together * plan.pitch * 128);
+    int loads = 0;
     for (int i = 0;; ++i) {
-      const int flags = item_flags(i);
-      if (flags & kEnd) break;
-      const Item it = sm.ring[i % kRing];
+      if (item_flags(i) & kEnd) break;
+      const int token = sm.ring[i % kRing].token;
       free_item(i);
-      const int all = it.lead + it.news;
-      bool waited = false;
-      for (int e0 = 0; e0 < all || !waited; e0 += 8 * kFillWarps) {
-        const int e = e0 + mine;
-        const bool in = e < all;
-        const int entry = e < it.lead ? e : it.from + e - it.lead;
-        const uint8_t* data = nullptr;
-        const uint8_t* sc = nullptr;
-        if (in) {
-          const uint32_t block = divide(entry, bs), off = entry - block * bs.value;
-          const int id = __ldcg(p.table + it.row * p.table_stride + block);
-          if (id >= 0 && id < p.nkb) {
-            const uint8_t* blk = p.kc + static_cast<int64_t>(id) * p.kc_stride0;
-            data = blk + static_cast<int64_t>(off) * kTokenStride;
-            sc = blk + p.kv_bs * kTokenStride + static_cast<int64_t>(off) * kScaleDim;
-          } else {
-            err |= C128_DEV_BAD_BLOCK;
-          }
-        }
-        Quarter x;
-        x.load<ALIGN16>(data, sc, sub);
-        bool poison = x.not_finite();
-        poison |= __shfl_xor_sync(0xffffffffu, static_cast<int>(poison), 1) != 0;
-        poison |= __shfl_xor_sync(0xffffffffu, static_cast<int>(poison), 2) != 0;
-        if (!waited) {  // the places are free
-          if (i > 0 && (flags & kSerial)) warp_wait(&sm.o_full[(i - 1) & 1], ((i - 1) >> 1) & 1);
-          else if (i > 1) warp_wait(&sm.o_full[i & 1], ((i - 2) >> 1) & 1);
-          waited = true;
-        }
-        if (in) {
-          int place = entry;
-          if (entry >= first) {
-            place = it.ring + entry - max(it.from, first);
-            place = first + (place >= circle ? place - circle : place);
-          }
-          if (sub == 0) sm.state[place] = data == nullptr ? kAbsent : poison ? kPoison : kThere;
-          const uint32_t row = k_at + place * 128, swz = static_cast<uint32_t>(place & 7) << 4;
-          const uint32_t dst0 = row + ((32u * sub) ^ swz), dst1 = row + ((32u * sub + 16u) ^ swz), dst_rope = row + 7 * kChunkBytes + ((16u * sub) ^ swz);
-#pragma unroll
-          for (int j = 0; j < 7; ++j) {
-            uint32_t o[8];
-            x.decode(j, o);
-            if (poison) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] = 0;
-            }
-            sts16(dst0 + j * kChunkBytes, o[0], o[1], o[2], o[3]);
-            sts16(dst1 + j * kChunkBytes, o[4], o[5], o[6], o[7]);
-          }
-          if (poison) x.raw[7] = x.raw[8] = make_uint4(0, 0, 0, 0);
-          sts16(dst_rope, x.raw[7].x, x.raw[7].y, x.raw[7].z, x.raw[7].w);
-          sts16(dst_rope ^ 64u, x.raw[8].x, x.raw[8].y, x.raw[8].z, x.raw[8].w);
+      if (i > 0 && lane < kChunks) prefetch_query_rows(&q_map, 64 * lane, head0, token);
+      // each half of the columns when S of the item before has been through it
+#pragma unroll 1
+      for (int half = 0; half < 2 && !*abort_flag; ++half) {
+        if (i > 0) warp_wait(&sm.q_free[half], (i - 1) & 1);
+        if (*abort_flag) break;
+        ++loads;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.q_full[half], q_bytes);
+          for (int c = kChunks / 2 * half; c < kChunks / 2 * (half + 1); ++c)
+            load_query_rows(sm.q + c * kQChunkBytes, &q_map, 64 * c, head0, token, &sm.q_full[half]);
         }
         __syncwarp();
       }
-      async_proxy_fence();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[i & 1]);
+      if (*abort_flag) break;
     }
-    if (err) atomicOr(p.err, err);
+    for (int k = max(loads - 2, 0); k < loads; ++k) decode_wait(&sm.q_full[k & 1], k >> 1 & 1, nullptr);  // nothing may be in flight when the CTA ends
+    __syncwarp();
+  } else if (warp == kDecodeWarp || (warp >= kSoftWarps && warp < kMmaWarp)) {
+    // ------------------------------------------------------------------- entries and results
+    const int w = warp & 3, own = 32 * ((warp >> 2) & 1);  // of results: TMEM lanes 32w .., rows own .. own + 31
+    const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
+    const bool busy = own < rows16, decodes = warp == kDecodeWarp;
+    // the row that this lane makes the factor of: its token and head in any item, and the head's sink
+    const int my_row = own + lane, my_token = static_cast<int>(my_row * plan.pitch_inv >> 16), my_head = my_row - my_token * plan.pitch;
+    const float sink = p.sink != nullptr && my_head < heads ? __ldcg(p.sink + head0 + my_head) * kLog2e : -INFINITY;
+    auto results = [&](int i) {
+      warp_wait(&sm.p_full[i & 1], (i >> 1) & 1);  // (its sums are there)
+      warp_wait(&sm.o_full[i % kRing], (i / kRing) & 1);
+      const Item& it = sm.ring[i % kRing];
+      const int64_t token0 = it.token;
+      const int count = it.count;
+      if (busy && !*abort_flag) {
+        tmem_fence_after();
+        const bool there = my_token < count && my_head < heads;
+        const float (&s)[4][kRows] = sm.sums[i & 1];
+        const float own_sum = (s[0][my_row] + s[1][my_row]) + (s[2][my_row] + s[3][my_row]), ref = sm.ref[i & 1][my_row];
+        {
+          uint32_t x[2][16];  // every row of L is the same
+          tmem_ld_32x16(tmem + lanes + kTmemL + own, x[0]);
+          tmem_ld_32x16(tmem + lanes + kTmemL + own + 16, x[1]);
+          tmem_wait_ld();
+          if (lane == 0) {  // (the four warps of a set write the same, here and below)
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(&sm.weights[own + k]) = make_uint4(x[k / 16][k % 16], x[k / 16][k % 16 + 1], x[k / 16][k % 16 + 2], x[k / 16][k % 16 + 3]);
+          }
+        }
+        __syncwarp();
+        // with a sink: one more score, with a value of zero
+        float sum = own_sum, to = ref, share = own_sum == 0.f ? 0.f : 1.f;
+        if (p.sink != nullptr) {
+          to = own_sum == 0.f ? (sink == -INFINITY ? 0.f : sink) : fmaxf(ref, sink);
+          const float entries = own_sum == 0.f ? 0.f : own_sum * ex2_approx(ref - to);
+          sum = entries + ex2_approx(sink - to);
+          if (own_sum != 0.f) share = entries / sum;
+        }
+        sm.inv[my_row] = share == 0.f ? 0.f : __fdividef(share, sm.weights[my_row]);
+        __syncwarp();
+#pragma unroll 1
+        for (int row0 = own; row0 < min(own + 32, rows); row0 += 16) {
+          float2 f[8];
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) *reinterpret_cast<float4*>(&f[k]) = *reinterpret_cast<const float4*>(&sm.inv[row0 + 2 * k]);
+          // eight rows are of one token: where they go, and how many there are
+          int64_t at[2];
+          int n[2];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int tk = static_cast<int>((row0 + 8 * g) * plan.pitch_inv >> 16), h0 = row0 + 8 * g - tk * plan.pitch;
+            n[g] = tk < count ? heads - h0 : 0;
+            at[g] = (token0 + tk) * p.out_stride_r + (head0 + h0) * p.out_stride_h + 32 * w;
+          }
+          if (p.out_f32) {
+#pragma unroll 1
+            for (int mt = 0; mt < 4; ++mt) {
+              uint32_t o[16];
+              tmem_ld_32x16(tmem + lanes + mt * kRows + row0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                float* dst = static_cast<float*>(p.out) + at[g] + 128 * mt + lane;
+#pragma unroll
+                for (int k = 0; k < 8; ++k, dst += p.out_stride_h)
+                  if (k < n[g]) *dst = __uint_as_float(o[8 * g + k]) * (k & 1 ? f[4 * g + k / 2].y : f[4 * g + k / 2].x);
+              }
+            }
+            continue;
+          }
+          // neighbouring lanes swap halves of a pair of rows, so that each stores two columns of one
+          const uint32_t halves = lane & 1 ? 0x3276 : 0x5410;
+          uint16_t* dst[8];
+          unsigned live = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            dst[k] = static_cast<uint16_t*>(p.out) + at[k / 4] + (2 * (k % 4) + (lane & 1)) * p.out_stride_h + (lane & ~1);
+            live |= static_cast<unsigned>(2 * (k % 4) + (lane & 1) < n[k / 4]) << k;
+          }
+#pragma unroll 1
+          for (int mt = 0; mt < 4; ++mt) {
+            uint32_t o[16];
+            tmem_ld_32x16(tmem + lanes + mt * kRows + row0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 v = mul2(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f[k]);
+              const uint32_t two = pack_bf16x2(v.x, v.y);
+              o[k] = __byte_perm(two, __shfl_xor_sync(0xffffffffu, two, 1), halves);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (live >> k & 1) *reinterpret_cast<uint32_t*>(dst[k]) = o[k];
+              dst[k] += 128;
+            }
+          }
+        }
+        tmem_fence_before();
+        if (w == 0 && there && p.lse != nullptr)
+          p.lse[(token0 + my_token) * p.lse_stride_r + (head0 + my_head) * p.lse_stride_h] =
+              sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718055994531f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_free);
+      free_item(i);
+    };
+    for (int i = 0;; ++i) {
+      const int flags = item_flags(i);
+      const bool fresh = flags & kFresh, end = flags & kEnd;
+      if (!end && (decodes || fresh)) {
+        if (fresh) decode_first<ALIGN16>(p, sm, i, decodes ? kOutWarps : warp - kSoftWarps);
+        else decode_next<ALIGN16>(p, sm, i, plan.lookahead);
+        if (lane == 0) mbar_arrive(decodes ? &sm.k_full[i % kRing] : &sm.k_help);
+      }
+      if (decodes && !end) free_item(i);
+      if (!decodes && i > 0) results(i - 1);
+      if (end) break;
+    }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------------ issue the products
     if (elect_one()) {
@@ -440,16 +606,25 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       const uint32_t q_at = desc_low(smem_addr(sm.q), 16), ks_at = desc_low(smem_addr(sm.k), 16);
       const uint32_t kv_at = desc_low(smem_addr(sm.k), kChunkBytes), p_at = desc_low(smem_addr(sm.p), 16);
       const uint32_t desc_s = mma_desc(kMain, rows16, false), desc_tail = mma_desc(64, rows16, false), desc_o = mma_desc(128, rows16, true);
-      auto product_s = [&](uint32_t d, uint32_t row0, uint32_t desc) {
+      const uint32_t desc_ones = mma_desc(64, rows16, false) | 1u << 16;  // (P the other way around)
+      const uint64_t ones = desc_plain(smem_addr(sm.ones));
+      auto half_of_s = [&](int half, bool tail) {
+        tmem_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
+        for (int c = kChunks / 2 * half; c < kChunks / 2 * (half + 1); ++c) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma(d, desc64(ks_at + ((row0 * 128 + c * kChunkBytes + ks * 32) >> 4)), desc64(q_at + ((c * kQChunkBytes + ks * 32) >> 4)), desc, c + ks > 0);
+            mma(tmem + kTmemS, desc64(ks_at + ((c * kChunkBytes + ks * 32) >> 4)), desc64(q_at + ((c * kQChunkBytes + ks * 32) >> 4)), desc_s, c + ks > 0);
+          if (!tail) continue;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma(tmem + kTmemTail, desc64(ks_at + ((kMain * 128 + c * kChunkBytes + ks * 32) >> 4)), desc64(q_at + ((c * kQChunkBytes + ks * 32) >> 4)), desc_tail,
+                c + ks > 0);
         }
+        mma_commit(&sm.q_free[half]);
       };
       auto product_o = [&](int i, int steps) {  // of item i
-        if (!wait(&sm.p_full, i & 1)) return false;
+        if (!wait(&sm.p_full[i & 1], (i >> 1) & 1)) return false;
         if (i > 0 && !wait(&sm.o_free, (i - 1) & 1)) return false;
         tmem_fence_after();
 #pragma unroll 1
@@ -458,24 +633,31 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
           for (int ks = 0; ks < steps; ++ks)
             mma(tmem + mt * kRows, desc64(kv_at + ((2 * mt * kChunkBytes + ks * 2048) >> 4)), desc64(p_at + (ks * 2048 >> 4)), desc_o, ks > 0);
         }
-        mma_commit(&sm.o_full[i & 1]);
+#pragma unroll 1
+        for (int ks = 0; ks < steps; ++ks) mma(tmem + kTmemL, ones, desc64(p_at + (ks * 2048 >> 4)), desc_ones, ks > 0);
+        mma_commit(&sm.o_full[i % kRing]);
         return true;
       };
-      int steps = 0;
+      int steps = 0, helped = 0;
       for (int i = 0;; ++i) {
         const int slot = i % kRing;
         if (!wait(&sm.ring_full[slot], (i / kRing) & 1)) break;
         const int flags = sm.ring[slot].flags;
         mbar_arrive(&sm.ring_free[slot]);
+        // S of this item before O of the one before, or (serial) behind it
         if (i > 0 && (flags & (kEnd | kSerial)) && !product_o(i - 1, steps)) break;
         if (flags & kEnd) break;
-        if (!wait(&sm.q_full, i & 1) || !wait(&sm.k_full[i & 1], (i >> 1) & 1)) break;
+        if (!wait(&sm.k_full[i % kRing], (i / kRing) & 1)) break;
+        if (flags & kFresh) {
+          if (!wait(&sm.k_help, helped & 1)) break;
+          ++helped;
+        }
         if (i > 0 && !wait(&sm.s_free, (i - 1) & 1)) break;
-        tmem_fence_after();
-        product_s(tmem + kTmemS, 0, desc_s);
-        if (flags & kTail) product_s(tmem + kTmemTail, kMain, desc_tail);
+        if (!wait(&sm.q_full[0], i & 1)) break;
+        half_of_s(0, flags & kTail);
+        if (!wait(&sm.q_full[1], i & 1)) break;
+        half_of_s(1, flags & kTail);
         mma_commit(&sm.s_full);
-        mma_commit(&sm.q_free);
         if (i > 0 && !(flags & kSerial) && !product_o(i - 1, steps)) break;
         steps = flags >> kStepShift;
       }
@@ -492,209 +674,137 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     const float c2 = p.scale * kLog2e;
     const bool busy = own < rows16;
     uint32_t set_phase = 0;
+    int helped = 0;
     auto set_sync = [&] {  // bounded, as every wait: a warp that has seen the abort flag does not come
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.set[set]);
       warp_wait(&sm.set[set], set_phase);
       set_phase ^= 1;
     };
-    // the results of item i
-    auto results = [&](int i) {
-      warp_wait(&sm.o_full[i & 1], (i >> 1) & 1);
-      const Item& it = sm.ring[i % kRing];
-      if (busy && !*abort_flag) {
-        tmem_fence_after();
-        const int row = own + lane, token = static_cast<int>(row * plan.pitch_inv >> 16), h = row - token * plan.pitch;
-        const bool there = token < it.count && h < heads;
-        const float (&s)[4][kRows] = sm.sums[i & 1];
-        const float (&r)[4][kRows] = sm.rounded[i & 1];
-        const float own_sum = (s[0][row] + s[1][row]) + (s[2][row] + s[3][row]);
-        const float rounded = (r[0][row] + r[1][row]) + (r[2][row] + r[3][row]), ref = sm.ref[i & 1][row];
-        float sum = own_sum, to = ref, share = own_sum == 0.f ? 0.f : 1.f;
-        if (p.sink != nullptr && there) {  // one more score, with a value of zero
-          const float sink = __ldcg(p.sink + head0 + h) * kLog2e;
-          to = own_sum == 0.f ? (sink == -INFINITY ? 0.f : sink) : fmaxf(ref, sink);
-          const float entries = own_sum == 0.f ? 0.f : own_sum * ex2_approx(ref - to);
-          sum = entries + ex2_approx(sink - to);
-          if (own_sum != 0.f) share = entries / sum;
-        }
-        // (the four warps of a set write the same)
-        sm.inv[row] = share == 0.f ? 0.f : share / rounded;
-        const int64_t out_token = static_cast<int64_t>(it.token) + token;
-        sm.at[row] = there ? out_token * p.out_stride_r + (head0 + h) * p.out_stride_h : -1;
-        if (w == 0 && there && p.lse != nullptr)
-          p.lse[out_token * p.lse_stride_r + (head0 + h) * p.lse_stride_h] =
-              sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718055994531f;
-        __syncwarp();
-#pragma unroll 1
-        for (int part = 0; part < 8; ++part) {  // 16 rows of 128 columns each
-          const int mt = part >> 1, row0 = own + 16 * (part & 1);
-          if (row0 >= rows) continue;
-          uint32_t o[16];
-          tmem_ld_32x16(tmem + lanes + mt * kRows + row0, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&sm.inv[row0 + k]);
-            o[k] = __float_as_uint(__uint_as_float(o[k]) * f.x), o[k + 1] = __float_as_uint(__uint_as_float(o[k + 1]) * f.y);
-            o[k + 2] = __float_as_uint(__uint_as_float(o[k + 2]) * f.z), o[k + 3] = __float_as_uint(__uint_as_float(o[k + 3]) * f.w);
-          }
-          const int col = mt * 128 + 32 * w + lane;
-          if (p.out_f32) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int64_t at = sm.at[row0 + k];
-              if (at >= 0) static_cast<float*>(p.out)[at + col] = __uint_as_float(o[k]);
-            }
-          } else {
-            // neighbouring lanes swap halves of a pair of rows, so that each stores two columns of one
-            const uint32_t halves = lane & 1 ? 0x3276 : 0x5410;
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const uint32_t two = pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1]));
-              const uint32_t both = __byte_perm(two, __shfl_xor_sync(0xffffffffu, two, 1), halves);
-              const int64_t at = sm.at[row0 + k + (lane & 1)];
-              if (at >= 0) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at + (col & ~1)) = both;
-            }
-          }
-        }
-        tmem_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.o_free);
-      free_item(i);
-    };
-
-    int i = 0;
-    for (;; ++i) {
+    for (int i = 0;; ++i) {
       const int flags = item_flags(i);
       if (flags & kEnd) break;
       const Item& it = sm.ring[i % kRing];
-      const bool serial = flags & kSerial, tail = (flags & kTail) && w == 0;
-      if (i > 0 && serial) {
-        warp_wait(&sm.p_full, (i - 1) & 1);  // (its sums are all there)
-        results(i - 1);
+      const bool tail = (flags & kTail) && w == 0;
+      warp_wait(&sm.k_full[i % kRing], (i / kRing) & 1);
+      if (flags & kFresh) {
+        warp_wait(&sm.k_help, helped & 1);
+        ++helped;
       }
-      // What this thread's entries are: their position, or out of sight (a position behind all). The tail's are 128 ..
-      // 135, in the first 16 lanes of TMEM.
-      int pos[5];
-      bool poison[5];
-      const int last = it.hi + it.count - 1;
-#pragma unroll
-      for (int k = 0; k < 5; ++k) {
-        const int place = k < 4 ? 32 * w + 8 * k + (lane >> 2) : kMain + (lane >> 2);
-        int d = it.newest - (place - first);
-        if (d < 0) d += circle;
-        pos[k] = place < first ? place : last - d;
-        if (place >= first && pos[k] < it.base) pos[k] = 0x7fffffff;
-        // (what other items' entries leave there is not looked at: their positions are out of sight)
-        poison[k] = false;
-      }
-      // Rows of one group of 8 are of one token; its lowest and highest entry.
-      int lo[4], hi[4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16);
-        hi[g] = it.hi + token;
-        lo[g] = token == 0 ? it.lo : max(hi[g] - window + 1, 0);
-      }
-      warp_wait(&sm.s_full, i & 1);
-      tmem_fence_after();
       if (busy) {
-        bool any_poison = false;
+        // This thread's entries are 32w + lane / 4 and on in steps of 8, and of the tail (in the first 16 lanes of TMEM) one.
+        // A score is at most `most`: -inf where the row does not see the entry, else +inf (which a NaN becomes, and in the
+        // difference from the largest NaN again). `plus` is NaN for an entry that is not finite, else 0.
+        float most[5][4], plus[5];
 #pragma unroll
         for (int k = 0; k < 5; ++k) {
           const int place = k < 4 ? 32 * w + 8 * k + (lane >> 2) : kMain + (lane >> 2);
+          int d = it.newest - (place - first);
+          if (d < 0) d += circle;
+          const int pos = place < first ? place : it.last - d;
           const uint8_t state = sm.state[place];
-          if (state == kAbsent) pos[k] = 0x7fffffff;
-          poison[k] = state == kPoison;
-          any_poison |= poison[k];
+          // it is seen from that many positions on, from its own; 0: there is none
+          const unsigned reach = state == kAbsent || (place >= first && pos < it.base) ? 0u : place < first ? 0x80000000u : window;
+          plus[k] = state == kPoison ? NAN : 0.f;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {  // eight rows are of one token
+            const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16);
+            most[k][g] = static_cast<unsigned>(it.hi + token - pos) < reach ? INFINITY : -INFINITY;
+          }
         }
-        uint32_t x[2][16], y[16];
-        tmem_ld_scores<32>(tmem + lanes + kTmemS + own, x[0]);
-        tmem_ld_scores<32>(tmem + lanes + (16u << 16) + kTmemS + own, x[1]);
-        if (tail) tmem_ld_scores<32>(tmem + lanes + kTmemTail + own, y);
-        tmem_wait_ld();
+        warp_wait(&sm.s_full, i & 1);
+        tmem_fence_after();
+        float2 v[5][4];  // scores of rows r0 + 8g and + 1 in v[..][g]
+        {
+          uint32_t x[2][16], y[16];
+          tmem_ld_scores<32>(tmem + lanes + kTmemS + own, x[0]);
+          tmem_ld_scores<32>(tmem + lanes + (16u << 16) + kTmemS + own, x[1]);
+          if (tail) tmem_ld_scores<32>(tmem + lanes + kTmemTail + own, y);
+          tmem_wait_ld();
+          auto score = [&](uint32_t a, uint32_t b, int k, int g) {
+            const float2 t = fma2(make_float2(__uint_as_float(a), __uint_as_float(b)), make_float2(c2, c2), make_float2(plus[k], plus[k]));
+            return make_float2(fminf(t.x, most[k][g]), fminf(t.y, most[k][g]));
+          };
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k][g] = score(x[k >> 1][4 * g + 2 * (k & 1)], x[k >> 1][4 * g + 2 * (k & 1) + 1], k, g);
+          }
+          if (tail) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) v[4][g] = score(y[4 * g], y[4 * g + 1], 4, g);
+          }
+        }
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.s_free);
-        // v[k][2g + e]: entry k, row r0 + 8g + e; -inf where the row does not see the entry
-        float v[5][8], top[8];
+        float top[8];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          top[2 * g] = fmaxf(fmaxf(v[0][g].x, v[1][g].x), fmaxf(v[2][g].x, v[3][g].x));
+          top[2 * g + 1] = fmaxf(fmaxf(v[0][g].y, v[1][g].y), fmaxf(v[2][g].y, v[3][g].y));
+        }
+        if (tail) {
 #pragma unroll
-          for (int k = 0; k < 5; ++k) {
-            const bool sees = pos[k] <= hi[g] && (pos[k] >= lo[g] || pos[k] < first) && (k < 4 || tail);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float s = __uint_as_float(k < 4 ? x[k >> 1][4 * g + 2 * (k & 1) + e] : y[4 * g + e]);
-              v[k][2 * g + e] = sees ? __fmul_rn(s, c2) : -INFINITY;
-              if (any_poison && poison[k] && sees) v[k][2 * g + e] = NAN;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(fmaxf(v[0][2 * g + e], v[1][2 * g + e]), fmaxf(v[2][2 * g + e], v[3][2 * g + e]));
-            top[2 * g + e] = fmaxf(m, v[4][2 * g + e]);
-          }
+          for (int g = 0; g < 4; ++g) top[2 * g] = fmaxf(top[2 * g], v[4][g].x), top[2 * g + 1] = fmaxf(top[2 * g + 1], v[4][g].y);
         }
         sm.by_max[i & 1][w][reduced] = reduce_rows(top, lane, [](float a, float b) { return fmaxf(a, b); });
         set_sync();
-        float sum[8], rounded[8];
-        uint32_t packed[5][4];
+        float2 ref[4];  // less than nothing: what is added to the scores
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           float2 m[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) m[k] = *reinterpret_cast<const float2*>(&sm.by_max[i & 1][k][r0 + 8 * g]);
-          float ref[2] = {fmaxf(fmaxf(m[0].x, m[1].x), fmaxf(m[2].x, m[3].x)), fmaxf(fmaxf(m[0].y, m[1].y), fmaxf(m[2].y, m[3].y))};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (ref[e] == -INFINITY) ref[e] = 0.f;
-            sum[2 * g + e] = rounded[2 * g + e] = 0.f;
-          }
-          if (w == 0 && lane < 4) *reinterpret_cast<float2*>(&sm.ref[i & 1][r0 + 8 * g]) = make_float2(ref[0], ref[1]);
-#pragma unroll
-          for (int k = 0; k < 5; ++k) {
-            const float a = ex2_approx(__fsub_rn(v[k][2 * g], ref[0])), b = ex2_approx(__fsub_rn(v[k][2 * g + 1], ref[1]));
-            packed[k][g] = pack_bf16x2(a, b);
-            sum[2 * g] += a, sum[2 * g + 1] += b;
-            rounded[2 * g] += __uint_as_float(packed[k][g] << 16), rounded[2 * g + 1] += __uint_as_float(packed[k][g] & 0xffff0000u);
-          }
+          ref[g] = make_float2(-fmaxf(fmaxf(m[0].x, m[1].x), fmaxf(m[2].x, m[3].x)), -fmaxf(fmaxf(m[0].y, m[1].y), fmaxf(m[2].y, m[3].y)));
+          if (ref[g].x == INFINITY) ref[g].x = 0.f;  // (of a row that sees nothing)
+          if (ref[g].y == INFINITY) ref[g].y = 0.f;
         }
-        const float sum1 = reduce_rows(sum, lane, [](float a, float b) { return a + b; });
-        const float rounded1 = reduce_rows(rounded, lane, [](float a, float b) { return a + b; });
+        float2 sum[4] = {};
+        uint32_t packed[5][4];
+        auto weigh = [&](int k, int g) {
+          const float2 t = add2(v[k][g], ref[g]), e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+          packed[k][g] = pack_bf16x2(e.x, e.y);
+          sum[g] = k == 0 ? e : add2(sum[g], e);
+        };
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) weigh(k, g);
+        }
+        if (tail) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) weigh(4, g);
+        }
+        const float sums8[8] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y, sum[2].x, sum[2].y, sum[3].x, sum[3].y};
+        const float sum1 = reduce_rows(sums8, lane, [](float a, float b) { return a + b; });
         // the weights of the item before have been used
-        if (i > 0) {
-          warp_wait(&sm.o_full[(i - 1) & 1], ((i - 1) >> 1) & 1);
-          warp_wait(&sm.p_full, (i - 1) & 1);  // (and its sums are all there)
+        if (i > 0) warp_wait(&sm.o_full[(i - 1) % kRing], ((i - 1) / kRing) & 1);
+        if (w == 0) {  // (and the references)
+          const float ref = fmaxf(fmaxf(sm.by_max[i & 1][0][own + lane], sm.by_max[i & 1][1][own + lane]),
+                                  fmaxf(sm.by_max[i & 1][2][own + lane], sm.by_max[i & 1][3][own + lane]));
+          sm.ref[i & 1][own + lane] = ref == -INFINITY ? 0.f : ref;
         }
         sm.sums[i & 1][w][reduced] = sum1;
-        sm.rounded[i & 1][w][reduced] = rounded1;
         const uint32_t swz = static_cast<uint32_t>(lane >> 2) << 4;  // of all its entries
+        const uint32_t p_at = smem_addr(sm.p) + (32 * w + (lane >> 2)) * 128 + 4 * (lane & 3);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const uint32_t at = smem_addr(sm.p) + (32 * w + (lane >> 2)) * 128 + 4 * (lane & 3) + ((16u * (own / 8 + g)) ^ swz);
+          const uint32_t at = p_at + ((16u * (own / 8 + g)) ^ swz);
 #pragma unroll
           for (int k = 0; k < 4; ++k) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + k * 1024), "r"(packed[k][g]) : "memory");
-          if (w == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + kMain * 128), "r"(packed[4][g]) : "memory");
+          if (tail) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + kMain * 128), "r"(packed[4][g]) : "memory");
         }
         async_proxy_fence();
       } else {
+        warp_wait(&sm.s_full, i & 1);
         if (lane == 0) mbar_arrive(&sm.s_free);
-        if (i > 0) {
-          warp_wait(&sm.o_full[(i - 1) & 1], ((i - 1) >> 1) & 1);
-          warp_wait(&sm.p_full, (i - 1) & 1);
-        }
+        if (i > 0) warp_wait(&sm.o_full[(i - 1) % kRing], ((i - 1) / kRing) & 1);
       }
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full);
-      if (i > 0 && !serial) results(i - 1);
-    }
-    if (i > 0) {
-      warp_wait(&sm.p_full, (i - 1) & 1);
-      results(i - 1);
+      if (lane == 0) mbar_arrive(&sm.p_full[i & 1]);
+      free_item(i);
     }
   }
   tmem_fence_before();
@@ -748,10 +858,10 @@ cudaError_t launch_window(const DecodeParams& p, int sm_count, cudaStream_t stre
   plan.pitch_inv = (65536 + plan.pitch - 1) / plan.pitch;
   const int room = kSlots - p.first - static_cast<int>(p.window) + 1;  // entries that a run may bring before O is done with those they replace
   int64_t together = plan.groups > 1 ? 1 : kRows / plan.pitch;
-  if (together > room) together = room;
+  if (together > room / 2) together = room / 2 > 0 ? room / 2 : 1;  // (so that entries of one item do not wait for O of the one before)
   if (together > (T + sm_count - 1) / sm_count) together = (T + sm_count - 1) / sm_count;
   plan.together = static_cast<int32_t>(together);
-  plan.lookahead = 2 * plan.together <= room ? 1 : 0;
+  plan.lookahead = room / plan.together < kRing ? room / plan.together : kRing;
   const int64_t most = sm_count / plan.groups > 0 ? sm_count / plan.groups : 1;
   plan.columns = static_cast<int32_t>(T < most ? T : most);
   CUtensorMap map;

@@ -268,3 +268,17 @@ def test_rows_that_are_not_finite():
     other = [h for h in range(16) if h != 5]
     ref_out, ref_lse = c.run()
     assert torch.equal(out[3, other], ref_out[3, other]) and torch.equal(out[9, 1:], ref_out[9, 1:])
+
+
+@pytest.mark.parametrize("H", [64, 16])
+def test_entries_of_any_magnitude_that_are_not_seen(H):
+    """Entries so large that a score with them has no room, beside tokens that do not see them."""
+    c = Case(42, consecutive(0, 0, 60), [60], H, 12, 2, 8, rubbish=False)
+    flat = c.cache.reshape(c.cache.shape[0], -1)
+    for j in (20, 33):
+        page, off = c.table[0, j // 8], j % 8
+        flat[page, 8 * 576 + off * 8:8 * 576 + off * 8 + 7] = 246  # 2^119
+        flat[page, off * 576:off * 576 + 448] = 0x7e               # 448
+    c.q[:] = c.q.abs()
+    out, lse = c.run()
+    c.check(out, lse, tokens=[t for t in range(60) if not (20 <= t < 32 or 33 <= t < 45)])
