@@ -86,7 +86,7 @@ struct WindowSmem {
   alignas(16) float sums[2][4][kRows];
   alignas(128) uint32_t ones[512];               // 64 x 16 of bf16, in any order
   alignas(16) float ref[2][kRows];
-  alignas(16) float inv[kRows], weights[kRows];  // 1 / L (with a sink: the entries' share / L); L
+  alignas(16) float inv[2][kRows], weights[kRows];  // 1 / L (with a sink: the entries' share / L), of even and odd items; L
   Item ring[kRing];
   uint64_t ring_full[kRing], ring_free[kRing];
   uint64_t k_full[kRing], o_full[kRing];
@@ -94,7 +94,8 @@ struct WindowSmem {
   uint64_t k_help;                    // the first entries of a run
   uint64_t q_full[2], q_free[2];      // of either half of the columns
   uint64_t set[2];                    // barriers of the softmax warps of either half
-  uint64_t s_full, s_free, o_free, drained;
+  uint64_t o_part[4], o_free[4];      // by 128 columns: O is there; it has been read
+  uint64_t s_full, s_free, drained;
   uint8_t state[kSlots];
   uint32_t tmem;
   volatile int abort;
@@ -131,10 +132,21 @@ __device__ __forceinline__ float reduce_rows(const float (&v)[8], int lane, F op
   return op(hi ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, hi ? b[0] : b[1], 4));
 }
 
-// A wait of a whole warp; as in the decode attention's kernel, one that runs out sets the abort flag, every wait then
-// returns at once, and the warps run on to the end, which the items' flags show them. No result is stored then.
+// The bounded wait of this kernel. Tries that let the thread rest: most warps wait most of the time, and each try passes
+// through the shared memory that the products' operands need. Short, since there are many of them.
+constexpr uint32_t kTries = 50000;  // of up to 20 us each: about a second
+__device__ __forceinline__ bool wait_for(volatile int* abort_flag, uint64_t* bar, uint32_t parity) {
+  uint32_t left = kTries;
+#pragma unroll 1
+  while (!mbar_try_wait_suspend(bar, parity)) {
+    if (*abort_flag || --left == 0) return false;
+  }
+  return true;
+}
+// Of a whole warp: as in the decode attention's kernel, one that runs out sets the abort flag, every wait then returns at
+// once, and the warps run on to the end, which the items' flags show them. No result is stored then.
 __device__ __forceinline__ void warp_wait(volatile int* abort_flag, uint64_t* bar, uint32_t parity) {
-  if (!decode_wait(bar, parity, abort_flag)) *abort_flag = 1;
+  if (!wait_for(abort_flag, bar, parity)) *abort_flag = 1;
   __syncwarp();
 }
 
@@ -294,7 +306,7 @@ __device__ __forceinline__ void decode_first(const DecodeParams& p, WindowSmem& 
   __syncwarp();
 }
 
-template <bool ALIGN16>
+template <bool ALIGN16, bool OUT_F32>
 __global__ void __launch_bounds__(kWindowThreads, 1)
     window_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ WindowPlan plan) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -320,10 +332,13 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     }
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.s_free, kSoftWarps);
-    mbar_init(&sm.o_free, kOutWarps);
     mbar_init(&sm.k_help, kOutWarps);
     mbar_init(&sm.drained, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.set[i], kSoftWarps / 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.o_part[i], 1);
+      mbar_init(&sm.o_free[i], kOutWarps);
+    }
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -356,7 +371,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
 
   if (warp == kItemWarp) {
     // --------------------------------------------------------------------------------- the items
-    const int64_t begin = p.requests * column / plan.columns, end = p.requests * (column + 1) / plan.columns;
+    const unsigned share = static_cast<unsigned>(p.requests) / static_cast<unsigned>(plan.columns);  // tokens of a column, the first `extra` one more
+    const int extra = static_cast<int>(p.requests) - static_cast<int>(share) * plan.columns;
+    const int64_t begin = static_cast<int64_t>(share) * column + min(column, extra), end = begin + share + (column < extra ? 1 : 0);
     unsigned int err = 0;
     int64_t batch = begin;  // lanes hold tokens batch .. batch + 31
     int lo = 0, hi = 0, req = 0;
@@ -484,103 +501,106 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     // the row that this lane makes the factor of: its token and head in any item, and the head's sink
     const int my_row = own + lane, my_token = static_cast<int>(my_row * plan.pitch_inv >> 16), my_head = my_row - my_token * plan.pitch;
     const float sink = p.sink != nullptr && my_head < heads ? __ldcg(p.sink + head0 + my_head) * kLog2e : -INFINITY;
+    const uint32_t halves = lane & 1 ? 0x3276 : 0x5410;
+    // Eight rows are of one token: where the first that this lane stores goes, from the item's first token on. (Of bf16 a lane
+    // stores every other row of pairs of columns.)
+    int64_t out_at[4], out_step = p.out_stride_h * 4;  // two rows of bf16, in bytes
+    asm volatile("" : "+l"(out_step));
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16), h0 = own + 8 * g - token * plan.pitch;
+      out_at[g] = token * p.out_stride_r + (head0 + h0 + (OUT_F32 ? 0 : lane & 1)) * p.out_stride_h + 32 * w + (OUT_F32 ? lane : lane & ~1);
+    }
     auto results = [&](int i) {
       warp_wait(&sm.p_full[i & 1], (i >> 1) & 1);  // (its sums are there)
-      warp_wait(&sm.o_full[i % kRing], (i / kRing) & 1);
       const Item& it = sm.ring[i % kRing];
       const int64_t token0 = it.token;
       const int count = it.count;
-      if (busy && !*abort_flag) {
-        tmem_fence_after();
-        const bool there = my_token < count && my_head < heads;
-        const float (&s)[4][kRows] = sm.sums[i & 1];
-        const float own_sum = (s[0][my_row] + s[1][my_row]) + (s[2][my_row] + s[3][my_row]), ref = sm.ref[i & 1][my_row];
-        {
-          uint32_t x[2][16];  // every row of L is the same
-          tmem_ld_32x16(tmem + lanes + kTmemL + own, x[0]);
-          tmem_ld_32x16(tmem + lanes + kTmemL + own + 16, x[1]);
-          tmem_wait_ld();
-          if (lane == 0) {  // (the four warps of a set write the same, here and below)
+      const bool there = my_token < count && my_head < heads;
+      const float (&s)[4][kRows] = sm.sums[i & 1];
+      const float own_sum = (s[0][my_row] + s[1][my_row]) + (s[2][my_row] + s[3][my_row]), ref = sm.ref[i & 1][my_row];
+      // with a sink: one more score, with a value of zero
+      float sum = own_sum, to = ref, share = own_sum == 0.f ? 0.f : 1.f;
+      if (p.sink != nullptr) {
+        to = own_sum == 0.f ? (sink == -INFINITY ? 0.f : sink) : fmaxf(ref, sink);
+        const float entries = own_sum == 0.f ? 0.f : own_sum * ex2_approx(ref - to);
+        sum = entries + ex2_approx(sink - to);
+        if (own_sum != 0.f) share = entries / sum;
+      }
+      const int64_t row0 = token0 * p.out_stride_r;
+      int limit[4];  // rows on from there that there are
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<uint4*>(&sm.weights[own + k]) = make_uint4(x[k / 16][k % 16], x[k / 16][k % 16 + 1], x[k / 16][k % 16 + 2], x[k / 16][k % 16 + 3]);
-          }
-        }
-        __syncwarp();
-        // with a sink: one more score, with a value of zero
-        float sum = own_sum, to = ref, share = own_sum == 0.f ? 0.f : 1.f;
-        if (p.sink != nullptr) {
-          to = own_sum == 0.f ? (sink == -INFINITY ? 0.f : sink) : fmaxf(ref, sink);
-          const float entries = own_sum == 0.f ? 0.f : own_sum * ex2_approx(ref - to);
-          sum = entries + ex2_approx(sink - to);
-          if (own_sum != 0.f) share = entries / sum;
-        }
-        sm.inv[my_row] = share == 0.f ? 0.f : __fdividef(share, sm.weights[my_row]);
-        __syncwarp();
+      for (int g = 0; g < 4; ++g) {
+        const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16), h0 = own + 8 * g - token * plan.pitch;
+        limit[g] = token < count ? heads - h0 - (OUT_F32 ? 0 : lane & 1) : 0;
+      }
+      warp_wait(&sm.o_part[0], i & 1);
+      tmem_fence_after();
+      uint32_t o[32];
+      tmem_ld_32x32(tmem + lanes + kTmemL + own, o);  // every row of L is the same
+      tmem_wait_ld();
+      if (lane == 0) {  // (the four warps of a set write the same, here and below)
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) *reinterpret_cast<uint4*>(&sm.weights[own + k]) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+      }
+      tmem_ld_32x32(tmem + lanes + own, o);
+      __syncwarp();
+      sm.inv[i & 1][my_row] = share == 0.f ? 0.f : __fdividef(share, sm.weights[my_row]);
+      __syncwarp();
 #pragma unroll 1
-        for (int row0 = own; row0 < min(own + 32, rows); row0 += 16) {
-          float2 f[8];
+      for (int mt = 0; mt < 4; ++mt) {  // 128 columns, of them 32 to a warp, of 32 rows
+        tmem_wait_ld();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_free[mt]);
+        const bool more = mt < 3;
+        if (more) {
+          warp_wait(&sm.o_part[mt + 1], i & 1);
+          tmem_fence_after();
+        }
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) *reinterpret_cast<float4*>(&f[k]) = *reinterpret_cast<const float4*>(&sm.inv[row0 + 2 * k]);
-          // eight rows are of one token: where they go, and how many there are
-          int64_t at[2];
-          int n[2];
+        for (int k = 0; k < 32; k += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm.inv[i & 1][own + k]);
+          const float2 v0 = mul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), make_float2(f.x, f.y));
+          const float2 v1 = mul2(make_float2(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])), make_float2(f.z, f.w));
+          o[k] = __float_as_uint(v0.x), o[k + 1] = __float_as_uint(v0.y);
+          o[k + 2] = __float_as_uint(v1.x), o[k + 3] = __float_as_uint(v1.y);
+        }
+        const bool store = busy && !*abort_flag;
+        if constexpr (OUT_F32) {
+          if (store) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const int tk = static_cast<int>((row0 + 8 * g) * plan.pitch_inv >> 16), h0 = row0 + 8 * g - tk * plan.pitch;
-            n[g] = tk < count ? heads - h0 : 0;
-            at[g] = (token0 + tk) * p.out_stride_r + (head0 + h0) * p.out_stride_h + 32 * w;
+            for (int g = 0; g < 4; ++g) {
+              float* dst = static_cast<float*>(p.out) + row0 + out_at[g] + 128 * mt;
+#pragma unroll
+              for (int k = 0; k < 8; ++k, dst += p.out_stride_h)
+                if (k < limit[g]) *dst = __uint_as_float(o[8 * g + k]);
+            }
           }
-          if (p.out_f32) {
-#pragma unroll 1
-            for (int mt = 0; mt < 4; ++mt) {
-              uint32_t o[16];
-              tmem_ld_32x16(tmem + lanes + mt * kRows + row0, o);
-              tmem_wait_ld();
+          if (more) tmem_ld_32x32(tmem + lanes + (mt + 1) * kRows + own, o);
+        } else {
+          uint32_t two[16];
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                float* dst = static_cast<float*>(p.out) + at[g] + 128 * mt + lane;
+          for (int k = 0; k < 16; ++k) two[k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+          if (more) tmem_ld_32x32(tmem + lanes + (mt + 1) * kRows + own, o);  // on its way as these are stored
+          if (store) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k, dst += p.out_stride_h)
-                  if (k < n[g]) *dst = __uint_as_float(o[8 * g + k]) * (k & 1 ? f[4 * g + k / 2].y : f[4 * g + k / 2].x);
+            for (int g = 0; g < 4; ++g) {
+              char* dst = reinterpret_cast<char*>(static_cast<uint16_t*>(p.out) + row0 + out_at[g] + 128 * mt);
+#pragma unroll
+              for (int k = 0; k < 4; ++k, dst += out_step) {
+                asm volatile("" : "+l"(dst));  // (a running sum: a product of 64 bits for each row takes five times the instructions)
+                // neighbouring lanes swap halves of a pair of rows, so that each stores two columns of one
+                const uint32_t both = __byte_perm(two[4 * g + k], __shfl_xor_sync(0xffffffffu, two[4 * g + k], 1), halves);
+                if (2 * k < limit[g]) *reinterpret_cast<uint32_t*>(dst) = both;
               }
             }
-            continue;
-          }
-          // neighbouring lanes swap halves of a pair of rows, so that each stores two columns of one
-          const uint32_t halves = lane & 1 ? 0x3276 : 0x5410;
-          uint16_t* dst[8];
-          unsigned live = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            dst[k] = static_cast<uint16_t*>(p.out) + at[k / 4] + (2 * (k % 4) + (lane & 1)) * p.out_stride_h + (lane & ~1);
-            live |= static_cast<unsigned>(2 * (k % 4) + (lane & 1) < n[k / 4]) << k;
-          }
-#pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
-            uint32_t o[16];
-            tmem_ld_32x16(tmem + lanes + mt * kRows + row0, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float2 v = mul2(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f[k]);
-              const uint32_t two = pack_bf16x2(v.x, v.y);
-              o[k] = __byte_perm(two, __shfl_xor_sync(0xffffffffu, two, 1), halves);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (live >> k & 1) *reinterpret_cast<uint32_t*>(dst[k]) = o[k];
-              dst[k] += 128;
-            }
           }
         }
-        tmem_fence_before();
-        if (w == 0 && there && p.lse != nullptr)
-          p.lse[(token0 + my_token) * p.lse_stride_r + (head0 + my_head) * p.lse_stride_h] =
-              sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718055994531f;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.o_free);
+      if (busy && w == 0 && there && p.lse != nullptr && !*abort_flag)
+        p.lse[(token0 + my_token) * p.lse_stride_r + (head0 + my_head) * p.lse_stride_h] =
+            sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718055994531f;
       free_item(i);
     };
     for (int i = 0;; ++i) {
@@ -599,7 +619,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     // ------------------------------------------------------------------------ issue the products
     if (elect_one()) {
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (decode_wait(bar, parity, abort_flag)) return true;
+        if (wait_for(abort_flag, bar, parity)) return true;
         *abort_flag = 1;
         return false;
       };
@@ -625,16 +645,19 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       };
       auto product_o = [&](int i, int steps) {  // of item i
         if (!wait(&sm.p_full[i & 1], (i >> 1) & 1)) return false;
-        if (i > 0 && !wait(&sm.o_free, (i - 1) & 1)) return false;
-        tmem_fence_after();
 #pragma unroll 1
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = 0; mt < 4; ++mt) {  // as the results of the item before leave it, L with the first
+          if (i > 0 && !wait(&sm.o_free[mt], (i - 1) & 1)) return false;
+          tmem_fence_after();
+          if (mt == 0) {
+#pragma unroll 1
+            for (int ks = 0; ks < steps; ++ks) mma(tmem + kTmemL, ones, desc64(p_at + (ks * 2048 >> 4)), desc_ones, ks > 0);
+          }
 #pragma unroll 1
           for (int ks = 0; ks < steps; ++ks)
             mma(tmem + mt * kRows, desc64(kv_at + ((2 * mt * kChunkBytes + ks * 2048) >> 4)), desc64(p_at + (ks * 2048 >> 4)), desc_o, ks > 0);
+          mma_commit(&sm.o_part[mt]);
         }
-#pragma unroll 1
-        for (int ks = 0; ks < steps; ++ks) mma(tmem + kTmemL, ones, desc64(p_at + (ks * 2048 >> 4)), desc_ones, ks > 0);
         mma_commit(&sm.o_full[i % kRing]);
         return true;
       };
@@ -696,6 +719,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         // A score is at most `most`: -inf where the row does not see the entry, else +inf (which a NaN becomes, and in the
         // difference from the largest NaN again). `plus` is NaN for an entry that is not finite, else 0.
         float most[5][4], plus[5];
+        int ahead[5];  // positions from the entry to the first token
+        unsigned reach[5];
 #pragma unroll
         for (int k = 0; k < 5; ++k) {
           const int place = k < 4 ? 32 * w + 8 * k + (lane >> 2) : kMain + (lane >> 2);
@@ -703,13 +728,21 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
           if (d < 0) d += circle;
           const int pos = place < first ? place : it.last - d;
           const uint8_t state = sm.state[place];
+          ahead[k] = it.hi - pos;
           // it is seen from that many positions on, from its own; 0: there is none
-          const unsigned reach = state == kAbsent || (place >= first && pos < it.base) ? 0u : place < first ? 0x80000000u : window;
+          reach[k] = state == kAbsent || (place >= first && pos < it.base) ? 0u : place < first ? 0x80000000u : window;
           plus[k] = state == kPoison ? NAN : 0.f;
+        }
+        if (plan.together == 1) {
+#pragma unroll
+          for (int k = 0; k < 5; ++k)
+            most[k][0] = most[k][1] = most[k][2] = most[k][3] = static_cast<unsigned>(ahead[k]) < reach[k] ? INFINITY : -INFINITY;
+        } else {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {  // eight rows are of one token
             const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16);
-            most[k][g] = static_cast<unsigned>(it.hi + token - pos) < reach ? INFINITY : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 5; ++k) most[k][g] = static_cast<unsigned>(ahead[k] + token) < reach[k] ? INFINITY : -INFINITY;
           }
         }
         warp_wait(&sm.s_full, i & 1);
@@ -816,8 +849,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
   }
 }
 
-const void* window_kernel_for(bool align16) {
-  return align16 ? reinterpret_cast<const void*>(window_kernel<true>) : reinterpret_cast<const void*>(window_kernel<false>);
+const void* window_kernel_for(bool align16, bool out_f32) {
+  if (out_f32) return align16 ? reinterpret_cast<const void*>(window_kernel<true, true>) : reinterpret_cast<const void*>(window_kernel<false, true>);
+  return align16 ? reinterpret_cast<const void*>(window_kernel<true, false>) : reinterpret_cast<const void*>(window_kernel<false, false>);
 }
 
 // The queries as [512, heads, tokens]; a box is 64 columns of the heads of an item's tokens.
@@ -840,9 +874,10 @@ bool window_fits(const DecodeParams& p) { return p.window + p.first <= kSlots; }
 
 cudaError_t prepare_window() {
   cudaError_t e = cudaSuccess;
-  for (int align16 = 0; align16 < 2; ++align16)
+  for (int variant = 0; variant < 4; ++variant)
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(window_kernel_for(align16 != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(WindowSmem));
+      e = cudaFuncSetAttribute(window_kernel_for((variant & 1) != 0, (variant & 2) != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               sizeof(WindowSmem));
   return e;
 }
 
@@ -877,7 +912,7 @@ cudaError_t launch_window(const DecodeParams& p, int sm_count, cudaStream_t stre
   lc.attrs = attr;
   lc.numAttrs = 1;
   void* args[] = {const_cast<DecodeParams*>(&p), &map, &plan};
-  return cudaLaunchKernelExC(&lc, window_kernel_for(p.kc_stride0 % 16 == 0), args);
+  return cudaLaunchKernelExC(&lc, window_kernel_for(p.kc_stride0 % 16 == 0, p.out_f32 != 0), args);
 }
 
 }  // namespace c128
