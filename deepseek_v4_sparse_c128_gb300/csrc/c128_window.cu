@@ -2,10 +2,8 @@
 // their entries decoded there, so that each entry is decoded once for all of them.
 //
 //   S^T = K Q^T            M = 128 entries (and the rest of them), N = rows, K = 512
-//   P^T = exp2(c S^T - m)  c = scale * log2(e), m the row's largest c S^T
-//   O^T = K^T P^T          M = 128 columns (4 times), N = rows, K = entries
-//   L = 1 P^T              the sums of P as the products see it, rounded to bf16: M = 64 rows of ones
-//   out = O / L; lse is of the exact sums, in fp32
+//   P^T = exp2(c S^T - m) / l   c = scale * log2(e), m the row's largest c S^T, l the sum (and the sink's share)
+//   O^T = K^T P^T          M = 128 columns (4 times), N = rows, K = entries; the result
 //
 // An entry is key and value: both products read it as their A, with the 512 columns along K, and with them along M. An
 // item is a token with its heads (up to 64 rows, padded to eights), or as many consecutive tokens as 64 rows hold. Entries
@@ -53,7 +51,7 @@ constexpr int kPass = 8 * (kOutWarps + 1);  // entries that are decoded at once 
 static_assert(2 * kPass >= kSlots, "two passes");
 constexpr int kWindowThreads = 32 * (kQueryWarp + 1);
 constexpr int kRing = 4;      // items that may be on their way
-constexpr int kTmemCols = 512, kTmemS = 256, kTmemTail = 320, kTmemL = 384;
+constexpr int kTmemCols = 512, kTmemS = 256, kTmemTail = 320;
 
 enum : int { kEnd = 1, kFresh = 2, kSerial = 4, kTail = 8, kStepShift = 4 };  // flags of an item; above: K steps of O
 enum : uint8_t { kThere = 0, kAbsent = 1, kPoison = 2 };          // what an entry's place holds
@@ -82,11 +80,8 @@ struct WindowSmem {
   alignas(1024) uint8_t zeros[1024];  // where the last K step of the last chunk reads on
   alignas(1024) uint8_t q[kRows * kHead * 2];
   alignas(1024) uint8_t p[kPBytes];
-  alignas(16) float by_max[2][4][kRows];         // of even and odd items: 32 entries each
-  alignas(16) float sums[2][4][kRows];
-  alignas(128) uint32_t ones[512];               // 64 x 16 of bf16, in any order
-  alignas(16) float ref[2][kRows];
-  alignas(16) float inv[2][kRows], weights[kRows];  // 1 / L (with a sink: the entries' share / L), of even and odd items; L
+  alignas(16) float by_warp[2][4][kRows];  // maxima, and sums, of 32 entries each
+  alignas(16) float ref[kRows], share[kRows];  // less the largest score; 1 / l
   Item ring[kRing];
   uint64_t ring_full[kRing], ring_free[kRing];
   uint64_t k_full[kRing], o_full[kRing];
@@ -345,7 +340,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
   // Places without an entry, and weights of those that there never are, have to be finite from the start.
   for (int i = threadIdx.x; i < (kKBytes + 1024) / 16; i += kWindowThreads) reinterpret_cast<uint4*>(sm.k)[i] = make_uint4(0, 0, 0, 0);
   for (int i = threadIdx.x; i < 1024 / 16; i += kWindowThreads) reinterpret_cast<uint4*>(sm.p + kSlots * 128)[i] = make_uint4(0, 0, 0, 0);
-  if (threadIdx.x < 512) sm.ones[threadIdx.x] = 0x3f803f80u;
   async_proxy_fence();  // (to the products, behind the barrier below)
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)), "n"(kTmemCols) : "memory");
@@ -498,9 +492,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     const int w = warp & 3, own = 32 * ((warp >> 2) & 1);  // of results: TMEM lanes 32w .., rows own .. own + 31
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     const bool busy = own < rows16, decodes = warp == kDecodeWarp;
-    // the row that this lane makes the factor of: its token and head in any item, and the head's sink
-    const int my_row = own + lane, my_token = static_cast<int>(my_row * plan.pitch_inv >> 16), my_head = my_row - my_token * plan.pitch;
-    const float sink = p.sink != nullptr && my_head < heads ? __ldcg(p.sink + head0 + my_head) * kLog2e : -INFINITY;
     const uint32_t halves = lane & 1 ? 0x3276 : 0x5410;
     // Eight rows are of one token: where the first that this lane stores goes, from the item's first token on. (Of bf16 a lane
     // stores every other row of pairs of columns.)
@@ -512,21 +503,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       out_at[g] = token * p.out_stride_r + (head0 + h0 + (OUT_F32 ? 0 : lane & 1)) * p.out_stride_h + 32 * w + (OUT_F32 ? lane : lane & ~1);
     }
     auto results = [&](int i) {
-      warp_wait(&sm.p_full[i & 1], (i >> 1) & 1);  // (its sums are there)
       const Item& it = sm.ring[i % kRing];
       const int64_t token0 = it.token;
       const int count = it.count;
-      const bool there = my_token < count && my_head < heads;
-      const float (&s)[4][kRows] = sm.sums[i & 1];
-      const float own_sum = (s[0][my_row] + s[1][my_row]) + (s[2][my_row] + s[3][my_row]), ref = sm.ref[i & 1][my_row];
-      // with a sink: one more score, with a value of zero
-      float sum = own_sum, to = ref, share = own_sum == 0.f ? 0.f : 1.f;
-      if (p.sink != nullptr) {
-        to = own_sum == 0.f ? (sink == -INFINITY ? 0.f : sink) : fmaxf(ref, sink);
-        const float entries = own_sum == 0.f ? 0.f : own_sum * ex2_approx(ref - to);
-        sum = entries + ex2_approx(sink - to);
-        if (own_sum != 0.f) share = entries / sum;
-      }
       const int64_t row0 = token0 * p.out_stride_r;
       int limit[4];  // rows on from there that there are
 #pragma unroll
@@ -534,19 +513,10 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16), h0 = own + 8 * g - token * plan.pitch;
         limit[g] = token < count ? heads - h0 - (OUT_F32 ? 0 : lane & 1) : 0;
       }
+      uint32_t o[32];
       warp_wait(&sm.o_part[0], i & 1);
       tmem_fence_after();
-      uint32_t o[32];
-      tmem_ld_32x32(tmem + lanes + kTmemL + own, o);  // every row of L is the same
-      tmem_wait_ld();
-      if (lane == 0) {  // (the four warps of a set write the same, here and below)
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) *reinterpret_cast<uint4*>(&sm.weights[own + k]) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-      }
       tmem_ld_32x32(tmem + lanes + own, o);
-      __syncwarp();
-      sm.inv[i & 1][my_row] = share == 0.f ? 0.f : __fdividef(share, sm.weights[my_row]);
-      __syncwarp();
 #pragma unroll 1
       for (int mt = 0; mt < 4; ++mt) {  // 128 columns, of them 32 to a warp, of 32 rows
         tmem_wait_ld();
@@ -557,14 +527,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         if (more) {
           warp_wait(&sm.o_part[mt + 1], i & 1);
           tmem_fence_after();
-        }
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm.inv[i & 1][own + k]);
-          const float2 v0 = mul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), make_float2(f.x, f.y));
-          const float2 v1 = mul2(make_float2(__uint_as_float(o[k + 2]), __uint_as_float(o[k + 3])), make_float2(f.z, f.w));
-          o[k] = __float_as_uint(v0.x), o[k + 1] = __float_as_uint(v0.y);
-          o[k + 2] = __float_as_uint(v1.x), o[k + 3] = __float_as_uint(v1.y);
         }
         const bool store = busy && !*abort_flag;
         if constexpr (OUT_F32) {
@@ -598,9 +560,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
           }
         }
       }
-      if (busy && w == 0 && there && p.lse != nullptr && !*abort_flag)
-        p.lse[(token0 + my_token) * p.lse_stride_r + (head0 + my_head) * p.lse_stride_h] =
-            sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718055994531f;
       free_item(i);
     };
     for (int i = 0;; ++i) {
@@ -626,8 +585,6 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       const uint32_t q_at = desc_low(smem_addr(sm.q), 16), ks_at = desc_low(smem_addr(sm.k), 16);
       const uint32_t kv_at = desc_low(smem_addr(sm.k), kChunkBytes), p_at = desc_low(smem_addr(sm.p), 16);
       const uint32_t desc_s = mma_desc(kMain, rows16, false), desc_tail = mma_desc(64, rows16, false), desc_o = mma_desc(128, rows16, true);
-      const uint32_t desc_ones = mma_desc(64, rows16, false) | 1u << 16;  // (P the other way around)
-      const uint64_t ones = desc_plain(smem_addr(sm.ones));
       auto half_of_s = [&](int half, bool tail) {
         tmem_fence_after();
 #pragma unroll 1
@@ -646,13 +603,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       auto product_o = [&](int i, int steps) {  // of item i
         if (!wait(&sm.p_full[i & 1], (i >> 1) & 1)) return false;
 #pragma unroll 1
-        for (int mt = 0; mt < 4; ++mt) {  // as the results of the item before leave it, L with the first
+        for (int mt = 0; mt < 4; ++mt) {  // as the results of the item before leave it
           if (i > 0 && !wait(&sm.o_free[mt], (i - 1) & 1)) return false;
           tmem_fence_after();
-          if (mt == 0) {
-#pragma unroll 1
-            for (int ks = 0; ks < steps; ++ks) mma(tmem + kTmemL, ones, desc64(p_at + (ks * 2048 >> 4)), desc_ones, ks > 0);
-          }
 #pragma unroll 1
           for (int ks = 0; ks < steps; ++ks)
             mma(tmem + mt * kRows, desc64(kv_at + ((2 * mt * kChunkBytes + ks * 2048) >> 4)), desc64(p_at + (ks * 2048 >> 4)), desc_o, ks > 0);
@@ -696,6 +649,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     const int reduced = own + 8 * (lane >> 4 << 1 | (lane >> 3 & 1)) + 2 * (lane & 3) + (lane >> 2 & 1);  // reduce_rows' row
     const float c2 = p.scale * kLog2e;
     const bool busy = own < rows16;
+    // the row that this lane has the statistics of: its token and head in any item, and the head's sink
+    const int my_row = own + lane, my_token = static_cast<int>(my_row * plan.pitch_inv >> 16), my_head = my_row - my_token * plan.pitch;
+    const float sink = p.sink != nullptr && my_head < heads ? __ldcg(p.sink + head0 + my_head) * kLog2e : -INFINITY;
     uint32_t set_phase = 0;
     int helped = 0;
     auto set_sync = [&] {  // bounded, as every wait: a warp that has seen the abort flag does not come
@@ -781,44 +737,57 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
 #pragma unroll
           for (int g = 0; g < 4; ++g) top[2 * g] = fmaxf(top[2 * g], v[4][g].x), top[2 * g + 1] = fmaxf(top[2 * g + 1], v[4][g].y);
         }
-        sm.by_max[i & 1][w][reduced] = reduce_rows(top, lane, [](float a, float b) { return fmaxf(a, b); });
+        sm.by_warp[0][w][reduced] = reduce_rows(top, lane, [](float a, float b) { return fmaxf(a, b); });
         set_sync();
-        float2 ref[4];  // less than nothing: what is added to the scores
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float2 m[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m[k] = *reinterpret_cast<const float2*>(&sm.by_max[i & 1][k][r0 + 8 * g]);
-          ref[g] = make_float2(-fmaxf(fmaxf(m[0].x, m[1].x), fmaxf(m[2].x, m[3].x)), -fmaxf(fmaxf(m[0].y, m[1].y), fmaxf(m[2].y, m[3].y)));
-          if (ref[g].x == INFINITY) ref[g].x = 0.f;  // (of a row that sees nothing)
-          if (ref[g].y == INFINITY) ref[g].y = 0.f;
-        }
+        // (the four warps of a set make and write the same, here and below)
+        const float largest = fmaxf(fmaxf(sm.by_warp[0][0][my_row], sm.by_warp[0][1][my_row]), fmaxf(sm.by_warp[0][2][my_row], sm.by_warp[0][3][my_row]));
+        const float m = largest == -INFINITY ? 0.f : largest;  // (of a row that sees nothing)
+        sm.ref[my_row] = -m;
+        __syncwarp();
         float2 sum[4] = {};
-        uint32_t packed[5][4];
-        auto weigh = [&](int k, int g) {
-          const float2 t = add2(v[k][g], ref[g]), e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-          packed[k][g] = pack_bf16x2(e.x, e.y);
-          sum[g] = k == 0 ? e : add2(sum[g], e);
+        auto weigh = [&](int k, int g, float2 ref) {
+          const float2 t = add2(v[k][g], ref);
+          v[k][g] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+          sum[g] = k == 0 ? v[k][g] : add2(sum[g], v[k][g]);
         };
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int g = 0; g < 4; ++g) {
+          const float2 ref = *reinterpret_cast<const float2*>(&sm.ref[r0 + 8 * g]);
 #pragma unroll
-          for (int g = 0; g < 4; ++g) weigh(k, g);
-        }
-        if (tail) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) weigh(4, g);
+          for (int k = 0; k < 4; ++k) weigh(k, g, ref);
+          if (tail) weigh(4, g, ref);
         }
         const float sums8[8] = {sum[0].x, sum[0].y, sum[1].x, sum[1].y, sum[2].x, sum[2].y, sum[3].x, sum[3].y};
-        const float sum1 = reduce_rows(sums8, lane, [](float a, float b) { return a + b; });
+        sm.by_warp[1][w][reduced] = reduce_rows(sums8, lane, [](float a, float b) { return a + b; });
+        set_sync();
+        {
+          const float own_sum = (sm.by_warp[1][0][my_row] + sm.by_warp[1][1][my_row]) + (sm.by_warp[1][2][my_row] + sm.by_warp[1][3][my_row]);
+          float sum = own_sum, to = m, share = 1.f;
+          if (p.sink != nullptr) {  // one more score, with a value of zero
+            to = own_sum == 0.f ? (sink == -INFINITY ? 0.f : sink) : fmaxf(m, sink);
+            share = own_sum == 0.f ? 0.f : ex2_approx(m - to);
+            sum = own_sum * share + ex2_approx(sink - to);
+          }
+          sm.share[my_row] = own_sum == 0.f ? 0.f : __fdividef(share, sum);
+          if (w == 0 && my_token < it.count && my_head < heads && p.lse != nullptr && !*abort_flag)
+            p.lse[(static_cast<int64_t>(it.token) + my_token) * p.lse_stride_r + (head0 + my_head) * p.lse_stride_h] =
+                sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718055994531f;
+          __syncwarp();
+        }
+        uint32_t packed[5][4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float2 share = *reinterpret_cast<const float2*>(&sm.share[r0 + 8 * g]);
+          auto pack = [&](int k) {
+            const float2 t = mul2(v[k][g], share);
+            packed[k][g] = pack_bf16x2(t.x, t.y);
+          };
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pack(k);
+          if (tail) pack(4);
+        }
         // the weights of the item before have been used
         if (i > 0) warp_wait(&sm.o_full[(i - 1) % kRing], ((i - 1) / kRing) & 1);
-        if (w == 0) {  // (and the references)
-          const float ref = fmaxf(fmaxf(sm.by_max[i & 1][0][own + lane], sm.by_max[i & 1][1][own + lane]),
-                                  fmaxf(sm.by_max[i & 1][2][own + lane], sm.by_max[i & 1][3][own + lane]));
-          sm.ref[i & 1][own + lane] = ref == -INFINITY ? 0.f : ref;
-        }
-        sm.sums[i & 1][w][reduced] = sum1;
         const uint32_t swz = static_cast<uint32_t>(lane >> 2) << 4;  // of all its entries
         const uint32_t p_at = smem_addr(sm.p) + (32 * w + (lane >> 2)) * 128 + 4 * (lane & 3);
 #pragma unroll
