@@ -301,6 +301,63 @@ __device__ __forceinline__ void decode_first(const DecodeParams& p, WindowSmem& 
   __syncwarp();
 }
 
+// 32 rows of one column of O, as they are stored: bf16 of two rows each, or as they are.
+template <bool OUT_F32>
+struct Packed {
+  uint32_t x[OUT_F32 ? 32 : 16];
+  __device__ __forceinline__ explicit Packed(const uint32_t (&o)[32]) {
+    if constexpr (OUT_F32) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] = o[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+    }
+  }
+};
+// Where a warp's 32 rows and 32 columns of 128 go. Eight rows are of one token: where the first of them that this lane stores
+// goes, from the item's first token on. (Of bf16 a lane stores every other row of pairs of columns.)
+template <bool OUT_F32>
+struct OutRows {
+  int64_t at[4], step;  // elements; bytes from a row to the next that this lane stores
+  __device__ __forceinline__ OutRows(const DecodeParams& p, const WindowPlan& plan, int head0, int own, int w, int lane) {
+    const int odd = OUT_F32 ? 0 : lane & 1;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16), h0 = own + 8 * g - token * plan.pitch;
+      at[g] = token * p.out_stride_r + (head0 + h0 + odd) * p.out_stride_h + 32 * w + (OUT_F32 ? lane : lane & ~1);
+    }
+    step = p.out_stride_h * 4;  // one row of fp32, two of bf16
+    asm volatile("" : "+l"(step));
+  }
+  // Of an item: where its first token's row is, and how many rows there are from `at` on.
+  __device__ __forceinline__ int64_t item(const DecodeParams& p, const WindowPlan& plan, const Item& it, int heads, int own, int lane,
+                                          int (&limit)[4]) const {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16), h0 = own + 8 * g - token * plan.pitch;
+      limit[g] = token < it.count ? heads - h0 - (OUT_F32 ? 0 : lane & 1) : 0;
+    }
+    return it.token * p.out_stride_r;
+  }
+  __device__ __forceinline__ void store(const DecodeParams& p, int64_t from, const int (&limit)[4], const Packed<OUT_F32>& v, int lane) const {
+    const uint32_t halves = lane & 1 ? 0x3276 : 0x5410;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      char* dst = static_cast<char*>(p.out) + (from + at[g]) * (OUT_F32 ? 4 : 2);
+#pragma unroll
+      for (int k = 0; k < (OUT_F32 ? 8 : 4); ++k) {
+        uint32_t x = v.x[(OUT_F32 ? 8 : 4) * g + k];
+        // neighbouring lanes swap halves of a pair of rows, so that each stores two columns of one
+        if constexpr (!OUT_F32) x = __byte_perm(x, __shfl_xor_sync(0xffffffffu, x, 1), halves);
+        if ((OUT_F32 ? k : 2 * k) < limit[g]) *reinterpret_cast<uint32_t*>(dst) = x;
+        dst += step;
+        asm volatile("" : "+l"(dst));  // (a running sum: a product of 64 bits for each row takes five times the instructions)
+      }
+    }
+  }
+};
+
 template <bool ALIGN16, bool OUT_F32>
 __global__ void __launch_bounds__(kWindowThreads, 1)
     window_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ WindowPlan plan) {
@@ -492,27 +549,11 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     const int w = warp & 3, own = 32 * ((warp >> 2) & 1);  // of results: TMEM lanes 32w .., rows own .. own + 31
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     const bool busy = own < rows16, decodes = warp == kDecodeWarp;
-    const uint32_t halves = lane & 1 ? 0x3276 : 0x5410;
-    // Eight rows are of one token: where the first that this lane stores goes, from the item's first token on. (Of bf16 a lane
-    // stores every other row of pairs of columns.)
-    int64_t out_at[4], out_step = p.out_stride_h * 4;  // two rows of bf16, in bytes
-    asm volatile("" : "+l"(out_step));
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16), h0 = own + 8 * g - token * plan.pitch;
-      out_at[g] = token * p.out_stride_r + (head0 + h0 + (OUT_F32 ? 0 : lane & 1)) * p.out_stride_h + 32 * w + (OUT_F32 ? lane : lane & ~1);
-    }
+    const OutRows<OUT_F32> to(p, plan, head0, own, w, lane);
     auto results = [&](int i) {
       const Item& it = sm.ring[i % kRing];
-      const int64_t token0 = it.token;
-      const int count = it.count;
-      const int64_t row0 = token0 * p.out_stride_r;
-      int limit[4];  // rows on from there that there are
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16), h0 = own + 8 * g - token * plan.pitch;
-        limit[g] = token < count ? heads - h0 - (OUT_F32 ? 0 : lane & 1) : 0;
-      }
+      int limit[4];
+      const int64_t row0 = to.item(p, plan, it, heads, own, lane, limit);
       uint32_t o[32];
       warp_wait(&sm.o_part[0], i & 1);
       tmem_fence_after();
@@ -523,42 +564,14 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_free[mt]);
-        const bool more = mt < 3;
+        const bool more = mt + 1 < 4;
         if (more) {
           warp_wait(&sm.o_part[mt + 1], i & 1);
           tmem_fence_after();
         }
-        const bool store = busy && !*abort_flag;
-        if constexpr (OUT_F32) {
-          if (store) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              float* dst = static_cast<float*>(p.out) + row0 + out_at[g] + 128 * mt;
-#pragma unroll
-              for (int k = 0; k < 8; ++k, dst += p.out_stride_h)
-                if (k < limit[g]) *dst = __uint_as_float(o[8 * g + k]);
-            }
-          }
-          if (more) tmem_ld_32x32(tmem + lanes + (mt + 1) * kRows + own, o);
-        } else {
-          uint32_t two[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) two[k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
-          if (more) tmem_ld_32x32(tmem + lanes + (mt + 1) * kRows + own, o);  // on its way as these are stored
-          if (store) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              char* dst = reinterpret_cast<char*>(static_cast<uint16_t*>(p.out) + row0 + out_at[g] + 128 * mt);
-#pragma unroll
-              for (int k = 0; k < 4; ++k, dst += out_step) {
-                asm volatile("" : "+l"(dst));  // (a running sum: a product of 64 bits for each row takes five times the instructions)
-                // neighbouring lanes swap halves of a pair of rows, so that each stores two columns of one
-                const uint32_t both = __byte_perm(two[4 * g + k], __shfl_xor_sync(0xffffffffu, two[4 * g + k], 1), halves);
-                if (2 * k < limit[g]) *reinterpret_cast<uint32_t*>(dst) = both;
-              }
-            }
-          }
-        }
+        const Packed<OUT_F32> packed(o);
+        if (more) tmem_ld_32x32(tmem + lanes + (mt + 1) * kRows + own, o);  // on its way as these are stored
+        if (busy && !*abort_flag) to.store(p, row0 + 128 * mt, limit, packed, lane);
       }
       free_item(i);
     };
@@ -670,6 +683,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         warp_wait(&sm.k_help, helped & 1);
         ++helped;
       }
+      float total = 0.f, base2 = 0.f;  // of this lane's row: the sum of weights (the sink's too) is total * 2^base2
       if (busy) {
         // This thread's entries are 32w + lane / 4 and on in steps of 8, and of the tail (in the first 16 lanes of TMEM) one.
         // A score is at most `most`: -inf where the row does not see the entry, else +inf (which a NaN becomes, and in the
@@ -711,7 +725,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
           if (tail) tmem_ld_scores<32>(tmem + lanes + kTmemTail + own, y);
           tmem_wait_ld();
           auto score = [&](uint32_t a, uint32_t b, int k, int g) {
-            const float2 t = fma2(make_float2(__uint_as_float(a), __uint_as_float(b)), make_float2(c2, c2), make_float2(plus[k], plus[k]));
+            const float2 t = __ffma2_rn(make_float2(__uint_as_float(a), __uint_as_float(b)), make_float2(c2, c2), make_float2(plus[k], plus[k]));
             return make_float2(fminf(t.x, most[k][g]), fminf(t.y, most[k][g]));
           };
 #pragma unroll
@@ -746,9 +760,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         __syncwarp();
         float2 sum[4] = {};
         auto weigh = [&](int k, int g, float2 ref) {
-          const float2 t = add2(v[k][g], ref);
+          const float2 t = __fadd2_rn(v[k][g], ref);
           v[k][g] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-          sum[g] = k == 0 ? v[k][g] : add2(sum[g], v[k][g]);
+          sum[g] = k == 0 ? v[k][g] : __fadd2_rn(sum[g], v[k][g]);
         };
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -769,9 +783,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
             sum = own_sum * share + ex2_approx(sink - to);
           }
           sm.share[my_row] = own_sum == 0.f ? 0.f : __fdividef(share, sum);
-          if (w == 0 && my_token < it.count && my_head < heads && p.lse != nullptr && !*abort_flag)
-            p.lse[(static_cast<int64_t>(it.token) + my_token) * p.lse_stride_r + (head0 + my_head) * p.lse_stride_h] =
-                sum == 0.f ? -INFINITY : (to + log2f(sum)) * 0.69314718055994531f;
+          total = sum, base2 = to;
           __syncwarp();
         }
         uint32_t packed[5][4];
@@ -779,7 +791,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         for (int g = 0; g < 4; ++g) {
           const float2 share = *reinterpret_cast<const float2*>(&sm.share[r0 + 8 * g]);
           auto pack = [&](int k) {
-            const float2 t = mul2(v[k][g], share);
+            const float2 t = __fmul2_rn(v[k][g], share);
             packed[k][g] = pack_bf16x2(t.x, t.y);
           };
 #pragma unroll
@@ -806,6 +818,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.p_full[i & 1]);
+      if (busy && w == 0 && my_token < it.count && my_head < heads && p.lse != nullptr && !*abort_flag)
+        p.lse[(static_cast<int64_t>(it.token) + my_token) * p.lse_stride_r + (head0 + my_head) * p.lse_stride_h] =
+            total == 0.f ? -INFINITY : (base2 + log2f(total)) * 0.69314718055994531f;
       free_item(i);
     }
   }
