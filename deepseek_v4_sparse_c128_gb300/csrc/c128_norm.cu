@@ -56,21 +56,28 @@ __device__ __forceinline__ void load_weight(const float* w, int lane, float (&x)
     x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
   }
 }
-// The four pairs x[8 ..] of lanes 24 .. 31 turned; c and s hold the angle of pair `lane` in every lane.
-__device__ __forceinline__ void turn(float (&x)[16], float c, float s, int lane) {
+// The angles of the four pairs x[8 ..] of lanes 24 .. 31 (of the other lanes: any).
+struct Angles {
+  float c[4], s[4];
+  __device__ __forceinline__ Angles(float cos_of_lane, float sin_of_lane, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int pair = 4 * (lane - 24) + i;  // (of the other lanes: any)
-    const float cc = __shfl_sync(0xffffffffu, c, pair & 31), ss = __shfl_sync(0xffffffffu, s, pair & 31);
-    const float e = x[8 + 2 * i], o = x[9 + 2 * i];
-    if (lane >= 24) {
-      x[8 + 2 * i] = __fsub_rn(__fmul_rn(e, cc), __fmul_rn(o, ss));
-      x[9 + 2 * i] = __fadd_rn(__fmul_rn(o, cc), __fmul_rn(e, ss));
+    for (int i = 0; i < 4; ++i) {
+      const int pair = (4 * (lane - 24) + i) & 31;
+      c[i] = __shfl_sync(0xffffffffu, cos_of_lane, pair), s[i] = __shfl_sync(0xffffffffu, sin_of_lane, pair);
     }
   }
-}
+  __device__ __forceinline__ void turn(float (&x)[16], int lane) const {
+    if (lane < 24) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = x[8 + 2 * i], o = x[9 + 2 * i];
+      x[8 + 2 * i] = __fsub_rn(__fmul_rn(e, c[i]), __fmul_rn(o, s[i]));
+      x[9 + 2 * i] = __fadd_rn(__fmul_rn(o, c[i]), __fmul_rn(e, s[i]));
+    }
+  }
+};
 
-// A token's angles, as `turn` takes them; false where it is skipped (and said why, by the warp with `report`).
+// A token's angles, of pair `lane`; false where it is skipped (and said why, by the warp with `report`).
 __device__ __forceinline__ bool token_angles(const NormParams& p, int64_t t, bool report, int lane, float& c, float& s) {
   const int64_t slot = p.slots[t], pos = p.positions[t];
   if (slot < 0 || pos < 0) return false;
@@ -96,6 +103,7 @@ __device__ __forceinline__ void queries(const NormParams& p, int64_t t, int head
     if (head0 + r < p.heads) row[r].load(src + r * p.q_stride_h * (F32 ? 4 : 2), lane);
   float c, s;
   if (!token_angles(p, t, report, lane, c, s)) return;
+  const Angles angles(c, s, lane);
   float w[16];
   if (p.q_w != nullptr) load_weight(p.q_w, lane, w);
 #pragma unroll
@@ -115,7 +123,7 @@ __device__ __forceinline__ void queries(const NormParams& p, int64_t t, int head
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = x[i] * w[i];
     }
-    turn(x, c, s, lane);
+    angles.turn(x, lane);
     const int64_t at = t * p.out_stride_t + (head0 + r) * p.out_stride_h + 8 * lane;
     if constexpr (OUT_F32) {
       float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.q_out) + at);
@@ -196,7 +204,7 @@ __device__ __forceinline__ void key(const NormParams& p, int64_t t, int lane, fl
   rrms = __shfl_sync(0xffffffffu, rrms, 0);
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = p.k_w != nullptr ? __fmul_rn(__fmul_rn(x[i], rrms), w[i]) : __fmul_rn(x[i], rrms);
-  turn(x, c, s, lane);
+  Angles(c, s, lane).turn(x, lane);
   uint32_t a[4], b[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) a[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]), b[i] = pack_bf16x2(x[8 + 2 * i], x[9 + 2 * i]);
@@ -253,7 +261,9 @@ cudaError_t launch_norm(const NormParams& p, int sm_count, cudaStream_t stream) 
   if (p.tokens == 0) return cudaSuccess;
   constexpr int kWarps = kNormThreads / 32;
   const int64_t rows = p.q != nullptr ? p.tokens * p.heads : 0;
-  const int per = rows > 32ll * sm_count ? 4 : 1;
+  // Heads of a token to a warp: 1 while every row has a warp to itself; 8 where there are rows for several waves of CTAs (64
+  // heads: 4,096 tokens 94.4 us with 4, 88.9 with 8; 1,024 tokens 25.2 and 25.0; 512 tokens 13.7 and 14.5)
+  const int per = rows <= 32ll * sm_count ? 1 : rows < 400ll * sm_count ? 4 : 8;
   uint32_t pieces = static_cast<uint32_t>(p.q != nullptr ? (p.heads + per - 1) / per : 0);
   int64_t key_warps = p.k != nullptr ? p.tokens : 0;
   const int64_t ctas = (key_warps + p.tokens * pieces + kWarps - 1) / kWarps;
@@ -269,7 +279,7 @@ cudaError_t launch_norm(const NormParams& p, int sm_count, cudaStream_t stream) 
   lc.attrs = attr;
   lc.numAttrs = 1;
   void* args[] = {const_cast<NormParams*>(&p), &pieces, &key_warps};
-  const void* kernel = per == 4 ? norm_kernel_for<4>(p.q_f32, p.out_f32) : norm_kernel_for<1>(p.q_f32, p.out_f32);
+  const void* kernel = per == 1 ? norm_kernel_for<1>(p.q_f32, p.out_f32) : per == 4 ? norm_kernel_for<4>(p.q_f32, p.out_f32) : norm_kernel_for<8>(p.q_f32, p.out_f32);
   return cudaLaunchKernelExC(&lc, kernel, args);
 }
 

@@ -12,36 +12,59 @@ namespace {
 // ------------------------------------------------------------------------------------------ table
 // cos and sin of position * step. A step is kept in 2^-64 turns, so the low 64 bits of the product are the
 // angle with its whole turns gone, exactly. The nearest quarter turn is taken off it (the two highest bits,
-// rounded), and what is left, under an eighth of a turn either way, becomes a float to its last bit: sines
-// near zero keep their relative precision.
+// rounded), and what is left, under an eighth of a turn either way, becomes a float: sines near zero keep their
+// relative precision. With |x| <= pi / 4 the Taylor series of both, to x^10 and x^11, are 2^-33 of a value off; their
+// steps in z = x^2 are the same, so a packed multiply-add takes both.
 constexpr int kTableThreads = 256;
 
-// A thread keeps its pair and goes from row to row, the angle by addition.
+__device__ __forceinline__ void cos_sin_of(uint64_t turn, float magnitude, float& c, float& s) {
+  const uint32_t high = static_cast<uint32_t>(turn >> 32), quarter = (high + (1u << 29)) >> 30;
+  const float rest = fmaf(static_cast<float>(static_cast<int32_t>(high - (quarter << 30))), 0x1p32f, static_cast<float>(static_cast<uint32_t>(turn)));
+  const float x = rest * (6.283185307179586f * 0x1p-64f), z = x * x, xm = x * magnitude;
+  const float2 zz = make_float2(z, z);
+  float2 p = make_float2(-1.f / 3628800.f, -1.f / 39916800.f);
+  p = __ffma2_rn(p, zz, make_float2(1.f / 40320.f, 1.f / 362880.f));
+  p = __ffma2_rn(p, zz, make_float2(-1.f / 720.f, -1.f / 5040.f));
+  p = __ffma2_rn(p, zz, make_float2(1.f / 24.f, 1.f / 120.f));
+  p = __ffma2_rn(p, zz, make_float2(-1.f / 2.f, -1.f / 6.f));
+  p = __fmul2_rn(p, zz);
+  const float a = fmaf(p.x, magnitude, magnitude), b = fmaf(p.y, xm, xm);
+  const bool swap = quarter & 1;
+  c = __uint_as_float(__float_as_uint(swap ? b : a) ^ ((quarter + 1) & 2) << 30);
+  s = __uint_as_float(__float_as_uint(swap ? a : b) ^ (quarter & 2) << 30);
+}
+
+// A thread keeps its N pairs and goes from row to row, the angles by addition.
+template <int N>
 __global__ void __launch_bounds__(kTableThreads) cos_sin_kernel(const __grid_constant__ CosSinParams p) {
   __shared__ uint64_t steps[kMaxTurned / 2];  // (parameters are slow to read by an index of the thread's own)
   for (int i = threadIdx.x; i < p.half; i += kTableThreads) steps[i] = p.step[i];
   launch_dependents();
   __syncthreads();
-  const unsigned at_once = kTableThreads / p.half, below = threadIdx.x / p.half, pair = threadIdx.x - below * p.half;
+  const unsigned threads = p.half / N, at_once = kTableThreads / threads, below = threadIdx.x / threads;
+  const unsigned pair = (threadIdx.x - below * threads) * N;
   if (below >= at_once) return;
-  const uint64_t step = steps[pair];
   const int64_t stride = static_cast<int64_t>(gridDim.x) * at_once;
   int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + below;
-  uint64_t turn = (p.first + row) * step;
+  uint64_t turn[N], add[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) turn[k] = (p.first + row) * steps[pair + k], add[k] = stride * steps[pair + k];
+  float* dst = p.table + row * p.stride + pair;
+  const int64_t next = stride * p.stride;
   grid_dependency_wait();  // the table may still be read by kernels before this one
-  for (; row < p.rows; row += stride, turn += stride * step) {
-    const uint64_t quarter = (turn + (1ull << 61)) >> 62;
-    const int64_t rest = static_cast<int64_t>(turn - (quarter << 62));
-    float s, c;
-    sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);  // of half turns
-    if (quarter & 1) {
-      const float t = s;
-      s = c, c = -t;
+  for (; row < p.rows; row += stride, dst += next) {
+    float c[N], s[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      cos_sin_of(turn[k], p.magnitude, c[k], s[k]);
+      turn[k] += add[k];
     }
-    if (quarter & 2) s = -s, c = -c;
-    float* dst = p.table + row * p.stride + pair;
-    dst[0] = c * p.magnitude;
-    dst[p.half] = s * p.magnitude;
+    if constexpr (N == 4) {
+      *reinterpret_cast<float4*>(dst) = make_float4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<float4*>(dst + p.half) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+      dst[0] = c[0], dst[p.half] = s[0];
+    }
   }
 }
 
@@ -49,7 +72,7 @@ __global__ void __launch_bounds__(kTableThreads) cos_sin_kernel(const __grid_con
 // A pass over memory. Work is dealt out in units: a vector of 16 bytes (of halves: one of either half) to
 // turn, or one to copy; a CTA takes kUnits of them, of one token or of several whole ones. Without the
 // alignment for vectors a unit is a pair, or a value to copy.
-constexpr int kRotateThreads = 128, kFlight = 4, kUnits = kRotateThreads * kFlight;
+constexpr int kRotateThreads = 128, kFlight = 2, kUnits = kRotateThreads * kFlight;
 
 template <typename T>
 struct Vec {  // 16 bytes of T
@@ -86,8 +109,18 @@ __device__ __forceinline__ void turn(float& u, float& v, float c, float s) {
   u = a, v = b;
 }
 
+// x / d as a product, where that is exact: x < 2^32 / d.
+struct Quotient {
+  uint32_t value, inverse;  // inverse 0: a division
+  Quotient() = default;
+  Quotient(int64_t d, int64_t most) : value(static_cast<uint32_t>(d)), inverse(0) {
+    // (2^32 / d rounded up is less than 1 too large, so the product is off by less than x / 2^32 < 1 / d)
+    if (d > 1 && d * most < 1ll << 32) inverse = static_cast<uint32_t>(((1ull << 32) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t x) const { return inverse ? __umulhi(x, inverse) : x / value; }
+};
 struct RotateShape {
-  Divisor units, token_units;  // of a row; of a token
+  Quotient units, token_units;  // of a row; of a token
   int32_t turned;              // units of a row to turn, the rest are copied
   uint32_t tokens_per_cta;     // with 1 of them, `pieces` CTAs to a token
   uint32_t pieces;
@@ -106,7 +139,9 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotatePara
   constexpr int kTwo = HALVES && VECTOR ? 2 : 1;  // vectors of a unit to turn
   const T* src[kFlight];
   T* dst[kFlight];
-  const float* cs[kFlight];  // NULL: to copy
+  int64_t pos[kFlight];
+  int pairs[kFlight];  // the first to turn; -1: to copy
+  bool first[kFlight];
   uint4 v[kFlight][kTwo];
   const int apart = HALVES ? p.half : 1;  // columns between the two of a pair
 #pragma unroll
@@ -114,14 +149,10 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotatePara
     const uint32_t at = begin + k * kRotateThreads + threadIdx.x;
     src[k] = nullptr;
     if (at >= end) continue;
-    const uint32_t t = divide(at, shape.token_units), in_token = at - t * shape.token_units.value;
-    const uint32_t h = divide(in_token, shape.units), unit = in_token - h * shape.units.value;
-    const int64_t token = token0 + t, pos = p.positions[token];
-    if (pos < 0) continue;
-    if (pos >= p.rows) {
-      if (in_token == 0) atomicOr(p.err, static_cast<unsigned int>(C128_DEV_BAD_COS_ROW));
-      continue;
-    }
+    const uint32_t t = shape.tokens_per_cta == 1 ? 0 : shape.token_units.of(at), in_token = at - t * shape.token_units.value;
+    const uint32_t h = shape.units.of(in_token), unit = in_token - h * shape.units.value;
+    const int64_t token = token0 + t;
+    pos[k] = p.positions[token];
     const bool turned = unit < static_cast<uint32_t>(shape.turned);
     int column, pair = 0;
     if (turned) {
@@ -133,7 +164,8 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotatePara
     }
     src[k] = static_cast<const T*>(p.x) + token * p.x_stride_t + h * p.x_stride_h + column;
     dst[k] = static_cast<T*>(p.out) + token * p.out_stride_t + h * p.out_stride_h + column;
-    cs[k] = turned ? p.cos_sin + pos * p.cs_stride + pair : nullptr;
+    pairs[k] = turned ? pair : -1;
+    first[k] = in_token == 0;
     if constexpr (VECTOR) {
       v[k][0] = load16(src[k]);
       if constexpr (HALVES)
@@ -142,8 +174,12 @@ __global__ void __launch_bounds__(kRotateThreads) rotate_kernel(const RotatePara
   }
 #pragma unroll
   for (int k = 0; k < kFlight; ++k) {
-    if (src[k] == nullptr) continue;
-    const float* c = cs[k];
+    if (src[k] == nullptr || pos[k] < 0) continue;  // (a skipped token's values have been read, and are not used)
+    if (pos[k] >= p.rows) {
+      if (first[k]) atomicOr(p.err, static_cast<unsigned int>(C128_DEV_BAD_COS_ROW));
+      continue;
+    }
+    const float* c = pairs[k] < 0 ? nullptr : p.cos_sin + pos[k] * p.cs_stride + pairs[k];
     if constexpr (!VECTOR) {
       float a = value(src[k]);
       if (c != nullptr) {
@@ -202,9 +238,12 @@ cudaError_t launch_pdl(const void* kernel, int64_t ctas, int threads, void** arg
 
 cudaError_t launch_cos_sin(const CosSinParams& p, int sm_count, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
-  const int64_t at_once = kTableThreads / p.half, need = (p.rows + at_once - 1) / at_once, most = 8ll * sm_count;
+  // four pairs to a thread, and stores of 16 bytes, where rows and their halves allow it
+  const bool four = p.half % 4 == 0 && p.stride % 4 == 0 && reinterpret_cast<uintptr_t>(p.table) % 16 == 0;
+  const int64_t at_once = kTableThreads / (p.half / (four ? 4 : 1)), need = (p.rows + at_once - 1) / at_once, most = 8ll * sm_count;
   void* args[] = {const_cast<CosSinParams*>(&p)};
-  return launch_pdl(reinterpret_cast<const void*>(cos_sin_kernel), need < most ? need : most, kTableThreads, args, stream);
+  return launch_pdl(four ? reinterpret_cast<const void*>(cos_sin_kernel<4>) : reinterpret_cast<const void*>(cos_sin_kernel<1>),
+                    need < most ? need : most, kTableThreads, args, stream);
 }
 
 cudaError_t launch_rotate(const RotateParams& p, cudaStream_t stream) {
@@ -221,9 +260,9 @@ cudaError_t launch_rotate(const RotateParams& p, cudaStream_t stream) {
   const int copied = p.in_place ? 0 : p.width - 2 * p.half;
   shape.turned = !vector ? p.half : p.halves ? p.half / n : 2 * p.half / n;
   const int64_t units = shape.turned + (vector ? copied / n : copied), token_units = units * p.heads;
-  shape.units = Divisor(units);
-  shape.token_units = Divisor(token_units);
   shape.tokens_per_cta = token_units >= kUnits ? 1 : static_cast<uint32_t>(kUnits / token_units);
+  shape.units = Quotient(units, token_units);
+  shape.token_units = Quotient(token_units, token_units * shape.tokens_per_cta);
   shape.pieces = static_cast<uint32_t>((token_units * shape.tokens_per_cta + kUnits - 1) / kUnits);
   const int64_t ctas = (p.tokens + shape.tokens_per_cta - 1) / shape.tokens_per_cta * shape.pieces;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
