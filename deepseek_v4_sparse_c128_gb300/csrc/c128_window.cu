@@ -21,7 +21,7 @@
 // Roles of the 20 warps (five to a scheduler leave them 96 registers; each wait is bounded):
 //   0..7   softmax, four warps for either half of the rows
 //   8..15  results, four warps for either half of the rows
-//          (and these decode entries at the start of a run)
+//          (and all of these decode entries at the start of a run)
 //   16     one thread issues the products
 //   17     makes the items
 //   18     decodes entries
@@ -47,8 +47,8 @@ constexpr int kQChunkBytes = kRows * 128;
 constexpr int kPBytes = (kSlots + 8) * 128;  // [entry][row]; K steps of 16 entries end at 144
 constexpr int kSoftWarps = 8, kOutWarps = 8;
 constexpr int kMmaWarp = kSoftWarps + kOutWarps, kItemWarp = kMmaWarp + 1, kDecodeWarp = kMmaWarp + 2, kQueryWarp = kMmaWarp + 3;
-constexpr int kPass = 8 * (kOutWarps + 1);  // entries that are decoded at once at the start of a run
-static_assert(2 * kPass >= kSlots, "two passes");
+constexpr int kHelpers = kSoftWarps + kOutWarps;  // decode entries at the start of a run, beside the decoding warp
+static_assert(8 * (kHelpers + 1) >= kSlots, "eight entries each");
 constexpr int kWindowThreads = 32 * (kQueryWarp + 1);
 constexpr int kRing = 4;      // items that may be on their way
 constexpr int kTmemCols = 512, kTmemS = 256, kTmemTail = 320;
@@ -226,49 +226,32 @@ __device__ __forceinline__ void decode_next(const DecodeParams& p, WindowSmem& s
   __syncwarp();
 }
 
-// The entries that a run begins with, once O has been through the item before: eight at a time to a warp, each by four
-// threads, which have the 16 bytes sub, sub + 4, ... of it (of the codes a quarter of each 64 columns, so piece j belongs to
-// scale j).
+// The entries that a run begins with, once O has been through the item before: eight to a warp, each by four threads, which
+// have the 16 bytes sub, sub + 4, ... of it (of the codes a quarter of each 64 columns, so piece j belongs to scale j).
 template <bool ALIGN16>
 __device__ __forceinline__ void decode_first(const DecodeParams& p, WindowSmem& sm, int i, int index) {
   const Item& it = sm.ring[i % kRing];
-  const int lane = threadIdx.x & 31, sub = lane & 3, all = it.lead + it.news, mine = 8 * index + (lane >> 2);
-  const uint8_t* data = nullptr;  // of this entry, and the next
-  const uint8_t* next = nullptr;
-  const uint8_t* scales_at = nullptr;
-  const uint8_t* scales_next = nullptr;
-  int place = 0, place_next = 0;
-  if (mine < all) {
-    const Source src(p, it, mine);
-    data = src.data, scales_at = src.scales, place = src.place;
-  }
-  if (mine + kPass < all) {
-    const Source src(p, it, mine + kPass);
-    next = src.data, scales_next = src.scales, place_next = src.place;
-    if (next != nullptr) {
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(next + 128 * sub));
-      if (sub == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + 512));
-      if (sub == 1) asm volatile("prefetch.global.L2 [%0];" ::"l"(scales_next));
+  const int lane = threadIdx.x & 31, sub = lane & 3, e = 8 * index + (lane >> 2);
+  const bool in = e < it.lead + it.news;
+  const uint8_t* data = nullptr;
+  int place = 0;
+  uint4 raw[9];
+  uint2 scales = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll
+  for (int j = 0; j < 9; ++j) raw[j] = make_uint4(0, 0, 0, 0);
+  if (in) {
+    const Source src(p, it, e);
+    data = src.data, place = src.place;
+    if (data != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 9; ++j) raw[j] = ALIGN16 ? ld16(data + 16 * sub + 64 * j) : ld8x2(data + 16 * sub + 64 * j);
+      scales = ld8(src.scales);
     }
   }
   __syncwarp();
-  bool waited = i == 0;
-#pragma unroll 1
-  for (int e = mine; e - (lane >> 2) < all || !waited; e += kPass) {
-    uint4 raw[9];
-    uint2 scales = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-#pragma unroll
-    for (int j = 0; j < 9; ++j) {
-      raw[j] = make_uint4(0, 0, 0, 0);
-      if (data != nullptr) raw[j] = ALIGN16 ? ld16(data + 16 * sub + 64 * j) : ld8x2(data + 16 * sub + 64 * j);
-    }
-    if (data != nullptr) scales = ld8(scales_at);
-    if (!waited) {
-      warp_wait(&sm.abort, &sm.o_full[(i - 1) % kRing], ((i - 1) / kRing) & 1);
-      waited = true;
-    }
+  if (i > 0) warp_wait(&sm.abort, &sm.o_full[(i - 1) % kRing], ((i - 1) / kRing) & 1);
+  if (__any_sync(0xffffffffu, in)) {
     const uint32_t row = smem_addr(sm.k) + place * 128, swz = static_cast<uint32_t>(place & 7) << 4;
-    const bool in = e < all;
     const uint32_t rope[8] = {raw[7].x, raw[7].y, raw[7].z, raw[7].w, raw[8].x, raw[8].y, raw[8].z, raw[8].w};  // bf16 already
     if (in) {
       const uint32_t at = row + 7 * kChunkBytes;
@@ -295,7 +278,6 @@ __device__ __forceinline__ void decode_first(const DecodeParams& p, WindowSmem& 
       for (int j = 0; j < 16; ++j) sts16(row + (j >> 1) * kChunkBytes + 32 * sub + 16 * (j & 1), 0, 0, 0, 0);
     }
     if (in && sub == 0) sm.state[place] = data == nullptr ? kAbsent : poison ? kPoison : kThere;
-    data = next, scales_at = scales_next, place = place_next;
   }
   async_proxy_fence();
   __syncwarp();
@@ -384,7 +366,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     }
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.s_free, kSoftWarps);
-    mbar_init(&sm.k_help, kOutWarps);
+    mbar_init(&sm.k_help, kHelpers);
     mbar_init(&sm.drained, 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.set[i], kSoftWarps / 2);
     for (int i = 0; i < 4; ++i) {
@@ -579,7 +561,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       const int flags = item_flags(i);
       const bool fresh = flags & kFresh, end = flags & kEnd;
       if (!end && (decodes || fresh)) {
-        if (fresh) decode_first<ALIGN16>(p, sm, i, decodes ? kOutWarps : warp - kSoftWarps);
+        if (fresh) decode_first<ALIGN16>(p, sm, i, decodes ? kHelpers : warp);
         else decode_next<ALIGN16>(p, sm, i, plan.lookahead);
         if (lane == 0) mbar_arrive(decodes ? &sm.k_full[i % kRing] : &sm.k_help);
       }
@@ -678,6 +660,10 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       if (flags & kEnd) break;
       const Item& it = sm.ring[i % kRing];
       const bool tail = (flags & kTail) && w == 0;
+      if (flags & kFresh) {
+        decode_first<ALIGN16>(p, sm, i, warp);
+        if (lane == 0) mbar_arrive(&sm.k_help);
+      }
       warp_wait(&sm.k_full[i % kRing], (i / kRing) & 1);
       if (flags & kFresh) {
         warp_wait(&sm.k_help, helped & 1);
