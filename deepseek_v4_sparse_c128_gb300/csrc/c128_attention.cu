@@ -196,7 +196,7 @@ __device__ __forceinline__ Seen seen_by(const DecodeParams& p, int64_t r, unsign
     }
     if (pos >= p.most) *err |= C128_DEV_BAD_BT_COL;
     const int end = static_cast<int>(min(pos, static_cast<int64_t>(p.most) - 1)) + 1;
-    const int begin = static_cast<int>(min(max(pos + 1 - p.window, static_cast<int64_t>(0)), static_cast<int64_t>(p.most)));
+    const int begin = static_cast<int>(min(max(pos - (p.window - 1), static_cast<int64_t>(0)), static_cast<int64_t>(p.most)));
     const int lead = min(p.first, begin);
     return Seen{lead + max(end - begin, 0), lead, begin - lead, row};
   }

@@ -6,7 +6,7 @@
 namespace c128 {
 namespace {
 
-// The bounded wait of this kernel, inline and on the SM's clock: a call would have to keep the many
+// The decode attention's bounded wait, inline and on the SM's clock: a call would have to keep the many
 // values that live across it out of registers, and the global timer takes longer than most waits. (Tries
 // without a time hint: a tile takes 4 % less.)
 constexpr uint32_t kWaitCycles = 2000000000u;  // about a second; the 32-bit clock wraps after two
@@ -133,13 +133,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, u;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 u, x, y, z;\n\tmov.b64 {%0, %1}, u;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {

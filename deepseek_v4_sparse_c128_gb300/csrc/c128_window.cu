@@ -196,11 +196,10 @@ __device__ __forceinline__ void decode_next(const DecodeParams& p, WindowSmem& s
   const int lane = threadIdx.x & 31, all = it.news;
   const bool rope = lane >= 28;
 #pragma unroll 1
-  for (int e = 0; e <= all; ++e) {  // (one more, for an item that brings none)
+  for (int e = 0; e < all; ++e) {  // (an item that goes on with a run brings one at least: its own)
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
     uint32_t scale = 127;
-    Source src(p, it, e < all ? e : 0);
-    if (e == all) src.data = nullptr;
+    const Source src(p, it, e);
     if (src.data != nullptr) {
       const uint8_t* from = src.data + 16 * lane;
       a = ALIGN16 ? ld16(from) : ld8x2(from);
@@ -208,7 +207,6 @@ __device__ __forceinline__ void decode_next(const DecodeParams& p, WindowSmem& s
       else asm("ld.global.cg.u8 %0, [%1];" : "=r"(scale) : "l"(src.scales + (lane >> 2)));
     }
     if (e == 0 && i >= back) warp_wait(&sm.abort, &sm.o_full[(i - back) % kRing], ((i - back) / kRing) & 1);
-    if (e == all) break;
     uint32_t o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     if (!rope) decode_codes(a, scale, o);
     const bool poison = __any_sync(0xffffffffu, not_finite(o) != 0);
@@ -425,8 +423,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         if (ok && pos >= p.most) err |= C128_DEV_BAD_BT_COL;
       }
       if (!ok) pos = -1;
-      hi = static_cast<int>(min(pos, static_cast<int64_t>(0x7ffff000)));  // (of a position behind the table, which goes alone: enough)
-      lo = static_cast<int>(min(max(pos + 1 - window, static_cast<int64_t>(0)), static_cast<int64_t>(p.most)));
+      // (A token behind the table begins a run, and goes alone: of the entries that it brings it sees all.)
+      hi = static_cast<int>(min(pos, static_cast<int64_t>(p.most)));
+      lo = static_cast<int>(min(max(pos - (window - 1), static_cast<int64_t>(0)), static_cast<int64_t>(p.most)));
       int64_t pos_before = __shfl_up_sync(0xffffffffu, pos, 1);
       int req_before = __shfl_up_sync(0xffffffffu, req, 1);
       if (lane == 0) pos_before = last_pos, req_before = last_req;
@@ -470,7 +469,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       it.row = __shfl_sync(0xffffffffu, req, j);
       const int lo_j = __shfl_sync(0xffffffffu, lo, j);
       it.hi = __shfl_sync(0xffffffffu, hi, j);
-      const int last = min(it.hi + count, p.most) - 1;
+      const int last = min(it.hi + (count - 1), p.most - 1);
       it.last = last;
       const bool fresh = i == 0 || !(goes_on >> j & 1);
       if (fresh) {
@@ -698,7 +697,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
           for (int g = 0; g < 4; ++g) {  // eight rows are of one token
             const int token = static_cast<int>((own + 8 * g) * plan.pitch_inv >> 16);
 #pragma unroll
-            for (int k = 0; k < 5; ++k) most[k][g] = static_cast<unsigned>(ahead[k] + token) < reach[k] ? INFINITY : -INFINITY;
+            for (int k = 0; k < 5; ++k) most[k][g] = static_cast<unsigned>(ahead[k]) + token < reach[k] ? INFINITY : -INFINITY;
           }
         }
         warp_wait(&sm.s_full, i & 1);

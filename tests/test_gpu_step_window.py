@@ -282,3 +282,23 @@ def test_entries_of_any_magnitude_that_are_not_seen(H):
     c.q[:] = c.q.abs()
     out, lse = c.run()
     c.check(out, lse, tokens=[t for t in range(60) if not (20 <= t < 32 or 33 <= t < 45)])
+
+
+@pytest.mark.parametrize("window,first", [(128, 4), (700, 4), (136, 0), (1, 135)])
+def test_the_last_positions_of_32_bits(window, first):
+    """A table of 2^31 - 1 entries, positions up to its end, behind it, and the largest of 64 bits."""
+    most, block, n = (1 << 31) - 1, 64, 70
+    rng = np.random.default_rng(6)
+    table = np.full((1, 1 << 25), -1, np.int32)
+    held = list(range(first // block + 1)) + list(range((most - n - window) // block, 1 << 25))
+    table[0, held] = rng.permutation(len(held))
+    tokens = consecutive(0, most - n, n + 2) + [(0, most + 100), (0, (1 << 63) - 1)]
+    c = Case(1, [(0, 0)], [1], 5, window, first, block)
+    c.tokens, c.table, c.most = tokens, table, most
+    c.cache = sref.make_cache(rng, len(held), block)
+    T = len(tokens)
+    c.q = torch.from_numpy(2 * rng.standard_normal((T, 5, 512))).bfloat16()
+    c.req, c.pos, c.slots = np.zeros(T, np.int32), np.array([p for _, p in tokens]), np.zeros(T, np.int64)
+    out, lse = c.run()
+    assert binding.device_errors() == 2  # a position behind the table
+    c.check(out, lse)
