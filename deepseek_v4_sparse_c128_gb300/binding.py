@@ -50,6 +50,7 @@ EXPORTS = (
     "c128_rotate",
     "c128_norm_rope_store",
     "c128_window_attention",
+    "c128_debug_stall_window_attention",
 )
 
 
@@ -149,6 +150,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     L.c128_decode_attention_workspace.argtypes = [i64, ctypes.POINTER(i64)]
     L.c128_merge_attention.argtypes = [T, T, T, T, vp]
     L.c128_window_attention.argtypes = [T, T, i64, T, T, T, T, i64, i64, ctypes.c_float, T, T, T, T, vp]
+    L.c128_debug_stall_window_attention.argtypes = L.c128_window_attention.argtypes
     L.c128_build_cos_sin.argtypes = [ctypes.POINTER(Rope), i64, T, vp]
     L.c128_rotate.argtypes = [T, T, T, i64, i32, i32, T, vp]
     L.c128_norm_rope_store.argtypes = [T, T, ctypes.c_float, T, T, T, T, T, T, T, i64, vp]
@@ -528,6 +530,13 @@ def window_attention(q, k_cache, kv_block_size: int, block_table, token_to_req_i
     decode_attention."""
     PreparedOp("window_attention", q, k_cache, kv_block_size, block_table, token_to_req_indices, positions, slot_mapping, window,
                scale, out, first=first, lse=lse, sink=sink, workspace=workspace, stream=stream)()
+
+
+def debug_stall_window_attention(*args, **kw) -> None:
+    """Test of window_attention's bounded waits (tests only): CTA 0 never learns of its tokens and gives up
+    with C128_DEV_TIMEOUT (read it with device_errors). Arguments as for window_attention."""
+    op = PreparedOp("window_attention", *args, **kw)
+    _check(lib().c128_debug_stall_window_attention(*op._args), "c128_debug_stall_window_attention")
 
 
 def call_status(*args, **kw) -> int:

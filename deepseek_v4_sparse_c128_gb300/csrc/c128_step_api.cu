@@ -81,6 +81,43 @@ int rope_steps(const c128_rope_t* rope, int turned, uint64_t* step) {
   return C128_OK;
 }
 
+// c128_window_attention; `stall`: the test of its waits.
+int window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
+                     const c128_tensor_t* block_table, const c128_tensor_t* token_to_req_indices,
+                     const c128_tensor_t* positions, const c128_tensor_t* slot_mapping, int64_t window,
+                     int64_t first, float scale, const c128_tensor_t* sink, const c128_tensor_t* out,
+                     const c128_tensor_t* lse, const c128_tensor_t* workspace, c128_stream_t stream, bool stall) {
+  c128::DecodeParams p{};
+  C128_TRY(check_attention(q, k_cache, kv_block_size, scale, sink, out, lse, workspace, &p));
+  const int64_t T = q->shape[0];
+  C128_TRY(check_desc(block_table, C128_I32, 2));
+  p.table_rows = block_table->shape[0];
+  if (p.table_rows > kMaxCount) return C128_ERR_ARG;
+  C128_TRY(check_table(block_table, p.table_rows, &p.table_stride));
+  C128_TRY(check_array(token_to_req_indices, C128_I32, T));
+  C128_TRY(check_array(positions, C128_I64, T));
+  C128_TRY(check_array(slot_mapping, C128_I64, T));
+  if (window < 1 || window > kMaxCount || first < 0 || first > kMaxCount) return C128_ERR_ARG;
+  if (T == 0 || q->shape[1] == 0) return C128_OK;
+  // what the table can hold, and what a token can see of it, in tiles of 64 entries: counted in 32 bits
+  const int64_t most = block_table->shape[1] > kMaxCount / kv_block_size ? kMaxCount : block_table->shape[1] * kv_block_size;
+  const int64_t seen = most < window + first ? most : window + first;
+  if (T * (seen / 64 + 2) > kMaxCount) return C128_ERR_ARG;
+  p.most = static_cast<int32_t>(most);
+  p.table = static_cast<const int32_t*>(block_table->data);
+  p.token_req = static_cast<const int32_t*>(token_to_req_indices->data);
+  p.positions = static_cast<const int64_t*>(positions->data);
+  p.slots = static_cast<const int64_t*>(slot_mapping->data);
+  p.window = window;
+  p.first = static_cast<int32_t>(first);
+  p.stall = stall ? 1 : 0;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  C128_TRY(c128::stream_errors(s, &p.err, &sms));
+  if (workspace->shape[0] < c128::decode_workspace_bytes(p.heads, sms)) return C128_ERR_ARG;
+  return done(c128::window_fits(p) ? c128::launch_window(p, sms, s) : c128::launch_decode(p, sms, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -218,34 +255,17 @@ int c128_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, 
                           const c128_tensor_t* positions, const c128_tensor_t* slot_mapping, int64_t window,
                           int64_t first, float scale, const c128_tensor_t* sink, const c128_tensor_t* out,
                           const c128_tensor_t* lse, const c128_tensor_t* workspace, c128_stream_t stream) {
-  c128::DecodeParams p{};
-  C128_TRY(check_attention(q, k_cache, kv_block_size, scale, sink, out, lse, workspace, &p));
-  const int64_t T = q->shape[0];
-  C128_TRY(check_desc(block_table, C128_I32, 2));
-  p.table_rows = block_table->shape[0];
-  if (p.table_rows > kMaxCount) return C128_ERR_ARG;
-  C128_TRY(check_table(block_table, p.table_rows, &p.table_stride));
-  C128_TRY(check_array(token_to_req_indices, C128_I32, T));
-  C128_TRY(check_array(positions, C128_I64, T));
-  C128_TRY(check_array(slot_mapping, C128_I64, T));
-  if (window < 1 || window > kMaxCount || first < 0 || first > kMaxCount) return C128_ERR_ARG;
-  if (T == 0 || q->shape[1] == 0) return C128_OK;
-  // what the table can hold, and what a token can see of it, in tiles of 64 entries: counted in 32 bits
-  const int64_t most = block_table->shape[1] > kMaxCount / kv_block_size ? kMaxCount : block_table->shape[1] * kv_block_size;
-  const int64_t seen = most < window + first ? most : window + first;
-  if (T * (seen / 64 + 2) > kMaxCount) return C128_ERR_ARG;
-  p.most = static_cast<int32_t>(most);
-  p.table = static_cast<const int32_t*>(block_table->data);
-  p.token_req = static_cast<const int32_t*>(token_to_req_indices->data);
-  p.positions = static_cast<const int64_t*>(positions->data);
-  p.slots = static_cast<const int64_t*>(slot_mapping->data);
-  p.window = window;
-  p.first = static_cast<int32_t>(first);
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int sms = 0;
-  C128_TRY(c128::stream_errors(s, &p.err, &sms));
-  if (workspace->shape[0] < c128::decode_workspace_bytes(p.heads, sms)) return C128_ERR_ARG;
-  return done(c128::window_fits(p) ? c128::launch_window(p, sms, s) : c128::launch_decode(p, sms, s));
+  return window_attention(q, k_cache, kv_block_size, block_table, token_to_req_indices, positions, slot_mapping, window, first,
+                          scale, sink, out, lse, workspace, stream, false);
+}
+
+int c128_debug_stall_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
+                                      const c128_tensor_t* block_table, const c128_tensor_t* token_to_req_indices,
+                                      const c128_tensor_t* positions, const c128_tensor_t* slot_mapping, int64_t window,
+                                      int64_t first, float scale, const c128_tensor_t* sink, const c128_tensor_t* out,
+                                      const c128_tensor_t* lse, const c128_tensor_t* workspace, c128_stream_t stream) {
+  return window_attention(q, k_cache, kv_block_size, block_table, token_to_req_indices, positions, slot_mapping, window, first,
+                          scale, sink, out, lse, workspace, stream, true);
 }
 
 }  // extern "C"

@@ -582,6 +582,13 @@ int c128_norm_rope_store(const c128_tensor_t* positions, const c128_tensor_t* sl
  * result be merged with that of c128_decode_attention over the compressed cache (c128_merge_attention; the sink in
  * one of them only).
  *
+ * Where window + first <= 136 a kernel keeps the entries of consecutive tokens in shared memory: they are decoded once
+ * for all of them. There the softmax weights are divided by their sum (and the sink's share) before they are rounded to
+ * bf16, so that of one entry out is that entry; lse is of the exact sums, in fp32. Larger windows run as
+ * c128_decode_attention does, a token at a time.
+ * An entry that holds NaN makes out and lse of the tokens that see it NaN, and of no others; so does an infinity, or the
+ * formula's value is stored.
+ *
  *   q                    [T, H, 512]   bf16   as for c128_decode_attention
  *   k_cache              [NKB, bs, W]  uint8  kv_block_size == bs
  *   block_table          [R, MB]       int32  k_cache block of entries b*bs .. b*bs + bs - 1 of a request. Blocks
@@ -592,7 +599,7 @@ int c128_norm_rope_store(const c128_tensor_t* positions, const c128_tensor_t* sl
  *   window                             1 <= window < 2^31
  *   first                              0 <= first < 2^31
  *   scale, sink [H], out [T, H, 512], lse [T, H], workspace: as for c128_decode_attention (the workspace is
- *                                      of c128_decode_attention_workspace bytes)
+ *                                      of c128_decode_attention_workspace bytes, whatever the window)
  *
  * The rows of out and lse of skipped tokens are left as they were.
  * Device error bits: C128_DEV_BAD_REQ - token_to_req_indices[t] outside [0, R) (the token is skipped);
@@ -605,6 +612,18 @@ int c128_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, 
                           const c128_tensor_t* positions, const c128_tensor_t* slot_mapping, int64_t window,
                           int64_t first, float scale, const c128_tensor_t* sink, const c128_tensor_t* out,
                           const c128_tensor_t* lse, const c128_tensor_t* workspace, c128_stream_t stream);
+
+/*
+ * Test of the failure handling, for tests only: c128_window_attention, except that CTA 0 never learns of its tokens. Its
+ * waits run out (after about a second), it ends with C128_DEV_TIMEOUT in the device error bits and stores nothing, and
+ * what it would have stored is left as it was. The context stays usable.
+ */
+int c128_debug_stall_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,
+                                      const c128_tensor_t* block_table, const c128_tensor_t* token_to_req_indices,
+                                      const c128_tensor_t* positions, const c128_tensor_t* slot_mapping,
+                                      int64_t window, int64_t first, float scale, const c128_tensor_t* sink,
+                                      const c128_tensor_t* out, const c128_tensor_t* lse,
+                                      const c128_tensor_t* workspace, c128_stream_t stream);
 
 /* Human-readable name of a return code (static string, never NULL). */
 const char* c128_status_string(int status);
