@@ -52,7 +52,7 @@ __device__ __forceinline__ void load_weight(const float* w, int lane, float (&x)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 f = w == nullptr ? make_float4(1.f, 1.f, 1.f, 1.f)
-                                  : __ldg(reinterpret_cast<const float4*>(w + 8 * lane + 4 * (i & 1) + 256 * (i >> 1)));
+                                  : *reinterpret_cast<const float4*>(w + 8 * lane + 4 * (i & 1) + 256 * (i >> 1));
     x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
   }
 }

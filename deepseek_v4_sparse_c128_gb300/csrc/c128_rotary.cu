@@ -34,12 +34,12 @@ __device__ __forceinline__ void cos_sin_of(uint64_t turn, float magnitude, float
   s = __uint_as_float(__float_as_uint(swap ? a : b) ^ (quarter & 2) << 30);
 }
 
-// A thread keeps its N pairs and goes from row to row, the angles by addition.
+// A thread keeps its N pairs and goes from row to row, the angles by addition. No kernel behind this one starts early: the
+// compressor's read tables as read-only data, which nobody may write while they are resident.
 template <int N>
 __global__ void __launch_bounds__(kTableThreads) cos_sin_kernel(const __grid_constant__ CosSinParams p) {
   __shared__ uint64_t steps[kMaxTurned / 2];  // (parameters are slow to read by an index of the thread's own)
   for (int i = threadIdx.x; i < p.half; i += kTableThreads) steps[i] = p.step[i];
-  launch_dependents();
   __syncthreads();
   const unsigned threads = p.half / N, at_once = kTableThreads / threads, below = threadIdx.x / threads;
   const unsigned pair = (threadIdx.x - below * threads) * N;
