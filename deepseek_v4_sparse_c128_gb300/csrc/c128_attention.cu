@@ -1,5 +1,6 @@
 // c128_decode_attention: attention of one new token per request over its entries of the paged FP8
-// cache, on the tcgen05 tensor cores.
+// cache, on the tcgen05 tensor cores. (And c128_window_attention with windows that do not fit into shared memory: WINDOW.
+// There each token is a request of its own.)
 //
 //   S^T = K Q^T            per tile of 64 entries: M = 64 entries, N = heads, K = 512
 //   P^T = exp2(c S^T - m)  c = scale * log2(e), m a running reference per head

@@ -3,9 +3,14 @@
 //   n = x * rrms * w,  rrms = 1 / sqrt(mean(x^2) + eps);  the last 64 columns: (e, o) -> (e c - o s, o c + e s)
 //
 // One pass: a warp takes a row of 512 values, 16 per lane in two pieces of 8 (columns 8l .. and 256 + 8l ..),
-// keeps it in registers between the sum and the result, and has kRows heads of one token on their way at
+// keeps it in registers between the sum and the result, and has ROWS heads of one token on their way at
 // once, for which it reads the token's position and angles once. Lanes 24 .. 31 hold the turned columns in
 // their second piece, four pairs each. A key's groups of 64 columns are eight lanes of a piece.
+//
+// A query is 1 KB read and 1 KB written (bf16) for some 180 instructions of a warp, so DRAM bounds it: 7,777 tokens of 64
+// heads and a key 163 us, 6.33 TB/s, 0.94 of the measured copy; 200 tokens of 128 heads and a key 11.9 us, 4.4 TB/s (the
+// launch and one chain position - angles - result stand before and behind 8 us of bytes); one token of 64 heads 3.6 us, a
+// launch and that chain. With 4 heads to a warp instead of 8 the 7,777 tokens took 178 us: too few loads on their way.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -261,7 +266,7 @@ cudaError_t launch_norm(const NormParams& p, int sm_count, cudaStream_t stream) 
   if (p.tokens == 0) return cudaSuccess;
   constexpr int kWarps = kNormThreads / 32;
   const int64_t rows = p.q != nullptr ? p.tokens * p.heads : 0;
-  // Heads of a token to a warp: 1 while every row has a warp to itself; 8 where there are rows for several waves of CTAs (64
+  // Heads of a token to a warp: 1 while every row has a warp to itself (one token of 64 heads, 64 warps); 8 where there are rows for several waves of CTAs (64
   // heads: 4,096 tokens 94.4 us with 4, 88.9 with 8; 1,024 tokens 25.2 and 25.0; 512 tokens 13.7 and 14.5)
   const int per = rows <= 32ll * sm_count ? 1 : rows < 400ll * sm_count ? 4 : 8;
   uint32_t pieces = static_cast<uint32_t>(p.q != nullptr ? (p.heads + per - 1) / per : 0);

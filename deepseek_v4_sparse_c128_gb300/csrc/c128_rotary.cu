@@ -15,6 +15,8 @@ namespace {
 // rounded), and what is left, under an eighth of a turn either way, becomes a float: sines near zero keep their
 // relative precision. With |x| <= pi / 4 the Taylor series of both, to x^10 and x^11, are 2^-33 of a value off; their
 // steps in z = x^2 are the same, so a packed multiply-add takes both.
+// Stores bound it where the table is long: a million positions of 32 pairs, 268 MB, 38.9 us, 6.9 TB/s (with the library's
+// cosine and sine of each angle, one pair to a thread, 67 us: instructions bound that). 16,384 positions 3.3 us: a launch.
 constexpr int kTableThreads = 256;
 
 __device__ __forceinline__ void cos_sin_of(uint64_t turn, float magnitude, float& c, float& s) {
@@ -69,9 +71,11 @@ __global__ void __launch_bounds__(kTableThreads) cos_sin_kernel(const __grid_con
 }
 
 // --------------------------------------------------------------------------------------- rotation
-// A pass over memory. Work is dealt out in units: a vector of 16 bytes (of halves: one of either half) to
+// A pass over memory, bound by it: 4,096 tokens x 64 heads x 512 columns 79.6 us, 6.75 TB/s, as the measured copy; 4,099 x 40
+// x 128 in fp32 28.4 us, 5.9 TB/s; 64 x 64 x 512, a decode step, 3.5 us, about a launch. Work is dealt out in units: a vector of 16 bytes (of halves: one of either half) to
 // turn, or one to copy; a CTA takes kUnits of them, of one token or of several whole ones. Without the
-// alignment for vectors a unit is a pair, or a value to copy.
+// alignment for vectors a unit is a pair, or a value to copy. Two units to a thread of 128: one took the three cases 3.8, 133.6
+// and 35.2 us, four 4.6, 81.7 and 32.8, eight 5.9, 112.9 and 49.5.
 constexpr int kRotateThreads = 128, kFlight = 2, kUnits = kRotateThreads * kFlight;
 
 template <typename T>
