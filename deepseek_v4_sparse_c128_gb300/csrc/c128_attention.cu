@@ -1,6 +1,6 @@
 // c128_decode_attention: attention of one new token per request over its entries of the paged FP8
-// cache, on the tcgen05 tensor cores. (And c128_window_attention with windows that do not fit into shared memory: WINDOW.
-// There each token is a request of its own.)
+// cache, on the tcgen05 tensor cores. (And c128_window_attention with windows that do not fit into shared memory: there
+// each token is a request of its own, or a run of tokens of few heads is one.)
 //
 //   S^T = K Q^T            per tile of 64 entries: M = 64 entries, N = heads, K = 512
 //   P^T = exp2(c S^T - m)  c = scale * log2(e), m a running reference per head
@@ -55,6 +55,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "c128_device.cuh"
 #include "c128_serving.h"
@@ -85,13 +86,22 @@ constexpr float kHigh = 0x1p32f, kLow = 0x1p-32f;  // weights may be up to, and 
 constexpr int kTmemCols = 512, kTmemS = 256, kTmemL = 384;  // O in columns 0..255, two S tiles and L behind it
 
 enum : int { kWhole = -1, kSkipped = -2 };  // parts that are none: a result to `out`; none (a token that is skipped)
-enum : int { kFirst = 1, kLast = 2, kEnd = 4, kRunShift = 3 };  // of its stretch of one request's tiles; above, the stretch's number mod 4
+// Of its stretch of one request's tiles; above, the stretch's number mod 4, whether tokens of a run see different entries here,
+// and that run's tokens less one.
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kRunShift = 3, kEdge = 32, kTokensShift = 6 };
+
+// What a kernel is for: decode attention; a window, each token a request (kWindow); a window and up to 16 heads (kTogether), where
+// up to four tokens that follow one another are one request, a run of tokens: each entry is decoded once for all of them,
+// and the rows of a tile are theirs, 16 for each. Entries that not all of them see are at the two ends of the run's.
+enum : int { kDecode = 0, kWindow = 1, kTogether = 2 };
+constexpr int kMostTogether = 4, kTokenRows = kGroup / kMostTogether;
+constexpr int kMember = -2;  // the entries of a token in a run that another one begins
 
 // In the place of a part's log-sum-exp: the part's CTA gave up. (None comes out so: a reference or a sum that is infinite makes NaN.)
 constexpr float kNotThere = INFINITY;
 
 struct Task {  // a request that a CTA starts and leaves to the columns behind it, if parts > 0
-  int32_t request, parts, column, group_heads;
+  int32_t request, parts, column, group_heads;  // (with kTogether: the run's tokens in the place of the last)
 };
 
 // How a call's heads and scratch are laid out for head groups of `group` heads (16, 32 or 64). CTA
@@ -124,7 +134,7 @@ struct Layout {
 };
 
 struct Layouts {  // made on the host: their divisions would stand in front of the kernel's work
-  Layout of[3];  // for groups of 16, 32 and 64 heads
+  Layout of[3];  // for groups of 16, 32 and 64 heads (the last with kTogether: for the rows of a run)
 };
 
 struct TileDesc {
@@ -134,6 +144,7 @@ struct TileDesc {
   int32_t flags, request;
   int32_t part;                  // kLast: slot of the partial result, kWhole, or kSkipped
   int32_t pad;
+  uint64_t seen[kMostTogether];  // the entries that each of them sees
 };
 
 struct DecodeSmem {
@@ -156,9 +167,11 @@ struct DecodeSmem {
   uint64_t inv_full[2];          // `inv` and `done` of a stretch are there
   uint64_t soft;                 // barrier of the softmax warps
   volatile int32_t off[2];       // 1 + the tile whose P in this buffer was made with a reference that is off, or will be
-  int32_t done_request[2], done_part[2];
+  int32_t done_request[2], done_part[2], done_tokens[2];
+  uint8_t poison[2][kTile];      // of a tile with kEdge: entries that are not finite
   int warp_sums[32];
   int32_t first_request, first_tile, first_entries;  // where the column's run begins, and that request's entries
+  int32_t first_lead, first_shift, first_row, first_tokens;  // (of a window, where the CTA that begins it has them: tokens > 0)
   int32_t end_request, end_tile;  // and the tile behind its end
   Layout lay;                    // read back where results are written, to keep registers free
   int32_t group, group_heads;
@@ -179,6 +192,7 @@ __device__ __forceinline__ bool too_large(uint2 scales, uint32_t values) {
 // token: its row is its request's, and n is -1 if it is skipped.
 struct Seen {
   int n, lead, shift, row;
+  int tokens = 1;  // of the run that begins here
 };
 template <bool WINDOW>
 __device__ __forceinline__ Seen seen_by(const DecodeParams& p, int64_t r, unsigned int* err) {
@@ -202,9 +216,38 @@ __device__ __forceinline__ Seen seen_by(const DecodeParams& p, int64_t r, unsign
     return Seen{lead + max(end - begin, 0), lead, begin - lead, row};
   }
 }
-template <bool WINDOW>
-__device__ __forceinline__ int entries_of(const DecodeParams& p, int64_t r, unsigned int* err) {
-  return seen_by<WINDOW>(p, r, err).n;
+// What the run that token r begins sees. (Runs do not pass a multiple of four tokens: each finds out with four loads at once.)
+__device__ __forceinline__ Seen seen_together(const DecodeParams& p, int64_t r, unsigned int* err) {
+  const int64_t block = r & ~static_cast<int64_t>(kMostTogether - 1);
+  int64_t pos[kMostTogether];
+  int row[kMostTogether];
+#pragma unroll
+  for (int i = 0; i < kMostTogether; ++i) {
+    pos[i] = -1;
+    if (block + i >= p.requests) continue;
+    const int64_t at = p.positions[block + i], slot = p.slots[block + i];
+    row[i] = p.token_req[block + i];
+    if (slot >= 0 && row[i] >= 0 && row[i] < p.table_rows) pos[i] = at;
+  }
+  unsigned goes_on = 0;  // bit i: with the run of the token before it
+#pragma unroll
+  for (int i = 1; i < kMostTogether; ++i)
+    if (pos[i] > 0 && pos[i] - 1 == pos[i - 1] && row[i] == row[i - 1] && pos[i] < p.most) goes_on |= 1u << i;
+  const int i = static_cast<int>(r - block);
+  Seen seen = seen_by<true>(p, r, err);
+  if (goes_on >> i & 1) {
+    seen.n = kMember;
+  } else {
+    const int behind = __ffs(~(goes_on >> (i + 1))) - 1;
+    seen.tokens = 1 + behind;
+    seen.n += behind;  // (their own entries; a token that is skipped has none behind it)
+  }
+  return seen;
+}
+template <int MODE>
+__device__ __forceinline__ Seen seen_of(const DecodeParams& p, int64_t r, unsigned int* err) {
+  if constexpr (MODE == kTogether) return seen_together(p, r, err);
+  else return seen_by<(MODE != kDecode)>(p, r, err);
 }
 // A request without entries still takes a (masked) tile: its results are written like any other's.
 // (So does a skipped token, whose results are not.)
@@ -220,6 +263,7 @@ static_assert(kTile == 64, "tiles_of");
 // (A cost of 2: 64 x 1,024 entries 4 % slower, 48 x 8,192 4 % faster; snap of 1 or 3: up to 6 % slower.)
 constexpr int kRunCost = 1;  // not 0: a cut at the end of one request would be in none
 constexpr int kSnap = 2;
+__device__ __forceinline__ int units_of(int entries) { return entries == kMember ? 0 : tiles_of(entries) + kRunCost; }
 struct Deal {
   int share, extra, snap;
   __device__ Deal(int total, int columns) {
@@ -238,17 +282,19 @@ struct Deal {
 
 // A stretch's results: O of all heads times 1 / sum, to the output or the workspace. The softmax and the
 // decoding warps share the work, four warps (`rank`) to each quarter of the TMEM lanes.
+template <int MODE>
 __device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams& p, int heads, int rank, int odd) {
   int tid = threadIdx.x;
   asm volatile("" : "+r"(tid));  // keeps what follows from being computed ahead, and in registers, in the callers' loops
-  const int warp = tid >> 5, lane = tid & 31, heads16 = (heads + 15) & ~15;
+  const int warp = tid >> 5, lane = tid & 31, heads16 = MODE == kTogether ? kGroup : (heads + 15) & ~15;
   const int64_t request = sm.done_request[odd];
   const int part = sm.done_part[odd];
   tmem_fence_after();
   const int quarter = warp & 3, group0 = sm.group * sm.group_heads;
   const uint32_t o_at = sm.tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+  if (MODE == kDecode || part != kSkipped)  // (in the loop's own start this costs registers that spill)
 #pragma unroll 1
-  for (int item = part == kSkipped ? heads16 : rank; item < heads16 / 4; item += (kFillWarps + kSoftWarps) / 4) {  // 16 heads of 128 columns each
+  for (int item = rank; item < heads16 / 4; item += (kFillWarps + kSoftWarps) / 4) {  // 16 heads of 128 columns each
     const int mt = item & 3, h = (item >> 2) * 16;
     const int col = mt * 128 + 32 * quarter + lane;
     uint32_t o[16];
@@ -267,12 +313,17 @@ __device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams
       for (int k = 0; k < 4; ++k) dst[32 * k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       continue;
     }
-    const int64_t row = request * p.out_stride_r + (group0 + h) * p.out_stride_h;
+    int token = 0, of_token = h;  // of a run; the first of the 16 heads
+    if constexpr (MODE == kTogether) {
+      token = h / kTokenRows, of_token = h % kTokenRows;
+      if (token >= sm.done_tokens[odd]) continue;
+    }
+    const int64_t row = (request + token) * p.out_stride_r + (group0 + of_token) * p.out_stride_h;
     if (p.out_f32) {
       float* dst = static_cast<float*>(p.out) + row + col;
 #pragma unroll
       for (int k = 0; k < 16; ++k, dst += p.out_stride_h)
-        if (h + k < heads) *dst = __uint_as_float(o[k]);
+        if (of_token + k < heads) *dst = __uint_as_float(o[k]);
     } else {
       // neighbouring lanes swap halves of a pair of heads, so that each stores two columns of one
       uint16_t* dst = static_cast<uint16_t*>(p.out) + row + (lane & 1) * p.out_stride_h + (col & ~1);
@@ -281,7 +332,7 @@ __device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams
       for (int k = 0; k < 16; k += 2, dst += 2 * p.out_stride_h) {
         const uint32_t two = pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1]));
         const uint32_t both = __byte_perm(two, __shfl_xor_sync(0xffffffffu, two, 1), halves);
-        if (h + k + (lane & 1) < heads) *reinterpret_cast<uint32_t*>(dst) = both;
+        if (of_token + k + (lane & 1) < heads) *reinterpret_cast<uint32_t*>(dst) = both;
       }
     }
   }
@@ -292,19 +343,43 @@ __device__ __forceinline__ void store_results(DecodeSmem& sm, const DecodeParams
 
 // The end of a CTA whose wait ran out. What it has in the workspace may be of any call: its parts are marked, and the
 // requests that they are of are not joined.
-__device__ __noinline__ void give_up(const DecodeSmem& sm, uint8_t* workspace, int all_heads, unsigned int* err) {
+__device__ __noinline__ void give_up(const DecodeSmem& sm, uint8_t* workspace, unsigned int* err) {
   if (threadIdx.x == 0) atomicOr(err, static_cast<unsigned int>(C128_DEV_TIMEOUT));
-  const int column = blockIdx.x / sm.lay.groups, heads = min(sm.group_heads, all_heads - sm.group * sm.group_heads);
+  const int column = blockIdx.x / sm.lay.groups, heads = sm.lay.heads;
   float* lse = reinterpret_cast<float*>(workspace + sm.lay.lse_at());
   for (int i = threadIdx.x; i < 2 * heads; i += kDecodeThreads)
     lse[sm.lay.row(2 * column + (i >= heads), sm.group, i >= heads ? i - heads : i)] = kNotThere;
 }
 
+// An entry that some tokens of a run see and others do not, as it has been stored (16 pieces of 16 bytes by each of four threads, at
+// dst0, dst1 and dst_rope): if a value of it is not finite it becomes zeros, since 0 times it has to be 0 for the others, and
+// true is returned, for its scores to be NaN.
+__device__ __forceinline__ bool hide_poison(uint32_t dst0, uint32_t dst1, uint32_t dst_rope) {
+  uint32_t most = 0;
+#pragma unroll 1
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t at = j < 14 ? (j & 1 ? dst1 : dst0) + (j >> 1) * kChunkBytes : dst_rope ^ (64u * (j - 14));
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    most |= (v.x & 0x7fff7fffu) + 0x00800080u, most |= (v.y & 0x7fff7fffu) + 0x00800080u;
+    most |= (v.z & 0x7fff7fffu) + 0x00800080u, most |= (v.w & 0x7fff7fffu) + 0x00800080u;
+  }
+  most |= __shfl_xor_sync(0xffffffffu, most, 1);
+  most |= __shfl_xor_sync(0xffffffffu, most, 2);
+  if ((most & 0x80008000u) == 0) return false;
+#pragma unroll 1
+  for (int j = 0; j < 16; ++j)
+    sts16(j < 14 ? (j & 1 ? dst1 : dst0) + (j >> 1) * kChunkBytes : dst_rope ^ (64u * (j - 14)), 0, 0, 0, 0);
+  return true;
+}
+
 constexpr int kBoxHeads = 16;  // heads of a TMA load of queries
 
-template <bool ALIGN16, int HEADS, bool WINDOW>
+template <bool ALIGN16, int HEADS, int MODE>
 __global__ void __launch_bounds__(kDecodeThreads, 1)
     decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ Layouts layouts) {
+  constexpr bool WINDOW = MODE != kDecode, TOGETHER = MODE == kTogether;
+  static_assert(!TOGETHER || HEADS == kGroup, "all rows");
   constexpr int kOwn = HEADS / 2;  // heads of four softmax warps
   extern __shared__ uint8_t smem_raw[];
   DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
@@ -358,9 +433,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // Sum the requests' units (each thread a stretch of requests)...
   const unsigned per = (static_cast<unsigned>(requests) + kDecodeThreads - 1) / kDecodeThreads;
   const int r_begin = min(threadIdx.x * per, static_cast<unsigned>(requests)), r_end = min(r_begin + per, static_cast<unsigned>(requests));
-  const int n_begin = r_begin < r_end ? entries_of<WINDOW>(p, r_begin, &err) : 0;
-  int mine = r_begin < r_end ? tiles_of(n_begin) + kRunCost : 0;
-  for (int r = r_begin + 1; r < r_end; ++r) mine += tiles_of(entries_of<WINDOW>(p, r, &err)) + kRunCost;
+  const Seen seen_begin = r_begin < r_end ? seen_of<MODE>(p, r_begin, &err) : Seen{0, 0, 0, 0};
+  int mine = r_begin < r_end ? units_of(seen_begin.n) : 0;
+  for (int r = r_begin + 1; r < r_end; ++r) mine += units_of(seen_of<MODE>(p, r, &err).n);
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -385,10 +460,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   int size = kSizes - 1, most = most_columns[kSizes - 1], column = column_for[kSizes - 1], group = group_for[kSizes - 1];
 #pragma unroll
   for (int k = kSizes - 2; k >= 0; --k)
-    if (tiles <= most_columns[k]) size = k, most = most_columns[k], column = column_for[k], group = group_for[k];
+    if (!TOGETHER && tiles <= most_columns[k]) size = k, most = most_columns[k], column = column_for[k], group = group_for[k];
   const int group_heads = 16 << size;
   const int heads = min(group_heads, p.heads - group * group_heads);
-  const int heads16 = (heads + 15) & ~15;
+  // Rows: heads; in a run of tokens those of each from a multiple of 16 on.
+  const int heads16 = TOGETHER ? kGroup : (heads + 15) & ~15;
+  auto token_of = [](int row) { return TOGETHER ? row / kTokenRows : 0; };
+  auto head_of = [](int row) { return TOGETHER ? row % kTokenRows : row; };
+  auto is_there = [&](int row, int tokens) { return head_of(row) < heads && token_of(row) < tokens; };
   // ...and find this column's run: its first request, and whether its last one goes on behind it.
   const int columns = min(most, total);
   const bool idle = column >= columns;
@@ -405,24 +484,32 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     int at = base;
     for (int r = r_begin; r < r_end && at <= cut1; ++r) {
       unsigned int ignore = 0;
-      const int entries = r == r_begin ? n_begin : entries_of<WINDOW>(p, r, &ignore), end = at + tiles_of(entries), next = end + kRunCost;
+      const Seen seen = r == r_begin ? seen_begin : seen_of<MODE>(p, r, &ignore);
+      if (TOGETHER && seen.n == kMember) continue;
+      const int entries = seen.n, end = at + tiles_of(entries), next = end + kRunCost, behind = TOGETHER ? r + seen.tokens : r + 1;
       const bool holds0 = cut0 >= at && cut0 < next, holds1 = cut1 >= at && cut1 < next;
       auto on = [&](int cut) { return cut >= end || (cut - at > deal.snap && end - cut <= deal.snap); };
       auto back = [&](int cut) { return cut < end && cut - at <= deal.snap; };
       if (holds0) {
         const bool begins = on(cut0);  // with the next request
-        sm.first_request = begins ? r + 1 : r;
+        sm.first_request = begins ? behind : r;
         sm.first_tile = begins || back(cut0) ? 0 : cut0 - at;
-        sm.first_entries = !begins ? entries : r + 1 < requests ? entries_of<WINDOW>(p, r + 1, &ignore) : 0;
+        if constexpr (WINDOW) {
+          sm.first_entries = entries, sm.first_lead = seen.lead, sm.first_shift = seen.shift, sm.first_row = seen.row;
+          sm.first_tokens = begins ? 0 : seen.tokens;
+        } else {
+          sm.first_entries = !begins ? entries : behind < requests ? seen_of<MODE>(p, behind, &ignore).n : 0;
+        }
       }
       if (holds1) {
         // cut inside: does the request begin in this column? Then this column's task is to join it,
         // with every column that has a cut of it as its begin
         const bool inside = !on(cut1) && !back(cut1);
-        sm.end_request = on(cut1) ? r + 1 : r;
+        sm.end_request = on(cut1) ? behind : r;
         sm.end_tile = inside ? cut1 - at : 0;
         *task = Task{r,
-                     inside && back(cut0) && group == 0 ? deal.column_of(end - deal.snap - 1) - column + 1 : 0, column, group_heads};
+                     inside && back(cut0) && group == 0 ? deal.column_of(end - deal.snap - 1) - column + 1 : 0, column,
+                     TOGETHER ? seen.tokens : group_heads};
       }
       at = next;
     }
@@ -461,7 +548,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     int64_t window = r;      // lanes hold what requests window .. window + 31 see
     unsigned int ignore = 0;
     int id[2];
-    int lead = 0, shift = 0;  // of this request, if WINDOW
+    int lead = 0, shift = 0, tokens = 1;  // of this request, if WINDOW
     int64_t row = r;
     auto entry = [&](uint32_t key) { return WINDOW && key >= static_cast<uint32_t>(lead) ? key + shift : key; };
     // Entries are fewer than 2^31, so an index past them does not wrap in 32 unsigned bits. (Not as read-only data: this
@@ -475,18 +562,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     };
     int stretch = 0;
     Seen lens{0, 0, 0, 0};
-    auto load_lens = [&] { lens = window + lane < p.requests ? seen_by<WINDOW>(p, window + lane, &ignore) : Seen{0, 0, 0, 0}; };
+    auto load_lens = [&] { lens = window + lane < p.requests ? seen_of<MODE>(p, window + lane, &ignore) : Seen{0, 0, 0, 0}; };
     auto take_request = [&] {
       if constexpr (WINDOW) {
         const int from = static_cast<int>(r - window);
         lead = __shfl_sync(0xffffffffu, lens.lead, from), shift = __shfl_sync(0xffffffffu, lens.shift, from);
         row = __shfl_sync(0xffffffffu, lens.row, from);
+        if constexpr (TOGETHER) tokens = __shfl_sync(0xffffffffu, lens.tokens, from);
       }
     };
     if constexpr (WINDOW) {
-      load_lens();
-      take_request();
-      if (!ends) load_ids();
+      if (sm.first_tokens == 0) {  // the run begins with a request that the one before was not cut of
+        load_lens();
+        n = __shfl_sync(0xffffffffu, lens.n, 0);
+        take_request();
+        if (!ends) load_ids();
+      } else {
+        lead = sm.first_lead, shift = sm.first_shift, row = sm.first_row, tokens = sm.first_tokens;
+        if (!ends) load_ids();
+        load_lens();
+      }
     } else {  // its length and blocks are read at once
       if (!ends) load_ids();
       load_lens();
@@ -503,7 +598,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         break;
       }
       const int tiles = tiles_of(n);
-      uint64_t mask = 0;
+      uint64_t mask = 0, seen[kMostTogether] = {};
       const uint8_t* from[2];
       const uint8_t* sc[2];
 #pragma unroll
@@ -519,12 +614,31 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         d.data[32 * h + lane] = from[h];
         d.scales[32 * h + lane] = sc[h];
         mask |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, ok)) << (32 * h);
+        if constexpr (TOGETHER) {
+          if (tokens > 1) {  // (they are within the table, so the run's last entry is the last token's own)
+            const int at = static_cast<int>(entry(key)), own = n + shift - tokens, window_of = static_cast<int>(p.window);
+#pragma unroll
+            for (int k = 0; k < kMostTogether; ++k) {
+              const bool sees = ok && k < tokens && at <= own + k && (at > own + k - window_of || at < p.first);
+              seen[k] |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, sees)) << (32 * h);
+            }
+          }
+        }
+      }
+      bool edge = false;
+      if constexpr (TOGETHER) {
+#pragma unroll
+        for (int k = 1; k < kMostTogether; ++k) edge |= k < tokens && seen[k] != seen[0];
       }
       const bool last_of_request = tile + 1 == tiles;
       if (lane == 0) {
         d.mask = mask;
-        d.flags = (tile == started ? kFirst : 0) | (last_of_request || (r == end_request && tile + 1 == end_tile) ? kLast : 0) | (stretch & 3) << kRunShift;
+        d.flags = (tile == started ? kFirst : 0) | (last_of_request || (r == end_request && tile + 1 == end_tile) ? kLast : 0) | (stretch & 3) << kRunShift | (edge ? kEdge : 0) | (tokens - 1) << kTokensShift;
         d.request = static_cast<int32_t>(r);
+        if constexpr (TOGETHER) {
+#pragma unroll
+          for (int k = 0; k < kMostTogether; ++k) d.seen[k] = seen[k];
+        }
         d.part = WINDOW && n < 0 ? kSkipped : started == 0 && last_of_request ? kWhole : 2 * column + (started == 0 ? 1 : 0);
       }
       __syncwarp();
@@ -540,7 +654,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       if (last_of_request) {
         ++stretch;
-        ++r;
+        r += TOGETHER ? tokens : 1;
         tile = started = 0;
         if (r - window >= 32) {
           window = r;
@@ -618,7 +732,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       warp_wait(&sm.k_free[i & 1][kQuarters - 1], (i / 2) & 1);
       // (that of the stretch after next needs a tile of these warps, so the parity means this one)
       warp_wait(&sm.inv_full[stretch & 1], stretch >> 1 & 1);
-      if (!*abort_flag) store_results(sm, p, heads, 2 + warp / 4, stretch & 1);
+      if (!*abort_flag) store_results<MODE>(sm, p, heads, 2 + warp / 4, stretch & 1);
     };
     fetch(0);
     load_scales();
@@ -694,6 +808,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         if (j >= 4 + kAhead) decode(j, o[at(j)]);
         store(j, o[at(j)]);
       }
+      if constexpr (TOGETHER) {
+        if (done1 & kEdge) {
+          const uint32_t at_buf = buf * kTileBytes;
+          const bool poison = hide_poison(dst0 + at_buf, dst1 + at_buf, dst_rope + at_buf);
+          if (sub == 0) sm.poison[buf][key] = poison;
+        }
+      }
       publish(1);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may be in flight when the CTA ends
@@ -749,7 +870,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             for (int b = 0; b < boxes; ++b)
               for (int c = 0; c < kChunks; ++c)
                 load_query_box(sm.q + c * (kGroup * 128) + b * (kBoxHeads * 128), &q_map, 64 * c,
-                               group * group_heads + b * kBoxHeads, request, &sm.q_full);
+                               group * group_heads + head_of(b * kBoxHeads), request + token_of(b * kBoxHeads), &sm.q_full);
             loading = true;
           }
           if (i >= 2 && !wait(&sm.s_free[buf], (i / 2 - 1) & 1)) break;
@@ -821,6 +942,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const float c2 = p.scale * kLog2e;
     float2 l[kOwn / 8];            // its sums: of heads h0 + 8g and + 1 in l[g]
     bool zero = true, fresh = true;  // the references are 0; the run has had no entry yet
+    unsigned fresh_tokens = ~0u;     // with TOGETHER: the tokens of the run that have had none,
+    unsigned absent = 0;             // and this thread's rows of no head or no token (bit g: h0 + 8g, bit 8 + g: and the next)
     uint32_t soft_phase = 0, p_phase = 0;  // p_phase: bit b of buffer b
     auto soft_sync = [&] {
       __syncwarp();
@@ -835,8 +958,30 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (flags & kEnd) break;
       // the P of two tiles ago has been used
       if (i >= 2) warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2 - 1) & 1);
-      const bool in0 = mask >> key0 & 1, in1 = mask >> key1 & 1;
+      // Whether this thread's entries are seen by the rows h0 + 8g: bit g, and bit 16 for one that is not finite.
+      std::conditional_t<TOGETHER, unsigned, bool> in0 = mask >> key0 & 1, in1 = mask >> key1 & 1;
       const bool first = flags & kFirst;
+      const int tokens = TOGETHER ? (flags >> kTokensShift) + 1 : 1;
+      if constexpr (TOGETHER) {
+        in0 = in0 ? 0xffu : 0u, in1 = in1 ? 0xffu : 0u;
+        if (flags & kEdge) {
+          in0 = in1 = 0;
+#pragma unroll
+          for (int g = 0; g < kOwn / 8; ++g) {
+            const uint64_t seen = sm.ring[slot].seen[token_of(own + 8 * g)];
+            in0 |= static_cast<unsigned>(seen >> key0 & 1) << g, in1 |= static_cast<unsigned>(seen >> key1 & 1) << g;
+          }
+          warp_wait(&sm.k_full[buf][1], (i / 2) & 1);
+          in0 |= sm.poison[buf][key0] << 16, in1 |= sm.poison[buf][key1] << 16;
+        }
+        if (first) {
+          fresh_tokens = ~0u, absent = 0;
+#pragma unroll
+          for (int g = 0; g < kOwn / 8; ++g)
+            absent |= (is_there(h0 + 8 * g, tokens) ? 0u : 1u << g) | (is_there(h0 + 8 * g + 1, tokens) ? 0u : 0x100u << g);
+        }
+      }
+      auto is_in = [](unsigned in, int g) { return TOGETHER ? (in >> g & 1) != 0 : in != 0; };
       const uint32_t s_at = tmem + lanes + kTmemS + buf * kGroup;
       if (first) {
         fresh = zero = true;
@@ -851,7 +996,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       float2 sums[kOwn / 8];
       for (bool again = false;; again = true) {
         bool off = false;
-        const bool any = fresh && __any_sync(0xffffffffu, in0 || in1);  // else no entry here speaks for a head
+        bool any = fresh && __any_sync(0xffffffffu, in0 || in1);  // else no entry here speaks for a head
         const uint32_t p_at = smem_addr(sm.p[buf]) + key0 * 128 + 4 * (lane & 3);
         const uint32_t swz = static_cast<uint32_t>(key0 & 7) << 4;  // key1 & 7 is the same
         // The sums of a thread's two weights stand for the higher of the two in these checks.
@@ -874,15 +1019,23 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
               t0 = make_float2(__fsub_rn(t0.x, ref.x), __fsub_rn(t0.y, ref.y));
               t1 = make_float2(__fsub_rn(t1.x, ref.x), __fsub_rn(t1.y, ref.y));
             }
-            if (!in0) t0 = make_float2(-INFINITY, -INFINITY);
-            if (!in1) t1 = make_float2(-INFINITY, -INFINITY);
+            if constexpr (TOGETHER) {
+              any = (fresh_tokens >> token_of(own + 8 * g) & 1) && __any_sync(0xffffffffu, is_in(in0, g) || is_in(in1, g));
+              if (in0 >> 16) t0 = make_float2(NAN, NAN);
+              if (in1 >> 16) t1 = make_float2(NAN, NAN);
+            }
+            if (!is_in(in0, g)) t0 = make_float2(-INFINITY, -INFINITY);
+            if (!is_in(in1, g)) t1 = make_float2(-INFINITY, -INFINITY);
             const float2 e0 = make_float2(ex2_approx(t0.x), ex2_approx(t0.y));
             const float2 e1 = make_float2(ex2_approx(t1.x), ex2_approx(t1.y));
             sums[g] = add2(e0, e1);
             packed[2 * g] = pack_bf16x2(e0.x, e0.y);
             packed[2 * g + 1] = pack_bf16x2(e1.x, e1.y);
             float2 s = sums[g];
-            if (heads < own + kOwn) {  // absent heads pass any check
+            if (TOGETHER) {  // absent heads pass any check
+              if (absent >> g & 1) s.x = 1.f;
+              if (absent >> (8 + g) & 1) s.y = 1.f;
+            } else if (heads < own + kOwn) {
               if (h0 + 8 * g >= heads) s.x = 1.f;
               if (h0 + 8 * g + 1 >= heads) s.y = 1.f;
             }
@@ -919,8 +1072,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           for (int g = 0; g < kOwn / 8; ++g) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float top = fmaxf(in0 ? __fmul_rn(__uint_as_float(x[4 * g + c]), c2) : -INFINITY,
-                                in1 ? __fmul_rn(__uint_as_float(x[4 * g + 2 + c]), c2) : -INFINITY);
+              float top = fmaxf(is_in(in0, g) ? __fmul_rn(__uint_as_float(x[4 * g + c]), c2) : -INFINITY,
+                                is_in(in1, g) ? __fmul_rn(__uint_as_float(x[4 * g + 2 + c]), c2) : -INFINITY);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
               if (lane < 4) sm.by_warp[w][h0 + 8 * g + c] = top;
@@ -936,8 +1089,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           const float top = fmaxf(fmaxf(sm.by_warp[0][h], sm.by_warp[1][h]), fmaxf(sm.by_warp[2][h], sm.by_warp[3][h]));
           const float was = zero ? 0.f : sm.ref[h];
           // without an entry so far sums and O are 0; a head of which all scores are -inf keeps its reference
-          to[a] = top == -INFINITY ? was : fresh ? top : fmaxf(top, was);
-          f[a] = fresh ? 1.f : ex2_approx(was - to[a]);
+          const bool none_yet = TOGETHER ? (fresh_tokens >> token_of(h) & 1) != 0 : fresh;
+          to[a] = top == -INFINITY ? was : none_yet ? top : fmaxf(top, was);
+          f[a] = none_yet ? 1.f : ex2_approx(was - to[a]);
         }
         soft_sync();  // all have read the old ones
         if (lead && w == 0) {
@@ -972,6 +1126,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         zero = fresh = false;
       }
       fresh = fresh && mask == 0;
+      if constexpr (TOGETHER) {
+        if (fresh_tokens != 0 && mask != 0) {
+          if (flags & kEdge) {
+#pragma unroll
+            for (int k = 0; k < kMostTogether; ++k)
+              if (sm.ring[slot].seen[k] != 0) fresh_tokens &= ~(1u << k);
+          } else {
+            fresh_tokens = 0;
+          }
+        }
+      }
 #pragma unroll
       for (int g = 0; g < kOwn / 8; ++g) l[g] = add2(l[g], sums[g]);  // of absent heads: unused
       const int request = sm.ring[slot].request, part = sm.ring[slot].part;
@@ -999,9 +1164,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       // lse, while the last product runs, and what the entries have of all weight (the sink's too) into `inv`: the
       // stretch before the last, which had this one, is stored, since the last one's O was done when these warps stored it
       const int stretch = flags >> kRunShift, odd = stretch & 1;
-      if (lead && w < 2 && 32 * w + lane < heads) {
+      if (lead && w < 2 && is_there(32 * w + lane, tokens)) {
         const int h = 32 * w + lane;
-        const int64_t head = group0 + h;
+        const int64_t head = group0 + head_of(h);
         const float own = (sm.by_warp[0][h] + sm.by_warp[1][h]) + (sm.by_warp[2][h] + sm.by_warp[3][h]), ref = zero ? 0.f : sm.ref[h];
         float sum = own, to = ref, share = own == 0.f ? 0.f : 1.f;
         if (whole && p.sink != nullptr) {  // one more score, with a value of zero
@@ -1017,11 +1182,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         if (!*abort_flag) {
           if (!whole)
             reinterpret_cast<float*>(p.workspace + sm.lay.lse_at())[sm.lay.row(part, sm.group, h)] = lse2;
-          else if (p.lse != nullptr && part != kSkipped)
-            p.lse[request * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
+          else if (p.lse != nullptr && (!WINDOW || part != kSkipped))
+            p.lse[(request + token_of(h)) * p.lse_stride_r + head * p.lse_stride_h] = lse2 * 0.69314718055994531f;
         }
       }
-      if (lead && w == 0 && lane == 0) sm.done_request[odd] = request, sm.done_part[odd] = part;
+      if (lead && w == 0 && lane == 0) {
+        sm.done_request[odd] = request, sm.done_part[odd] = part;
+        if constexpr (TOGETHER) sm.done_tokens[odd] = tokens;
+      }
       warp_wait(&sm.k_free[buf][kQuarters - 1], (i / 2) & 1);
       if (lead && w < 2 && 32 * w < heads16) {
         tmem_fence_after();
@@ -1036,17 +1204,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           }
         }
         __syncwarp();
-        if (32 * w + lane < heads && sm.inv[odd][32 * w + lane] != 0.f) sm.inv[odd][32 * w + lane] /= sm.sums[32 * w + lane];
+        if (is_there(32 * w + lane, tokens) && sm.inv[odd][32 * w + lane] != 0.f) sm.inv[odd][32 * w + lane] /= sm.sums[32 * w + lane];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.inv_full[odd]);
       warp_wait(&sm.inv_full[odd], stretch >> 1 & 1);
-      if (!*abort_flag) store_results(sm, p, heads, lead ? 0 : 1, odd);
+      if (!*abort_flag) store_results<MODE>(sm, p, heads, lead ? 0 : 1, odd);
     }
   }
   tmem_fence_before();
   __syncthreads();
-  if (*abort_flag) give_up(sm, p.workspace, p.heads, p.err);
+  if (*abort_flag) give_up(sm, p.workspace, p.err);
   if (warp == kMmaWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
@@ -1070,12 +1238,11 @@ __device__ __forceinline__ float4 ld16_if(bool p, const float* from) {
   return v;
 }
 
-// Heads head .. head + 3, columns 32 * block .. of BLOCKS blocks.
+// Heads head .. head + 3 (of rows of a run's token: `h` the first row), columns 32 * block .. of BLOCKS blocks.
 template <int BLOCKS>
-__device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout& lay, const Task t, int head, int block) {
+__device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout& lay, const Task t, int token, int head, int group, int h, int block) {
   constexpr int kFlight = 16 / BLOCKS;  // parts whose values are on their way at once
   const int lane = threadIdx.x & 31;
-  const int size = t.group_heads >> 5, group = head >> (4 + size), h = head & (t.group_heads - 1);
   // (at most 2 * 1024 * 64 rows of 512 floats: in 32 bits)
   const int first = ((2 * t.column + 1) * lay.groups + group) * lay.heads, step = 2 * lay.groups * lay.heads;
   auto row = [&](int k) { return first + k * step - (k > 0 ? lay.groups * lay.heads : 0); };  // slots 2c + 1, 2c + 2, 2c + 4, ...
@@ -1140,7 +1307,7 @@ __device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout
     const float f = __shfl_sync(0xffffffffu, inv, e);
     if (head + e >= p.heads) break;
     if (gone >> e & 1) continue;
-    const int64_t at = t.request * p.out_stride_r + (head + e) * p.out_stride_h + 32 * block + lane;
+    const int64_t at = static_cast<int64_t>(token) * p.out_stride_r + (head + e) * p.out_stride_h + 32 * block + lane;
 #pragma unroll
     for (int b = 0; b < BLOCKS; ++b) {
       const float x = acc[b][e] * f;
@@ -1149,10 +1316,11 @@ __device__ __forceinline__ void join_columns(const DecodeParams& p, const Layout
     }
   }
   if (p.lse != nullptr && block == 0 && lane < 4 && real && !(gone >> lane & 1))
-    p.lse[t.request * p.lse_stride_r + (head + lane) * p.lse_stride_h] =
+    p.lse[static_cast<int64_t>(token) * p.lse_stride_r + (head + lane) * p.lse_stride_h] =
         sum == 0.f ? -INFINITY : (shift + log2f(sum)) * 0.69314718055994531f;
 }
 
+template <bool TOGETHER>
 __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) join_kernel(const DecodeParams p, const __grid_constant__ Layouts layouts) {
   launch_dependents();
   grid_dependency_wait();
@@ -1183,7 +1351,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) join_kernel(const De
     if (lane >= o) behind += u;
   }
   const int count = __shfl_sync(0xffffffffu, behind, 31), before = behind - __popc(votes);
-  const int heads4 = (p.heads + 3) / 4;
+  const int heads4 = TOGETHER ? kGroup / 4 : (p.heads + 3) / 4;
   const int warps = gridDim.x * (kJoinThreads / 32);
   // Few: a warp for each 32 columns. Many: 128 columns, so that with the few parts of each there is enough on
   // its way, and a request's statistics are made less often.
@@ -1199,9 +1367,17 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) join_kernel(const De
     const int rank = n - __shfl_sync(0xffffffffu, before, word);
     const int bit = __ffs(__ballot_sync(0xffffffffu, (bits >> lane & 1) && __popc(bits & ((1u << lane) - 1)) == rank)) - 1;
     const Task t = tasks[32 * word + bit];
-    const Layout& lay = layouts.of[t.group_heads >> 5];  // 16, 32, 64 -> 0, 1, 2
-    if (many) join_columns<4>(p, lay, t, 4 * head4, 4 * block);
-    else join_columns<1>(p, lay, t, 4 * head4, block);
+    const int size = TOGETHER ? 2 : t.group_heads >> 5;  // 16, 32, 64 -> 0, 1, 2
+    const Layout& lay = layouts.of[size];
+    int token = t.request, head = 4 * head4, group = 0, h = head;
+    if constexpr (TOGETHER) {
+      token += h / kTokenRows, head = h % kTokenRows;
+      if (h / kTokenRows >= t.group_heads || head >= p.heads) continue;
+    } else {
+      group = head >> (4 + size), h = head & (t.group_heads - 1);
+    }
+    if (many) join_columns<4>(p, lay, t, token, head, group, h, 4 * block);
+    else join_columns<1>(p, lay, t, token, head, group, h, block);
   }
 }
 
@@ -1228,34 +1404,48 @@ bool encode_query_map(const DecodeParams& p, CUtensorMap* map) {
 namespace {
 // The kernel for caches whose records start on 16 or 8 bytes, and for all heads in one group of 16 or
 // 32 (which frees registers) or in groups of up to 64.
-template <bool WINDOW>
+template <int MODE>
 const void* decode_kernel_for(bool align16, int heads) {
-  if (heads <= 16) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 16, WINDOW> : decode_kernel<false, 16, WINDOW>);
-  if (heads <= 32) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 32, WINDOW> : decode_kernel<false, 32, WINDOW>);
-  return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 64, WINDOW> : decode_kernel<false, 64, WINDOW>);
+  if constexpr (MODE != kTogether) {
+    if (heads <= 16) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 16, MODE> : decode_kernel<false, 16, MODE>);
+    if (heads <= 32) return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 32, MODE> : decode_kernel<false, 32, MODE>);
+  }
+  return reinterpret_cast<const void*>(align16 ? decode_kernel<true, 64, MODE> : decode_kernel<false, 64, MODE>);
 }
-const void* decode_kernel_for(bool align16, int heads, bool window) {
-  return window ? decode_kernel_for<true>(align16, heads) : decode_kernel_for<false>(align16, heads);
+const void* decode_kernel_for(int mode, bool align16, int heads) {
+  return mode == kDecode ? decode_kernel_for<kDecode>(align16, heads)
+         : mode == kWindow ? decode_kernel_for<kWindow>(align16, heads) : decode_kernel_for<kTogether>(align16, heads);
 }
 }  // namespace
 
 cudaError_t prepare_decode() {
   cudaError_t e = cudaSuccess;
-  for (int heads = 16; heads <= 64; heads *= 2)
-    for (int variant = 0; variant < 4; ++variant)
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel_for((variant & 1) != 0, heads, (variant & 2) != 0),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kDecodeSmemBytes);
+  for (int mode = kDecode; mode <= kTogether; ++mode)
+    for (int heads = 16; heads <= 64; heads *= 2)
+      for (int align16 = 0; align16 < 2; ++align16)
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(decode_kernel_for(mode, align16 != 0, heads), cudaFuncAttributeMaxDynamicSharedMemorySize, kDecodeSmemBytes);
   return e;
 }
 
-int64_t decode_workspace_bytes(int heads, int sm_count) { return Layout(heads, sm_count, kGroup).bytes(); }
+// (of few heads: room for the rows of a run of tokens)
+int64_t decode_workspace_bytes(int heads, int sm_count) { return Layout(heads <= kTokenRows ? kGroup : heads, sm_count, kGroup).bytes(); }
 
 cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stream) {
   CUtensorMap map;
   if (!encode_query_map(p, &map)) return cudaErrorInvalidValue;
   Layouts layouts;
   for (int i = 0; i < 3; ++i) layouts.of[i] = Layout(p.heads, sm_count, 16 << i);
+  // Runs of tokens where there are three to a row of the table or more, so that many follow one another, and nine tiles to an SM:
+  // a tile of 64 rows takes a fifth longer than one of 16, and a part of a result is four times as long to store and join. (16
+  // heads, a window of 4,096 and four first entries, 4 tokens of each of 64 requests 83.3 us, one token after the other 175.1;
+  // of 16: 39.3 and 55.1; of 6, 1,560 tiles: 26.0 and 28.7; of 4, 1,040 tiles: 27.6 and 25.0. 3 tokens of each of 16, of which
+  // the multiples of four cut some: 43.7 and 46.5. A window of 300, 4 of each of 100: 31.2 and 34.3; of 30: 21.1 and 16.2. 1 token
+  // of each of 16 requests, of which there are no runs, takes 35.8 in tiles of 64 rows and 27.7 in tiles of 16.)
+  const int64_t seen = p.window + p.first < p.most ? p.window + p.first : p.most;
+  const bool runs = p.heads <= kTokenRows && p.requests >= 3 * p.table_rows && p.requests * (seen / kTile + 1) >= 9ll * sm_count;
+  const int mode = p.kv_lens != nullptr ? kDecode : runs ? kTogether : kWindow;
+  if (mode == kTogether) layouts.of[2] = Layout(kGroup, sm_count, kGroup);
   const int ctas = layouts.of[2].ctas;
   if (ctas > kMaxCtas) return cudaErrorInvalidValue;
   const bool align16 = p.kc_stride0 % 16 == 0;  // records then start on 16 bytes, else on 8
@@ -1270,14 +1460,15 @@ cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stre
   lc.attrs = attr;
   lc.numAttrs = 1;
   void* args[] = {const_cast<DecodeParams*>(&p), &map, &layouts};
-  const cudaError_t e = cudaLaunchKernelExC(&lc, decode_kernel_for(align16, p.heads, p.kv_lens == nullptr), args);
+  const cudaError_t e = cudaLaunchKernelExC(&lc, decode_kernel_for(mode, align16, p.heads), args);
   if (e != cudaSuccess) return e;
   const int64_t cut = p.requests < ctas ? p.requests : ctas;  // requests that can be cut
-  const int64_t join_ctas = (cut * ((p.heads + 3) / 4) * 16 + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  const int heads4 = mode == kTogether ? kGroup / 4 : (p.heads + 3) / 4;
+  const int64_t join_ctas = (cut * heads4 * 16 + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
   lc.gridDim = dim3(static_cast<unsigned>(join_ctas < kJoinPerSm * sm_count ? join_ctas : kJoinPerSm * sm_count));
   lc.blockDim = dim3(kJoinThreads);
   lc.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&lc, join_kernel, p, layouts);
+  return cudaLaunchKernelEx(&lc, mode == kTogether ? join_kernel<true> : join_kernel<false>, p, layouts);
 }
 
 }  // namespace c128

@@ -71,6 +71,8 @@ class Case:
             k = np.stack([self.keys[r, j] for j in at]) if at else np.zeros((0, 512))
             k = k[~np.isnan(k).any(1)]  # (pages that are not there)
             want, l, tol, ltol = sref.attention(self.q[t].double().numpy(), k, self.scale, sink, half)
+            # fp32 has no weight below 2^-126, and neither type a result: each such is 0, off by less than 2^-126 of its entry
+            tol = tol + 2.0 ** -126 * (1 + np.abs(k).sum(0))
             assert (np.abs(out[t] - want) <= tol).all(), (t, np.max(np.abs(out[t] - want) / np.maximum(tol, 1e-300)))
             fine = np.isfinite(l)
             assert (np.abs(lse[t] - l)[fine] <= ltol[fine]).all() and (lse[t][~fine] == l[~fine]).all(), t
@@ -302,3 +304,124 @@ def test_the_last_positions_of_32_bits(window, first):
     out, lse = c.run()
     assert binding.device_errors() == 2  # a position behind the table
     c.check(out, lse)
+
+
+def drafts(begins, counts):
+    """Some consecutive tokens of each request."""
+    return [(r, p) for r, (b, n) in enumerate(zip(begins, counts)) for p in range(b, b + n)]
+
+
+# Long windows of few heads, where tokens that follow one another are taken together. (That is done where there is work enough
+# for the whole GPU and three tokens to a row of the table, so one more request has a long prompt.)
+RUNS = {
+    "four_each": dict(tokens=drafts([1000, 3, 700, 150, 0, 436], [4] * 6), lens=[1004, 7, 704, 154, 4, 440], H=16, window=300, first=4, block=16),
+    "no_first": dict(tokens=drafts([2000, 511], [4, 4]), lens=[2004, 515], H=16, window=1024, first=0, block=64, sink=True),
+    "uneven": dict(tokens=drafts([90, 801, 402, 300, 222, 10], [3, 1, 5, 9, 2, 6]), lens=[93, 802, 407, 309, 224, 16], H=13, window=201, first=3,
+                   block=2, sink=True),
+    "wide_blocks": dict(tokens=drafts([600, 601, 60], [7, 8, 8]), lens=[607, 609, 68], H=12, window=333, first=0, block=67, width=592),
+    "many_first": dict(tokens=drafts([600, 199, 250], [7, 8, 4]), lens=[607, 207, 254], H=5, window=137, first=200, block=16),
+    "one_head": dict(tokens=drafts([100, 900], [40, 41]), lens=[140, 941], H=1, window=450, first=1, block=64),
+    "skipped": dict(tokens=drafts([500, 700], [12, 12]), lens=[512, 712], H=16, window=190, first=2, block=8, skip=[0, 5, 6, 11, 12, 23]),
+    "apart": dict(tokens=[(r, 300 + 7 * r) for r in range(12)] + drafts([50], [8]), lens=[301 + 7 * r for r in range(12)], H=16, window=160,
+                  first=4, block=16),
+    "one_long": dict(tokens=drafts([5000], [4]), lens=[5004], H=8, window=4096, first=4, block=16, sink=True),
+    "twice": dict(tokens=drafts([400], [4]) + drafts([400], [4]) + [(0, 402)] * 3, lens=[404], H=16, window=150, first=0, block=16),
+}
+
+
+def with_a_prompt(tokens, lens, window, first, **rest):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n = -(-9 * sms // (min(window + first, max(lens)) // 64 + 1))
+    return dict(tokens=tokens + consecutive(len(lens), 0, n), lens=lens + [n], window=window, first=first, **rest)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("name", RUNS)
+def test_runs_of_tokens(name, kind):
+    c = Case(len(name) + 100, **with_a_prompt(**RUNS[name]))
+    n = len(RUNS[name]["tokens"])
+    c.check(*c.run(kind), tokens=[*range(n), *range(n, len(c.tokens), 19)])
+    assert binding.device_errors() == 0
+
+
+@pytest.mark.parametrize("H", [16, 3])
+def test_runs_with_entries_that_are_not_finite(H):
+    """Entries that some tokens of a run see and others do not: at either end of the window, and the tokens' own."""
+    tokens = drafts([400, 300, 500], [8, 8, 8])
+    c = Case(43, **with_a_prompt(tokens, [408, 308, 508], 200, 2, H=H, block=8, rubbish=False))
+    flat = c.cache.reshape(c.cache.shape[0], -1)
+
+    def entry(r, j):
+        page, off = c.table[r, j // 8], j % 8
+        return flat[page, off * 576:off * 576 + 576], flat[page, 8 * 576 + off * 8:8 * 576 + off * 8 + 8]
+
+    bad_entries = [(0, 403), (1, 102), (2, 504), (2, 303)]
+    entry(0, 403)[0][100] = 0xff
+    entry(1, 102)[0][448:].view(np.uint16)[5] = 0x7f80
+    entry(2, 504)[1][3] = 255
+    entry(2, 303)[0][448:].view(np.uint16)[63] = 0xffc0
+    out, lse = c.run()
+    bad = torch.tensor([any((r, j) in bad_entries for j in ref.seen(p, 200, 2, 1 << 20)) for r, p in tokens], device="cuda")
+    assert 0 < bad.sum() < len(tokens)
+    assert torch.isnan(out[:24][bad].float()).all() and torch.isnan(lse[:24][bad]).all()
+    c.check(out, lse, tokens=[t for t in range(len(tokens)) if not bad[t]] + [30, 99, len(c.tokens) - 1])
+
+
+@pytest.mark.parametrize("factor", [1.0, 30.0, -2000.0])
+def test_runs_whose_first_entries_are_not_there(factor):
+    """Pages that are not there, so that of a run's first tile the last token sees nothing, and the first tokens an entry each."""
+    tokens = drafts([500, 800], [4, 4])
+    c = Case(44, **with_a_prompt(tokens, [504, 804], 200, 0, H=16, block=1, rubbish=False))
+    c.q = (c.q.float() * factor).bfloat16()
+    c.table[0, 304:430] = -1
+    c.table[1, 601:660] = c.cache.shape[0] + 5
+    out, lse = c.run()
+    assert binding.device_errors() == 4
+    c.check(out, lse, tokens=range(30))
+
+
+@pytest.mark.parametrize("H", [16, 7])
+def test_runs_and_large_entries_that_are_not_seen(H):
+    """Entries so large that a score with them has no room, seen by some tokens of a run: the others are not touched."""
+    tokens = drafts([400, 600], [8, 8])
+    c = Case(45, **with_a_prompt(tokens, [408, 608], 180, 2, H=H, block=8, rubbish=False))
+    flat = c.cache.reshape(c.cache.shape[0], -1)
+    large = [(0, 402), (0, 226), (1, 605), (1, 422)]
+    for r, j in large:
+        page, off = c.table[r, j // 8], j % 8
+        flat[page, 8 * 576 + off * 8:8 * 576 + off * 8 + 7] = 246  # 2^119
+        flat[page, off * 576:off * 576 + 448] = 0x7e               # 448
+    c.q[:] = c.q.abs()
+    out, lse = c.run()
+    c.check(out, lse, tokens=[t for t, (r, p) in enumerate(tokens) if not any((r, j) in large for j in ref.seen(p, 180, 2, 1 << 20))])
+
+
+def test_runs_with_strides_from_a_graph_and_scores_of_any_size():
+    tokens = drafts([400, 600, 17], [8, 7, 9])
+    for factor in (1.0, 40.0):
+        c = Case(46, **with_a_prompt(tokens, [408, 607, 26], 180, 2, H=10, block=16, sink=True))
+        c.q = (c.q.float() * factor).bfloat16()
+        T = len(c.tokens)
+        q = torch.zeros(10, T + 4, 520, dtype=torch.bfloat16, device="cuda")[:, 3:T + 3, 8:].transpose(0, 1).copy_(c.q)
+        out = torch.full((T, 11, 520), 3.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((10, T), 7.0, device="cuda")
+        c.run(out=out[:, 1:, :512], lse=lse.t(), q=q)
+        c.check(out[:, 1:, :512], lse.t(), tokens=[*range(24), *range(24, T, 29)])
+        assert (out[:, 0] == 3).all() and (out[:, :, 512:] == 3).all()
+        dev = [torch.from_numpy(a).cuda() for a in (c.cache, c.table, c.req, c.pos, c.slots)]
+        out2, sink = torch.zeros(T, 10, 512, dtype=torch.bfloat16, device="cuda"), c.sink.cuda()
+        ws = torch.empty(binding.decode_attention_workspace(10), dtype=torch.uint8, device="cuda")
+        s = torch.cuda.Stream()
+        binding.reserve_workspace(1, s)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                binding.window_attention(q, dev[0], c.block, *dev[1:], c.window, c.scale, out2, first=c.first, sink=sink, workspace=ws)
+        for _ in range(2):
+            ws.fill_(255)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out2, out[:, 1:, :512])
+        binding.release_stream(s)
