@@ -408,6 +408,8 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     if (lane == 0) mbar_arrive(&sm.ring_free[i % kRing]);
   };
 
+  int last = -1;  // the last item, of which the softmax warps, which are done by then, store half of the results
+
   if (warp == kItemWarp) {
     // --------------------------------------------------------------------------------- the items
     const unsigned share = static_cast<unsigned>(p.requests) / static_cast<unsigned>(plan.columns);  // tokens of a column, the first `extra` one more
@@ -536,8 +538,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
   } else if (warp == kDecodeWarp || (warp >= kSoftWarps && warp < kMmaWarp)) {
     // ------------------------------------------------------------------- entries and results
     const int w = warp & 3, own = 32 * ((warp >> 2) & 1);  // of results: TMEM lanes 32w .., rows own .. own + 31
+    const bool decodes = warp == kDecodeWarp;
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
-    const bool busy = own < rows16, decodes = warp == kDecodeWarp;
+    const bool busy = own < rows16;
     const OutRows<OUT_F32> to(p, plan, head0, own, w, lane);
     auto results = [&](int i) {
       const Item& it = sm.ring[i % kRing];
@@ -573,8 +576,13 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         if (lane == 0) mbar_arrive(decodes ? &sm.k_full[i % kRing] : &sm.k_help);
       }
       if (decodes && !end) free_item(i);
-      if (!decodes && i > 0) results(i - 1);
-      if (end) break;
+      if (end) {
+        last = i - 1;
+        break;
+      }
+      if (!decodes && i > 0) {
+        results(i - 1);
+      }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------------ issue the products
@@ -625,13 +633,13 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         // S of this item before O of the one before, or (serial) behind it
         if (i > 0 && (flags & (kEnd | kSerial)) && !product_o(i - 1, steps)) break;
         if (flags & kEnd) break;
+        if (i > 0 && !wait(&sm.s_free, (i - 1) & 1)) break;
+        if (!wait(&sm.q_full[0], i & 1)) break;
         if (!wait(&sm.k_full[i % kRing], (i / kRing) & 1)) break;
         if (flags & kFresh) {
           if (!wait(&sm.k_help, helped & 1)) break;
           ++helped;
         }
-        if (i > 0 && !wait(&sm.s_free, (i - 1) & 1)) break;
-        if (!wait(&sm.q_full[0], i & 1)) break;
         half_of_s(0, flags & kTail);
         if (!wait(&sm.q_full[1], i & 1)) break;
         half_of_s(1, flags & kTail);
@@ -664,7 +672,10 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     };
     for (int i = 0;; ++i) {
       const int flags = item_flags(i);
-      if (flags & kEnd) break;
+      if (flags & kEnd) {
+        last = i - 1;
+        break;
+      }
       const Item& it = sm.ring[i % kRing];
       const bool tail = (flags & kTail) && w == 0;
       if (flags & kFresh) {
@@ -815,6 +826,23 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
         p.lse[(static_cast<int64_t>(it.token) + my_token) * p.lse_stride_r + (head0 + my_head) * p.lse_stride_h] =
             total == 0.f ? -INFINITY : (base2 + log2f(total)) * 0.69314718055994531f;
       free_item(i);
+    }
+  }
+  if (warp < kMmaWarp && last >= 0) {
+    const int w = warp & 3, own = 32 * ((warp >> 2) & 1);
+    const bool soft = warp < kSoftWarps;  // (these wait for all of O: only of that have they seen every phase)
+    const OutRows<OUT_F32> to(p, plan, head0, own, w, lane);
+    int limit[4];
+    const int64_t row0 = to.item(p, plan, sm.ring[last % kRing], heads, own, lane, limit);
+    if (soft) warp_wait(&sm.o_full[last % kRing], (last / kRing) & 1);
+#pragma unroll 1
+    for (int mt = soft ? 2 : 0, end = mt + 2; mt < end; ++mt) {
+      if (!soft) warp_wait(&sm.o_part[mt], last & 1);
+      tmem_fence_after();
+      uint32_t o[32];
+      tmem_ld_32x32(tmem + (static_cast<uint32_t>(32 * w) << 16) + mt * kRows + own, o);
+      tmem_wait_ld();
+      if (own < rows16 && !*abort_flag) to.store(p, row0 + 128 * mt, limit, Packed<OUT_F32>(o), lane);
     }
   }
   tmem_fence_before();
