@@ -79,6 +79,7 @@ struct WindowPlan {
   int32_t pitch;                // rows of a token: its heads, padded to eights
   int32_t together;             // tokens of an item, at most
   int32_t columns;              // CTAs that share the tokens
+  int32_t stride;               // from a column's token to its next: 1, or all columns (and items of one token)
   int32_t lookahead;            // an item's entries have room beside those of so many items, itself among them
   uint32_t pitch_inv;           // 2^16 / pitch, rounded up
 };
@@ -414,18 +415,19 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     // --------------------------------------------------------------------------------- the items
     const unsigned share = static_cast<unsigned>(p.requests) / static_cast<unsigned>(plan.columns);  // tokens of a column, the first `extra` one more
     const int extra = static_cast<int>(p.requests) - static_cast<int>(share) * plan.columns;
-    const int64_t begin = static_cast<int64_t>(share) * column + min(column, extra), end = begin + share + (column < extra ? 1 : 0);
+    const int64_t begin = plan.stride > 1 ? column : static_cast<int64_t>(share) * column + min(column, extra);
+    const int64_t end = share + (column < extra ? 1 : 0);  // `t` counts the column's tokens up to here
     unsigned int err = 0;
-    int64_t batch = begin;  // lanes hold tokens batch .. batch + 31
+    int64_t batch = 0;  // lanes hold tokens batch .. batch + 31
     int lo = 0, hi = 0, req = 0;
     unsigned live = 0, goes_on = 0;  // tokens that are not skipped; those that follow the one before
     int64_t last_pos = -1;           // of the token before the batch
     int last_req = -1;
     auto load_batch = [&] {
-      const int64_t t = batch + lane;
+      const int64_t t = begin + (batch + lane) * plan.stride;
       int64_t pos = -1;
       bool ok = false;
-      if (t < end) {
+      if (batch + lane < end) {
         pos = p.positions[t];
         req = p.token_req[t];
         ok = pos >= 0 && p.slots[t] >= 0;
@@ -444,10 +446,10 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       last_pos = __shfl_sync(0xffffffffu, pos, 31);
       last_req = __shfl_sync(0xffffffffu, req, 31);
     };
-    if (begin < end) load_batch();
+    if (end > 0) load_batch();
     int base = 0, newest = -1, seen_to = -1;  // the run's
     bool stalled = p.stall && blockIdx.x == 0;
-    int64_t t = begin;
+    int64_t t = 0;
     for (int i = 0; !stalled; ++i) {
       while (t < end) {  // the next token that is not skipped
         if (t - batch >= 32) {
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       const unsigned behind = ~(j < 31 ? goes_on >> (j + 1) : 0u);
       const int count = min(__ffs(behind), plan.together);
       Item it;
-      it.token = static_cast<int>(t);
+      it.token = static_cast<int>(begin + t * plan.stride);
       it.count = count;
       it.row = __shfl_sync(0xffffffffu, req, j);
       const int lo_j = __shfl_sync(0xffffffffu, lo, j);
@@ -900,10 +902,15 @@ cudaError_t launch_window(const DecodeParams& p, int sm_count, cudaStream_t stre
   int64_t together = plan.groups > 1 ? 1 : kRows / plan.pitch;
   if (together > room / 2) together = room / 2 > 0 ? room / 2 : 1;  // (so that entries of one item do not wait for O of the one before)
   if (together > (T + sm_count - 1) / sm_count) together = (T + sm_count - 1) / sm_count;
-  plan.together = static_cast<int32_t>(together);
-  plan.lookahead = room / plan.together < kRing ? room / plan.together : kRing;
   const int64_t most = sm_count / plan.groups > 0 ? sm_count / plan.groups : 1;
   plan.columns = static_cast<int32_t>(T < most ? T : most);
+  // A decode step's tokens, less than two to a row of the table: dealt out in turn, so that a batch padded at its end is shared by
+  // all CTAs (130 requests padded to 256 tokens 13.8 us, in order 21.1). Else in order, for the entries that neighbours share (200
+  // requests of two tokens each, 16 heads, 20.3 us, in turn 27.0).
+  plan.stride = T < 2 * p.table_rows ? plan.columns : 1;
+  if (plan.stride > 1) together = 1;
+  plan.together = static_cast<int32_t>(together);
+  plan.lookahead = room / plan.together < kRing ? room / plan.together : kRing;
   CUtensorMap map;
   if (!encode_query_rows(p, plan, &map)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t lc = {};

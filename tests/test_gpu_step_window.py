@@ -425,3 +425,14 @@ def test_runs_with_strides_from_a_graph_and_scores_of_any_size():
             torch.cuda.synchronize()
             assert torch.equal(out2, out[:, 1:, :512])
         binding.release_stream(s)
+
+
+@pytest.mark.parametrize("H", [64, 16, 3])
+def test_a_decode_batch_padded_at_its_end(H):
+    """More tokens than CTAs, less than two to a request: dealt out in turn."""
+    rng = np.random.default_rng(60)
+    lens = [int(n) for n in rng.integers(1, 300, 330)]
+    tokens = [(r, n - 1) for r, n in enumerate(lens)] + [(5, lens[5] - 1), (5, max(0, lens[5] - 2))] + [(0, 0)] * 180
+    c = Case(61, tokens, lens, H, 40, 3, 1, sink=True, skip=[0, 17, *range(332, 512)])
+    c.check(*c.run())
+    assert binding.device_errors() == 0
