@@ -11,9 +11,9 @@
 // the place of one that no token sees any more. A run (consecutive positions of one request) begins with all that its
 // first item sees; then an item brings an entry for each of its tokens.
 //
-// Measured, device time per call: 5,119 tokens of 64 heads, window 128 and 4 first entries, 152.7 us (as decode attention, token
-// by token, 341 us); 200 requests of one token each, 24.6 us; one token 9.8 us.
-// The least that a run takes is its queries and results, 2 KB a row (100 us of the 152.7); next are the tensor cores, which
+// Measured, device time per call: 5,119 tokens of 64 heads, window 128 and 4 first entries, 155 us (as decode attention, token
+// by token, 341 us); 200 requests of one token each, 24.2 us; one token 9.0 us.
+// The least that a run takes is its queries and results, 2 KB a row (100 us of the 155); next are the tensor cores, which
 // work 3,900 of the 8,900 cycles of an item of 64 rows, and the 16,600 instructions of its warps, half the issue slots. No unit
 // is full: an item's stages wait for one another, over one set of weights and one O, which is what TMEM's 512 columns
 // and shared memory leave room for. So the products of one item cover what lies between those of the next: S of
@@ -29,7 +29,7 @@
 // Roles of the 20 warps (five to a scheduler leave them 96 registers; each wait is bounded):
 //   0..7   softmax, four warps for either half of the rows
 //   8..15  results, four warps for either half of the rows
-//          (and all of these decode entries at the start of a run)
+//          (all of these decode entries at the start of a run, and store the last item's results: one token 9.7 us without that)
 //   16     one thread issues the products
 //   17     makes the items
 //   18     decodes entries

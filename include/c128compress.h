@@ -447,8 +447,8 @@ int c128_debug_stall_decode_attention(const c128_tensor_t* q, const c128_tensor_
                                       const c128_tensor_t* out, const c128_tensor_t* lse,
                                       const c128_tensor_t* workspace, c128_stream_t stream);
 
-/* Bytes of workspace that c128_decode_attention needs on the current device for `num_heads` heads,
- * whatever the requests and their lengths. */
+/* Bytes of workspace that c128_decode_attention and c128_window_attention need on the current device for `num_heads`
+ * heads, whatever the requests and their lengths. */
 int c128_decode_attention_workspace(int64_t num_heads, int64_t* bytes);
 
 /*
