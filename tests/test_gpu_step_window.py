@@ -436,3 +436,46 @@ def test_a_decode_batch_padded_at_its_end(H):
     c = Case(61, tokens, lens, H, 40, 3, 1, sink=True, skip=[0, 17, *range(332, 512)])
     c.check(*c.run())
     assert binding.device_errors() == 0
+
+
+def test_runs_with_queries_that_are_not_finite():
+    """A query with NaN or infinity, in a run: its own row, and no other."""
+    tokens = drafts([400, 600], [8, 8])
+    c = Case(47, **with_a_prompt(tokens, [408, 608], 180, 2, H=9, block=8))
+    clean = c.run()
+    c.check(*clean, tokens=range(16))
+    c.q[2, 5, 100] = float("nan")
+    c.q[13, 0, 500] = float("inf")
+    out, lse = c.run()
+    torch.cuda.synchronize()
+    assert torch.isnan(out[2, 5]).all() and torch.isnan(lse[2, 5])
+    c.q[2, 5, 100] = c.q[13, 0, 500] = 0
+    c.check(out, lse, tokens=[t for t in range(16) if t not in (2, 13)])
+    rest = [h for h in range(9) if h != 5]
+    # (other rows of the two tokens: weights relative to other references, so not bit for bit)
+    assert not torch.isnan(out[2, rest]).any() and not torch.isnan(out[13, 1:]).any()
+
+
+def test_runs_past_the_table_and_of_requests_that_do_not_fit():
+    tokens = drafts([500, 700, 300], [8, 8, 8])
+    c = Case(48, **with_a_prompt(tokens, [508, 708, 308], 190, 3, H=16, block=4, rubbish=False))
+    c.table, c.most = c.table[:, :176].copy(), 704   # the second request's tokens pass 704 within a run
+    c.req[[16, 21]] = -1, len(c.table)
+    c.skip.update((16, 21))
+    c.slots[18] = -1
+    c.skip.add(18)
+    out, lse = c.run()
+    assert binding.device_errors() == 2 | 1
+    c.check(out, lse, tokens=[*range(24), 30, 99])
+
+
+def test_a_run_over_many_tokens_in_every_place_of_four():
+    """Requests of one to nine tokens, so that runs begin and end in every place, with skipped rows between."""
+    rng = np.random.default_rng(62)
+    counts = [int(n) for n in rng.integers(1, 10, 90)]
+    begins = [int(n) for n in rng.integers(0, 400, 90)]
+    tokens = drafts(begins, counts)
+    skip = sorted(rng.choice(len(tokens), 40, replace=False).tolist())
+    c = Case(63, tokens, [b + n for b, n in zip(begins, counts)], 7, 230, 5, 1, sink=True, skip=skip)
+    c.check(*c.run())
+    assert binding.device_errors() == 0
