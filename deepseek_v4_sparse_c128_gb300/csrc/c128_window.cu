@@ -277,12 +277,14 @@ __device__ __forceinline__ void decode_first(const DecodeParams& p, WindowSmem& 
       }
       poison |= not_finite(o);
     }
-    // An entry with a value that is not finite (a code of NaN, a bf16 that is not, a product without room): zeros.
+    // An entry with a value that is not finite (a code of NaN, a bf16 that is not, a product without room): zeros, by each
+    // thread where it has stored itself, since nothing orders its stores and those of another one.
     poison |= __shfl_xor_sync(0xffffffffu, poison, 1);
     poison |= __shfl_xor_sync(0xffffffffu, poison, 2);
     if (in && poison) {
 #pragma unroll 1
-      for (int j = 0; j < 16; ++j) sts16(row + (j >> 1) * kChunkBytes + 32 * sub + 16 * (j & 1), 0, 0, 0, 0);
+      for (int j = 0; j < 16; ++j)
+        sts16(row + (j >> 1) * kChunkBytes + ((j < 14 ? 32u * sub + 16u * (j & 1) : 16u * sub + 64u * (j & 1)) ^ swz), 0, 0, 0, 0);
     }
     if (in && sub == 0) sm.state[place] = data == nullptr ? kAbsent : poison ? kPoison : kThere;
   }
