@@ -707,8 +707,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
           const int pos = place < first ? place : it.last - d;
           const uint8_t state = sm.state[place];
           ahead[k] = it.hi - pos;
-          // it is seen from that many positions on, from its own; 0: there is none
-          reach[k] = state == kAbsent || (place >= first && pos < it.base) ? 0u : place < first ? 0x80000000u : window;
+          // it is seen from that many positions on, from its own; 0: there is none (a token behind the table has first entries up to
+          // the table's end only; what stands in the places of the others, and in `state`, is of no entry)
+          reach[k] = state == kAbsent || (place < first ? place > it.last : pos < it.base) ? 0u : place < first ? 0x80000000u : window;
           plus[k] = state == kPoison ? NAN : 0.f;
         }
         if (plan.together == 1) {
