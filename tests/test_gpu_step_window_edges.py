@@ -1,4 +1,4 @@
-"""c128_window_attention at the end of its table, and with nothing to see."""
+"""c128_window_attention at the end of its table, with nothing to see, and what the rounding of its weights may do."""
 import numpy as np
 import pytest
 import torch
@@ -46,3 +46,28 @@ def test_nothing_to_see_has_the_sink_as_its_lse(sink):
             assert ((lse - c.sink.cuda()).abs() <= 2.0 ** -22 * c.sink.cuda().abs()).all()
         else:
             assert (lse == -np.inf).all()
+
+
+@pytest.mark.parametrize("H", [64, 16, 5])
+@pytest.mark.parametrize("sink", [False, True], ids=["", "sink"])
+@pytest.mark.parametrize("window,first", [(128, 4), (13, 0), (300, 4)])
+def test_columns_that_all_entries_have_in_common(window, first, sink, H):
+    """Columns 0 .. 191 are the same in every entry, so there the result is theirs, whatever the weights of the entries are and
+    however these are rounded: times what the entries have of all weight, where there is a sink. (fp32 sums of at most 2^10 terms,
+    which the tensor cores cut: 2^-23 of them each, 2^-13 at most and 2^-16 in earnest, as in the other tests; the factor of their
+    sums and the sink's share 2^-20.)"""
+    n = 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    c = Case(93, consecutive(0, 5, n), [n + 5], H, window, first, 16, sink=sink, rubbish=False)
+    flat = c.cache.reshape(len(c.cache), -1)
+    for j in range(16):
+        flat[:, j * 576:j * 576 + 192] = flat[0, :192]
+        flat[:, 16 * 576 + 8 * j:16 * 576 + 8 * j + 3] = flat[0, 16 * 576:16 * 576 + 3]
+    common = torch.from_numpy(c.entry(0, 0)[:192]).cuda()
+    out, lse = c.run(torch.float32)
+    assert binding.device_errors() == 0
+    share = torch.ones_like(lse).double() if not sink else 1 - torch.exp(c.sink.cuda().double() - lse.double())
+    want = share[..., None] * common
+    # (lse is off by 2^-16, and so is the sink's share of it)
+    tol = 2.0 ** -16 * want.abs() + (2.0 ** -20 + 2.0 ** -15 * (1 - share[..., None])) * common.abs()
+    assert ((out[..., :192].double() - want).abs() <= tol).all()
+    c.check(out, lse, tokens=range(0, n, 37))
