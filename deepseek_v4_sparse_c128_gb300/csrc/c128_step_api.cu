@@ -49,6 +49,9 @@ int check_weight(const c128_tensor_t* t) {
 
 bool positive(double x) { return x > 0 && std::isfinite(x); }
 
+// Turns per position that a step may have. (In 53 bits, 33 or more of them behind the point; past 2^53 nothing would be left.)
+constexpr double kMostTurns = 0x1p20;
+
 // The steps of c128_rope_t in turns per position, as fractions of 2^64.
 int rope_steps(const c128_rope_t* rope, int turned, uint64_t* step) {
   if (rope == nullptr) return C128_ERR_NULL_PTR;
@@ -74,7 +77,9 @@ int rope_steps(const c128_rope_t* rope, int turned, uint64_t* step) {
       const double g = std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0), 1);
       f = f * (1 - g) + f / rope->factor * g;
     }
-    const double turns = f / kTurn, part = turns - std::floor(turns);
+    const double turns = f / kTurn;
+    if (!(turns <= kMostTurns)) return C128_ERR_ARG;  // NaN too: of an infinite step times a ramp of 0
+    const double part = turns - std::floor(turns);
     const double scaled = std::nearbyint(part * 0x1p64);
     step[i] = scaled >= 0x1p64 ? 0 : static_cast<uint64_t>(scaled);
   }

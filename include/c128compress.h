@@ -486,6 +486,7 @@ int c128_merge_attention(const c128_tensor_t* part_out, const c128_tensor_t* par
  *                     min(ceil(pair(beta_slow)), R - 1), g_i = (i - low) / max(high - low, 0.001) cut
  *                     to [0, 1]
  * `magnitude` multiplies every cosine and sine (YaRN's attention factor; 1 for none).
+ * A step over 2^20 turns per position, which a tiny factor makes, is refused (C128_ERR_ARG).
  */
 enum {
     C128_ROPE_PLAIN = 0,
