@@ -510,9 +510,10 @@ typedef struct c128_rope {
  *   cos_sin_cache [MP, R] fp32  stride[1] == 1, stride[0] >= R; R even, 2 .. 512
  *   first_position        0 <= first_position, first_position + MP <= 2^32
  *
- * Angles are kept as 64-bit fractions of a turn, which whole turns drop out of without rounding, so far
- * positions are as exact as near ones: an angle is within 2^-30 + 2^-48 * (its turns) of position * step,
- * which is the rounding of the steps to 64 bits, and each value within 2^-22 of its own size for that angle.
+ * Angles are kept as 64-bit fractions of a turn, which whole turns drop out of without rounding, so the product
+ * of position and step adds no error. The steps are made in double, and their rounding grows with the position: an
+ * angle is within 2^-30 + 2^-46 * (its turns, scaled or not, whichever are more) of position * step, so 2^-29.3 for
+ * the first pair at position 2^18 and 2^-16.6 at 2^32; and each value is within 2^-22 of its own size for that angle.
  */
 int c128_build_cos_sin(const c128_rope_t* rope, int64_t first_position, const c128_tensor_t* cos_sin_cache,
                        c128_stream_t stream);

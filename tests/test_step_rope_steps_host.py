@@ -5,7 +5,7 @@ import math
 import pytest
 
 from deepseek_v4_sparse_c128_gb300 import binding, build
-from test_abi_host import FAKE, _t
+from test_abi_host import _t
 
 F32 = binding.C128_F32
 ARG, OK = 7, 0
