@@ -50,6 +50,7 @@ EXPORTS = (
     "c128_rotate",
     "c128_norm_rope_store",
     "c128_window_attention",
+    "c128_window_attention_workspace",
     "c128_debug_stall_window_attention",
 )
 
@@ -150,6 +151,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     L.c128_decode_attention_workspace.argtypes = [i64, ctypes.POINTER(i64)]
     L.c128_merge_attention.argtypes = [T, T, T, T, vp]
     L.c128_window_attention.argtypes = [T, T, i64, T, T, T, T, i64, i64, ctypes.c_float, T, T, T, T, vp]
+    L.c128_window_attention_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
     L.c128_debug_stall_window_attention.argtypes = L.c128_window_attention.argtypes
     L.c128_build_cos_sin.argtypes = [ctypes.POINTER(Rope), i64, T, vp]
     L.c128_rotate.argtypes = [T, T, T, i64, i32, i32, T, vp]
@@ -371,21 +373,21 @@ def _build_slot_maps(seq_lens, query_lens, state_table, state_block: int, kv_tab
                                     _whole(compress_ratio, 32, "compress_ratio"), *a[4:]), ()
 
 
-def _scratch(num_heads: int, device, stream):
-    """A workspace of decode_attention out of torch's pool of the stream that will use it: what the pool hands out may still
+def _scratch(size: int, device, stream):
+    """A workspace of that many bytes out of torch's pool of the stream that will use it: what the pool hands out may still
     be in use by calls on its own stream that have not run yet, and goes back to calls on that stream."""
     import torch
     if stream is not None and not hasattr(stream, "cuda_stream"):
         # (torch takes a handle of 0 for none given, and makes a stream of its own)
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     with torch.cuda.stream(stream):  # None: the current stream
-        return torch.empty(decode_attention_workspace(num_heads), dtype=torch.uint8, device=device)
+        return torch.empty(size, dtype=torch.uint8, device=device)
 
 
 def _decode_attention(q, k_cache, kv_block_size: int, block_table, kv_lens, scale: float, out, lse=None, sink=None,
                       workspace=None, stream=None):
     if workspace is None:
-        workspace = _scratch(q.shape[1], q.device, stream)
+        workspace = _scratch(decode_attention_workspace(q.shape[1]), q.device, stream)
     a = _refs(q, k_cache, block_table, kv_lens, sink, out, lse, workspace)
     return "c128_decode_attention", (*a[:2], _whole(kv_block_size, 64, "kv_block_size"), *a[2:4], float(scale),
                                      *a[4:]), (workspace,)
@@ -414,11 +416,18 @@ def _norm_rope_store(positions, slot_mapping, eps: float, cos_sin_cache, q=None,
 
 def _window_attention(q, k_cache, kv_block_size: int, block_table, token_to_req_indices, positions, slot_mapping, window: int,
                       scale: float, out, first: int = 0, lse=None, sink=None, workspace=None, stream=None):
+    window, first = _whole(window, 64, "window"), _whole(first, 64, "first")
+    heads = q.shape[1]
     if workspace is None:
-        workspace = _scratch(q.shape[1], q.device, stream)
+        workspace = _scratch(window_attention_workspace(heads, window, first), q.device, stream)
+    elif heads > 0:
+        # One of decode_attention's size may be too small for tokens to be taken together: the call then takes one of its own.
+        need = window_attention_workspace(heads, window, first)
+        if need > workspace.numel() >= decode_attention_workspace(heads):
+            workspace = _scratch(need, q.device, stream)
     a = _refs(q, k_cache, block_table, token_to_req_indices, positions, slot_mapping, sink, out, lse, workspace)
-    return "c128_window_attention", (*a[:2], _whole(kv_block_size, 64, "kv_block_size"), *a[2:6], _whole(window, 64, "window"),
-                                     _whole(first, 64, "first"), float(scale), *a[6:]), (workspace,)
+    return "c128_window_attention", (*a[:2], _whole(kv_block_size, 64, "kv_block_size"), *a[2:6], window, first, float(scale),
+                                     *a[6:]), (workspace,)
 
 
 _OPS = {"extend_block_tables": _extend_block_tables, "build_slot_maps": _build_slot_maps,
@@ -527,9 +536,17 @@ def window_attention(q, k_cache, kv_block_size: int, block_table, token_to_req_i
                      scale: float, out, first: int = 0, lse=None, sink=None, workspace=None, stream=None) -> None:
     """Attention of each token to the last ``window`` entries of its request up to its own, and the ``first`` ones
     (c128_window_attention in include/c128compress.h); ``out`` and ``lse`` are written. ``workspace`` as for
-    decode_attention."""
+    decode_attention, of window_attention_workspace bytes."""
     PreparedOp("window_attention", q, k_cache, kv_block_size, block_table, token_to_req_indices, positions, slot_mapping, window,
                scale, out, first=first, lse=lse, sink=sink, workspace=workspace, stream=stream)()
+
+
+def window_attention_workspace(num_heads: int, window: int, first: int = 0) -> int:
+    """Bytes of workspace a window_attention call with ``num_heads`` heads takes: 0 where window + first <= 136."""
+    n = ctypes.c_int64(0)
+    _check(lib().c128_window_attention_workspace(_whole(num_heads, 64, "num_heads"), _whole(window, 64, "window"),
+                                                 _whole(first, 64, "first"), ctypes.byref(n)), "c128_window_attention_workspace")
+    return n.value
 
 
 def debug_stall_window_attention(*args, **kw) -> None:

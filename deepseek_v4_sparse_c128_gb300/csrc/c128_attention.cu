@@ -1428,10 +1428,10 @@ cudaError_t prepare_decode() {
   return e;
 }
 
-// (of few heads: room for the rows of a run of tokens)
-int64_t decode_workspace_bytes(int heads, int sm_count) { return Layout(heads <= kTokenRows ? kGroup : heads, sm_count, kGroup).bytes(); }
+int64_t decode_workspace_bytes(int heads, int sm_count) { return Layout(heads, sm_count, kGroup).bytes(); }
+int64_t runs_workspace_bytes(int heads, int sm_count) { return Layout(heads <= kTokenRows ? kGroup : heads, sm_count, kGroup).bytes(); }
 
-cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stream) {
+cudaError_t launch_decode(const DecodeParams& p, int64_t workspace_bytes, int sm_count, cudaStream_t stream) {
   CUtensorMap map;
   if (!encode_query_map(p, &map)) return cudaErrorInvalidValue;
   Layouts layouts;
@@ -1443,7 +1443,9 @@ cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stre
   // the multiples of four cut some: 43.7 and 46.5. A window of 300, 4 of each of 100: 31.2 and 34.3; of 30: 21.1 and 16.2. 1 token
   // of each of 16 requests, of which there are no runs, takes 35.8 in tiles of 64 rows and 27.7 in tiles of 16.)
   const int64_t seen = p.window + p.first < p.most ? p.window + p.first : p.most;
-  const bool runs = p.heads <= kTokenRows && p.requests >= 3 * p.table_rows && p.requests * (seen / kTile + 1) >= 9ll * sm_count;
+  // (And room for their parts, which have 64 rows: a caller may have given what decode attention takes.)
+  const bool runs = p.heads <= kTokenRows && p.requests >= 3 * p.table_rows && p.requests * (seen / kTile + 1) >= 9ll * sm_count &&
+                    workspace_bytes >= runs_workspace_bytes(p.heads, sm_count);
   const int mode = p.kv_lens != nullptr ? kDecode : runs ? kTogether : kWindow;
   if (mode == kTogether) layouts.of[2] = Layout(kGroup, sm_count, kGroup);
   const int ctas = layouts.of[2].ctas;

@@ -85,9 +85,10 @@ struct DecodeParams {
   int32_t stall;                 // test only: CTA 0 never learns of its tiles, and its waits run out
   unsigned int* err;
 };
-cudaError_t launch_decode(const DecodeParams& p, int sm_count, cudaStream_t stream);
+cudaError_t launch_decode(const DecodeParams& p, int64_t workspace_bytes, int sm_count, cudaStream_t stream);
 cudaError_t prepare_decode();  // function attributes, once per device
 int64_t decode_workspace_bytes(int heads, int sm_count);
+int64_t runs_workspace_bytes(int heads, int sm_count);  // where tokens that follow one another may be taken together
 
 struct MergeParams {
   const void* part;

@@ -35,7 +35,7 @@ int decode(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_bloc
   int sms = 0;
   C128_TRY(c128::stream_errors(s, &p.err, &sms));
   if (workspace->shape[0] < c128::decode_workspace_bytes(p.heads, sms)) return C128_ERR_ARG;
-  return done(c128::launch_decode(p, sms, s));
+  return done(c128::launch_decode(p, workspace->shape[0], sms, s));
 }
 
 }  // namespace

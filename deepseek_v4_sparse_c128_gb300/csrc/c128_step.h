@@ -64,7 +64,7 @@ cudaError_t launch_norm(const NormParams& p, int sm_count, cudaStream_t stream);
 
 // c128_window_attention's parameters are DecodeParams (kv_lens NULL). Windows that fit into shared memory have a kernel of
 // their own, which takes no workspace.
-bool window_fits(const DecodeParams& p);
+bool window_fits(int64_t window, int64_t first);
 cudaError_t prepare_window();  // function attributes, once per device
 cudaError_t launch_window(const DecodeParams& p, int sm_count, cudaStream_t stream);
 

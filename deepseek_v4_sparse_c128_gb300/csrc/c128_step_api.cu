@@ -119,8 +119,9 @@ int window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int sms = 0;
   C128_TRY(c128::stream_errors(s, &p.err, &sms));
+  if (c128::window_fits(window, first)) return done(c128::launch_window(p, sms, s));
   if (workspace->shape[0] < c128::decode_workspace_bytes(p.heads, sms)) return C128_ERR_ARG;
-  return done(c128::window_fits(p) ? c128::launch_window(p, sms, s) : c128::launch_decode(p, sms, s));
+  return done(c128::launch_decode(p, workspace->shape[0], sms, s));
 }
 
 }  // namespace
@@ -262,6 +263,20 @@ int c128_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, 
                           const c128_tensor_t* lse, const c128_tensor_t* workspace, c128_stream_t stream) {
   return window_attention(q, k_cache, kv_block_size, block_table, token_to_req_indices, positions, slot_mapping, window, first,
                           scale, sink, out, lse, workspace, stream, false);
+}
+
+int c128_window_attention_workspace(int64_t num_heads, int64_t window, int64_t first, int64_t* bytes) {
+  if (bytes == nullptr) return C128_ERR_NULL_PTR;
+  if (num_heads < 1 || num_heads > c128::kMaxDecodeHeads) return C128_ERR_UNSUPPORTED;
+  if (window < 1 || window > kMaxCount || first < 0 || first > kMaxCount) return C128_ERR_ARG;
+  *bytes = 0;
+  if (c128::window_fits(window, first)) return C128_OK;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return C128_ERR_CUDA;
+  *bytes = c128::runs_workspace_bytes(static_cast<int>(num_heads), sms);
+  return C128_OK;
 }
 
 int c128_debug_stall_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, int64_t kv_block_size,

@@ -916,7 +916,7 @@ bool encode_query_rows(const DecodeParams& p, const WindowPlan& plan, CUtensorMa
 
 }  // namespace
 
-bool window_fits(const DecodeParams& p) { return p.window + p.first <= kSlots; }
+bool window_fits(int64_t window, int64_t first) { return window + first <= kSlots; }
 
 cudaError_t prepare_window() {
   cudaError_t e = cudaSuccess;

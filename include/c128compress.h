@@ -447,8 +447,8 @@ int c128_debug_stall_decode_attention(const c128_tensor_t* q, const c128_tensor_
                                       const c128_tensor_t* out, const c128_tensor_t* lse,
                                       const c128_tensor_t* workspace, c128_stream_t stream);
 
-/* Bytes of workspace that c128_decode_attention and c128_window_attention need on the current device for `num_heads`
- * heads, whatever the requests and their lengths. */
+/* Bytes of workspace that c128_decode_attention needs on the current device for `num_heads` heads, whatever the
+ * requests and their lengths. */
 int c128_decode_attention_workspace(int64_t num_heads, int64_t* bytes);
 
 /*
@@ -602,8 +602,10 @@ int c128_norm_rope_store(const c128_tensor_t* positions, const c128_tensor_t* sl
  *   slot_mapping         [T]           int64  only its sign is used: < 0, the token is skipped
  *   window                             1 <= window < 2^31
  *   first                              0 <= first < 2^31
- *   scale, sink [H], out [T, H, 512], lse [T, H], workspace: as for c128_decode_attention (the workspace is
- *                                      of c128_decode_attention_workspace bytes, whatever the window)
+ *   scale, sink [H], out [T, H, 512], lse [T, H]: as for c128_decode_attention
+ *   workspace            [n]           uint8  c128_window_attention_workspace bytes (0 of a short window: nothing is read or
+ *                                             written), else as for c128_decode_attention. With up to 16 heads fewer
+ *                                             will do, c128_decode_attention_workspace bytes: every token goes alone then
  *
  * The rows of out and lse of skipped tokens are left as they were.
  * Device error bits: C128_DEV_BAD_REQ - token_to_req_indices[t] outside [0, R) (the token is skipped);
@@ -616,6 +618,9 @@ int c128_window_attention(const c128_tensor_t* q, const c128_tensor_t* k_cache, 
                           const c128_tensor_t* positions, const c128_tensor_t* slot_mapping, int64_t window,
                           int64_t first, float scale, const c128_tensor_t* sink, const c128_tensor_t* out,
                           const c128_tensor_t* lse, const c128_tensor_t* workspace, c128_stream_t stream);
+
+/* Bytes of workspace for c128_window_attention on the current device, whatever the tokens: 0 where window + first <= 136. */
+int c128_window_attention_workspace(int64_t num_heads, int64_t window, int64_t first, int64_t* bytes);
 
 /*
  * Test of the failure handling, for tests only: c128_window_attention, except that CTA 0 never learns of its tokens. Its
