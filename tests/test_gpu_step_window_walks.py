@@ -157,3 +157,94 @@ def test_a_run_whose_oldest_entry_is_not_finite(H):
     assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
     assert torch.isfinite(out[~bad].float()).all()
     c.check(out, lse, tokens=[t for t in range(0, len(tokens), 7) if not bad[t]])
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("name", WALKS)
+def test_walk(name, kind):
+    """All tokens of three CTAs, with a sink."""
+    H, window, first, each, begin = WALKS[name]
+    c = Walk(len(name) + 20, H, window, first, each, begin, sink=True)
+    out, lse = c.walk(kind)
+    assert binding.device_errors() == 0
+    c.check_tokens(out, lse, c.of_ctas())
+    # (of the others: that none was left out, and that no weight of 0 met what is not finite)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all() and not (out == 3).all(-1).any() and not (lse == 7).any()
+
+
+@pytest.mark.parametrize("name", ["one_an_item", "two_an_item", "small_ring_five_heads", "no_room_few_heads", "much_room_few_heads", "group_of_37_heads"])
+def test_queries_that_are_not_finite(name):
+    """Their own row, and no other: not the token's other heads, nor the tokens beside it in the item and in the items around it."""
+    H, window, first, each, begin = WALKS[name]
+    c = Walk(len(name) + 40, H, window, first, each, begin)
+    clean = [x.clone() for x in c.walk()]
+    n = len(c.tokens)
+    rows = [(t, (5 * t) % H) for t in range(7, n, 29)]
+    for i, (t, h) in enumerate(rows):
+        c.on_gpu[t, h, (31 * t) % 512] = float("nan") if i % 2 else float("inf")
+    out, lse = c.walk()
+    torch.cuda.synchronize()
+    hit = torch.zeros(n, H, dtype=torch.bool, device="cuda")
+    hit[[t for t, _ in rows], [h for _, h in rows]] = True
+    nan = torch.zeros_like(hit)
+    nan[[t for t, _ in rows[1::2]], [h for _, h in rows[1::2]]] = True
+    assert torch.isnan(out[nan].float()).all() and torch.isnan(lse[nan]).all()
+    assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
+@pytest.mark.parametrize("name", ["one_an_item", "two_an_item", "small_ring_two", "much_room_few_heads"])
+@pytest.mark.parametrize("factor", [30.0, 1e-3, 2000.0])
+def test_scores_of_any_size(name, factor):
+    H, window, first, each, begin = WALKS[name]
+    c = Walk(len(name) + 60, H, window, first, each, begin)
+    c.on_gpu = (c.on_gpu.float() * factor).bfloat16()
+    out, lse = c.walk()
+    c.check_tokens(out, lse, c.of_ctas()[::2])
+
+
+@pytest.mark.parametrize("name", ["one_an_item", "small_ring", "small_ring_two", "much_room_few_heads"])
+def test_entries_of_any_magnitude_that_are_not_seen(name):
+    """Entries so large that a score with them has no room, come and gone: tokens that do not see them are not touched."""
+    H, window, first, each, begin = WALKS[name]
+    c = Walk(len(name) + 80, H, window, first, each, begin)
+    flat, n = c.cache.reshape(len(c.cache), -1), len(c.tokens)
+    sees = torch.zeros(n, dtype=torch.bool)
+    for j in range(max(first, begin) + 3, begin + n, 3 * window + 1):
+        page, off = c.table[0, j // BLOCK], j % BLOCK
+        flat[page, BLOCK * 576 + off * 8:BLOCK * 576 + off * 8 + 7] = 246  # 2^119
+        flat[page, off * 576:off * 576 + 448] = 0x7e                      # 448
+        sees[max(0, j - begin):j - begin + window] = True
+    c.on_gpu = c.on_gpu.abs()
+    out, lse = c.walk()
+    assert 0 < sees.sum() < n
+    assert torch.isfinite(out[~sees.cuda()].float()).all()
+    c.check_tokens(out, lse, [t for t in c.of_ctas() + list(range(0, n, 61)) if not sees[t]])
+
+
+@pytest.mark.parametrize("H,window,first", [(65, 300, 4), (128, 200, 0), (128, 137, 0), (17, 600, 2), (100, 1000, 140)])
+def test_long_windows_of_many_heads(H, window, first):
+    """Some hundred tokens, more than there are CTAs for their head groups; results and their parts of several groups."""
+    tokens = consecutive(0, 150, 170) + consecutive(1, 0, 80) + [(2, 2500), (2, 7), (3, 900)] * 7
+    c = Case(73 + H, tokens, [320, 80, 2501, 901], H, window, first, BLOCK, sink=True, skip=[0, 77, 200])
+    for kind in (torch.bfloat16, torch.float32):
+        out, lse = c.run(kind)
+        assert binding.device_errors() == 0
+        c.check(out, lse, tokens=[0, 77, 200, *range(1, len(tokens), 11), *range(250, len(tokens))])
+
+
+@pytest.mark.parametrize("H", [128, 65, 16, 7])
+def test_prompts_of_several_requests(H):
+    """Prompts and parts of prompts, some tokens skipped, over CTAs of several tokens each; the same rows in another order."""
+    n = 3 * sms()
+    tokens = consecutive(0, 0, n) + consecutive(1, 500, n // 2) + [(2, 60)] + consecutive(3, 131, n // 3 + 1)
+    lens = [n, 500 + n // 2, 61, 132 + n // 3]
+    skip = [0, 1, n - 1, n, n + 40, n + 41, len(tokens) - 1]
+    c = Case(74 + H, tokens, lens, H, 128, 4, 64, sink=True, skip=skip)
+    out, lse = c.run()
+    assert binding.device_errors() == 0
+    c.check(out, lse, tokens=[*skip, *range(2, len(tokens), 23), *range(n - 9, n + 9)])
+    order = np.random.default_rng(75).permutation(len(tokens))
+    c.tokens, c.skip = [c.tokens[t] for t in order], {i for i, t in enumerate(order) if t in c.skip}
+    c.q, c.req, c.pos, c.slots = c.q[order], c.req[order], c.pos[order], c.slots[order]
+    out, lse = c.run()
+    c.check(out, lse, tokens=[*sorted(c.skip), *range(0, len(tokens), 29)])
