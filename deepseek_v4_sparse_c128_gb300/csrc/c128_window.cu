@@ -83,7 +83,7 @@ struct WindowPlan {
   int32_t pitch;                // rows of a token: its heads, padded to eights
   int32_t together;             // tokens of an item, at most
   int32_t columns;              // CTAs that share the tokens
-  int32_t stride;               // from a column's token to its next: 1, or all columns (and items of one token)
+  int32_t stride;               // from a column's token to its next: 1, or (items of one token) 0, 1 or all columns as the tokens show
   int32_t lookahead;            // an item's entries have room beside those of so many items, itself among them
   uint32_t pitch_inv;           // 2^16 / pitch, rounded up
 };
@@ -427,7 +427,9 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     // --------------------------------------------------------------------------------- the items
     const unsigned share = static_cast<unsigned>(p.requests) / static_cast<unsigned>(plan.columns);  // tokens of a column, the first `extra` one more
     const int extra = static_cast<int>(p.requests) - static_cast<int>(share) * plan.columns;
-    const int64_t begin = plan.stride > 1 ? column : static_cast<int64_t>(share) * column + min(column, extra);
+    const int64_t in_order = static_cast<int64_t>(share) * column + min(column, extra);
+    int stride = plan.stride;
+    int64_t begin = in_order;
     const int64_t end = share + (column < extra ? 1 : 0);  // `t` counts the column's tokens up to here
     unsigned int err = 0;
     int64_t batch = 0;  // lanes hold tokens batch .. batch + 31
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
     int64_t last_pos = -1;           // of the token before the batch
     int last_req = -1;
     auto load_batch = [&] {
-      const int64_t t = begin + (batch + lane) * plan.stride;
+      const int64_t t = begin + (batch + lane) * stride;
       int64_t pos = -1;
       bool ok = false;
       if (batch + lane < end) {
@@ -458,7 +460,22 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       last_pos = __shfl_sync(0xffffffffu, pos, 31);
       last_req = __shfl_sync(0xffffffffu, req, 31);
     };
-    if (end > 0) load_batch();
+    if (stride == 0) {
+      // Some tokens and those behind them, the same for all CTAs: where most follow one another they go in order, else in turn
+      // (as which this CTA's are on their way meanwhile).
+      const int64_t t = (p.requests - 1) * lane / 32;
+      const int64_t pos0 = p.positions[t], pos1 = p.positions[t + 1], slot0 = p.slots[t], slot1 = p.slots[t + 1];
+      const int req0 = p.token_req[t], req1 = p.token_req[t + 1];
+      stride = plan.columns, begin = column;
+      load_batch();
+      const bool live0 = pos0 >= 0 && slot0 >= 0, follows = live0 && slot1 >= 0 && pos1 == pos0 + 1 && req1 == req0;
+      if (2 * __popc(__ballot_sync(0xffffffffu, follows)) > __popc(__ballot_sync(0xffffffffu, live0))) {
+        stride = 1, begin = in_order, last_pos = -1, last_req = -1;
+        load_batch();
+      }
+    } else if (end > 0) {
+      load_batch();
+    }
     int base = 0, newest = -1, seen_to = -1;  // the run's
     bool stalled = p.stall && blockIdx.x == 0;
     int64_t t = 0;
@@ -488,7 +505,7 @@ __global__ void __launch_bounds__(kWindowThreads, 1)
       const unsigned behind = ~(j < 31 ? goes_on >> (j + 1) : 0u);
       const int count = min(__ffs(behind), plan.together);
       Item it;
-      it.token = static_cast<int>(begin + t * plan.stride);
+      it.token = static_cast<int>(begin + t * stride);
       it.count = count;
       it.row = __shfl_sync(0xffffffffu, req, j);
       const int lo_j = __shfl_sync(0xffffffffu, lo, j);
@@ -943,11 +960,13 @@ cudaError_t launch_window(const DecodeParams& p, int sm_count, cudaStream_t stre
   if (together > (T + sm_count - 1) / sm_count) together = (T + sm_count - 1) / sm_count;
   const int64_t most = sm_count / plan.groups > 0 ? sm_count / plan.groups : 1;
   plan.columns = static_cast<int32_t>(T < most ? T : most);
-  // A decode step's tokens, less than two to a row of the table: dealt out in turn, so that a batch padded at its end is shared by
-  // all CTAs (130 requests padded to 256 tokens 13.8 us, in order 21.1). Else in order, for the entries that neighbours share (200
-  // requests of two tokens each, 16 heads, 20.3 us, in turn 27.0).
-  plan.stride = T < 2 * p.table_rows ? plan.columns : 1;
-  if (plan.stride > 1) together = 1;
+  // A decode step's tokens are dealt out in turn, so that a batch padded at its end is shared by all CTAs (130 requests padded to 256
+  // tokens 13.8 us, in order 21.1); others in order, for the entries that neighbours share (200 requests of two tokens each, 16
+  // heads, 20.3 us, in turn 27.0). With less than two tokens to a row of the table the step can be either (a table may have rows
+  // for more requests than there are in the step: 5,119 tokens of 5 of its 4,096 rows in turn 248 us, in order 157), and the
+  // tokens decide; their items are of one token then.
+  plan.stride = T > plan.columns && T < 2 * p.table_rows ? 0 : 1;
+  if (plan.stride == 0) together = 1;
   plan.together = static_cast<int32_t>(together);
   plan.lookahead = room / plan.together < kRing ? room / plan.together : kRing;
   CUtensorMap map;

@@ -248,3 +248,44 @@ def test_prompts_of_several_requests(H):
     c.q, c.req, c.pos, c.slots = c.q[order], c.req[order], c.pos[order], c.slots[order]
     out, lse = c.run()
     c.check(out, lse, tokens=[*sorted(c.skip), *range(0, len(tokens), 29)])
+
+
+@pytest.mark.parametrize("H,each", [(64, 12), (128, 7), (5, 12)])
+def test_a_table_with_rows_for_more_requests(H, each):
+    """Whether tokens go over the CTAs in order, and which entries they share, does not depend on rows that no token is of: items of one
+    token (of 64 heads and more all are) give the same bits. Padding, and tokens of requests that are not there, change nothing."""
+    c = Walk(H, H, 128, 4, each, 300, sink=True)
+    n = len(c.tokens)
+    want = [x.clone() for x in c.walk()]
+    c.check_tokens(*want, c.of_ctas())
+    c.table = np.concatenate([c.table, np.full((n, c.table.shape[1]), -1, np.int32)])
+    out, lse = c.walk()
+    assert binding.device_errors() == 0
+    if H >= 64:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    c.check_tokens(out, lse, c.of_ctas())
+    c.req[5::9] = -1
+    c.slots[3::7] = -1
+    c.skip = {t for t in range(n) if t % 7 == 3 or t % 9 == 5}
+    out, lse = c.walk()
+    assert binding.device_errors() == 1
+    left = torch.tensor([t in c.skip for t in range(n)], device="cuda")
+    assert (out[left] == 3).all() and (lse[left] == 7).all()
+    c.skip = set()
+    c.check_tokens(out, lse, [t for t in c.of_ctas() if not left[t]])
+
+
+def test_a_decode_step_with_a_few_drafts():
+    """Tokens of which some follow one another, some do not: either way of dealing them out."""
+    rng = np.random.default_rng(76)
+    for follow in (0.2, 0.8):
+        tokens, lens = [], []
+        while len(tokens) < 3 * sms():
+            p, k = int(rng.integers(0, 300)), 2 if rng.random() < follow else 1
+            tokens += consecutive(len(lens), p, k)
+            lens.append(p + k)
+        lens += [1] * (2 * len(tokens))
+        c = Case(77, tokens, lens, 9, 100, 4, BLOCK, sink=True, skip=[0, 50, len(tokens) - 1])
+        out, lse = c.run()
+        assert binding.device_errors() == 0
+        c.check(out, lse)
