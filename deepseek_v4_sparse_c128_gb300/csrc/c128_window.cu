@@ -11,9 +11,10 @@
 // the place of one that no token sees any more. A run (consecutive positions of one request) begins with all that its
 // first item sees; then an item brings an entry for each of its tokens.
 //
-// Measured, device time per call: 5,119 tokens of 64 heads, window 128 and 4 first entries, 155 us (as decode attention, token
-// by token, 341 us); 200 requests of one token each, 24.2 us; one token 9.0 us.
-// The least that a run takes is its queries and results, 2 KB a row (100 us of the 155); next are the tensor cores, which
+// Measured, device time per call: 5,119 tokens of 64 heads, window 128 and 4 first entries, 156 us (as decode attention, token
+// by token, 341 us); 200 requests of one token each, 24.2 us; one token 9.2 us. With few heads an item's chain of waits is the
+// same, and two tokens at most share one: 16 heads 92 us, 1 head 86.
+// The least that a run takes is its queries and results, 2 KB a row (100 us of the 156); next are the tensor cores, which
 // work 3,900 of the 8,900 cycles of an item of 64 rows, and the 16,600 instructions of its warps, half the issue slots. No unit
 // is full: an item's stages wait for one another, over one set of weights and one O, which is what TMEM's 512 columns
 // and shared memory leave room for. So the products of one item cover what lies between those of the next: S of
@@ -22,7 +23,7 @@
 // A masked entry has weight 0, and 0 times what stands there has to be 0 for every row: so an entry with a value that is
 // not finite is stored as zeros and marked, and its scores are NaN for the rows that see it, and for no other.
 //
-// Weights are rounded to bf16 for the second product (2^-9 of each on average). For bf16 results they are divided by their sum,
+// Weights are rounded to bf16 for the second product (2^-8 of each at most). For bf16 results they are divided by their sum,
 // which is in fp32 and of the exact weights, before that: so O is the result, a result of one entry is that entry, and nothing is
 // left to do between TMEM and memory but to round and store. For fp32 results they are rounded as they are, the largest 1, and O
 // is multiplied by the entries' share of all weight over the sum of the rounded ones (as in decode attention), so that their

@@ -585,12 +585,13 @@ int c128_norm_rope_store(const c128_tensor_t* positions, const c128_tensor_t* sl
  * one of them only).
  *
  * Where window + first <= 136 a kernel keeps the entries of consecutive tokens in shared memory: in a step of which most
- * tokens follow one another they are decoded once for all of them. There, for bf16 results, the softmax weights are divided by their sum (and the sink's share) before they
- * are rounded to bf16, so that of one entry out is that entry; for fp32 results out is divided by the sums of the rounded
- * weights, as for c128_decode_attention, which halves its error. lse is of the exact sums, in fp32. Larger windows run as
- * c128_decode_attention does, a token at a time; with up to 16 heads, and three tokens to a row of the table or more,
- * tokens that follow one another (four at most, between multiples of four) are taken together. (So there a step wants
- * the table's rows of its own requests, a slice, rather than those of all that there may be.)
+ * tokens follow one another they are decoded once for all of them. There, for bf16 results, the softmax weights are divided
+ * by their sum (and the sink's share) before they are rounded to bf16, so that of one entry out is that entry; for fp32
+ * results out is divided by the sums of the rounded weights, as for c128_decode_attention, which halves its error. lse is of
+ * the exact sums, in fp32. Larger windows run as c128_decode_attention does, a token at a time; with up to 16 heads, and
+ * three tokens to a row of the table or more, tokens that follow one another (four at most, between multiples of four) are
+ * taken together. (So there a step wants the table's rows of its own requests, a slice, rather than those of all that there
+ * may be.)
  * An entry that holds NaN makes out and lse of the tokens that see it NaN, and of no others; so does an infinity, or the
  * formula's value is stored.
  *
