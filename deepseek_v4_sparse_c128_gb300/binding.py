@@ -536,7 +536,8 @@ def window_attention(q, k_cache, kv_block_size: int, block_table, token_to_req_i
                      scale: float, out, first: int = 0, lse=None, sink=None, workspace=None, stream=None) -> None:
     """Attention of each token to the last ``window`` entries of its request up to its own, and the ``first`` ones
     (c128_window_attention in include/c128compress.h); ``out`` and ``lse`` are written. ``workspace`` as for
-    decode_attention, of window_attention_workspace bytes."""
+    decode_attention, of window_attention_workspace bytes. (One of decode_attention_workspace bytes is taken too; where that is
+    less, as for long windows of up to 16 heads, it is left alone, and the call takes another as if none had been given.)"""
     PreparedOp("window_attention", q, k_cache, kv_block_size, block_table, token_to_req_indices, positions, slot_mapping, window,
                scale, out, first=first, lse=lse, sink=sink, workspace=workspace, stream=stream)()
 
